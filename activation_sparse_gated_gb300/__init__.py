@@ -9,9 +9,13 @@ The functions mirror the C ABI one to one (``sffn_create``, ``sffn_set_live_frac
 ``sffn_forward``, ``sffn_active_counts``, ``sffn_active_mask``,
 ``sffn_synchronize``, ``sffn_destroy``, ``sffn_strerror``, ``sffn_last_error``,
 ``sffn_version``, ``sffn_debug_timeout_probe``, ``sffn_forward_noalloc``,
-``sffn_set_weights_int8``, ``sffn_get_weights_int8``).  Tensor arguments are passed by
+``sffn_set_weights_int8``, ``sffn_get_weights_int8``, and the handle-free operators ``sffn_route``,
+``sffn_quantize_tokens``, ``sffn_matmul_int8``, ``sffn_grouped_matmul``, ``sffn_experts_forward``
+with ``sffn_check``).  Tensor arguments are passed by
 their data pointer; ``stream`` defaults to the current torch stream.
-``SparseFFN`` wraps one handle.
+``SparseFFN`` wraps one handle; ``route``, ``quantize_tokens``, ``matmul_int8``, ``grouped_matmul``
+and ``experts_forward`` (module ``operators``) take and return torch tensors, and ``MoEFFN`` is the
+router with its experts as one layer.
 """
 from __future__ import annotations
 
@@ -28,12 +32,18 @@ SFFN_ERR_ARG, SFFN_ERR_ALIGN, SFFN_ERR_DTYPE, SFFN_ERR_CUDA = -1, -2, -3, -4
 SFFN_ERR_TIMEOUT, SFFN_ERR_STATE, SFFN_ERR_NOMEM, SFFN_ERR_DEVICE = -5, -6, -7, -8
 SFFN_MAX_BATCH = 128
 SFFN_GATE_TILED_G, SFFN_GATE_RMSNORM, SFFN_DOUBLE_ACT, SFFN_DETERMINISTIC = 1, 2, 4, 8
+SFFN_I8 = 4
+SFFN_MAX_EXPERTS, SFFN_MAX_CHOICES, SFFN_MAX_SUM, SFFN_MAX_ROWS = 1024, 32, 65536, 268435456
+SFFN_ROUTE_SIGMOID, SFFN_ROUTE_NORMALIZE = 1, 2
+SFFN_W_KN = 1
 
 #: every symbol include/sffn.h declares
 EXPORTS = ("sffn_create", "sffn_create_ex", "sffn_set_live_threshold", "sffn_set_live_fraction_hint", "sffn_set_weights", "sffn_forward", "sffn_active_counts",
            "sffn_active_mask", "sffn_synchronize", "sffn_destroy", "sffn_strerror",
            "sffn_last_error", "sffn_version", "sffn_debug_timeout_probe", "sffn_forward_noalloc",
-           "sffn_set_weights_int8", "sffn_get_weights_int8")
+           "sffn_set_weights_int8", "sffn_get_weights_int8",
+           "sffn_route_workspace", "sffn_route", "sffn_quantize_tokens", "sffn_matmul_int8", "sffn_grouped_matmul",
+           "sffn_experts_workspace", "sffn_experts_forward", "sffn_check")
 
 _lib = None
 
@@ -54,6 +64,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                           "(there is no CPU fallback)")
     lib = ctypes.CDLL(path)
     vp, ip, cp = ctypes.c_void_p, ctypes.c_int, ctypes.c_char_p
+    ll, sz = ctypes.c_longlong, ctypes.c_size_t
     sig = {
         "sffn_create": (vp, [ip, ip, ip, ip, ip]),
         "sffn_create_ex": (vp, [ip, ip, ip, ip, ip, ip]),
@@ -72,6 +83,14 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "sffn_forward_noalloc": (ip, [vp, vp, vp, vp, vp, vp, ip, ip, ip, ip, ip, vp]),
         "sffn_set_weights_int8": (ip, [vp] * 8),
         "sffn_get_weights_int8": (ip, [vp] * 8),
+        "sffn_route_workspace": (sz, [ip] * 3),
+        "sffn_route": (ip, [vp, ll, vp, vp, vp, vp, ip, ip, ip, ip, ip, vp, sz, vp]),
+        "sffn_quantize_tokens": (ip, [vp, ll, vp, vp, ip, ip, vp]),
+        "sffn_matmul_int8": (ip, [vp, ll, vp, vp, vp, vp, ll, ip, ip, ip, ip, vp]),
+        "sffn_grouped_matmul": (ip, [vp, ll, vp, vp, vp, vp, vp, ip, vp, ll] + [ip] * 8 + [vp]),
+        "sffn_experts_workspace": (sz, [ip] * 4),
+        "sffn_experts_forward": (ip, [vp, ll] + [vp] * 8 + [ip] * 6 + [vp, sz, vp]),
+        "sffn_check": (ip, [vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -196,6 +215,47 @@ def sffn_get_weights_int8(h, W1q, s1, W3q, s3, W2q, s2, stream=None):
                                                 _ptr(s2), _stream(stream)))
 
 
+def sffn_route_workspace(T: int, E: int, k: int) -> int:
+    return load().sffn_route_workspace(T, E, k)
+
+
+def sffn_route(logits, ld, weights, ids, offsets, rows, T: int, E: int, k: int, dtype: int, flags: int,
+               workspace=None, workspace_bytes: int = 0, stream=None):
+    return _check(load().sffn_route(_ptr(logits), ld, _ptr(weights), _ptr(ids), _ptr(offsets), _ptr(rows), T, E, k,
+                                    dtype, flags, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def sffn_quantize_tokens(x, ldx, q, scales, T: int, K: int, stream=None):
+    return _check(load().sffn_quantize_tokens(_ptr(x), ldx, _ptr(q), _ptr(scales), T, K, _stream(stream)))
+
+
+def sffn_matmul_int8(xq, ldx, sx, wq, sw, y, ldy, T: int, N: int, K: int, y_dtype: int, stream=None):
+    return _check(load().sffn_matmul_int8(_ptr(xq), ldx, _ptr(sx), _ptr(wq), _ptr(sw), _ptr(y), ldy, T, N, K,
+                                          y_dtype, _stream(stream)))
+
+
+def sffn_grouped_matmul(x, ldx, sx, w, sw, offsets, index, index_div: int, y, ldy, R: int, XR: int, N: int, K: int,
+                        E: int, dtype: int, y_dtype: int, flags: int = 0, stream=None):
+    return _check(load().sffn_grouped_matmul(_ptr(x), ldx, _ptr(sx), _ptr(w), _ptr(sw), _ptr(offsets), _ptr(index),
+                                             index_div, _ptr(y), ldy, R, XR, N, K, E, dtype, y_dtype, flags,
+                                             _stream(stream)))
+
+
+def sffn_experts_workspace(T: int, k: int, D: int, H: int) -> int:
+    return load().sffn_experts_workspace(T, k, D, H)
+
+
+def sffn_experts_forward(x, ldx, weights, ids, offsets, rows, W1, W3, W2t, y, T: int, E: int, k: int, D: int, H: int,
+                         act: int, workspace, workspace_bytes: int, stream=None):
+    return _check(load().sffn_experts_forward(_ptr(x), ldx, _ptr(weights), _ptr(ids), _ptr(offsets), _ptr(rows),
+                                              _ptr(W1), _ptr(W3), _ptr(W2t), _ptr(y), T, E, k, D, H, act,
+                                              _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def sffn_check(stream=None):
+    return _check(load().sffn_check(_stream(stream)))
+
+
 class SparseFFN:
     """One FFN layer held by the library (a wrapper around one handle).
 
@@ -280,3 +340,14 @@ class SparseFFN:
             self.close()
         except Exception:
             pass
+
+
+_OPERATORS = ("MoEFFN", "Routing", "experts_forward", "grouped_matmul", "matmul_int8", "quantize_tokens", "route")
+
+
+def __getattr__(name):  # the tensor operators import torch: only when they are asked for
+    if name in _OPERATORS:
+        from . import operators
+        globals().update({n: getattr(operators, n) for n in _OPERATORS})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

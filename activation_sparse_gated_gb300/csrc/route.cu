@@ -1,0 +1,284 @@
+// route.cu -- the router's choice and the grouping of its choices by expert.
+//
+// Per token the k largest of E logits (ties to the lowest index; -inf and NaN
+// are closed experts and are never chosen), their weights
+//   softmax   w_j = exp(z_j - m) / sum_i exp(z_i - m), i over the chosen
+//             (normalised) or over all E
+//   sigmoid   w_j = 1 / (1 + exp(-z_j)), over their sum when normalised,
+// and a stable counting sort of the T k choices by expert: offsets[E + 1] and,
+// for every grouped row, the choice token * k + place that it serves.
+//
+// One warp takes a token: the logits sit in registers (E / 32 a lane) as
+// order-preserving integer keys, and a choice is one warp-wide maximum of the
+// keys and one minimum of the indexes that hold it (redux, no shuffle trees).
+// The sort is exact integer work, so its result does not depend on timing:
+// blocks own consecutive tokens, count their choices per expert, and a second
+// kernel adds the counts of the blocks before it.  Up to ROUTE_ONE choices one
+// block does both.
+#include "common.cuh"
+#include "ops.h"
+
+namespace sffn {
+namespace {
+
+constexpr int ROUTE_WARPS = 16;
+constexpr int ROUTE_THREADS = 32 * ROUTE_WARPS;
+constexpr int ROUTE_ONE = 2048;   // choices that one block sorts by itself
+constexpr int ROUTE_BLOCKS = 128; // most blocks of the two-kernel form
+
+// Larger float <-> larger key; NaN and -inf share the key 0 (closed).
+__device__ __forceinline__ uint32_t order_key(float v) {
+  if (!(v > -INFINITY)) return 0u;
+  const uint32_t b = __float_as_uint(v + 0.f);  // -0 ties with 0
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+
+// exp(v - m) for v <= m, with equal infinities counting as equal
+__device__ __forceinline__ float exp_below(float v, float m) { return v == m ? 1.f : expf(v - m); }
+
+// One token by one warp: lane j < k ends up with choice j.  L: logits a lane.
+template <int L>
+__device__ __forceinline__ int choose(const RouteArgs& a, int t, int lane) {
+  uint32_t key[L];
+  const size_t base = (size_t)t * a.ld;
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    const int e = lane + 32 * i;
+    float v = -INFINITY;
+    if (e < a.E)
+      v = a.bf16 ? __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(a.logits)[base + e] << 16)
+                 : reinterpret_cast<const float*>(a.logits)[base + e];
+    key[i] = order_key(v);
+  }
+  uint32_t ck = 0;
+  int ce = -1;
+  float all = 0.f, m = 0.f;
+  for (int j = 0; j < a.k; ++j) {
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < L; ++i) best = max(best, key[i]);
+    best = __reduce_max_sync(0xffffffffu, best);
+    if (best == 0) break;  // no open expert is left
+    uint32_t at = 0xffffffffu;
+#pragma unroll
+    for (int i = L - 1; i >= 0; --i)
+      if (key[i] == best) at = (uint32_t)(lane + 32 * i);
+    at = __reduce_min_sync(0xffffffffu, at);
+    if (j == 0) {
+      m = key_value(best);
+      if (!a.sigmoid && !a.normalize) {  // the sum over every open expert
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+          if (key[i]) all += exp_below(key_value(key[i]), m);
+        all = warp_sum(all);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+      if (at == (uint32_t)(lane + 32 * i)) key[i] = 0;
+    if (lane == j) {
+      ck = best;
+      ce = (int)at;
+    }
+  }
+  float w = 0.f;
+  if (ce >= 0) w = a.sigmoid ? 1.f / (1.f + expf(-key_value(ck))) : exp_below(key_value(ck), m);
+  float total = 1.f;
+  if (a.normalize) total = warp_sum(w);
+  else if (!a.sigmoid) total = all;
+  if (lane < a.k) {
+    a.weights[(size_t)t * a.k + lane] = total > 0.f ? w / total : 0.f;
+    a.ids[(size_t)t * a.k + lane] = ce;
+  }
+  return ce;
+}
+
+// Tokens [t0, t1) of this block: choices, then counts per expert in s_hist.
+template <int L>
+__device__ __forceinline__ void choose_block(const RouteArgs& a, int t0, int t1, int* s_hist) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int e = threadIdx.x; e < a.E; e += ROUTE_THREADS) s_hist[e] = 0;
+  __syncthreads();
+  for (int t = t0 + warp; t < t1; t += ROUTE_WARPS) {
+    const int e = choose<L>(a, t, lane);
+    if (lane < a.k && e >= 0) atomicAdd(&s_hist[e], 1);
+  }
+  __syncthreads();
+}
+
+// Grouped rows of this block's choices, given s_base[e] = the row of its first
+// choice of expert e.  Warps take consecutive spans of choices; s_cnt[w][e]
+// counts span w, and the spans before a warp's own give its first row.
+__device__ __forceinline__ void scatter_block(const RouteArgs& a, int t0, int t1, const int* s_base, int* s_cnt,
+                                              int warps) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int p0 = t0 * a.k, n = (t1 - t0) * a.k;
+  const int span = ((n + warps - 1) / warps + 31) / 32 * 32;
+  for (int i = threadIdx.x; i < warps * a.E; i += ROUTE_THREADS) s_cnt[i] = 0;
+  __syncthreads();
+  const int b = min(n, warp * span), c = warp < warps ? min(n, b + span) : b;
+  for (int i = b + lane; i < c; i += 32) {
+    const int e = a.ids[p0 + i];
+    if (e >= 0) atomicAdd(&s_cnt[warp * a.E + e], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += ROUTE_THREADS) {
+    int at = s_base[e];
+    for (int w = 0; w < warps; ++w) {
+      const int v = s_cnt[w * a.E + e];
+      s_cnt[w * a.E + e] = at;
+      at += v;
+    }
+  }
+  __syncthreads();
+  for (int i0 = b; i0 < c; i0 += 32) {
+    const int i = i0 + lane;
+    const int e = i < c ? a.ids[p0 + i] : -1;
+    const uint32_t same = __match_any_sync(0xffffffffu, e);
+    if (e >= 0) {
+      const int rank = __popc(same & ((1u << lane) - 1));
+      const int at = s_cnt[warp * a.E + e] + rank;
+      a.rows[at] = p0 + i;
+    }
+    __syncwarp();
+    if (e >= 0 && (same >> lane) == 1u) s_cnt[warp * a.E + e] += __popc(same);  // the last lane of its expert
+    __syncwarp();
+  }
+}
+
+// Exclusive sums of s_v[0 .. E) into s_v, the total in s_v[E] (whole block).
+__device__ __forceinline__ void exclusive_scan(int* s_v, int E, int* s_w) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int carry = 0;
+  for (int e0 = 0; e0 < E; e0 += ROUTE_THREADS) {
+    const int e = e0 + tid;
+    const int v = e < E ? s_v[e] : 0;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_w[warp] = x;
+    __syncthreads();
+    int before = carry, total = carry;
+    for (int w = 0; w < ROUTE_WARPS; ++w) {
+      if (w < warp) before += s_w[w];
+      total += s_w[w];
+    }
+    if (e < E) s_v[e] = before + x - v;
+    carry = total;
+    __syncthreads();
+  }
+  if (tid == 0) s_v[E] = carry;
+  __syncthreads();
+}
+
+template <int L>
+__global__ void __launch_bounds__(ROUTE_THREADS) route_one_kernel(const RouteArgs a, int warps) {
+  extern __shared__ int sm[];
+  int* s_base = sm;               // [E + 1]
+  int* s_w = s_base + a.E + 1;    // [ROUTE_WARPS]
+  int* s_cnt = s_w + ROUTE_WARPS; // [warps][E]
+  pdl_launch_dependents();
+  pdl_wait();
+  choose_block<L>(a, 0, a.T, s_base);
+  exclusive_scan(s_base, a.E, s_w);
+  for (int e = threadIdx.x; e <= a.E; e += ROUTE_THREADS) a.offsets[e] = s_base[e];
+  const int total = s_base[a.E];
+  for (int i = total + threadIdx.x; i < a.T * a.k; i += ROUTE_THREADS) a.rows[i] = -1;
+  scatter_block(a, 0, a.T, s_base, s_cnt, warps);
+}
+
+template <int L>
+__global__ void __launch_bounds__(ROUTE_THREADS) route_choose_kernel(const RouteArgs a, int per) {
+  extern __shared__ int sm[];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int t0 = min(a.T, (int)blockIdx.x * per), t1 = min(a.T, t0 + per);
+  choose_block<L>(a, t0, t1, sm);
+  for (int e = threadIdx.x; e < a.E; e += ROUTE_THREADS) a.hist[(size_t)blockIdx.x * a.E + e] = sm[e];
+}
+
+__global__ void __launch_bounds__(ROUTE_THREADS) route_group_kernel(const RouteArgs a, int per, int nb, int warps) {
+  extern __shared__ int sm[];
+  int* s_base = sm;
+  int* s_w = s_base + a.E + 1;
+  int* s_mine = s_w + ROUTE_WARPS;  // [E] choices of the blocks before this one
+  int* s_cnt = s_mine + a.E;
+  pdl_launch_dependents();
+  pdl_wait();
+  for (int e = threadIdx.x; e < a.E; e += ROUTE_THREADS) {
+    int before = 0, total = 0;
+#pragma unroll 8
+    for (int b = 0; b < nb; ++b) {
+      const int v = a.hist[(size_t)b * a.E + e];
+      if (b < (int)blockIdx.x) before += v;
+      total += v;
+    }
+    s_mine[e] = before;
+    s_base[e] = total;
+  }
+  __syncthreads();
+  exclusive_scan(s_base, a.E, s_w);
+  const int total = s_base[a.E], t0 = min(a.T, (int)blockIdx.x * per), t1 = min(a.T, t0 + per);
+  if (blockIdx.x == 0) {
+    for (int e = threadIdx.x; e <= a.E; e += ROUTE_THREADS) a.offsets[e] = s_base[e];
+  }
+  for (int i = total + blockIdx.x * ROUTE_THREADS + threadIdx.x; i < a.T * a.k; i += gridDim.x * ROUTE_THREADS)
+    a.rows[i] = -1;
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += ROUTE_THREADS) s_base[e] += s_mine[e];
+  __syncthreads();
+  scatter_block(a, t0, t1, s_base, s_cnt, warps);
+}
+
+// warps that take part in the scatter: as many as 48 KB of shared counts have room for
+int scatter_warps(int E, int fixed_ints) {
+  const int w = (48 * 1024 / 4 - fixed_ints) / E;
+  return w < 1 ? 1 : w > ROUTE_WARPS ? ROUTE_WARPS : w;
+}
+
+int route_blocks(int T, int* per) {
+  *per = (T + ROUTE_BLOCKS - 1) / ROUTE_BLOCKS;
+  if (*per < ROUTE_WARPS) *per = ROUTE_WARPS;
+  return (T + *per - 1) / *per;
+}
+
+template <int L>
+cudaError_t route_l(const RouteArgs& a, cudaStream_t s) {
+  if ((long long)a.T * a.k <= ROUTE_ONE) {
+    const int fixed = a.E + 1 + ROUTE_WARPS, warps = scatter_warps(a.E, fixed);
+    return ops_launch(route_one_kernel<L>, dim3(1), ROUTE_THREADS, sizeof(int) * (fixed + warps * a.E), s, 1, a, warps);
+  }
+  int per;
+  const int nb = route_blocks(a.T, &per);
+  cudaError_t e = ops_launch(route_choose_kernel<L>, dim3(nb), ROUTE_THREADS, sizeof(int) * a.E, s, 1, a, per);
+  if (e != cudaSuccess) return e;
+  const int fixed = 2 * a.E + 1 + ROUTE_WARPS, warps = scatter_warps(a.E, fixed);
+  return ops_launch(route_group_kernel, dim3(nb), ROUTE_THREADS, sizeof(int) * (fixed + warps * a.E), s, 1, a, per, nb,
+                    warps);
+}
+
+}  // namespace
+
+size_t route_workspace(int T, int E, int k) {
+  if ((long long)T * k <= ROUTE_ONE) return 0;
+  int per;
+  return sizeof(int) * (size_t)route_blocks(T, &per) * E;
+}
+
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t s) {
+  const int l = (a.E + 31) / 32;
+  if (l <= 1) return route_l<1>(a, s);
+  if (l <= 2) return route_l<2>(a, s);
+  if (l <= 4) return route_l<4>(a, s);
+  if (l <= 8) return route_l<8>(a, s);
+  if (l <= 16) return route_l<16>(a, s);
+  return route_l<32>(a, s);
+}
+
+}  // namespace sffn

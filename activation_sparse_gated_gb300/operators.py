@@ -1,0 +1,250 @@
+"""The mixture-of-experts and 8-bit operators on torch tensors.
+
+Thin wrappers over the handle-free calls of include/sffn.h: they check shapes,
+types and strides, allocate outputs and scratch on the stream the call runs on,
+and pass pointers.  ``stream`` is a torch stream (default: the current one);
+tensors used on another stream than their own are the caller's to order, as
+with any torch operation.  Nothing here is differentiable, and a tensor that
+requires a gradient is refused while gradients are recorded.
+"""
+from __future__ import annotations
+
+from typing import NamedTuple
+
+import torch
+
+from . import (SFFN_ACT_RELU, SFFN_ACT_RSP, SFFN_ACT_SILU, SFFN_BF16, SFFN_F32, SFFN_I8, SFFN_OK,
+               SFFN_ROUTE_NORMALIZE, SFFN_ROUTE_SIGMOID, SFFN_W_KN, SffnError, load, sffn_last_error, sffn_strerror)
+
+_ACT = {"relu": SFFN_ACT_RELU, "rsp": SFFN_ACT_RSP, "silu": SFFN_ACT_SILU}
+_OUT = {"bf16": (torch.bfloat16, SFFN_BF16), "f32": (torch.float32, SFFN_F32),
+        torch.bfloat16: (torch.bfloat16, SFFN_BF16), torch.float32: (torch.float32, SFFN_F32)}
+
+
+class Routing(NamedTuple):
+    """``route``'s result: weights [T, k] fp32, ids [T, k], offsets [E + 1] and rows [T * k] (int32)."""
+    weights: torch.Tensor
+    ids: torch.Tensor
+    offsets: torch.Tensor
+    rows: torch.Tensor
+
+
+def _raw(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _done(rc):
+    if rc != SFFN_OK:
+        raise SffnError(rc, sffn_last_error() or sffn_strerror(rc))
+
+
+def _operand(name, t, dtypes, dim, device=None):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor")
+    if t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dimensions, not {t.dim()}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has type {t.dtype}, not {' or '.join(str(d) for d in dtypes)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not {device}")
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient: the operators have none")
+
+
+def _pitch(name, t):
+    """Row pitch of a matrix whose rows are dense (a single row or column: any stride will do)."""
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    return t.stride(0) if rows > 1 else cols
+
+
+def _dense(name, t):
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def route(logits, k: int, score: str = "softmax", normalize: bool = True, stream=None) -> Routing:
+    """The k largest of each token's logits [T, E] (fp32 or bf16), their weights and their grouping by expert."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return route(logits, k, score, normalize)
+    _operand("logits", logits, (torch.float32, torch.bfloat16), 2)
+    if score not in ("softmax", "sigmoid"):
+        raise ValueError(f"score {score!r} is neither 'softmax' nor 'sigmoid'")
+    T, E = logits.shape
+    if not 1 <= k <= E:
+        raise ValueError(f"k={k} outside 1..{E}")
+    device, lib, n = logits.device, load(), T * k
+    ld = _pitch("logits", logits)
+    buf = torch.empty(3 * n + E + 1, dtype=torch.int32, device=device)
+    weights, ids, rows, offsets = buf.split((n, n, n, E + 1))
+    weights, ids = weights.view(torch.float32).view(T, k), ids.view(T, k)
+    nb = lib.sffn_route_workspace(T, E, k)
+    ws = torch.empty(nb, dtype=torch.uint8, device=device) if nb else None
+    flags = (SFFN_ROUTE_SIGMOID if score == "sigmoid" else 0) | (SFFN_ROUTE_NORMALIZE if normalize else 0)
+    at = buf.data_ptr()
+    _done(lib.sffn_route(logits.data_ptr(), ld, at, at + 4 * n, at + 12 * n, at + 8 * n, T, E, k,
+                         SFFN_F32 if logits.dtype == torch.float32 else SFFN_BF16, flags,
+                         ws.data_ptr() if nb else None, nb, _raw(device)))
+    return Routing(weights, ids, offsets, rows)
+
+
+def quantize_tokens(x, stream=None):
+    """(codes int8 [T, K], scales fp32 [T]) of bf16 tokens x [T, K]."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return quantize_tokens(x)
+    _operand("x", x, (torch.bfloat16,), 2)
+    T, K = x.shape
+    q = torch.empty((T, K), dtype=torch.int8, device=x.device)
+    s = torch.empty(T, dtype=torch.float32, device=x.device)
+    _done(load().sffn_quantize_tokens(x.data_ptr(), _pitch("x", x), q.data_ptr(), s.data_ptr(), T, K, _raw(x.device)))
+    return q, s
+
+
+def _result(out, dtype, shape, device):
+    if dtype not in _OUT:
+        raise ValueError(f"dtype {dtype!r} is neither bf16 nor f32")
+    want, code = _OUT[dtype]
+    if out is None:
+        return torch.empty(shape, dtype=want, device=device), code, shape[1]
+    _operand("out", out, (torch.bfloat16, torch.float32), 2, device)
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"out has shape {tuple(out.shape)}, not {tuple(shape)}")
+    return out, _OUT[out.dtype][1], _pitch("out", out)
+
+
+def matmul_int8(xq, sx, wq, sw, dtype="bf16", out=None, stream=None):
+    """y[t, n] = sx[t] sw[n] sum_k xq[t, k] wq[n, k]; codes xq [T, K], wq [N, K], y of ``dtype`` (or ``out``'s)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return matmul_int8(xq, sx, wq, sw, dtype, out)
+    _operand("xq", xq, (torch.int8,), 2)
+    device = xq.device
+    _operand("wq", wq, (torch.int8,), 2, device)
+    _operand("sx", sx, (torch.float32,), 1, device)
+    _operand("sw", sw, (torch.float32,), 1, device)
+    T, K = xq.shape
+    N = wq.shape[0]
+    if wq.shape[1] != K:
+        raise ValueError(f"wq has {wq.shape[1]} columns, xq {K}")
+    if sx.shape[0] != T or sw.shape[0] != N:
+        raise ValueError("one scale per token and per row of wq")
+    for name, t in (("wq", wq), ("sx", sx), ("sw", sw)):
+        _dense(name, t)
+    y, code, ldy = _result(out, dtype, (T, N), device)
+    _done(load().sffn_matmul_int8(xq.data_ptr(), _pitch("xq", xq), sx.data_ptr(), wq.data_ptr(), sw.data_ptr(),
+                                  y.data_ptr(), ldy, T, N, K, code, _raw(device)))
+    return y
+
+
+def grouped_matmul(x, w, offsets, sx=None, sw=None, index=None, index_div: int = 1, transposed: bool = False,
+                   dtype="bf16", out=None, stream=None):
+    """Row r of expert e (offsets[e] <= r < offsets[e + 1]) of y is w[e] @ x[r]; with ``index``, w[e] @ x[index[r] //
+    index_div].  bf16 x [rows, K] and w [E, N, K] ([E, K, N] with ``transposed``), or int8 codes with their scales sx
+    [rows] and sw [E, N].  Rows past offsets[E] are not written."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return grouped_matmul(x, w, offsets, sx, sw, index, index_div, transposed, dtype, out)
+    _operand("x", x, (torch.bfloat16, torch.int8), 2)
+    device, i8 = x.device, x.dtype == torch.int8
+    _operand("w", w, (x.dtype,), 3, device)
+    _operand("offsets", offsets, (torch.int32,), 1, device)
+    XR, K = x.shape
+    E, N = w.shape[0], w.shape[2 if transposed else 1]
+    if w.shape[1 if transposed else 2] != K:
+        raise ValueError(f"w {tuple(w.shape)} does not go with x {tuple(x.shape)}")
+    if offsets.shape[0] != E + 1:
+        raise ValueError(f"offsets has {offsets.shape[0]} entries, not {E + 1}")
+    _dense("w", w)
+    _dense("offsets", offsets)
+    R = XR
+    if index is not None:
+        _operand("index", index, (torch.int32,), 1, device)
+        _dense("index", index)
+        R = index.shape[0]
+    if i8:
+        if sx is None or sw is None:
+            raise ValueError("int8 operands need sx and sw")
+        _operand("sx", sx, (torch.float32,), 1, device)
+        _operand("sw", sw, (torch.float32,), 2, device)
+        if sx.shape[0] != XR or tuple(sw.shape) != (E, N):
+            raise ValueError("one scale per row of x and per expert and row of w")
+        _dense("sx", sx)
+        _dense("sw", sw)
+    elif sx is not None or sw is not None:
+        raise ValueError("scales go with int8 operands")
+    y, code, ldy = _result(out, dtype, (R, N), device)
+    _done(load().sffn_grouped_matmul(
+        x.data_ptr(), _pitch("x", x), sx.data_ptr() if i8 else None, w.data_ptr(), sw.data_ptr() if i8 else None,
+        offsets.data_ptr(), index.data_ptr() if index is not None else None, index_div, y.data_ptr(), ldy, R, XR, N, K,
+        E, SFFN_I8 if i8 else SFFN_BF16, code, SFFN_W_KN if transposed else 0, _raw(device)))
+    return y
+
+
+def experts_forward(x, routing: Routing, W1, W3, W2t, act: str = "relu", out=None, stream=None):
+    """y[t] = sum_j weights[t, j] W2_e (A(W1_e x_t) * (W3_e x_t)) over the routing's choices e = ids[t, j]; x [T, D],
+    W1, W3 and W2t (W2 transposed) [E, H, D], all bf16."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return experts_forward(x, routing, W1, W3, W2t, act, out)
+    _operand("x", x, (torch.bfloat16,), 2)
+    device = x.device
+    if act not in _ACT:
+        raise ValueError(f"act {act!r} is none of {', '.join(_ACT)}")
+    T, D = x.shape
+    for name, t in (("W1", W1), ("W3", W3), ("W2t", W2t)):
+        _operand(name, t, (torch.bfloat16,), 3, device)
+        if t.shape != W1.shape or t.shape[2] != D:
+            raise ValueError(f"{name} {tuple(t.shape)} does not go with x {tuple(x.shape)} and W1 {tuple(W1.shape)}")
+        _dense(name, t)
+    E, H = W1.shape[0], W1.shape[1]
+    weights, ids, offsets, rows = routing
+    for name, t, dtype, dim in (("weights", weights, torch.float32, 2), ("ids", ids, torch.int32, 2),
+                                ("offsets", offsets, torch.int32, 1), ("rows", rows, torch.int32, 1)):
+        _operand(name, t, (dtype,), dim, device)
+        _dense(name, t)
+    k = weights.shape[1]
+    if weights.shape[0] != T or ids.shape != weights.shape or rows.shape[0] != T * k or offsets.shape[0] != E + 1:
+        raise ValueError("the routing is of other tokens or experts")
+    if out is None:
+        out = torch.empty((T, D), dtype=torch.bfloat16, device=device)
+    else:
+        _operand("out", out, (torch.bfloat16,), 2, device)
+        if tuple(out.shape) != (T, D):
+            raise ValueError(f"out has shape {tuple(out.shape)}, not {(T, D)}")
+        _dense("out", out)
+    lib = load()
+    nb = lib.sffn_experts_workspace(T, k, D, H)
+    ws = torch.empty(nb, dtype=torch.uint8, device=device)
+    _done(lib.sffn_experts_forward(
+        x.data_ptr(), _pitch("x", x), weights.data_ptr(), ids.data_ptr(), offsets.data_ptr(), rows.data_ptr(),
+        W1.data_ptr(), W3.data_ptr(), W2t.data_ptr(), out.data_ptr(), T, E, k, D, H, _ACT[act], ws.data_ptr(), nb,
+        _raw(device)))
+    return out
+
+
+class MoEFFN:
+    """A mixture of gated experts behind its router, ``y = moe(x)`` for x [T, D] bf16.
+
+    ``Wr`` [E, D] is the router's matrix (its logits are an fp32 product by torch), W1, W3 [E, H, D] and
+    W2 [E, D, H] the experts' weights; W2 is laid out once as [E, H, D], so that a live unit's column is
+    one contiguous row.  ``k`` choices a token, ``score`` and ``normalize`` as in :func:`route`.
+    """
+
+    def __init__(self, Wr, W1, W3, W2, k: int, act: str = "relu", score: str = "softmax", normalize: bool = True):
+        self.Wr = Wr.float()
+        self.W1, self.W3 = W1.contiguous(), W3.contiguous()
+        self.W2t = W2.transpose(1, 2).contiguous()
+        self.k, self.act, self.score, self.normalize = k, act, score, normalize
+
+    def route(self, x):
+        return route(x.float() @ self.Wr.T, self.k, self.score, self.normalize)
+
+    def forward(self, x):
+        return experts_forward(x, self.route(x), self.W1, self.W3, self.W2t, self.act)
+
+    __call__ = forward

@@ -322,6 +322,112 @@ int sffn_debug_timeout_probe(sffn_t h, int limit_us, void* stream);
 int sffn_forward_noalloc(const void* W1, const void* W3, const void* W2t, const void* x, void* y,
                          int* counts, int D, int H, int B, int act, int dtype, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Mixture-of-experts and 8-bit operators.
+ *
+ * A served cast model runs its experts as many small gated FFNs ("Model Casting
+ * and Low-Parameter Gating" casts the expert FFNs of a mixture as well) and
+ * batches of int8 tokens as products of codes.  These calls have no handle:
+ * weights stay where the caller keeps them, scratch is the caller's
+ * `workspace` (16-byte aligned, contents don't matter, must not be shared by
+ * calls that may overlap), and nothing is kept from one call to the next.
+ * Every call is asynchronous and ordered on `stream`, may be captured into a
+ * graph, checks its arguments before it touches the device, and takes empty
+ * inputs (T or R = 0).  All pointers are device pointers; sums are fp32 (int8
+ * products: exact integers as long as fp32 holds them), results are rounded
+ * once to y's type and do not depend on timing, so a call repeated on the same
+ * inputs gives the same bits.
+ * The operators are inference only, like the rest of the library.
+ */
+
+/* int8 codes of both operands (the operators below; not a handle's dtype) */
+enum { SFFN_I8 = 4 };
+#define SFFN_MAX_EXPERTS 1024
+#define SFFN_MAX_CHOICES 32
+#define SFFN_MAX_SUM 65536      /* longest sum (K, D, H) of the operators */
+#define SFFN_MAX_ROWS 268435456 /* most rows (R, T * k) and columns (N) */
+
+/*
+ * The router's choice and its grouping by expert.  Of each token's E logits
+ * (row t at logits + t * ld elements; dtype SFFN_F32 or SFFN_BF16) the k
+ * largest are chosen, the largest first, ties to the lowest index; -inf and NaN
+ * mark a closed expert, which is never chosen.
+ *   weights [T, k] fp32: exp(z_j - m) / sum exp(z_i - m), summed over all open
+ *     experts, or over the chosen ones with SFFN_ROUTE_NORMALIZE;
+ *     SFFN_ROUTE_SIGMOID: 1 / (1 + exp(-z_j)), over the chosen ones' sum with
+ *     SFFN_ROUTE_NORMALIZE.  0 for a place without an open expert.
+ *   ids [T, k]: the chosen experts, -1 for a place without an open expert.
+ *   offsets [E + 1], rows [T * k]: the choices in order of (expert, token,
+ *     place): grouped row r of expert e, offsets[e] <= r < offsets[e + 1], is
+ *     choice rows[r] = token * k + place; rows past offsets[E] hold -1.
+ * 1 <= E <= SFFN_MAX_EXPERTS, 1 <= k <= min(E, SFFN_MAX_CHOICES).  The workspace
+ * holds sffn_route_workspace(T, E, k) bytes (0 for small T k: NULL is fine).
+ */
+enum { SFFN_ROUTE_SIGMOID = 1, SFFN_ROUTE_NORMALIZE = 2 };
+size_t sffn_route_workspace(int T, int E, int k);
+int sffn_route(const void* logits, long long ld, float* weights, int* ids, int* offsets, int* rows, int T, int E,
+               int k, int dtype, int flags, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Symmetric int8 codes of bf16 tokens, x row t at x + t * ldx elements:
+ * scales[t] = max|x_t| / 127, q[t, i] = round-half-to-even(x[t, i] / scales[t]),
+ * both decided in binary32 (the rule of the library's weight codes).  An
+ * all-zero token gets scale 0 and codes 0; a token that holds a NaN or an
+ * infinity gets scale NaN and codes 0.  Any K >= 1.
+ */
+int sffn_quantize_tokens(const void* x, long long ldx, int8_t* q, float* scales, int T, int K, void* stream);
+
+/*
+ * y[t, n] = sx[t] sw[n] sum_k xq[t, k] wq[n, k]: int8 codes xq [T, K] (row
+ * pitch ldx) and wq [N, K] with one scale per token and per output channel;
+ * y [T, N] (row pitch ldy) bf16 or f32.  K % 16 == 0, ldx % 16 == 0, xq and wq
+ * 16-byte aligned.
+ */
+int sffn_matmul_int8(const int8_t* xq, long long ldx, const float* sx, const int8_t* wq, const float* sw, void* y,
+                     long long ldy, int T, int N, int K, int y_dtype, void* stream);
+
+/*
+ * Products grouped by expert with ragged sizes: for the rows r of expert e,
+ * offsets[e] <= r < offsets[e + 1] (device ints, non-decreasing from 0; groups
+ * may be empty; offsets may be NULL for E == 1: all R rows),
+ *     y[r, n] = sum_k x[s(r), k] w[e, n, k]          (dtype SFFN_BF16), or
+ *     y[r, n] = sx[s(r)] sw[e, n] sum_k ...          (dtype SFFN_I8)
+ * with s(r) = r, or index[r] / index_div when index is given (the rows of
+ * sffn_route with index_div = k read the tokens themselves, with no gathered
+ * copy); a source row outside 0 .. XR - 1 reads as zeros.  x [XR, K] (row pitch
+ * ldx), w [E, N, K] dense, y [R, N] (row pitch ldy) bf16 or f32; rows of y past
+ * offsets[E] are left as they are, offsets past R are cut to R.  SFFN_W_KN
+ * (bf16): w is [E, K, N].  K % 8 == 0 (bf16) or K % 16 == 0 (int8), ldx
+ * likewise, N % 8 == 0 with SFFN_W_KN; x and w 16-byte aligned; y overlaps
+ * neither.
+ */
+enum { SFFN_W_KN = 1 };
+int sffn_grouped_matmul(const void* x, long long ldx, const float* sx, const void* w, const float* sw,
+                        const int* offsets, const int* index, int index_div, void* y, long long ldy, int R, int XR,
+                        int N, int K, int E, int dtype, int y_dtype, int flags, void* stream);
+
+/*
+ * The gated experts behind the router:
+ *     y_t = sum_j weights[t, j] W2_e (A(W1_e x_t) .* (W3_e x_t)),  e = ids[t, j]
+ * in bf16 with fp32 sums.  weights, ids, offsets, rows are sffn_route's outputs
+ * for the same T, E, k; W1, W3 are [E, H, D] and W2t is W2 transposed, [E, H, D]
+ * (row i of expert e is column i of W2_e), dense; x [T, D] (row pitch ldx), y
+ * [T, D] dense, fully written: a token without an open expert gets 0, a choice
+ * of weight 0 adds nothing.  D % 8 == 0, any H >= 1.  x, W1, W3, W2t and y are
+ * 16-byte aligned and y overlaps none of them; the workspace holds
+ * sffn_experts_workspace(T, k, D, H) bytes.
+ */
+size_t sffn_experts_workspace(int T, int k, int D, int H);
+int sffn_experts_forward(const void* x, long long ldx, const float* weights, const int* ids, const int* offsets,
+                         const int* rows, const void* W1, const void* W3, const void* W2t, void* y, int T, int E, int k,
+                         int D, int H, int act, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Wait for `stream` and report (and clear) a device-side error that any of the
+ * operators above recorded on this device: SFFN_ERR_TIMEOUT, SFFN_ERR_DEVICE.
+ */
+int sffn_check(void* stream);
+
 #ifdef __cplusplus
 }
 #endif

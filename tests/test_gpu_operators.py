@@ -1,0 +1,446 @@
+"""The mixture-of-experts and 8-bit operators against plain implementations in 64 bits.
+
+Tolerances count roundings: a result rounded to type t is off by eps(t) / 2 of itself, and an fp32
+sum of K products by at most K * 2^-23 of the sum of their magnitudes (each step one rounding, or
+one truncation on the tensor cores).
+"""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+import activation_sparse_gated_gb300 as sffn  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+BF, DEV = torch.bfloat16, "cuda"
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+
+
+@pytest.fixture(autouse=True)
+def no_device_error(cuda_ok):
+    yield
+    sffn.sffn_check()
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def close(y, ref, bound):
+    """|y - ref| <= bound + half a step of y's type, everywhere; NaN and infinities in the same places."""
+    y64 = y.double()
+    assert torch.equal(torch.isnan(y64), torch.isnan(ref))
+    ok = torch.isfinite(ref)
+    off = (y64 - ref).abs() - HALF[y.dtype] * 1.01 * ref.abs() - bound
+    worst = off[ok].max().item() if ok.any() else 0.0
+    assert worst <= 1e-30, f"off by {worst} more than the bound"
+
+
+# ------------------------------------------------------------------ route
+
+
+def plain_route(z, k, score, normalize):
+    z = z.double().cpu()
+    T, E = z.shape
+    z = torch.where(torch.isnan(z), torch.full_like(z, -math.inf), z)
+    order = torch.sort(-z, dim=1, stable=True).indices[:, :k]  # equal values keep the order of their indices
+    v = z.gather(1, order)
+    is_open = v > -math.inf
+    m = torch.where(is_open[:, :1], v[:, :1], torch.zeros_like(v[:, :1]))
+    ex = lambda a: torch.where(a == m, torch.ones_like(a), torch.exp(a - m))  # noqa: E731
+    w = ex(v) if score == "softmax" else torch.sigmoid(v)
+    w = torch.where(is_open, w, torch.zeros_like(w))
+    if normalize:
+        total = w.sum(1, keepdim=True)
+    else:
+        total = torch.where(z > -math.inf, ex(z), torch.zeros_like(z)).sum(1, keepdim=True)
+        total = total if score == "softmax" else torch.ones_like(total)
+    w = torch.where(total > 0, w / total, torch.zeros_like(w))
+    ids = torch.where(is_open, order, torch.full_like(order, -1))
+    flat = ids.reshape(-1)
+    groups = [torch.nonzero(flat == e).reshape(-1).tolist() for e in range(E)]
+    rows, offsets = sum(groups, []), [0]
+    for part in groups:
+        offsets.append(offsets[-1] + len(part))
+    return w, ids, offsets, rows + [-1] * (T * k - len(rows))
+
+
+def check_route(z, k, score, normalize):
+    w, ids, offsets, rows = sffn.route(z, k, score=score, normalize=normalize)
+    pw, pids, poff, prows = plain_route(z, k, score, normalize)
+    assert torch.equal(ids.cpu().long(), pids)
+    assert offsets.tolist() == poff
+    assert rows.tolist() == prows
+    # exp (2 ulp of its own and the rounded difference), a sum of E terms, a quotient
+    tol = (z.shape[1] + 8) * 2.0 ** -23
+    torch.testing.assert_close(w.double().cpu(), pw, rtol=tol, atol=1e-30 if score == "softmax" else 1e-37)
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 64, 8), (3, 7, 7), (17, 33, 4), (128, 64, 8), (255, 256, 8),
+                                   (257, 8, 8), (300, 100, 32), (513, 1024, 5), (2049, 16, 1), (1000, 96, 3)])
+@pytest.mark.parametrize("score,normalize", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
+def test_route_sizes(T, E, k, score, normalize):
+    check_route(torch.randn(T, E, generator=gen(T + E), device=DEV), k, score, normalize)
+
+
+@pytest.mark.parametrize("T", [5, 700])
+def test_route_ties_masks_and_odd_values(T):
+    z = torch.randn(T, 48, generator=gen(1), device=DEV).round()  # many ties, zeros of both signs among them
+    z[0] = -math.inf                 # a token with no expert
+    z[1] = math.nan
+    z[2] = 0.0
+    z[3, 5] = math.inf
+    z[3, 9] = math.inf
+    z[4] = torch.finfo(torch.float32).min
+    z[4, 7] = math.nan
+    for score in ("softmax", "sigmoid"):
+        check_route(z, 6, score, True)
+    check_route(z.to(BF), 6, "softmax", True)
+
+
+def test_route_negative_zero_ties_with_zero():
+    z = torch.full((1, 8), -1.0, device=DEV)
+    z[0, 2], z[0, 5] = -0.0, 0.0
+    assert sffn.route(z, 2).ids.tolist() == [[2, 5]]
+
+
+def test_route_strided_logits_and_empty():
+    z = torch.randn(300, 96, generator=gen(2), device=DEV)
+    a, b = sffn.route(z[:, :64], 8), sffn.route(z[:, :64].contiguous(), 8)
+    for p, q in zip(a, b):
+        assert torch.equal(p, q)
+    empty = sffn.route(z[:0], 8)
+    assert empty.offsets.tolist() == [0] * 97 and empty.ids.shape == (0, 8)
+
+
+# ------------------------------------------------------------------ quantize
+
+
+@pytest.mark.parametrize("T,K", [(1, 1), (1, 2560), (3, 17), (64, 384), (5, 1000), (33, 1024), (7, 4096), (9, 8200),
+                                 (4, 14336), (2, 20000), (3, 65536)])
+def test_quantize_tokens(T, K):
+    x = torch.randn(T, K, generator=gen(K), device=DEV).to(BF)
+    if T > 1:
+        x[1] = 0
+    if T > 2:
+        x[2] = x[2] * 1e30
+    q, s = sffn.quantize_tokens(x)
+    xc = x.float().cpu().numpy()
+    sc = abs(xc).max(1) / xc.dtype.type(127)
+    code = (xc / (sc + (sc == 0))[:, None]).round().clip(-127, 127)
+    assert (s.cpu().numpy() == sc).all()
+    assert (q.cpu().numpy() == code).all()
+
+
+def test_quantize_special_values_and_strides():
+    x = torch.randn(6, 512, generator=gen(3), device=DEV).to(BF)
+    x[1, 3], x[2, 5], x[3, 7] = math.nan, math.inf, -math.inf
+    x[4] = 1e-40  # below the smallest normal value
+    q, s = sffn.quantize_tokens(x)
+    assert torch.isnan(s[1:4]).all() and (q[1:4] == 0).all()
+    assert torch.isfinite(s[[0, 4, 5]]).all()
+    big = torch.randn(5, 300, generator=gen(4), device=DEV).to(BF)
+    for view in (big[:, 3:203], big[:, 8:264], big[::2]):
+        a, b = sffn.quantize_tokens(view), sffn.quantize_tokens(view.contiguous())
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+# ------------------------------------------------------------------ products
+
+
+def int8_operands(g, rows, K, full=False):
+    q = torch.randint(-128 if full else -127, 128, (rows, K), generator=g, device=DEV, dtype=torch.int8)
+    return q, torch.rand(rows, generator=g, device=DEV) + 0.5
+
+
+def int8_bound(xq, wq, scale):
+    """fp32 holds the integer sums below 2^24; past it each step may lose 2^-23 of the magnitudes."""
+    mag = xq.double().abs() @ wq.double().abs().T
+    return torch.where(mag < 2 ** 24, torch.zeros_like(mag), mag * xq.shape[1] * 2.0 ** -23) * scale
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 1, 16), (1, 7168, 2560), (2, 129, 64), (3, 100, 400), (8, 1024, 384),
+                                   (9, 257, 1040), (16, 2560, 512), (17, 128, 128), (31, 300, 2560), (77, 2560, 7168),
+                                   (64, 1000, 4096), (128, 128, 144), (129, 513, 640), (257, 384, 1024),
+                                   (500, 1001, 272), (1030, 520, 2048), (40, 90, 65536)])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_matmul_int8(T, N, K, out):
+    g = gen(T * 7 + N)
+    xq, sx = int8_operands(g, T, K, full=True)
+    wq, sw = int8_operands(g, N, K)
+    y = sffn.matmul_int8(xq, sx, wq, sw, dtype=out)
+    scale = torch.outer(sx.double(), sw.double())
+    ref = (xq.double() @ wq.double().T) * scale
+    close(y, ref, 3 * 2.0 ** -24 * ref.abs() + int8_bound(xq, wq, scale))
+
+
+def test_matmul_int8_strides_zero_scales_and_out():
+    g = gen(11)
+    big, sx = int8_operands(g, 40, 512)
+    wq, sw = int8_operands(g, 70, 256)
+    sx[3], sx[5] = 0.0, math.nan
+    x = big[:, 128:384]
+    y = sffn.matmul_int8(x, sx, wq, sw, dtype="f32")
+    ref = (x.double() @ wq.double().T) * torch.outer(sx.double(), sw.double())
+    close(y, ref, 3 * 2.0 ** -24 * ref.abs())
+    assert (y[3] == 0).all() and torch.isnan(y[5]).all()
+    wide = torch.full((40, 100), 7.0, device=DEV)
+    sffn.matmul_int8(x, sx, wq, sw, out=wide[:, 10:80])
+    assert torch.equal(wide[:, 10:80].nan_to_num(), y.nan_to_num())
+    assert (wide[:, :10] == 7).all() and (wide[:, 80:] == 7).all()
+
+
+def offsets_of(counts):
+    return torch.tensor([0] + counts, device=DEV).cumsum(0).to(torch.int32)
+
+
+GROUPS = [[1], [0, 1, 0], [1, 1, 1, 1], [3, 0, 5, 1], [16, 17, 0, 31, 1], [0, 0, 40, 0], [130, 1, 0, 127],
+          [300, 5, 129, 256, 257, 0, 2], [0] * 30 + [2, 1] + [0] * 30 + [9]]
+
+
+@pytest.mark.parametrize("counts", GROUPS, ids=str)
+@pytest.mark.parametrize("N,K", [(1, 8), (100, 72), (128, 64), (256, 384), (1000, 520)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_grouped_matmul_bf16(counts, N, K, out):
+    g, R, E = gen(N + K), sum(counts), len(counts)
+    x = torch.randn(R, K, generator=g, device=DEV).to(BF)
+    w = torch.randn(E, N, K, generator=g, device=DEV).to(BF)
+    off = offsets_of(counts)
+    y = sffn.grouped_matmul(x, w, off, dtype=out)
+    b = off.tolist()
+    for e in range(E):
+        xe, we = x[b[e]:b[e + 1]].double(), w[e].double()
+        close(y[b[e]:b[e + 1]], xe @ we.T, K * 2.0 ** -23 * (xe.abs() @ we.abs().T))
+
+
+@pytest.mark.parametrize("counts", GROUPS, ids=str)
+@pytest.mark.parametrize("N,K", [(8, 8), (104, 70), (128, 64), (256, 384), (1000, 519)])
+def test_grouped_matmul_transposed_weights(counts, N, K):
+    g, R, E = gen(N + K), sum(counts), len(counts)
+    pitch = (K + 7) // 8 * 8
+    x = torch.zeros(R, pitch, device=DEV, dtype=BF)
+    x[:, :K] = torch.randn(R, K, generator=g, device=DEV).to(BF)
+    w = torch.zeros(E, pitch, N, device=DEV, dtype=BF)
+    w[:, :K] = torch.randn(E, K, N, generator=g, device=DEV).to(BF)
+    off = offsets_of(counts)
+    y = sffn.grouped_matmul(x, w, off, transposed=True)
+    b = off.tolist()
+    for e in range(E):
+        xe, we = x[b[e]:b[e + 1]].double(), w[e].double()
+        close(y[b[e]:b[e + 1]], xe @ we, K * 2.0 ** -23 * (xe.abs() @ we.abs()))
+
+
+@pytest.mark.parametrize("counts", GROUPS, ids=str)
+@pytest.mark.parametrize("N,K", [(1, 16), (100, 80), (256, 384), (1000, 528)])
+def test_grouped_matmul_int8(counts, N, K):
+    g, R, E = gen(N + K), sum(counts), len(counts)
+    x, sx = int8_operands(g, R, K)
+    w, sw = int8_operands(g, E * N, K, full=True)
+    w, sw = w.view(E, N, K), sw.view(E, N)
+    off = offsets_of(counts)
+    y = sffn.grouped_matmul(x, w, off, sx=sx, sw=sw, dtype="f32")
+    b = off.tolist()
+    for e in range(E):
+        r = slice(b[e], b[e + 1])
+        scale = torch.outer(sx[r].double(), sw[e].double())
+        ref = (x[r].double() @ w[e].double().T) * scale
+        close(y[r], ref, 3 * 2.0 ** -24 * ref.abs() + int8_bound(x[r], w[e], scale))
+
+
+@pytest.mark.parametrize("T,k", [(3, 2), (50, 3), (300, 2)])
+def test_grouped_matmul_reads_tokens_through_an_index(T, k):
+    g, E, N, K = gen(T), 5, 200, 136
+    routing = sffn.route(torch.randn(T, E, generator=g, device=DEV), k)
+    big = torch.randn(T, K + 24, generator=g, device=DEV).to(BF)
+    x = big[:, 8:8 + K]
+    w = torch.randn(E, N, K, generator=g, device=DEV).to(BF)
+    y = sffn.grouped_matmul(x, w, routing.offsets, index=routing.rows, index_div=k, dtype="f32")
+    z = sffn.grouped_matmul(x[(routing.rows // k).long()].contiguous(), w, routing.offsets, dtype="f32")
+    assert torch.equal(y, z)
+
+
+def test_grouped_matmul_int8_reads_tokens_through_an_index():
+    g, T, k, E, N, K = gen(61), 120, 3, 5, 200, 144
+    routing = sffn.route(torch.randn(T, E, generator=g, device=DEV), k)
+    x, sx = int8_operands(g, T, K)
+    w, sw = int8_operands(g, E * N, K)
+    w, sw = w.view(E, N, K), sw.view(E, N)
+    src = (routing.rows // k).long()
+    y = sffn.grouped_matmul(x, w, routing.offsets, sx=sx, sw=sw, index=routing.rows, index_div=k, dtype="f32")
+    z = sffn.grouped_matmul(x[src].contiguous(), w, routing.offsets, sx=sx[src].contiguous(), sw=sw, dtype="f32")
+    assert torch.equal(y, z)
+
+
+def test_grouped_matmul_source_rows_out_of_range_read_as_zeros():
+    g = gen(21)
+    x = torch.randn(10, 64, generator=g, device=DEV).to(BF)
+    w = torch.randn(2, 128, 64, generator=g, device=DEV).to(BF)
+    for n in (4, 40):
+        index = torch.arange(n, dtype=torch.int32, device=DEV) % 10
+        index[1], index[2] = 10, -7
+        y = sffn.grouped_matmul(x, w, offsets_of([n // 2, n - n // 2]), index=index, dtype="f32")
+        assert (y[1:3] == 0).all()
+        assert (y[0] != 0).any() and torch.isfinite(y).all()
+
+
+@pytest.mark.parametrize("n", [6, 200])
+def test_grouped_matmul_keeps_rows_past_the_groups(n):
+    g = gen(22)
+    x = torch.randn(n, 64, generator=g, device=DEV).to(BF)
+    x[n // 2:] = math.nan  # rows of no group
+    w = torch.randn(3, 96, 64, generator=g, device=DEV).to(BF)
+    y = torch.full((n, 96), 5.0, device=DEV)
+    sffn.grouped_matmul(x, w, offsets_of([1, 0, n // 2 - 1]), out=y)
+    assert torch.isfinite(y).all() and (y[n // 2:] == 5).all()
+    # a broken list of offsets stays inside the buffers: cut to R, never below the group's start
+    guard = torch.full((n + 4, 96), 5.0, device=DEV)
+    bad = torch.tensor([0, n + 50, -3, 2 * n], dtype=torch.int32, device=DEV)
+    sffn.grouped_matmul(x, w, bad, out=guard[2:n + 2])
+    assert (guard[:2] == 5).all() and (guard[n + 2:] == 5).all()
+
+
+def test_grouped_matmul_keeps_nan_and_infinity_to_their_rows():
+    g = gen(23)
+    for n in (4, 60):
+        x = torch.randn(2 * n, 128, generator=g, device=DEV).to(BF)
+        w = torch.randn(2, 72, 128, generator=g, device=DEV).to(BF)
+        clean = sffn.grouped_matmul(x, w, offsets_of([n, n]))
+        x[1, 5], x[n, 7] = math.nan, math.inf
+        y = sffn.grouped_matmul(x, w, offsets_of([n, n]))
+        keep = [r for r in range(2 * n) if r not in (1, n)]
+        assert torch.equal(y[keep], clean[keep])
+        assert torch.isnan(y[1]).all() and not torch.isfinite(y[n]).any()
+
+
+# ------------------------------------------------------------------ the experts
+
+
+def act64(z, act):
+    if act == "relu":
+        return z.clamp(min=0)
+    v = z * torch.sigmoid(z)
+    return v if act == "silu" else torch.where(z > 0, v, torch.zeros_like(v))
+
+
+def check_experts(x, routing, W1, W3, W2t, act, y):
+    """Against 64 bits.  h may be off by the fp32 sums of its two factors and one rounding to bf16; a choice's
+    product by its sum; the combination by k sums."""
+    T, D = x.shape
+    k, E, H = routing.ids.shape[1], W1.shape[0], W1.shape[1]
+    ref, bound = torch.zeros(T, D, dtype=torch.float64, device=DEV), torch.zeros(T, D, dtype=torch.float64, device=DEV)
+    for e in range(E):
+        t, j = torch.nonzero(routing.ids == e, as_tuple=True)
+        if not len(t):
+            continue
+        xe, w1, w3, w2 = x[t].double(), W1[e].double(), W3[e].double(), W2t[e].double()
+        z, u = xe @ w1.T, xe @ w3.T
+        a = act64(z, act)
+        dz, du = (D * 2.0 ** -23 * (xe.abs() @ w.abs().T) for w in (w1, w3))
+        h = a * u
+        dh = 1.1 * dz * u.abs() + (a.abs() + 1.1 * dz) * du + 2.0 ** -8 * 1.01 * h.abs() + 2.0 ** -20 * h.abs()
+        w = routing.weights[t, j].double()[:, None]
+        mag = h.abs() @ w2.abs()
+        ref.index_add_(0, t, w * (h @ w2))
+        bound.index_add_(0, t, w * (dh @ w2.abs() + (H + k + 4) * 2.0 ** -23 * mag))
+    close(y, ref, bound)
+
+
+@pytest.mark.parametrize("T,E,k,D,H", [(1, 1, 1, 8, 1), (1, 8, 2, 128, 100), (1, 64, 8, 2560, 1024), (2, 4, 3, 264, 65),
+                                       (5, 16, 4, 384, 130), (33, 8, 2, 520, 200), (64, 64, 8, 256, 96),
+                                       (200, 6, 2, 384, 257), (513, 5, 3, 256, 128), (300, 128, 4, 136, 72)])
+@pytest.mark.parametrize("act", ["relu", "rsp", "silu"])
+def test_experts_forward(T, E, k, D, H, act):
+    g = gen(T + D + H)
+    x = torch.randn(T, D, generator=g, device=DEV).to(BF)
+    W1, W3 = ((torch.randn(E, H, D, generator=g, device=DEV) * D ** -0.5).to(BF) for _ in range(2))
+    W2t = (torch.randn(E, H, D, generator=g, device=DEV) * H ** -0.5).to(BF)
+    x[:, -1] = 1
+    W1[:, :, -1] = -1.0
+    routing = sffn.route(torch.randn(T, E, generator=g, device=DEV), k)
+    y = sffn.experts_forward(x, routing, W1, W3, W2t, act=act)
+    check_experts(x, routing, W1, W3, W2t, act, y)
+    again = sffn.experts_forward(x, routing, W1, W3, W2t, act=act)
+    assert torch.equal(y, again)
+
+
+@pytest.mark.parametrize("T", [3, 90])
+def test_experts_closed_tokens_strides_and_streams(T):
+    g, E, k, D, H = gen(T), 6, 2, 256, 96
+    big = torch.randn(T, 2 * D, generator=g, device=DEV).to(BF)
+    x = big[:, D // 2:D // 2 + D]
+    W1, W3, W2t = ((torch.randn(E, H, D, generator=g, device=DEV) * 0.1).to(BF) for _ in range(3))
+    z = torch.randn(T, E, generator=g, device=DEV)
+    z[1] = -math.inf                        # no expert at all
+    z[2, :] = -math.inf
+    z[2, 3] = 0.5                           # one expert for two places
+    z[:, 5] = -math.inf                     # an expert that nobody takes
+    routing = sffn.route(z, k)
+    y = sffn.experts_forward(x, routing, W1, W3, W2t)
+    assert (y[1] == 0).all()
+    check_experts(x.contiguous(), routing, W1, W3, W2t, "relu", y)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    r2 = sffn.route(z, k, stream=side)
+    y2 = sffn.experts_forward(x, r2, W1, W3, W2t, stream=side)
+    side.synchronize()
+    assert torch.equal(y, y2)
+
+
+def test_moe_layer_and_graph_capture():
+    g, T, E, k, D, H = gen(31), 40, 8, 2, 256, 160
+    x = torch.randn(T, D, generator=g, device=DEV).to(BF)
+    Wr = torch.randn(E, D, generator=g, device=DEV)
+    W1, W3 = ((torch.randn(E, H, D, generator=g, device=DEV) * 0.1).to(BF) for _ in range(2))
+    W2 = (torch.randn(E, D, H, generator=g, device=DEV) * 0.1).to(BF)
+    moe = sffn.MoEFFN(Wr, W1, W3, W2, k, act="rsp")
+    y = moe(x)
+    check_experts(x, moe.route(x), W1, W3, W2.transpose(1, 2), "rsp", y)
+    for n in (1, T):
+        xs, z = x[:n].clone(), torch.randn(n, E, generator=g, device=DEV)
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            sffn.experts_forward(xs, sffn.route(z, k), moe.W1, moe.W3, moe.W2t)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = sffn.experts_forward(xs, sffn.route(z, k), moe.W1, moe.W3, moe.W2t)
+        for _ in range(2):
+            z.copy_(torch.randn(n, E, generator=g, device=DEV))
+            xs.copy_(xs.flip(0))
+            graph.replay()
+            want = sffn.experts_forward(xs, sffn.route(z, k), moe.W1, moe.W3, moe.W2t)
+            assert torch.equal(out, want)
+
+
+def test_int8_linear_of_quantised_tokens():
+    """The two int8 operators as a served linear layer uses them."""
+    g, T, N, K = gen(41), 50, 384, 1024
+    x = torch.randn(T, K, generator=g, device=DEV).to(BF)
+    w = torch.randn(N, K, generator=g, device=DEV).to(BF)
+    wq, sw = sffn.quantize_tokens(w)  # the same rule gives one scale per output channel
+    xq, sx = sffn.quantize_tokens(x)
+    y = sffn.matmul_int8(xq, sx, wq, sw)
+    ref = x.double() @ w.double().T
+    # half a code step on either side of every product
+    bound = (sx.double()[:, None] / 2 * 1.001) * w.double().abs().sum(1) + \
+        x.double().abs().sum(1)[:, None] * (sw.double() / 2 * 1.001) + K * torch.outer(sx.double(), sw.double()) / 4
+    close(y, ref, bound * (1 + 2.0 ** -7))
+
+
+def test_wrappers_refuse_on_the_gpu():
+    x, w = torch.zeros(4, 64, dtype=BF, device=DEV), torch.zeros(2, 8, 64, dtype=BF, device=DEV)
+    off = offsets_of([2, 2])
+    with pytest.raises(ValueError, match="offsets"):
+        sffn.grouped_matmul(x, w, off[:2])
+    with pytest.raises(ValueError, match="gradient"):
+        sffn.grouped_matmul(x.clone().requires_grad_(), w, off)
+    with pytest.raises(ValueError, match="contiguous"):
+        sffn.grouped_matmul(x, w.transpose(0, 1), off[:1].repeat(9))
+    with pytest.raises(ValueError, match="contiguous"):
+        sffn.quantize_tokens(x.T)
+    with pytest.raises(ValueError, match="routing"):
+        sffn.experts_forward(x, sffn.route(torch.zeros(3, 2, device=DEV), 1), w, w, w)
+    with pytest.raises(sffn.SffnError, match="K=60"):
+        sffn.grouped_matmul(x[:, :60], w[:, :, :60].contiguous(), off)
+    with pytest.raises(sffn.SffnError, match="overlap"):
+        sffn.grouped_matmul(x, w, off, out=x[:, :8])
