@@ -1,0 +1,665 @@
+// gmm_tc.cu -- products grouped by expert on the tensor cores (tcgen05), for
+// groups of more than a few rows:
+//
+//   plain   y[r, n] = sum_k x[s(r), k] w[e, n, k]
+//   gated   h[r, n] = A(sum_k x w1) * (sum_k x w3)      (two products, one pass over x)
+//   int8    y[r, n] = sx sw sum_k xq wq
+//
+// The weights are the M side of the MMA (128 rows of w a block, 256 a pair of
+// blocks with cta_group::2) and the rows of x the N side, whose width is any
+// multiple of 16 (32 for a pair): a group of 5 rows costs 16 columns, one of
+// 130 costs 144 or two tiles of 80, so ragged groups waste little.  A block
+// walks the tiles of all groups (persistent, tile ids strided by the grid); the
+// tile list is a prefix sum over the groups that every block makes for itself
+// from the device's offsets, so the host never waits for them.  One warp feeds
+// a ring of shared stages by TMA, one thread issues the MMAs, four warps empty
+// one of two TMEM accumulators while the MMAs fill the other.
+//
+// Rows of x come as 2D tiles, or, through an index, by gather4 (four rows a
+// copy), so the grouped copy of x is never made.
+//
+// int8: this part's int8 MMA rate is far below its 16-bit rate, and int8 codes are
+// exact in fp16 with exact products and fp32 sums that are exact below 2^24.  So
+// the raw codes arrive by TMA and eight warps widen them into the fp16 operand
+// tiles: half the memory traffic of 16-bit weights at the 16-bit MMA's rate.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cstdio>
+#include <cstdlib>
+#include <mutex>
+
+#include "common.cuh"
+#include "ops.h"
+#include "tc.cuh"
+
+namespace sffn {
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();  // ffn_tc.cu
+
+namespace {
+
+constexpr int TG_EPI_WARP0 = 4;   // warps 4..7: epilogue (TMEM lane quarter = warp % 4)
+constexpr int TG_CONV_WARP0 = 8;  // warps 8..15: int8 -> fp16
+constexpr int TG_CONV_WARPS = 8;
+constexpr uint64_t TG_TIMEOUT_NS = 250000000ull;
+constexpr size_t TG_SMEM = 227 * 1024;
+constexpr int TG_G = 8;           // weight tiles of one raster group
+
+struct TgArgs {
+  GmmArgs g;
+  int NT;      // most rows of x a tile
+  int bxr;     // rows of an x box (no index)
+  int MT;      // weight tiles: ceil(N / (128 CTAS))
+  int KC;      // 64-wide K chunks
+  int S;       // operand stages
+  int SR;      // raw stages (int8)
+  int cols;    // TMEM columns allocated
+  int* err;
+};
+
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// Bounded wait that also sees what the other block of the pair released.
+__device__ __forceinline__ bool tg_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if ((i & 63u) == 0) {
+      if (*abort) return false;
+      if (globaltimer_ns() - t0 > TG_TIMEOUT_NS) {
+        *abort = 1;
+        atomicOr(err, DEV_ERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+template <int CTAS>
+__device__ __forceinline__ void tma_w3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  if constexpr (CTAS == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
+        "{%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+template <int CTAS>
+__device__ __forceinline__ void tma_x2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  if constexpr (CTAS == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
+        "{%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+// four rows y[0..3] of the map (box one row high), 128 bytes each
+template <int CTAS>
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int x, const int (&y)[4],
+                                            uint32_t bar) {
+  if constexpr (CTAS == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(bar)
+        : "memory");
+}
+
+template <int CTAS>
+__device__ __forceinline__ void tg_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  if constexpr (CTAS == 2)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+        : "memory");
+  else
+    tc_mma(d, a, b, idesc, acc);
+}
+
+// Arrive on `bar` (in both blocks of a pair) when the MMAs issued so far are done.
+template <int CTAS>
+__device__ __forceinline__ void tg_commit(uint64_t* bar) {
+  if constexpr (CTAS == 2)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    tc_commit(bar);
+}
+
+template <int CTAS>
+__device__ __forceinline__ void tg_alloc(uint32_t* slot, uint32_t ncols) {
+  if constexpr (CTAS == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    tmem_alloc(slot, ncols);
+  }
+}
+template <int CTAS>
+__device__ __forceinline__ void tg_dealloc(uint32_t taddr, uint32_t ncols) {
+  if constexpr (CTAS == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+  else
+    tmem_dealloc(taddr, ncols);
+}
+
+// 32 consecutive fp32 columns of this thread's lane, not waited for.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// 16 int8 codes -> 16 fp16 values, exactly: a code plus 128 is a byte u, the
+// half with bits 0x6400 | u is 1024 + u, and 1024 + u - 1152 is the code.
+__device__ __forceinline__ void widen4(uint32_t v, uint32_t* out) {
+  const uint32_t u = v ^ 0x80808080u;
+  uint32_t lo, hi;
+  asm("prmt.b32 %0, %1, %2, 0x4140;" : "=r"(lo) : "r"(u), "r"(0x64646464u));
+  asm("prmt.b32 %0, %1, %2, 0x4342;" : "=r"(hi) : "r"(u), "r"(0x64646464u));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(out[0]) : "r"(lo), "r"(0x64806480u));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(out[1]) : "r"(hi), "r"(0x64806480u));
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint4 lds16a(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+
+// One tile: expert, weight tile, rows [r0, r1) of x and the MMA width n.
+struct Tile {
+  int e, mt, r0, r1, n;
+};
+
+template <int CTAS>
+__device__ __forceinline__ Tile tile_at(const TgArgs& p, const int* s_off, const int* s_pre, int t) {
+  int lo = 0, hi = p.g.E;  // the last expert whose first tile is <= t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (s_pre[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  Tile q;
+  q.e = lo;
+  const int m = s_off[lo + 1] - s_off[lo];
+  const int tt = (m + p.NT - 1) / p.NT;
+  constexpr int Q = 16 * CTAS;
+  const int per = ((m + tt - 1) / tt + Q - 1) / Q * Q;
+  const int i = t - s_pre[lo];
+  const int g = i / (TG_G * tt), rest = i - g * TG_G * tt, gm = min(TG_G, p.MT - g * TG_G);
+  q.mt = g * TG_G + rest % gm;
+  q.r0 = s_off[lo] + (rest / gm) * per;
+  q.r1 = min(s_off[lo + 1], q.r0 + per);
+  q.n = (q.r1 - q.r0 + Q - 1) / Q * Q;
+  return q;
+}
+
+template <int CTAS, bool GATED, bool I8, bool KN>
+__global__ void __launch_bounds__(I8 ? 512 : 256, 1)
+    gmm_tc_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mW3,
+                  const __grid_constant__ CUtensorMap mX, const TgArgs p) {
+  extern __shared__ uint8_t smraw[];
+  uint8_t* sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
+  constexpr uint32_t AB = 128u * 128u;  // one A region: 128 rows x 128 bytes
+  const uint32_t NTl = (uint32_t)p.NT / CTAS;
+  const uint32_t bb = (NTl + 7) / 8 * 1024u;                 // B region
+  const uint32_t st_bytes = (GATED ? 2 : 1) * AB + bb;       // operand stage
+  const uint32_t raw0 = (uint32_t)p.S * st_bytes;            // raw stages (int8) follow
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + raw0 + (I8 ? (uint32_t)p.SR * st_bytes : 0u));
+  uint64_t* full = bars;
+  uint64_t* empty = full + p.S;
+  uint64_t* rfull = empty + p.S;
+  uint64_t* rempty = rfull + p.SR;
+  uint64_t* accf = rempty + p.SR;  // [2]
+  uint64_t* acce = accf + 2;       // [2]
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(acce + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+  int* s_off = reinterpret_cast<int*>(tslot + 2);  // [E + 1]
+  int* s_pre = s_off + p.g.E + 1;                  // [E + 1]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = CTAS == 2 ? cluster_rank() : 0;
+
+  if (tid == 0) {
+    for (int s = 0; s < p.S; ++s) {
+      mbar_init(&full[s], I8 ? TG_CONV_WARPS * CTAS : 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < p.SR; ++s) {
+      mbar_init(&rfull[s], 1);
+      mbar_init(&rempty[s], TG_CONV_WARPS);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&accf[b], 1);
+      mbar_init(&acce[b], 4 * CTAS);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_map(&mW);
+    tma_prefetch_map(&mX);
+    if (GATED) tma_prefetch_map(&mW3);
+  }
+  if (warp == 2) tg_alloc<CTAS>(tslot, (uint32_t)p.cols);
+  pdl_wait();  // the offsets, x and the index come from earlier kernels
+  if (warp == 3) {  // group bounds and the prefix sum of their tiles
+    // bounds that go back or past the end are cut: a group starts where the ones before it ended at the latest
+    int carry = 0, last = p.g.offsets ? min(max(p.g.offsets[0], 0), p.g.R) : 0;
+    for (int e0 = 0; e0 < p.g.E; e0 += 32) {
+      const int e = e0 + lane;
+      int hi = 0;  // the end of group e, then the largest end up to it
+      if (e < p.g.E) hi = p.g.offsets ? min(max(p.g.offsets[e + 1], 0), p.g.R) : p.g.R;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, hi, o);
+        if (lane >= o) hi = max(hi, v);
+      }
+      hi = max(hi, last);
+      int before = __shfl_up_sync(0xffffffffu, hi, 1);
+      if (lane == 0) before = last;
+      const int v = (hi - before + p.NT - 1) / p.NT * p.MT;
+      int x = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (e < p.g.E) {
+        s_off[e] = before;
+        s_pre[e] = carry + x - v;
+        if (e == p.g.E - 1) {
+          s_off[e + 1] = hi;
+          s_pre[e + 1] = carry + x;
+        }
+      }
+      carry += __shfl_sync(0xffffffffu, x, 31);
+      last = __shfl_sync(0xffffffffu, hi, 31);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (CTAS == 2) cluster_sync_all();  // the other block's barriers exist before anything arrives on them
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  if (tid == 0) pdl_launch_dependents();
+  const int total = s_pre[p.g.E];
+  const int first = blockIdx.x / CTAS, step = gridDim.x / CTAS;
+  const uint32_t smb = smem_u32(sm);
+  const int n0r = 128 * (int)rank;  // this block's rows inside a weight tile
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA producer
+    uint64_t* fb = I8 ? rfull : full;
+    uint64_t* eb = I8 ? rempty : empty;
+    const int S = I8 ? p.SR : p.S, KCH = I8 ? (p.g.K + 127) / 128 : p.KC, KW = I8 ? 128 : 64;
+    const uint32_t base = I8 ? smb + raw0 : smb;
+    uint32_t it = 0;
+    bool ok = true;
+    for (int t = first; t < total && ok; t += step) {
+      const Tile q = tile_at<CTAS>(p, s_off, s_pre, t);
+      const int nl = q.n / CTAS, nb = q.mt * 128 * CTAS + n0r;
+      const int xr = q.r0 + (int)rank * nl;  // this block's rows of x
+      int gy[2][4];
+      if (p.g.index) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int r = xr + (lane + 32 * h) * 4 + j;
+            int src = p.g.XR;  // out of range: zeros
+            if (r < q.r1) {
+              const int i = p.g.index[r];
+              if (i >= 0) src = min(i / p.g.index_div, p.g.XR);
+            }
+            gy[h][j] = src;
+          }
+      }
+      const int boxes = p.g.index ? nl / 4 : (nl + p.bxr - 1) / p.bxr;
+      const uint32_t xbytes = p.g.index ? (uint32_t)nl * 128u : (uint32_t)(boxes * p.bxr) * 128u;
+      const uint32_t tx = ((GATED ? 2 : 1) * AB + xbytes) * (I8 ? 1 : CTAS);
+      for (int c = 0; c < KCH; ++c, ++it) {
+        const int s = it % S;
+        const uint32_t use = it / S;
+        int good = 1;
+        if (lane == 0 && use > 0) good = tg_wait(&eb[s], (use - 1) & 1, abort_flag, p.err);
+        if (!__shfl_sync(0xffffffffu, good, 0)) {
+          ok = false;
+          break;
+        }
+        const uint32_t st = base + (uint32_t)s * st_bytes;
+        // a pair's 16-bit stages complete on the first block's barrier
+        const uint32_t bar = CTAS == 2 && !I8 ? cluster_map(smem_u32(&fb[s]), 0) : smem_u32(&fb[s]);
+        if (lane == 0) {
+          if (I8 || rank == 0) mbar_arrive_expect_tx(&fb[s], tx);
+          if constexpr (KN) {
+            tma_w3d<I8 ? 1 : CTAS>(st, &mW, nb, c * KW, q.e, bar);
+            tma_w3d<I8 ? 1 : CTAS>(st + AB / 2, &mW, nb + 64, c * KW, q.e, bar);
+          } else {
+            tma_w3d<I8 ? 1 : CTAS>(st, &mW, c * KW, nb, q.e, bar);
+          }
+          if (GATED) tma_w3d<I8 ? 1 : CTAS>(st + AB, &mW3, c * KW, nb, q.e, bar);
+        }
+        __syncwarp();
+        const uint32_t bst = st + (GATED ? 2 : 1) * AB;
+        if (p.g.index) {
+          if (lane < boxes) tma_gather4<I8 ? 1 : CTAS>(bst + lane * 512u, &mX, c * KW, gy[0], bar);
+          if (lane + 32 < boxes) tma_gather4<I8 ? 1 : CTAS>(bst + (lane + 32) * 512u, &mX, c * KW, gy[1], bar);
+        } else if (lane < boxes) {
+          tma_x2d<I8 ? 1 : CTAS>(bst + (uint32_t)(lane * p.bxr) * 128u, &mX, c * KW, xr + lane * p.bxr, bar);
+        }
+      }
+    }
+    // after a failed wait copies may still be in flight: let them land before the block ends
+    if (!ok && lane == 0 && (I8 || rank == 0))
+      for (int s = 0; s < S && (uint32_t)s < it; ++s) {
+        const uint32_t use = (it - 1 - s) / S;
+        mbar_wait_drain(&fb[s], use & 1, TG_TIMEOUT_NS);
+      }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer (first block of a pair)
+    if (rank == 0 && lane == 0) {
+      uint32_t it = 0, tl = 0;
+      bool ok = true;
+      for (int t = first; t < total && ok; t += step, ++tl) {
+        const Tile q = tile_at<CTAS>(p, s_off, s_pre, t);
+        const uint32_t idesc = (I8 ? 1u << 4 : (1u << 4) | (1u << 7) | (1u << 10)) | ((KN ? 1u : 0u) << 15) |
+                               ((uint32_t)(q.n >> 3) << 17) | ((uint32_t)(128 * CTAS >> 4) << 24);
+        const uint32_t b = tl & 1, use = tl >> 1;
+        if (use > 0 && !tg_wait(&acce[b], (use - 1) & 1, abort_flag, p.err)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + b * (uint32_t)((GATED ? 2 : 1) * p.NT);
+        for (int c = 0; c < p.KC; ++c, ++it) {
+          const int s = it % p.S;
+          if (!tg_wait(&full[s], (it / p.S) & 1, abort_flag, p.err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t st = smb + (uint32_t)s * st_bytes;
+          const uint64_t ad = KN ? smem_desc(st, AB / 2, 1024, SMEM_LAYOUT_SW128) : smem_desc(st, 16, 1024, SMEM_LAYOUT_SW128);
+          const uint64_t bd = smem_desc(st + (GATED ? 2 : 1) * AB, 16, 1024, SMEM_LAYOUT_SW128);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t ak = ad + (KN ? (k * 2048) >> 4 : 2 * k);
+            tg_mma<CTAS>(d, ak, bd + 2 * k, idesc, c > 0 || k > 0);
+            if (GATED) tg_mma<CTAS>(d + p.NT, ak + (AB >> 4), bd + 2 * k, idesc, c > 0 || k > 0);
+          }
+          tg_commit<CTAS>(&empty[s]);
+        }
+        if (ok) tg_commit<CTAS>(&accf[b]);
+      }
+    }
+    __syncwarp();
+  } else if (I8 && warp >= TG_CONV_WARP0) {
+    // ---------------------------------------------------------------- int8 -> fp16 operand tiles
+    const int cw = warp - TG_CONV_WARP0, row8 = lane & 7, cj = lane >> 3;
+    uint32_t it = 0, rt = 0;
+    bool ok = true;
+    for (int t = first; t < total && ok; t += step) {
+      const Tile q = tile_at<CTAS>(p, s_off, s_pre, t);
+      const int groups = 16 + q.n / CTAS / 8;  // 8-row groups: A, then B (both regions are dense)
+      for (int c = 0; c < p.KC && ok; ++c, ++it) {
+        const int rs = rt % p.SR, s = it % p.S;
+        const int half = c & 1;
+        if (half == 0 && !tg_wait(&rfull[rs], (rt / p.SR) & 1, abort_flag, p.err)) ok = false;
+        if (ok && it >= (uint32_t)p.S && !tg_wait(&empty[s], (it / p.S - 1) & 1, abort_flag, p.err)) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t src = smb + raw0 + (uint32_t)rs * st_bytes, dst = smb + (uint32_t)s * st_bytes;
+        for (int gi = cw; gi < groups; gi += TG_CONV_WARPS) {
+          const uint32_t rowb = (uint32_t)gi * 1024u + (uint32_t)row8 * 128u;
+          const uint4 v = lds16a(src + rowb + ((uint32_t)((half * 4 + cj) ^ row8) << 4));
+          uint32_t o[8];
+          widen4(v.x, o);
+          widen4(v.y, o + 2);
+          widen4(v.z, o + 4);
+          widen4(v.w, o + 6);
+          sts16(dst + rowb + ((uint32_t)((2 * cj) ^ row8) << 4), o[0], o[1], o[2], o[3]);
+          sts16(dst + rowb + ((uint32_t)((2 * cj + 1) ^ row8) << 4), o[4], o[5], o[6], o[7]);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          if (CTAS == 2)
+            arrive_remote(cluster_map(smem_u32(&full[s]), 0));
+          else
+            mbar_arrive(&full[s]);
+        }
+        if (half == 1 || c == p.KC - 1) {
+          if (lane == 0) mbar_arrive(&rempty[rs]);
+          ++rt;
+        }
+      }
+    }
+  } else if (warp >= TG_EPI_WARP0 && warp < TG_EPI_WARP0 + 4) {
+    // ---------------------------------------------------------------- epilogue: lane = one row of w
+    const int ew = warp - TG_EPI_WARP0;
+    uint32_t tl = 0;
+    for (int t = first; t < total; t += step, ++tl) {
+      const Tile q = tile_at<CTAS>(p, s_off, s_pre, t);
+      const uint32_t b = tl & 1;
+      const int n = q.mt * 128 * CTAS + n0r + 32 * ew + lane;
+      if (!__all_sync(0xffffffffu, tg_wait(&accf[b], (tl >> 1) & 1, abort_flag, p.err))) break;
+      tc_fence_after();
+      const uint32_t ta = tmem + b * (uint32_t)((GATED ? 2 : 1) * p.NT) + ((uint32_t)(32 * ew) << 16);
+      const float sw = I8 && n < p.g.N ? p.g.sw[(size_t)q.e * p.g.N + n] : 0.f;
+      const int rows = q.r1 - q.r0;
+      for (int c0 = 0; c0 < rows; c0 += 32) {
+        uint32_t v[32];
+        tmem_ld32(ta + c0, v);
+        if constexpr (GATED) {
+          uint32_t u[32];
+          tmem_ld32(ta + p.NT + c0, u);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            v[j] = __float_as_uint(activation(p.g.act, __uint_as_float(v[j])) * __uint_as_float(u[j]));
+        } else {
+          tmem_ld_wait();
+        }
+        const int m = min(32, rows - c0);
+        if (n < p.g.N) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            if (j >= m) break;
+            const int r = q.r0 + c0 + j;
+            float f = __uint_as_float(v[j]);
+            if (I8) {
+              int src = r;
+              if (p.g.index) {
+                const int i = p.g.index[r];
+                src = i >= 0 && i / p.g.index_div < p.g.XR ? i / p.g.index_div : -1;
+              }
+              f = f * (src >= 0 ? p.g.sx[src] : 0.f) * sw;
+            }
+            const size_t at = (size_t)(p.g.out_index ? p.g.out_index[r] : r) * p.g.ldy + n;
+            if (p.g.y_f32)
+              reinterpret_cast<float*>(p.g.y)[at] = f;
+            else
+              reinterpret_cast<__nv_bfloat16*>(p.g.y)[at] = __float2bfloat16_rn(f);
+          }
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CTAS == 2)
+          arrive_remote(cluster_map(smem_u32(&acce[b]), 0));
+        else
+          mbar_arrive(&acce[b]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (CTAS == 2) cluster_sync_all();  // no block leaves while the other may still signal its barriers
+  tc_fence_after();
+  if (warp == 2) tg_dealloc<CTAS>(tmem, (uint32_t)p.cols);
+}
+
+// ------------------------------------------------------------------ host side
+
+bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box, bool i8) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base),
+            dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_w(CUtensorMap* m, const void* w, const GmmArgs& a) {
+  const cuuint64_t eb = a.i8 ? 1 : 2, N = (cuuint64_t)a.N, K = (cuuint64_t)a.K;
+  const cuuint64_t in = a.kn ? N : K, out = a.kn ? K : N;
+  const cuuint64_t dims[3] = {in, out, (cuuint64_t)a.E};
+  const cuuint64_t strides[2] = {in * eb, N * K * eb};
+  const cuuint32_t box[3] = {a.i8 ? 128u : 64u, a.kn ? 64u : 128u, 1u};
+  return encode(m, w, 3, dims, strides, box, a.i8 != 0);
+}
+
+template <int CTAS, bool GATED, bool I8, bool KN>
+cudaError_t tg_go(const CUtensorMap& mW, const CUtensorMap& mW3, const CUtensorMap& mX, const TgArgs& p, size_t smem,
+                  int sms, cudaStream_t s) {
+  auto kernel = gmm_tc_kernel<CTAS, GATED, I8, KN>;
+  static std::once_flag once;
+  static cudaError_t attr = cudaSuccess;
+  static int clusters = 0;
+  std::call_once(once, [&] {
+    attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TG_SMEM);
+    clusters = sms / CTAS;
+    if (attr == cudaSuccess && CTAS == 2) {  // pairs that fit at once
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((unsigned)(sms / 2 * 2));
+      cfg.blockDim = dim3(I8 ? 512 : 256);
+      cfg.dynamicSmemBytes = TG_SMEM;
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = 2;
+      at[0].val.clusterDim.y = 1;
+      at[0].val.clusterDim.z = 1;
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0) clusters = std::min(clusters, n);
+    }
+  });
+  if (attr != cudaSuccess) return attr;
+  const GmmArgs& a = p.g;
+  const long long most = (long long)p.MT * ((long long)a.R / p.NT + std::min(a.E, a.R));  // tiles at most
+  const int n = (int)std::min<long long>(clusters, std::max(1ll, most));
+  return ops_launch(kernel, dim3((unsigned)(n * CTAS)), I8 ? 512 : 256, smem, s, CTAS, mW, mW3, mX, p);
+}
+
+}  // namespace
+
+cudaError_t launch_gmm_tc(const GmmArgs& a, int ctas, int nt, cudaStream_t s) {
+  TgArgs p;
+  p.g = a;
+  p.NT = nt;
+  p.MT = (a.N + 128 * ctas - 1) / (128 * ctas);
+  p.KC = (a.K + 63) / 64;
+  const bool gated = a.w3 != nullptr;
+  cudaError_t e = ops_error_word(&p.err);
+  if (e != cudaSuccess) return e;
+  const int ntl = nt / ctas;
+  const uint32_t st = (gated ? 2u : 1u) * 16384u + (uint32_t)(ntl + 7) / 8 * 1024u;
+  const size_t fixed = 1024 + 8 * (2 * 16 + 2 * 16 + 4) + 8 + sizeof(int) * 2 * (size_t)(a.E + 1) + 64;
+  const int slots = std::min(24, (int)((TG_SMEM - fixed) / st));
+  p.S = a.i8 ? std::min(4, slots / 2) : std::min(16, slots);
+  p.SR = a.i8 ? std::min(12, slots - p.S) : 0;
+  int cols = 32;
+  while (cols < 2 * (gated ? 2 : 1) * nt) cols <<= 1;
+  p.cols = cols;
+  // rows of an x box: whole tile in one to eight copies of at most 64 rows
+  p.bxr = std::min(ntl, 64);
+  CUtensorMap mW, mW3, mX;
+  if (!encode_w(&mW, a.w, a) || !encode_w(&mW3, gated ? a.w3 : a.w, a)) return cudaErrorInvalidValue;
+  {
+    const cuuint64_t eb = a.i8 ? 1 : 2;
+    const cuuint64_t dims[2] = {(cuuint64_t)a.K, (cuuint64_t)a.XR}, strides[1] = {(cuuint64_t)a.ldx * eb};
+    const cuuint32_t box[2] = {a.i8 ? 128u : 64u, a.index ? 1u : (cuuint32_t)p.bxr};
+    if (!encode(&mX, a.x, 2, dims, strides, box, a.i8 != 0)) return cudaErrorInvalidValue;
+  }
+  const size_t smem = fixed + (size_t)(p.S + p.SR) * st;
+  const int sms = ops_num_sms();
+  if (a.i8)
+    return ctas == 2 ? tg_go<2, false, true, false>(mW, mW3, mX, p, smem, sms, s)
+                     : tg_go<1, false, true, false>(mW, mW3, mX, p, smem, sms, s);
+  if (gated)
+    return ctas == 2 ? tg_go<2, true, false, false>(mW, mW3, mX, p, smem, sms, s)
+                     : tg_go<1, true, false, false>(mW, mW3, mX, p, smem, sms, s);
+  if (a.kn)
+    return ctas == 2 ? tg_go<2, false, false, true>(mW, mW3, mX, p, smem, sms, s)
+                     : tg_go<1, false, false, true>(mW, mW3, mX, p, smem, sms, s);
+  return ctas == 2 ? tg_go<2, false, false, false>(mW, mW3, mX, p, smem, sms, s)
+                   : tg_go<1, false, false, false>(mW, mW3, mX, p, smem, sms, s);
+}
+
+cudaError_t launch_gmm(const GmmArgs& a, cudaStream_t s) {
+  if (const char* v = std::getenv("SFFN_GMM_TUNE")) {
+    int c = 0, n = 0;
+    if (std::sscanf(v, "%d,%d", &c, &n) == 2 && c > 0) return launch_gmm_tc(a, c, n, s);
+    return launch_gmm_rows(a, s);
+  }
+  const int busy = std::min(a.E, a.R);
+  if (a.R <= 4 * busy) return launch_gmm_rows(a, s);
+  if (a.R >= 96 * busy) return launch_gmm_tc(a, 2, 256, s);
+  return launch_gmm_tc(a, 1, 128, s);
+}
+
+}  // namespace sffn

@@ -44,6 +44,8 @@ struct GmmArgs {
   int i8 = 0, y_f32 = 0, kn = 0, act = 0;
 };
 cudaError_t launch_gmm_rows(const GmmArgs& a, cudaStream_t s);
+cudaError_t launch_gmm_tc(const GmmArgs& a, int ctas, int nt, cudaStream_t s);  // ctas 1 or 2, nt 32 .. 256 (gated: 128)
+cudaError_t launch_gmm(const GmmArgs& a, cudaStream_t s);
 
 // ---- experts.cu
 struct ExpertsArgs {

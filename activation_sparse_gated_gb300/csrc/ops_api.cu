@@ -180,7 +180,7 @@ int sffn_grouped_matmul(const void* x, long long ldx, const float* sx, const voi
   a.i8 = i8;
   a.y_f32 = y_dtype == SFFN_F32;
   a.kn = kn;
-  const cudaError_t e = launch_gmm_rows(a, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_gmm(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SFFN_OK : cuda_fail(fn, e);
 }
 
