@@ -49,7 +49,7 @@ constexpr int TG_G = 8;           // weight tiles of one raster group
 struct TgArgs {
   GmmArgs g;
   int NT;      // most rows of x a tile
-  int bxr;     // rows of an x box (no index)
+  int bxr;     // rows of a small x box (no index); the large one has NT / CTAS
   int MT;      // weight tiles: ceil(N / (128 CTAS))
   int KC;      // 64-wide K chunks
   int S;       // operand stages
@@ -251,7 +251,7 @@ __device__ __forceinline__ Tile tile_at(const TgArgs& p, const int* s_off, const
 template <int CTAS, bool GATED, bool I8, bool KN>
 __global__ void __launch_bounds__(I8 ? 512 : 256, 1)
     gmm_tc_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mW3,
-                  const __grid_constant__ CUtensorMap mX, const TgArgs p) {
+                  const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mXb, const TgArgs p) {
   extern __shared__ uint8_t smraw[];
   uint8_t* sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
   constexpr uint32_t AB = 128u * 128u;  // one A region: 128 rows x 128 bytes
@@ -339,20 +339,24 @@ __global__ void __launch_bounds__(I8 ? 512 : 256, 1)
   const uint32_t smb = smem_u32(sm);
   const int n0r = 128 * (int)rank;  // this block's rows inside a weight tile
 
-  if (warp == 0) {
-    // ---------------------------------------------------------------- TMA producer
+  if (warp == 0 || warp == 3) {
+    // ---------------------------------------------------------------- TMA producers: warp 0 w, warp 3 x
+    const bool xside = warp == 3;
     uint64_t* fb = I8 ? rfull : full;
     uint64_t* eb = I8 ? rempty : empty;
     const int S = I8 ? p.SR : p.S, KCH = I8 ? (p.g.K + 127) / 128 : p.KC, KW = I8 ? 128 : 64;
     const uint32_t base = I8 ? smb + raw0 : smb;
-    uint32_t it = 0;
+    uint32_t it = 0, s = 0, par = 1;  // par: parity of the wait for stage s (a fresh barrier passes parity 1)
     bool ok = true;
     for (int t = first; t < total && ok; t += step) {
       const Tile q = tile_at<CTAS>(p, s_off, s_pre, t);
       const int nl = q.n / CTAS, nb = q.mt * 128 * CTAS + n0r;
       const int xr = q.r0 + (int)rank * nl;  // this block's rows of x
+      const bool big = nl > p.bxr;           // one copy of the whole region, or one small box
+      const uint32_t xbytes = p.g.index ? (uint32_t)nl * 128u : (big ? NTl : (uint32_t)p.bxr) * 128u;
+      const uint32_t tx = ((GATED ? 2 : 1) * AB + xbytes) * (I8 ? 1 : CTAS);
       int gy[2][4];
-      if (p.g.index) {
+      if (xside && p.g.index) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -366,52 +370,51 @@ __global__ void __launch_bounds__(I8 ? 512 : 256, 1)
             gy[h][j] = src;
           }
       }
-      const int boxes = p.g.index ? nl / 4 : (nl + p.bxr - 1) / p.bxr;
-      const uint32_t xbytes = p.g.index ? (uint32_t)nl * 128u : (uint32_t)(boxes * p.bxr) * 128u;
-      const uint32_t tx = ((GATED ? 2 : 1) * AB + xbytes) * (I8 ? 1 : CTAS);
       for (int c = 0; c < KCH; ++c, ++it) {
-        const int s = it % S;
-        const uint32_t use = it / S;
-        int good = 1;
-        if (lane == 0 && use > 0) good = tg_wait(&eb[s], (use - 1) & 1, abort_flag, p.err);
-        if (!__shfl_sync(0xffffffffu, good, 0)) {
+        if (!__all_sync(0xffffffffu, tg_wait(&eb[s], par, abort_flag, p.err))) {
           ok = false;
           break;
         }
-        const uint32_t st = base + (uint32_t)s * st_bytes;
+        const uint32_t st = base + s * st_bytes;
         // a pair's 16-bit stages complete on the first block's barrier
         const uint32_t bar = CTAS == 2 && !I8 ? cluster_map(smem_u32(&fb[s]), 0) : smem_u32(&fb[s]);
-        if (lane == 0) {
-          if (I8 || rank == 0) mbar_arrive_expect_tx(&fb[s], tx);
-          if constexpr (KN) {
-            tma_w3d<I8 ? 1 : CTAS>(st, &mW, nb, c * KW, q.e, bar);
-            tma_w3d<I8 ? 1 : CTAS>(st + AB / 2, &mW, nb + 64, c * KW, q.e, bar);
-          } else {
-            tma_w3d<I8 ? 1 : CTAS>(st, &mW, c * KW, nb, q.e, bar);
+        if (!xside) {
+          if (lane == 0) {
+            if (I8 || rank == 0) mbar_arrive_expect_tx(&fb[s], tx);
+            if constexpr (KN) {
+              tma_w3d<I8 ? 1 : CTAS>(st, &mW, nb, c * KW, q.e, bar);
+              tma_w3d<I8 ? 1 : CTAS>(st + AB / 2, &mW, nb + 64, c * KW, q.e, bar);
+            } else {
+              tma_w3d<I8 ? 1 : CTAS>(st, &mW, c * KW, nb, q.e, bar);
+            }
+            if (GATED) tma_w3d<I8 ? 1 : CTAS>(st + AB, &mW3, c * KW, nb, q.e, bar);
           }
-          if (GATED) tma_w3d<I8 ? 1 : CTAS>(st + AB, &mW3, c * KW, nb, q.e, bar);
+        } else {
+          const uint32_t bst = st + (GATED ? 2 : 1) * AB;
+          if (p.g.index) {
+            if (lane < nl / 4) tma_gather4<I8 ? 1 : CTAS>(bst + lane * 512u, &mX, c * KW, gy[0], bar);
+            if (lane + 32 < nl / 4) tma_gather4<I8 ? 1 : CTAS>(bst + (lane + 32) * 512u, &mX, c * KW, gy[1], bar);
+          } else if (lane == 0) {
+            tma_x2d<I8 ? 1 : CTAS>(bst, big ? &mXb : &mX, c * KW, xr, bar);
+          }
         }
-        __syncwarp();
-        const uint32_t bst = st + (GATED ? 2 : 1) * AB;
-        if (p.g.index) {
-          if (lane < boxes) tma_gather4<I8 ? 1 : CTAS>(bst + lane * 512u, &mX, c * KW, gy[0], bar);
-          if (lane + 32 < boxes) tma_gather4<I8 ? 1 : CTAS>(bst + (lane + 32) * 512u, &mX, c * KW, gy[1], bar);
-        } else if (lane < boxes) {
-          tma_x2d<I8 ? 1 : CTAS>(bst + (uint32_t)(lane * p.bxr) * 128u, &mX, c * KW, xr + lane * p.bxr, bar);
+        if (++s == (uint32_t)S) {
+          s = 0;
+          par ^= 1;
         }
       }
     }
     // after a failed wait copies may still be in flight: let them land before the block ends
     if (!ok && lane == 0 && (I8 || rank == 0))
-      for (int s = 0; s < S && (uint32_t)s < it; ++s) {
-        const uint32_t use = (it - 1 - s) / S;
-        mbar_wait_drain(&fb[s], use & 1, TG_TIMEOUT_NS);
+      for (int i = 0; i < S && (uint32_t)i < it; ++i) {
+        const uint32_t use = (it - 1 - i) / S;
+        mbar_wait_drain(&fb[i], use & 1, TG_TIMEOUT_NS);
       }
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer (first block of a pair)
     if (rank == 0 && lane == 0) {
-      uint32_t it = 0, tl = 0;
+      uint32_t s = 0, par = 0, tl = 0;
       bool ok = true;
       for (int t = first; t < total && ok; t += step, ++tl) {
         const Tile q = tile_at<CTAS>(p, s_off, s_pre, t);
@@ -421,14 +424,13 @@ __global__ void __launch_bounds__(I8 ? 512 : 256, 1)
         if (use > 0 && !tg_wait(&acce[b], (use - 1) & 1, abort_flag, p.err)) break;
         tc_fence_after();
         const uint32_t d = tmem + b * (uint32_t)((GATED ? 2 : 1) * p.NT);
-        for (int c = 0; c < p.KC; ++c, ++it) {
-          const int s = it % p.S;
-          if (!tg_wait(&full[s], (it / p.S) & 1, abort_flag, p.err)) {
+        for (int c = 0; c < p.KC; ++c) {
+          if (!tg_wait(&full[s], par, abort_flag, p.err)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t st = smb + (uint32_t)s * st_bytes;
+          const uint32_t st = smb + s * st_bytes;
           const uint64_t ad = KN ? smem_desc(st, AB / 2, 1024, SMEM_LAYOUT_SW128) : smem_desc(st, 16, 1024, SMEM_LAYOUT_SW128);
           const uint64_t bd = smem_desc(st + (GATED ? 2 : 1) * AB, 16, 1024, SMEM_LAYOUT_SW128);
 #pragma unroll
@@ -438,6 +440,10 @@ __global__ void __launch_bounds__(I8 ? 512 : 256, 1)
             if (GATED) tg_mma<CTAS>(d + p.NT, ak + (AB >> 4), bd + 2 * k, idesc, c > 0 || k > 0);
           }
           tg_commit<CTAS>(&empty[s]);
+          if (++s == (uint32_t)p.S) {
+            s = 0;
+            par ^= 1;
+          }
         }
         if (ok) tg_commit<CTAS>(&accf[b]);
       }
@@ -573,8 +579,8 @@ bool encode_w(CUtensorMap* m, const void* w, const GmmArgs& a) {
 }
 
 template <int CTAS, bool GATED, bool I8, bool KN>
-cudaError_t tg_go(const CUtensorMap& mW, const CUtensorMap& mW3, const CUtensorMap& mX, const TgArgs& p, size_t smem,
-                  int sms, cudaStream_t s) {
+cudaError_t tg_go(const CUtensorMap& mW, const CUtensorMap& mW3, const CUtensorMap& mX, const CUtensorMap& mXb,
+                  const TgArgs& p, size_t smem, int sms, cudaStream_t s) {
   auto kernel = gmm_tc_kernel<CTAS, GATED, I8, KN>;
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
@@ -602,7 +608,7 @@ cudaError_t tg_go(const CUtensorMap& mW, const CUtensorMap& mW3, const CUtensorM
   const GmmArgs& a = p.g;
   const long long most = (long long)p.MT * ((long long)a.R / p.NT + std::min(a.E, a.R));  // tiles at most
   const int n = (int)std::min<long long>(clusters, std::max(1ll, most));
-  return ops_launch(kernel, dim3((unsigned)(n * CTAS)), I8 ? 512 : 256, smem, s, CTAS, mW, mW3, mX, p);
+  return ops_launch(kernel, dim3((unsigned)(n * CTAS)), I8 ? 512 : 256, smem, s, CTAS, mW, mW3, mX, mXb, p);
 }
 
 }  // namespace
@@ -625,29 +631,30 @@ cudaError_t launch_gmm_tc(const GmmArgs& a, int ctas, int nt, cudaStream_t s) {
   int cols = 32;
   while (cols < 2 * (gated ? 2 : 1) * nt) cols <<= 1;
   p.cols = cols;
-  // rows of an x box: whole tile in one to eight copies of at most 64 rows
-  p.bxr = std::min(ntl, 64);
-  CUtensorMap mW, mW3, mX;
+  p.bxr = std::min(ntl, 32);
+  CUtensorMap mW, mW3, mX, mXb;
   if (!encode_w(&mW, a.w, a) || !encode_w(&mW3, gated ? a.w3 : a.w, a)) return cudaErrorInvalidValue;
   {
     const cuuint64_t eb = a.i8 ? 1 : 2;
     const cuuint64_t dims[2] = {(cuuint64_t)a.K, (cuuint64_t)a.XR}, strides[1] = {(cuuint64_t)a.ldx * eb};
     const cuuint32_t box[2] = {a.i8 ? 128u : 64u, a.index ? 1u : (cuuint32_t)p.bxr};
-    if (!encode(&mX, a.x, 2, dims, strides, box, a.i8 != 0)) return cudaErrorInvalidValue;
+    const cuuint32_t boxb[2] = {a.i8 ? 128u : 64u, a.index ? 1u : (cuuint32_t)ntl};
+    if (!encode(&mX, a.x, 2, dims, strides, box, a.i8 != 0) || !encode(&mXb, a.x, 2, dims, strides, boxb, a.i8 != 0))
+      return cudaErrorInvalidValue;
   }
   const size_t smem = fixed + (size_t)(p.S + p.SR) * st;
   const int sms = ops_num_sms();
   if (a.i8)
-    return ctas == 2 ? tg_go<2, false, true, false>(mW, mW3, mX, p, smem, sms, s)
-                     : tg_go<1, false, true, false>(mW, mW3, mX, p, smem, sms, s);
+    return ctas == 2 ? tg_go<2, false, true, false>(mW, mW3, mX, mXb, p, smem, sms, s)
+                     : tg_go<1, false, true, false>(mW, mW3, mX, mXb, p, smem, sms, s);
   if (gated)
-    return ctas == 2 ? tg_go<2, true, false, false>(mW, mW3, mX, p, smem, sms, s)
-                     : tg_go<1, true, false, false>(mW, mW3, mX, p, smem, sms, s);
+    return ctas == 2 ? tg_go<2, true, false, false>(mW, mW3, mX, mXb, p, smem, sms, s)
+                     : tg_go<1, true, false, false>(mW, mW3, mX, mXb, p, smem, sms, s);
   if (a.kn)
-    return ctas == 2 ? tg_go<2, false, false, true>(mW, mW3, mX, p, smem, sms, s)
-                     : tg_go<1, false, false, true>(mW, mW3, mX, p, smem, sms, s);
-  return ctas == 2 ? tg_go<2, false, false, false>(mW, mW3, mX, p, smem, sms, s)
-                   : tg_go<1, false, false, false>(mW, mW3, mX, p, smem, sms, s);
+    return ctas == 2 ? tg_go<2, false, false, true>(mW, mW3, mX, mXb, p, smem, sms, s)
+                     : tg_go<1, false, false, true>(mW, mW3, mX, mXb, p, smem, sms, s);
+  return ctas == 2 ? tg_go<2, false, false, false>(mW, mW3, mX, mXb, p, smem, sms, s)
+                   : tg_go<1, false, false, false>(mW, mW3, mX, mXb, p, smem, sms, s);
 }
 
 cudaError_t launch_gmm(const GmmArgs& a, cudaStream_t s) {
