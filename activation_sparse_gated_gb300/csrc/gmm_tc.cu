@@ -70,12 +70,13 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
   return ok != 0;
 }
 
-// Bounded wait that also sees what the other block of the pair released.
+// Bounded wait; PAIR: it also sees what threads of the pair's other block released.
+template <bool PAIR>
 __device__ __forceinline__ bool tg_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
+  if (PAIR ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if (PAIR ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
     if ((i & 63u) == 0) {
       if (*abort) return false;
       if (globaltimer_ns() - t0 > TG_TIMEOUT_NS) {
@@ -145,29 +146,40 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// The MMA warp stays converged, so that descriptors live in uniform registers;
+// `one` (lane 0) issues.
 template <int CTAS>
-__device__ __forceinline__ void tg_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void tg_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc, uint32_t one) {
   if constexpr (CTAS == 2)
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(one)
         : "memory");
   else
-    tc_mma(d, a, b, idesc, acc);
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(one)
+        : "memory");
 }
 
 // Arrive on `bar` (in both blocks of a pair) when the MMAs issued so far are done.
 template <int CTAS>
-__device__ __forceinline__ void tg_commit(uint64_t* bar) {
+__device__ __forceinline__ void tg_commit(uint64_t* bar, uint32_t one) {
   if constexpr (CTAS == 2)
     asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            smem_u32(bar)),
-        "h"((uint16_t)3)
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::
+            "r"(smem_u32(bar)),
+        "h"((uint16_t)3), "r"(one)
         : "memory");
   else
-    tc_commit(bar);
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(one)
+        : "memory");
 }
 
 template <int CTAS>
@@ -371,7 +383,7 @@ __global__ void __launch_bounds__(I8 ? 512 : 256, 1)
           }
       }
       for (int c = 0; c < KCH; ++c, ++it) {
-        if (!__all_sync(0xffffffffu, tg_wait(&eb[s], par, abort_flag, p.err))) {
+        if (!__all_sync(0xffffffffu, tg_wait<false>(&eb[s], par, abort_flag, p.err))) {
           ok = false;
           break;
         }
@@ -413,7 +425,8 @@ __global__ void __launch_bounds__(I8 ? 512 : 256, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer (first block of a pair)
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
+      const uint32_t one = lane == 0 ? 1u : 0u;
       uint32_t s = 0, par = 0, tl = 0;
       bool ok = true;
       for (int t = first; t < total && ok; t += step, ++tl) {
@@ -421,11 +434,11 @@ __global__ void __launch_bounds__(I8 ? 512 : 256, 1)
         const uint32_t idesc = (I8 ? 1u << 4 : (1u << 4) | (1u << 7) | (1u << 10)) | ((KN ? 1u : 0u) << 15) |
                                ((uint32_t)(q.n >> 3) << 17) | ((uint32_t)(128 * CTAS >> 4) << 24);
         const uint32_t b = tl & 1, use = tl >> 1;
-        if (use > 0 && !tg_wait(&acce[b], (use - 1) & 1, abort_flag, p.err)) break;
+        if (use > 0 && !__all_sync(0xffffffffu, tg_wait<CTAS == 2>(&acce[b], (use - 1) & 1, abort_flag, p.err))) break;
         tc_fence_after();
         const uint32_t d = tmem + b * (uint32_t)((GATED ? 2 : 1) * p.NT);
         for (int c = 0; c < p.KC; ++c) {
-          if (!tg_wait(&full[s], par, abort_flag, p.err)) {
+          if (!__all_sync(0xffffffffu, tg_wait<I8 && CTAS == 2>(&full[s], par, abort_flag, p.err))) {
             ok = false;
             break;
           }
@@ -436,16 +449,16 @@ __global__ void __launch_bounds__(I8 ? 512 : 256, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const uint64_t ak = ad + (KN ? (k * 2048) >> 4 : 2 * k);
-            tg_mma<CTAS>(d, ak, bd + 2 * k, idesc, c > 0 || k > 0);
-            if (GATED) tg_mma<CTAS>(d + p.NT, ak + (AB >> 4), bd + 2 * k, idesc, c > 0 || k > 0);
+            tg_mma<CTAS>(d, ak, bd + 2 * k, idesc, c > 0 || k > 0, one);
+            if (GATED) tg_mma<CTAS>(d + p.NT, ak + (AB >> 4), bd + 2 * k, idesc, c > 0 || k > 0, one);
           }
-          tg_commit<CTAS>(&empty[s]);
+          tg_commit<CTAS>(&empty[s], one);
           if (++s == (uint32_t)p.S) {
             s = 0;
             par ^= 1;
           }
         }
-        if (ok) tg_commit<CTAS>(&accf[b]);
+        if (ok) tg_commit<CTAS>(&accf[b], one);
       }
     }
     __syncwarp();
@@ -460,8 +473,8 @@ __global__ void __launch_bounds__(I8 ? 512 : 256, 1)
       for (int c = 0; c < p.KC && ok; ++c, ++it) {
         const int rs = rt % p.SR, s = it % p.S;
         const int half = c & 1;
-        if (half == 0 && !tg_wait(&rfull[rs], (rt / p.SR) & 1, abort_flag, p.err)) ok = false;
-        if (ok && it >= (uint32_t)p.S && !tg_wait(&empty[s], (it / p.S - 1) & 1, abort_flag, p.err)) ok = false;
+        if (half == 0 && !tg_wait<false>(&rfull[rs], (rt / p.SR) & 1, abort_flag, p.err)) ok = false;
+        if (ok && it >= (uint32_t)p.S && !tg_wait<false>(&empty[s], (it / p.S - 1) & 1, abort_flag, p.err)) ok = false;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t src = smb + raw0 + (uint32_t)rs * st_bytes, dst = smb + (uint32_t)s * st_bytes;
@@ -498,7 +511,7 @@ __global__ void __launch_bounds__(I8 ? 512 : 256, 1)
       const Tile q = tile_at<CTAS>(p, s_off, s_pre, t);
       const uint32_t b = tl & 1;
       const int n = q.mt * 128 * CTAS + n0r + 32 * ew + lane;
-      if (!__all_sync(0xffffffffu, tg_wait(&accf[b], (tl >> 1) & 1, abort_flag, p.err))) break;
+      if (!__all_sync(0xffffffffu, tg_wait<false>(&accf[b], (tl >> 1) & 1, abort_flag, p.err))) break;
       tc_fence_after();
       const uint32_t ta = tmem + b * (uint32_t)((GATED ? 2 : 1) * p.NT) + ((uint32_t)(32 * ew) << 16);
       const float sw = I8 && n < p.g.N ? p.g.sw[(size_t)q.e * p.g.N + n] : 0.f;
