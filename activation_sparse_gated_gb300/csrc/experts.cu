@@ -91,19 +91,91 @@ __global__ void __launch_bounds__(32 * ED_WARPS) experts_down_kernel(const Exper
   if (nn < a.D) reinterpret_cast<__nv_bfloat16*>(a.y)[(size_t)t * a.D + nn] = __float2bfloat16_rn(v);
 }
 
+// y[t] = sum_j weights[t, j] o[t k + j] in the order of the places; a place
+// without an expert or of weight 0 is not read (its row of o was not written).
+// Bound by reading o; 16-byte pieces, one thread per four columns and token.
+constexpr int EC_THREADS = 256;
+__global__ void __launch_bounds__(EC_THREADS) experts_combine_kernel(const ExpertsArgs a, const float* __restrict__ o) {
+  const int t = blockIdx.y, c = (blockIdx.x * EC_THREADS + threadIdx.x) * 4;
+  pdl_launch_dependents();
+  pdl_wait();
+  if (c >= a.D) return;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int j = 0; j < a.k; ++j) {
+    const int p = t * a.k + j;
+    const float w = a.ids[p] >= 0 ? a.weights[p] : 0.f;
+    if (w != 0.f) {
+      const float4 v = __ldcs(reinterpret_cast<const float4*>(o + (size_t)p * a.D + c));
+      sum.x = fmaf(w, v.x, sum.x);
+      sum.y = fmaf(w, v.y, sum.y);
+      sum.z = fmaf(w, v.z, sum.z);
+      sum.w = fmaf(w, v.w, sum.w);
+    }
+  }
+  *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.y) + (size_t)t * a.D + c) =
+      make_uint2(pack_bf16x2_rn(sum.x, sum.y), pack_bf16x2_rn(sum.z, sum.w));
+}
+
+size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
+
+// Few choices: the gate-first passes above; more: the grouped products on the tensor cores.
+bool few(int T, int k) { return (long long)T * k <= 64; }
+
 }  // namespace
 
 size_t experts_workspace(int T, int k, int D, int H) {
-  (void)D;
-  return sizeof(float) * (size_t)T * k * H;
+  const size_t R = (size_t)T * k;
+  if (few(T, k)) return sizeof(float) * R * H;
+  return round_up(2 * R * round_up(H, 8), 256) + sizeof(float) * R * D;  // h, then the choices' products
 }
 
 cudaError_t launch_experts(const ExpertsArgs& a, cudaStream_t s) {
-  float* h = static_cast<float*>(a.workspace);
-  cudaError_t e = ops_launch(experts_gate_kernel, dim3((a.H + EG_WARPS - 1) / EG_WARPS, a.T * a.k), 32 * EG_WARPS, 0, s,
-                             1, a, h);
-  if (e != cudaSuccess) return e;
-  return ops_launch(experts_down_kernel, dim3((a.D + 255) / 256, a.T), 32 * ED_WARPS, 0, s, 1, a, (const float*)h);
+  cudaError_t e;
+  if (few(a.T, a.k)) {
+    float* h = static_cast<float*>(a.workspace);
+    if ((e = ops_launch(experts_gate_kernel, dim3((a.H + EG_WARPS - 1) / EG_WARPS, a.T * a.k), 32 * EG_WARPS, 0, s, 1, a,
+                        h)) != cudaSuccess)
+      return e;
+    return ops_launch(experts_down_kernel, dim3((a.D + 255) / 256, a.T), 32 * ED_WARPS, 0, s, 1, a, (const float*)h);
+  }
+  const int R = a.T * a.k, Hp = (int)round_up(a.H, 8);
+  float* o = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + round_up(2 * (size_t)R * Hp, 256));
+  GmmArgs up;
+  up.x = a.x;
+  up.ldx = a.ldx;
+  up.w = a.W1;
+  up.w3 = a.W3;
+  up.offsets = a.offsets;
+  up.index = a.rows;
+  up.index_div = a.k;
+  up.y = a.workspace;
+  up.ldy = Hp;
+  up.R = R;
+  up.XR = a.T;
+  up.N = a.H;
+  up.K = a.D;
+  up.E = a.E;
+  up.act = a.act;
+  if ((e = launch_gmm(up, s)) != cudaSuccess) return e;
+  GmmArgs down;
+  down.x = a.workspace;
+  down.ldx = Hp;
+  down.w = a.W2t;
+  down.kn = 1;
+  down.offsets = a.offsets;
+  down.out_index = a.rows;
+  down.y = o;
+  down.y_f32 = 1;
+  down.ldy = a.D;
+  down.R = R;
+  down.XR = R;
+  down.N = a.D;
+  down.K = a.H;
+  down.E = a.E;
+  if ((e = launch_gmm(down, s)) != cudaSuccess) return e;
+  return ops_launch(experts_combine_kernel, dim3((a.D + 4 * EC_THREADS - 1) / (4 * EC_THREADS), a.T), EC_THREADS, 0, s, 1,
+                    a, (const float*)o);
 }
 
 }  // namespace sffn

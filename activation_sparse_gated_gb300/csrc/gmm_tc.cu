@@ -40,8 +40,9 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn();  // ffn_tc.cu
 namespace {
 
 constexpr int TG_EPI_WARP0 = 4;   // warps 4..7: epilogue (TMEM lane quarter = warp % 4)
-constexpr int TG_CONV_WARP0 = 8;  // warps 8..15: int8 -> fp16
-constexpr int TG_CONV_WARPS = 8;
+constexpr int TG_CONV_WARP0 = 8;  // warps 8..23: int8 -> fp16
+constexpr int TG_CONV_WARPS = 16;
+constexpr int TG_THREADS = 256, TG_THREADS_I8 = 32 * (TG_CONV_WARP0 + TG_CONV_WARPS);
 constexpr uint64_t TG_TIMEOUT_NS = 250000000ull;
 constexpr size_t TG_SMEM = 227 * 1024;
 constexpr int TG_G = 8;           // weight tiles of one raster group
@@ -261,7 +262,7 @@ __device__ __forceinline__ Tile tile_at(const TgArgs& p, const int* s_off, const
 }
 
 template <int CTAS, bool GATED, bool I8, bool KN>
-__global__ void __launch_bounds__(I8 ? 512 : 256, 1)
+__global__ void __launch_bounds__(I8 ? TG_THREADS_I8 : TG_THREADS, 1)
     gmm_tc_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mW3,
                   const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mXb, const TgArgs p) {
   extern __shared__ uint8_t smraw[];
@@ -478,16 +479,27 @@ __global__ void __launch_bounds__(I8 ? 512 : 256, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t src = smb + raw0 + (uint32_t)rs * st_bytes, dst = smb + (uint32_t)s * st_bytes;
-        for (int gi = cw; gi < groups; gi += TG_CONV_WARPS) {
-          const uint32_t rowb = (uint32_t)gi * 1024u + (uint32_t)row8 * 128u;
-          const uint4 v = lds16a(src + rowb + ((uint32_t)((half * 4 + cj) ^ row8) << 4));
-          uint32_t o[8];
-          widen4(v.x, o);
-          widen4(v.y, o + 2);
-          widen4(v.z, o + 4);
-          widen4(v.w, o + 6);
-          sts16(dst + rowb + ((uint32_t)((2 * cj) ^ row8) << 4), o[0], o[1], o[2], o[3]);
-          sts16(dst + rowb + ((uint32_t)((2 * cj + 1) ^ row8) << 4), o[4], o[5], o[6], o[7]);
+        // at most 48 groups: three a warp, their loads together
+        uint4 v[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const int gi = cw + i * TG_CONV_WARPS;
+          if (gi < groups)
+            v[i] = lds16a(src + (uint32_t)gi * 1024u + (uint32_t)row8 * 128u + ((uint32_t)((half * 4 + cj) ^ row8) << 4));
+        }
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const int gi = cw + i * TG_CONV_WARPS;
+          if (gi < groups) {
+            const uint32_t rowb = dst + (uint32_t)gi * 1024u + (uint32_t)row8 * 128u;
+            uint32_t o[8];
+            widen4(v[i].x, o);
+            widen4(v[i].y, o + 2);
+            widen4(v[i].z, o + 4);
+            widen4(v[i].w, o + 6);
+            sts16(rowb + ((uint32_t)((2 * cj) ^ row8) << 4), o[0], o[1], o[2], o[3]);
+            sts16(rowb + ((uint32_t)((2 * cj + 1) ^ row8) << 4), o[4], o[5], o[6], o[7]);
+          }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
@@ -604,7 +616,7 @@ cudaError_t tg_go(const CUtensorMap& mW, const CUtensorMap& mW3, const CUtensorM
     if (attr == cudaSuccess && CTAS == 2) {  // pairs that fit at once
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3((unsigned)(sms / 2 * 2));
-      cfg.blockDim = dim3(I8 ? 512 : 256);
+      cfg.blockDim = dim3(I8 ? TG_THREADS_I8 : TG_THREADS);
       cfg.dynamicSmemBytes = TG_SMEM;
       cudaLaunchAttribute at[1];
       at[0].id = cudaLaunchAttributeClusterDimension;
@@ -621,7 +633,7 @@ cudaError_t tg_go(const CUtensorMap& mW, const CUtensorMap& mW3, const CUtensorM
   const GmmArgs& a = p.g;
   const long long most = (long long)p.MT * ((long long)a.R / p.NT + std::min(a.E, a.R));  // tiles at most
   const int n = (int)std::min<long long>(clusters, std::max(1ll, most));
-  return ops_launch(kernel, dim3((unsigned)(n * CTAS)), I8 ? 512 : 256, smem, s, CTAS, mW, mW3, mX, mXb, p);
+  return ops_launch(kernel, dim3((unsigned)(n * CTAS)), I8 ? TG_THREADS_I8 : TG_THREADS, smem, s, CTAS, mW, mW3, mX, mXb, p);
 }
 
 }  // namespace
@@ -673,11 +685,12 @@ cudaError_t launch_gmm_tc(const GmmArgs& a, int ctas, int nt, cudaStream_t s) {
 cudaError_t launch_gmm(const GmmArgs& a, cudaStream_t s) {
   if (const char* v = std::getenv("SFFN_GMM_TUNE")) {
     int c = 0, n = 0;
-    if (std::sscanf(v, "%d,%d", &c, &n) == 2 && c > 0) return launch_gmm_tc(a, c, n, s);
+    if (std::sscanf(v, "%d,%d", &c, &n) == 2 && c > 0) return launch_gmm_tc(a, c, a.w3 ? std::min(128, n) : n, s);
     return launch_gmm_rows(a, s);
   }
   const int busy = std::min(a.E, a.R);
-  if (a.R <= 4 * busy) return launch_gmm_rows(a, s);
+  if (a.w3) return launch_gmm_tc(a, a.R >= 96 * busy ? 2 : 1, 128, s);
+  if (a.R < 16 || (a.i8 && a.R <= 4 * busy)) return launch_gmm_rows(a, s);
   if (a.R >= 96 * busy) return launch_gmm_tc(a, 2, 256, s);
   return launch_gmm_tc(a, 1, 128, s);
 }
