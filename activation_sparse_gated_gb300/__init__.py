@@ -43,7 +43,7 @@ EXPORTS = ("sffn_create", "sffn_create_ex", "sffn_set_live_threshold", "sffn_set
            "sffn_last_error", "sffn_version", "sffn_debug_timeout_probe", "sffn_forward_noalloc",
            "sffn_set_weights_int8", "sffn_get_weights_int8",
            "sffn_route_workspace", "sffn_route", "sffn_quantize_tokens", "sffn_matmul_int8", "sffn_grouped_matmul",
-           "sffn_experts_workspace", "sffn_experts_forward", "sffn_check")
+           "sffn_grouped_workspace",            "sffn_experts_workspace", "sffn_experts_forward", "sffn_check")
 
 _lib = None
 
@@ -86,8 +86,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "sffn_route_workspace": (sz, [ip] * 3),
         "sffn_route": (ip, [vp, ll, vp, vp, vp, vp, ip, ip, ip, ip, ip, vp, sz, vp]),
         "sffn_quantize_tokens": (ip, [vp, ll, vp, vp, ip, ip, vp]),
-        "sffn_matmul_int8": (ip, [vp, ll, vp, vp, vp, vp, ll, ip, ip, ip, ip, vp]),
-        "sffn_grouped_matmul": (ip, [vp, ll, vp, vp, vp, vp, vp, ip, vp, ll] + [ip] * 8 + [vp]),
+        "sffn_matmul_int8": (ip, [vp, ll, vp, vp, vp, vp, ll, ip, ip, ip, ip, vp, sz, vp]),
+        "sffn_grouped_workspace": (sz, [ip] * 6),
+        "sffn_grouped_matmul": (ip, [vp, ll, vp, vp, vp, vp, vp, ip, vp, ll] + [ip] * 8 + [vp, sz, vp]),
         "sffn_experts_workspace": (sz, [ip] * 4),
         "sffn_experts_forward": (ip, [vp, ll] + [vp] * 8 + [ip] * 6 + [vp, sz, vp]),
         "sffn_check": (ip, [vp]),
@@ -229,16 +230,22 @@ def sffn_quantize_tokens(x, ldx, q, scales, T: int, K: int, stream=None):
     return _check(load().sffn_quantize_tokens(_ptr(x), ldx, _ptr(q), _ptr(scales), T, K, _stream(stream)))
 
 
-def sffn_matmul_int8(xq, ldx, sx, wq, sw, y, ldy, T: int, N: int, K: int, y_dtype: int, stream=None):
+def sffn_grouped_workspace(R: int, XR: int, N: int, K: int, E: int, dtype: int) -> int:
+    return load().sffn_grouped_workspace(R, XR, N, K, E, dtype)
+
+
+def sffn_matmul_int8(xq, ldx, sx, wq, sw, y, ldy, T: int, N: int, K: int, y_dtype: int, workspace=None,
+                     workspace_bytes: int = 0, stream=None):
     return _check(load().sffn_matmul_int8(_ptr(xq), ldx, _ptr(sx), _ptr(wq), _ptr(sw), _ptr(y), ldy, T, N, K,
-                                          y_dtype, _stream(stream)))
+                                          y_dtype, _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
 def sffn_grouped_matmul(x, ldx, sx, w, sw, offsets, index, index_div: int, y, ldy, R: int, XR: int, N: int, K: int,
-                        E: int, dtype: int, y_dtype: int, flags: int = 0, stream=None):
+                        E: int, dtype: int, y_dtype: int, flags: int = 0, workspace=None, workspace_bytes: int = 0,
+                        stream=None):
     return _check(load().sffn_grouped_matmul(_ptr(x), ldx, _ptr(sx), _ptr(w), _ptr(sw), _ptr(offsets), _ptr(index),
                                              index_div, _ptr(y), ldy, R, XR, N, K, E, dtype, y_dtype, flags,
-                                             _stream(stream)))
+                                             _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
 def sffn_experts_workspace(T: int, k: int, D: int, H: int) -> int:

@@ -45,6 +45,8 @@ constexpr int TG_CONV_WARPS = 16;
 constexpr int TG_THREADS = 256, TG_THREADS_I8 = 32 * (TG_CONV_WARP0 + TG_CONV_WARPS);
 constexpr uint64_t TG_TIMEOUT_NS = 250000000ull;
 constexpr size_t TG_SMEM = 227 * 1024;
+// what a kernel multiplies: bf16; bf16 gate and up together; int8 codes widened in flight; fp16 copies of codes
+enum { TG_BF16, TG_GATED, TG_I8, TG_F16 };
 constexpr int TG_G = 8;           // weight tiles of one raster group
 
 struct TgArgs {
@@ -261,10 +263,11 @@ __device__ __forceinline__ Tile tile_at(const TgArgs& p, const int* s_off, const
   return q;
 }
 
-template <int CTAS, bool GATED, bool I8, bool KN>
-__global__ void __launch_bounds__(I8 ? TG_THREADS_I8 : TG_THREADS, 1)
+template <int CTAS, int MODE, bool KN>
+__global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
     gmm_tc_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mW3,
                   const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mXb, const TgArgs p) {
+  constexpr bool GATED = MODE == TG_GATED, I8 = MODE == TG_I8, F16 = MODE == TG_I8 || MODE == TG_F16;
   extern __shared__ uint8_t smraw[];
   uint8_t* sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
   constexpr uint32_t AB = 128u * 128u;  // one A region: 128 rows x 128 bytes
@@ -288,12 +291,12 @@ __global__ void __launch_bounds__(I8 ? TG_THREADS_I8 : TG_THREADS, 1)
 
   if (tid == 0) {
     for (int s = 0; s < p.S; ++s) {
-      mbar_init(&full[s], I8 ? TG_CONV_WARPS * CTAS : 1);
+      mbar_init(&full[s], I8 ? 4 * CTAS : 1);
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < p.SR; ++s) {
       mbar_init(&rfull[s], 1);
-      mbar_init(&rempty[s], TG_CONV_WARPS);
+      mbar_init(&rempty[s], 8);  // four warps, two halves
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&accf[b], 1);
@@ -432,7 +435,7 @@ __global__ void __launch_bounds__(I8 ? TG_THREADS_I8 : TG_THREADS, 1)
       bool ok = true;
       for (int t = first; t < total && ok; t += step, ++tl) {
         const Tile q = tile_at<CTAS>(p, s_off, s_pre, t);
-        const uint32_t idesc = (I8 ? 1u << 4 : (1u << 4) | (1u << 7) | (1u << 10)) | ((KN ? 1u : 0u) << 15) |
+        const uint32_t idesc = (F16 ? 1u << 4 : (1u << 4) | (1u << 7) | (1u << 10)) | ((KN ? 1u : 0u) << 15) |
                                ((uint32_t)(q.n >> 3) << 17) | ((uint32_t)(128 * CTAS >> 4) << 24);
         const uint32_t b = tl & 1, use = tl >> 1;
         if (use > 0 && !__all_sync(0xffffffffu, tg_wait<CTAS == 2>(&acce[b], (use - 1) & 1, abort_flag, p.err))) break;
@@ -465,41 +468,45 @@ __global__ void __launch_bounds__(I8 ? TG_THREADS_I8 : TG_THREADS, 1)
     __syncwarp();
   } else if (I8 && warp >= TG_CONV_WARP0) {
     // ---------------------------------------------------------------- int8 -> fp16 operand tiles
-    const int cw = warp - TG_CONV_WARP0, row8 = lane & 7, cj = lane >> 3;
-    uint32_t it = 0, rt = 0;
+    // Four groups of four warps take every fourth chunk each: a chunk's chain of load, widen, store, fence and
+    // arrival is longer than its MMAs, four of them overlap.
+    const int cg = (warp - TG_CONV_WARP0) >> 2, cw = warp & 3, row8 = lane & 7, cj = lane >> 3;
+    const int KCH = (p.g.K + 127) / 128;
+    uint32_t it0 = 0, rt0 = 0;  // chunks and raw stages of the tiles before
     bool ok = true;
     for (int t = first; t < total && ok; t += step) {
       const Tile q = tile_at<CTAS>(p, s_off, s_pre, t);
       const int groups = 16 + q.n / CTAS / 8;  // 8-row groups: A, then B (both regions are dense)
-      for (int c = 0; c < p.KC && ok; ++c, ++it) {
-        const int rs = rt % p.SR, s = it % p.S;
+      for (int c = (int)((cg - it0) & 3u); c < p.KC; c += 4) {
+        const uint32_t it = it0 + c, rt = rt0 + (c >> 1), s = it % p.S, rs = rt % p.SR;
         const int half = c & 1;
-        if (half == 0 && !tg_wait<false>(&rfull[rs], (rt / p.SR) & 1, abort_flag, p.err)) ok = false;
-        if (ok && it >= (uint32_t)p.S && !tg_wait<false>(&empty[s], (it / p.S - 1) & 1, abort_flag, p.err)) ok = false;
+        // A parity wait must not run two phases ahead.  With four stages a group meets every phase of its stage's
+        // `empty`; that wait shows that chunk it - 4 and all before it are multiplied, so of the raw stage every
+        // phase before this one is over (its last chunk is at most 2 (rt - SR) + 1 <= it - 4 for SR >= 3).
+        ok = it < (uint32_t)p.S || tg_wait<false>(&empty[s], (it / p.S - 1) & 1, abort_flag, p.err);
+        if (ok) ok = tg_wait<false>(&rfull[rs], (rt / p.SR) & 1, abort_flag, p.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint32_t src = smb + raw0 + (uint32_t)rs * st_bytes, dst = smb + (uint32_t)s * st_bytes;
-        // at most 48 groups: three a warp, their loads together
-        uint4 v[3];
+        const uint32_t src = smb + raw0 + rs * st_bytes + (uint32_t)row8 * 128u + ((uint32_t)((half * 4 + cj) ^ row8) << 4);
+        const uint32_t dst = smb + s * st_bytes + (uint32_t)row8 * 128u;
+        const uint32_t d0 = dst + ((uint32_t)((2 * cj) ^ row8) << 4), d1 = dst + ((uint32_t)((2 * cj + 1) ^ row8) << 4);
+        for (int g0 = cw; g0 < groups; g0 += 16) {
+          uint4 v[4];
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          const int gi = cw + i * TG_CONV_WARPS;
-          if (gi < groups)
-            v[i] = lds16a(src + (uint32_t)gi * 1024u + (uint32_t)row8 * 128u + ((uint32_t)((half * 4 + cj) ^ row8) << 4));
-        }
+          for (int i = 0; i < 4; ++i)
+            if (g0 + 4 * i < groups) v[i] = lds16a(src + (uint32_t)(g0 + 4 * i) * 1024u);
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          const int gi = cw + i * TG_CONV_WARPS;
-          if (gi < groups) {
-            const uint32_t rowb = dst + (uint32_t)gi * 1024u + (uint32_t)row8 * 128u;
-            uint32_t o[8];
-            widen4(v[i].x, o);
-            widen4(v[i].y, o + 2);
-            widen4(v[i].z, o + 4);
-            widen4(v[i].w, o + 6);
-            sts16(rowb + ((uint32_t)((2 * cj) ^ row8) << 4), o[0], o[1], o[2], o[3]);
-            sts16(rowb + ((uint32_t)((2 * cj + 1) ^ row8) << 4), o[4], o[5], o[6], o[7]);
-          }
+          for (int i = 0; i < 4; ++i)
+            if (g0 + 4 * i < groups) {
+              const uint32_t off = (uint32_t)(g0 + 4 * i) * 1024u;
+              uint32_t o[8];
+              widen4(v[i].x, o);
+              widen4(v[i].y, o + 2);
+              widen4(v[i].z, o + 4);
+              widen4(v[i].w, o + 6);
+              sts16(d0 + off, o[0], o[1], o[2], o[3]);
+              sts16(d1 + off, o[4], o[5], o[6], o[7]);
+            }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
@@ -508,12 +515,12 @@ __global__ void __launch_bounds__(I8 ? TG_THREADS_I8 : TG_THREADS, 1)
             arrive_remote(cluster_map(smem_u32(&full[s]), 0));
           else
             mbar_arrive(&full[s]);
-        }
-        if (half == 1 || c == p.KC - 1) {
-          if (lane == 0) mbar_arrive(&rempty[rs]);
-          ++rt;
+          mbar_arrive(&rempty[rs]);
+          if (half == 0 && c == p.KC - 1) mbar_arrive(&rempty[rs]);  // no second half: its arrival as well
         }
       }
+      it0 += p.KC;
+      rt0 += KCH;
     }
   } else if (warp >= TG_EPI_WARP0 && warp < TG_EPI_WARP0 + 4) {
     // ---------------------------------------------------------------- epilogue: lane = one row of w
@@ -526,7 +533,7 @@ __global__ void __launch_bounds__(I8 ? TG_THREADS_I8 : TG_THREADS, 1)
       if (!__all_sync(0xffffffffu, tg_wait<false>(&accf[b], (tl >> 1) & 1, abort_flag, p.err))) break;
       tc_fence_after();
       const uint32_t ta = tmem + b * (uint32_t)((GATED ? 2 : 1) * p.NT) + ((uint32_t)(32 * ew) << 16);
-      const float sw = I8 && n < p.g.N ? p.g.sw[(size_t)q.e * p.g.N + n] : 0.f;
+      const float sw = F16 && n < p.g.N ? p.g.sw[(size_t)q.e * p.g.N + n] : 0.f;
       const int rows = q.r1 - q.r0;
       for (int c0 = 0; c0 < rows; c0 += 32) {
         uint32_t v[32];
@@ -548,7 +555,7 @@ __global__ void __launch_bounds__(I8 ? TG_THREADS_I8 : TG_THREADS, 1)
             if (j >= m) break;
             const int r = q.r0 + c0 + j;
             float f = __uint_as_float(v[j]);
-            if (I8) {
+            if (F16) {
               int src = r;
               if (p.g.index) {
                 const int i = p.g.index[r];
@@ -603,10 +610,11 @@ bool encode_w(CUtensorMap* m, const void* w, const GmmArgs& a) {
   return encode(m, w, 3, dims, strides, box, a.i8 != 0);
 }
 
-template <int CTAS, bool GATED, bool I8, bool KN>
+template <int CTAS, int MODE, bool KN>
 cudaError_t tg_go(const CUtensorMap& mW, const CUtensorMap& mW3, const CUtensorMap& mX, const CUtensorMap& mXb,
                   const TgArgs& p, size_t smem, int sms, cudaStream_t s) {
-  auto kernel = gmm_tc_kernel<CTAS, GATED, I8, KN>;
+  auto kernel = gmm_tc_kernel<CTAS, MODE, KN>;
+  constexpr int threads = MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS;
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
   static int clusters = 0;
@@ -616,7 +624,7 @@ cudaError_t tg_go(const CUtensorMap& mW, const CUtensorMap& mW3, const CUtensorM
     if (attr == cudaSuccess && CTAS == 2) {  // pairs that fit at once
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3((unsigned)(sms / 2 * 2));
-      cfg.blockDim = dim3(I8 ? TG_THREADS_I8 : TG_THREADS);
+      cfg.blockDim = dim3(threads);
       cfg.dynamicSmemBytes = TG_SMEM;
       cudaLaunchAttribute at[1];
       at[0].id = cudaLaunchAttributeClusterDimension;
@@ -633,7 +641,7 @@ cudaError_t tg_go(const CUtensorMap& mW, const CUtensorMap& mW3, const CUtensorM
   const GmmArgs& a = p.g;
   const long long most = (long long)p.MT * ((long long)a.R / p.NT + std::min(a.E, a.R));  // tiles at most
   const int n = (int)std::min<long long>(clusters, std::max(1ll, most));
-  return ops_launch(kernel, dim3((unsigned)(n * CTAS)), I8 ? TG_THREADS_I8 : TG_THREADS, smem, s, CTAS, mW, mW3, mX, mXb, p);
+  return ops_launch(kernel, dim3((unsigned)(n * CTAS)), threads, smem, s, CTAS, mW, mW3, mX, mXb, p);
 }
 
 }  // namespace
@@ -647,14 +655,17 @@ cudaError_t launch_gmm_tc(const GmmArgs& a, int ctas, int nt, cudaStream_t s) {
   const bool gated = a.w3 != nullptr;
   cudaError_t e = ops_error_word(&p.err);
   if (e != cudaSuccess) return e;
-  const int ntl = nt / ctas;
-  const uint32_t st = (gated ? 2u : 1u) * 16384u + (uint32_t)(ntl + 7) / 8 * 1024u;
   const size_t fixed = 1024 + 8 * (2 * 16 + 2 * 16 + 4) + 8 + sizeof(int) * 2 * (size_t)(a.E + 1) + 64;
-  const int slots = std::min(24, (int)((TG_SMEM - fixed) / st));
-  p.S = a.i8 ? std::min(4, slots / 2) : std::min(16, slots);
-  p.SR = a.i8 ? std::min(12, slots - p.S) : 0;
+  auto stage_bytes = [&] { return (gated ? 2u : 1u) * 16384u + (uint32_t)(p.NT / ctas + 7) / 8 * 1024u; };
+  auto slots = [&] { return (int)((TG_SMEM - fixed) / stage_bytes()); };
+  // int8: the converters' four groups need four operand stages and three raw ones
+  while (a.i8 && slots() < 7) p.NT >>= 1;
+  const int ntl = p.NT / ctas;
+  const uint32_t st = stage_bytes();
+  p.S = a.i8 ? 4 : std::min(16, slots());
+  p.SR = a.i8 ? std::min(12, slots() - 4) : 0;
   int cols = 32;
-  while (cols < 2 * (gated ? 2 : 1) * nt) cols <<= 1;
+  while (cols < 2 * (gated ? 2 : 1) * p.NT) cols <<= 1;
   p.cols = cols;
   p.bxr = std::min(ntl, 32);
   CUtensorMap mW, mW3, mX, mXb;
@@ -670,16 +681,50 @@ cudaError_t launch_gmm_tc(const GmmArgs& a, int ctas, int nt, cudaStream_t s) {
   const size_t smem = fixed + (size_t)(p.S + p.SR) * st;
   const int sms = ops_num_sms();
   if (a.i8)
-    return ctas == 2 ? tg_go<2, false, true, false>(mW, mW3, mX, mXb, p, smem, sms, s)
-                     : tg_go<1, false, true, false>(mW, mW3, mX, mXb, p, smem, sms, s);
+    return ctas == 2 ? tg_go<2, TG_I8, false>(mW, mW3, mX, mXb, p, smem, sms, s)
+                     : tg_go<1, TG_I8, false>(mW, mW3, mX, mXb, p, smem, sms, s);
+  if (a.f16) return tg_go<2, TG_F16, false>(mW, mW3, mX, mXb, p, smem, sms, s);
   if (gated)
-    return ctas == 2 ? tg_go<2, true, false, false>(mW, mW3, mX, mXb, p, smem, sms, s)
-                     : tg_go<1, true, false, false>(mW, mW3, mX, mXb, p, smem, sms, s);
+    return ctas == 2 ? tg_go<2, TG_GATED, false>(mW, mW3, mX, mXb, p, smem, sms, s)
+                     : tg_go<1, TG_GATED, false>(mW, mW3, mX, mXb, p, smem, sms, s);
   if (a.kn)
-    return ctas == 2 ? tg_go<2, false, false, true>(mW, mW3, mX, mXb, p, smem, sms, s)
-                     : tg_go<1, false, false, true>(mW, mW3, mX, mXb, p, smem, sms, s);
-  return ctas == 2 ? tg_go<2, false, false, false>(mW, mW3, mX, mXb, p, smem, sms, s)
-                   : tg_go<1, false, false, false>(mW, mW3, mX, mXb, p, smem, sms, s);
+    return ctas == 2 ? tg_go<2, TG_BF16, true>(mW, mW3, mX, mXb, p, smem, sms, s)
+                     : tg_go<1, TG_BF16, true>(mW, mW3, mX, mXb, p, smem, sms, s);
+  return ctas == 2 ? tg_go<2, TG_BF16, false>(mW, mW3, mX, mXb, p, smem, sms, s)
+                   : tg_go<1, TG_BF16, false>(mW, mW3, mX, mXb, p, smem, sms, s);
+}
+
+// fp16 copies of x's and w's codes for the products whose groups are long.
+__global__ void __launch_bounds__(256) widen_kernel(const uint8_t* __restrict__ x, long long ldx, int K16,
+                                                    long long nx, const uint4* __restrict__ w, long long nw,
+                                                    uint4* __restrict__ out) {
+  pdl_launch_dependents();
+  pdl_wait();
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < nx + nw; i += (long long)gridDim.x * 256) {
+    uint4 v;
+    if (i < nx) {
+      const long long r = i / K16;
+      v = *reinterpret_cast<const uint4*>(x + r * ldx + (i - r * K16) * 16);
+    } else {
+      v = __ldcs(w + (i - nx));
+    }
+    uint32_t o[8];
+    widen4(v.x, o);
+    widen4(v.y, o + 2);
+    widen4(v.z, o + 4);
+    widen4(v.w, o + 6);
+    out[2 * i] = make_uint4(o[0], o[1], o[2], o[3]);
+    out[2 * i + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+// Rows per expert from which fp16 copies pay.
+constexpr int TG_WIDE_ROWS = 768;
+
+bool wide(int R, int E, int i8) { return i8 && R / E >= TG_WIDE_ROWS; }
+
+size_t gmm_workspace(int R, int XR, int N, int K, int E, int i8) {
+  return wide(R, E, i8) ? 2 * ((size_t)XR * K + (size_t)E * N * K) : 0;
 }
 
 cudaError_t launch_gmm(const GmmArgs& a, cudaStream_t s) {
@@ -689,6 +734,20 @@ cudaError_t launch_gmm(const GmmArgs& a, cudaStream_t s) {
     return launch_gmm_rows(a, s);
   }
   const int busy = std::min(a.E, a.R);
+  if (wide(a.R, a.E, a.i8) && a.workspace) {
+    const long long nx = (long long)a.XR * (a.K / 16), nw = (long long)a.E * a.N * (a.K / 16);
+    const int grid = (int)std::min<long long>((nx + nw + 255) / 256, 8ll * ops_num_sms());
+    const cudaError_t e = ops_launch(widen_kernel, dim3((unsigned)grid), 256, 0, s, 1, (const uint8_t*)a.x, a.ldx,
+                                     a.K / 16, nx, (const uint4*)a.w, nw, (uint4*)a.workspace);
+    if (e != cudaSuccess) return e;
+    GmmArgs b = a;
+    b.x = a.workspace;
+    b.w = static_cast<uint16_t*>(a.workspace) + 16 * nx;
+    b.ldx = a.K;
+    b.i8 = 0;
+    b.f16 = 1;
+    return launch_gmm_tc(b, 2, 256, s);
+  }
   if (a.w3) return launch_gmm_tc(a, a.R >= 96 * busy ? 2 : 1, 128, s);
   if (a.R < 16 || (a.i8 && a.R <= 4 * busy)) return launch_gmm_rows(a, s);
   if (a.R >= 96 * busy) return launch_gmm_tc(a, 2, 256, s);

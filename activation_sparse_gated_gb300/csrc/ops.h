@@ -42,10 +42,13 @@ struct GmmArgs {
   long long ldx = 0, ldy = 0;
   int R = 0, XR = 0, N = 0, K = 0, E = 1;  // XR: rows of x
   int i8 = 0, y_f32 = 0, kn = 0, act = 0;
+  int f16 = 0;                    // x and w are fp16 copies of int8 codes (with their scales)
+  void* workspace = nullptr;      // gmm_workspace() bytes
 };
 cudaError_t launch_gmm_rows(const GmmArgs& a, cudaStream_t s);
 cudaError_t launch_gmm_tc(const GmmArgs& a, int ctas, int nt, cudaStream_t s);  // ctas 1 or 2, nt 32 .. 256 (gated: 128)
 cudaError_t launch_gmm(const GmmArgs& a, cudaStream_t s);
+size_t gmm_workspace(int R, int XR, int N, int K, int E, int i8);
 
 // ---- experts.cu
 struct ExpertsArgs {

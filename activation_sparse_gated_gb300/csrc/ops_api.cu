@@ -131,7 +131,8 @@ int sffn_quantize_tokens(const void* x, long long ldx, int8_t* q, float* scales,
 
 int sffn_grouped_matmul(const void* x, long long ldx, const float* sx, const void* w, const float* sw,
                         const int* offsets, const int* index, int index_div, void* y, long long ldy, int R, int XR,
-                        int N, int K, int E, int dtype, int y_dtype, int flags, void* stream) {
+                        int N, int K, int E, int dtype, int y_dtype, int flags, void* workspace,
+                        size_t workspace_bytes, void* stream) {
   const char* fn = "sffn_grouped_matmul";
   if (dtype != SFFN_BF16 && dtype != SFFN_I8) return fail(SFFN_ERR_DTYPE, "%s: operands are bf16 or int8 codes", fn);
   if (y_dtype != SFFN_BF16 && y_dtype != SFFN_F32) return fail(SFFN_ERR_DTYPE, "%s: y is bf16 or f32", fn);
@@ -156,12 +157,17 @@ int sffn_grouped_matmul(const void* x, long long ldx, const float* sx, const voi
   if (misaligned(y, y_dtype == SFFN_F32 ? 4 : 2) || misaligned(offsets, 4) || misaligned(index, 4) ||
       (i8 && (misaligned(sx, 4) || misaligned(sw, 4))))
     return fail(SFFN_ERR_ALIGN, "%s: a pointer is not aligned to its element", fn);
+  const size_t need = gmm_workspace(R, XR, N, K, E, i8);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(SFFN_ERR_ARG, "%s: workspace of %zu bytes, %zu needed", fn, workspace ? workspace_bytes : (size_t)0, need);
+  if (need > 0 && misaligned(workspace, 16)) return fail(SFFN_ERR_ALIGN, "%s: workspace is not 16-byte aligned", fn);
   const unsigned long long eb = i8 ? 1 : 2, yb = y_dtype == SFFN_F32 ? 4 : 2;
   const unsigned long long ny = ((unsigned long long)(R - 1) * ldy + N) * yb;
   if (overlap(x, ((unsigned long long)(XR - 1) * ldx + K) * eb, y, ny) ||
-      overlap(w, (unsigned long long)E * N * K * eb, y, ny))
-    return fail(SFFN_ERR_ARG, "%s: y overlaps an operand", fn);
+      overlap(w, (unsigned long long)E * N * K * eb, y, ny) || (need > 0 && overlap(workspace, need, y, ny)))
+    return fail(SFFN_ERR_ARG, "%s: y overlaps an operand or the workspace", fn);
   GmmArgs a;
+  a.workspace = need > 0 ? workspace : nullptr;
   a.x = x;
   a.w = w;
   a.sx = i8 ? sx : nullptr;
@@ -184,10 +190,16 @@ int sffn_grouped_matmul(const void* x, long long ldx, const float* sx, const voi
   return e == cudaSuccess ? SFFN_OK : cuda_fail(fn, e);
 }
 
+size_t sffn_grouped_workspace(int R, int XR, int N, int K, int E, int dtype) {
+  if (R < 1 || XR < 1 || N < 1 || K < 1 || E < 1) return 0;
+  return gmm_workspace(R, XR, N, K, E, dtype == SFFN_I8);
+}
+
 int sffn_matmul_int8(const int8_t* xq, long long ldx, const float* sx, const int8_t* wq, const float* sw, void* y,
-                     long long ldy, int T, int N, int K, int y_dtype, void* stream) {
+                     long long ldy, int T, int N, int K, int y_dtype, void* workspace, size_t workspace_bytes,
+                     void* stream) {
   return sffn_grouped_matmul(xq, ldx, sx, wq, sw, nullptr, nullptr, 1, y, ldy, T, T, N, K, 1, SFFN_I8, y_dtype, 0,
-                             stream);
+                             workspace, workspace_bytes, stream);
 }
 
 size_t sffn_experts_workspace(int T, int k, int D, int H) {

@@ -105,6 +105,10 @@ def quantize_tokens(x, stream=None):
     return q, s
 
 
+def _scratch(nb, device):
+    return (torch.empty(nb, dtype=torch.uint8, device=device) if nb else None), nb
+
+
 def _result(out, dtype, shape, device):
     if dtype not in _OUT:
         raise ValueError(f"dtype {dtype!r} is neither bf16 nor f32")
@@ -136,8 +140,10 @@ def matmul_int8(xq, sx, wq, sw, dtype="bf16", out=None, stream=None):
     for name, t in (("wq", wq), ("sx", sx), ("sw", sw)):
         _dense(name, t)
     y, code, ldy = _result(out, dtype, (T, N), device)
-    _done(load().sffn_matmul_int8(xq.data_ptr(), _pitch("xq", xq), sx.data_ptr(), wq.data_ptr(), sw.data_ptr(),
-                                  y.data_ptr(), ldy, T, N, K, code, _raw(device)))
+    lib = load()
+    ws, nb = _scratch(lib.sffn_grouped_workspace(T, T, N, K, 1, SFFN_I8), device)
+    _done(lib.sffn_matmul_int8(xq.data_ptr(), _pitch("xq", xq), sx.data_ptr(), wq.data_ptr(), sw.data_ptr(),
+                               y.data_ptr(), ldy, T, N, K, code, nb and ws.data_ptr(), nb, _raw(device)))
     return y
 
 
@@ -178,10 +184,13 @@ def grouped_matmul(x, w, offsets, sx=None, sw=None, index=None, index_div: int =
     elif sx is not None or sw is not None:
         raise ValueError("scales go with int8 operands")
     y, code, ldy = _result(out, dtype, (R, N), device)
-    _done(load().sffn_grouped_matmul(
+    lib = load()
+    ws, nb = _scratch(lib.sffn_grouped_workspace(R, XR, N, K, E, SFFN_I8) if i8 else 0, device)
+    _done(lib.sffn_grouped_matmul(
         x.data_ptr(), _pitch("x", x), sx.data_ptr() if i8 else None, w.data_ptr(), sw.data_ptr() if i8 else None,
         offsets.data_ptr(), index.data_ptr() if index is not None else None, index_div, y.data_ptr(), ldy, R, XR, N, K,
-        E, SFFN_I8 if i8 else SFFN_BF16, code, SFFN_W_KN if transposed else 0, _raw(device)))
+        E, SFFN_I8 if i8 else SFFN_BF16, code, SFFN_W_KN if transposed else 0,
+        nb and ws.data_ptr(), nb, _raw(device)))
     return y
 
 

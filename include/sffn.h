@@ -381,10 +381,12 @@ int sffn_quantize_tokens(const void* x, long long ldx, int8_t* q, float* scales,
  * y[t, n] = sx[t] sw[n] sum_k xq[t, k] wq[n, k]: int8 codes xq [T, K] (row
  * pitch ldx) and wq [N, K] with one scale per token and per output channel;
  * y [T, N] (row pitch ldy) bf16 or f32.  K % 16 == 0, ldx % 16 == 0, xq and wq
- * 16-byte aligned.
+ * 16-byte aligned.  The workspace holds sffn_grouped_workspace(T, T, N, K, 1,
+ * SFFN_I8) bytes (0 for short batches: NULL is fine).
  */
 int sffn_matmul_int8(const int8_t* xq, long long ldx, const float* sx, const int8_t* wq, const float* sw, void* y,
-                     long long ldy, int T, int N, int K, int y_dtype, void* stream);
+                     long long ldy, int T, int N, int K, int y_dtype, void* workspace, size_t workspace_bytes,
+                     void* stream);
 
 /*
  * Products grouped by expert with ragged sizes: for the rows r of expert e,
@@ -399,12 +401,15 @@ int sffn_matmul_int8(const int8_t* xq, long long ldx, const float* sx, const int
  * offsets[E] are left as they are, offsets past R are cut to R.  SFFN_W_KN
  * (bf16): w is [E, K, N].  K % 8 == 0 (bf16) or K % 16 == 0 (int8), ldx
  * likewise, N % 8 == 0 with SFFN_W_KN; x and w 16-byte aligned; y overlaps
- * neither.
+ * neither.  The workspace holds sffn_grouped_workspace() bytes (0 for bf16 and
+ * for short int8 groups; else fp16 copies of the codes).
  */
 enum { SFFN_W_KN = 1 };
+size_t sffn_grouped_workspace(int R, int XR, int N, int K, int E, int dtype);
 int sffn_grouped_matmul(const void* x, long long ldx, const float* sx, const void* w, const float* sw,
                         const int* offsets, const int* index, int index_div, void* y, long long ldy, int R, int XR,
-                        int N, int K, int E, int dtype, int y_dtype, int flags, void* stream);
+                        int N, int K, int E, int dtype, int y_dtype, int flags, void* workspace,
+                        size_t workspace_bytes, void* stream);
 
 /*
  * The gated experts behind the router:

@@ -271,6 +271,51 @@ def test_grouped_matmul_int8_reads_tokens_through_an_index():
     assert torch.equal(y, z)
 
 
+def test_grouped_matmul_int8_long_groups():
+    """Groups long enough for the fp16 copies of the codes, strided rows, with and without an index."""
+    g, T, k, E, N, K = gen(62), 1300, 2, 3, 264, 400
+    routing = sffn.route(torch.randn(T, E, generator=g, device=DEV), k)
+    big, sx = int8_operands(g, T, K + 48, full=True)
+    x = big[:, 32:32 + K]
+    w, sw = int8_operands(g, E * N, K)
+    w, sw = w.view(E, N, K), sw.view(E, N)
+    assert sffn.sffn_grouped_workspace(T * k, T, N, K, E, sffn.SFFN_I8) > 0
+    src = (routing.rows // k).long()
+    y = sffn.grouped_matmul(x, w, routing.offsets, sx=sx, sw=sw, index=routing.rows, index_div=k, dtype="f32")
+    z = sffn.grouped_matmul(x[src].contiguous(), w, routing.offsets, sx=sx[src].contiguous(), sw=sw, dtype="f32")
+    assert torch.equal(y, z)
+    b = routing.offsets.tolist()
+    for e in range(E):
+        r = slice(b[e], b[e + 1])
+        xe = x[src[r]]
+        scale = torch.outer(sx[src[r]].double(), sw[e].double())
+        ref = (xe.double() @ w[e].double().T) * scale
+        close(y[r], ref, 3 * 2.0 ** -24 * ref.abs() + int8_bound(xe, w[e], scale))
+
+
+@pytest.mark.parametrize("E", [200, 1000])
+def test_grouped_matmul_many_experts(E):
+    """Tables of many groups, most of them empty or short."""
+    g, N, K = gen(E), 136, 160
+    counts = torch.randint(0, 24, (E,), generator=torch.Generator().manual_seed(E)).tolist()
+    off = offsets_of(counts)
+    R, b = sum(counts), off.tolist()
+    x = torch.randn(R, K, generator=g, device=DEV).to(BF)
+    w = torch.randn(E, N, K, generator=g, device=DEV).to(BF)
+    q, sx = int8_operands(g, R, K)
+    wq, sw = int8_operands(g, E * N, K)
+    wq, sw = wq.view(E, N, K), sw.view(E, N)
+    y = sffn.grouped_matmul(x, w, off, dtype="f32")
+    z = sffn.grouped_matmul(q, wq, off, sx=sx, sw=sw, dtype="f32")
+    for e in range(0, E, 7):
+        r = slice(b[e], b[e + 1])
+        xe, we = x[r].double(), w[e].double()
+        close(y[r], xe @ we.T, K * 2.0 ** -23 * (xe.abs() @ we.abs().T))
+        scale = torch.outer(sx[r].double(), sw[e].double())
+        ref = (q[r].double() @ wq[e].double().T) * scale
+        close(z[r], ref, 3 * 2.0 ** -24 * ref.abs() + int8_bound(q[r], wq[e], scale))
+
+
 def test_grouped_matmul_source_rows_out_of_range_read_as_zeros():
     g = gen(21)
     x = torch.randn(10, 64, generator=g, device=DEV).to(BF)

@@ -56,10 +56,11 @@ def test_quantize_refuses(lib, bad, code):
 
 def grouped(lib, **bad):
     a = dict(x=X, ldx=64, sx=S, w=W, sw=S, offsets=O, index=None, div=1, y=Y, ldy=32, R=8, XR=8, N=32, K=64, E=4,
-             dtype=sffn.SFFN_BF16, ydt=sffn.SFFN_BF16, flags=0)
+             dtype=sffn.SFFN_BF16, ydt=sffn.SFFN_BF16, flags=0, ws=None, nws=0)
     a.update(bad)
     return lib.sffn_grouped_matmul(*[a[k] for k in ("x", "ldx", "sx", "w", "sw", "offsets", "index", "div", "y", "ldy",
-                                                   "R", "XR", "N", "K", "E", "dtype", "ydt", "flags")], None)
+                                                   "R", "XR", "N", "K", "E", "dtype", "ydt", "flags", "ws", "nws")],
+                                   None)
 
 
 @pytest.mark.parametrize("bad,code", [
@@ -75,7 +76,11 @@ def grouped(lib, **bad):
     (dict(dtype=sffn.SFFN_I8, sw=None), sffn.SFFN_ERR_ARG), (dict(flags=sffn.SFFN_W_KN, N=36, ldy=36), sffn.SFFN_ERR_ARG),
     (dict(x=None), sffn.SFFN_ERR_ARG), (dict(offsets=None), sffn.SFFN_ERR_ARG), (dict(x=X + 8), sffn.SFFN_ERR_ALIGN),
     (dict(w=W + 2), sffn.SFFN_ERR_ALIGN), (dict(y=Y + 1), sffn.SFFN_ERR_ALIGN), (dict(offsets=O + 2), sffn.SFFN_ERR_ALIGN),
-    (dict(y=X + 64), sffn.SFFN_ERR_ARG), (dict(y=W), sffn.SFFN_ERR_ARG)])
+    (dict(y=X + 64), sffn.SFFN_ERR_ARG), (dict(y=W), sffn.SFFN_ERR_ARG),
+    (dict(dtype=sffn.SFFN_I8, R=8192, XR=8192), sffn.SFFN_ERR_ARG),
+    (dict(dtype=sffn.SFFN_I8, R=8192, XR=8192, ws=WS, nws=64), sffn.SFFN_ERR_ARG),
+    (dict(dtype=sffn.SFFN_I8, R=8192, XR=8192, ws=WS + 8, nws=1 << 24), sffn.SFFN_ERR_ALIGN),
+    (dict(dtype=sffn.SFFN_I8, R=8192, XR=8192, ws=Y, nws=1 << 24), sffn.SFFN_ERR_ARG)])
 def test_grouped_matmul_refuses(lib, bad, code):
     assert grouped(lib, **bad) == code
     assert "sffn_grouped_matmul" in sffn.sffn_last_error()
@@ -83,14 +88,14 @@ def test_grouped_matmul_refuses(lib, bad, code):
 
 def test_empty_calls_touch_nothing(lib):
     assert grouped(lib, R=0) == sffn.SFFN_OK
-    assert lib.sffn_matmul_int8(X, 64, S, W, S, Y, 32, 0, 32, 64, sffn.SFFN_BF16, None) == sffn.SFFN_OK
+    assert lib.sffn_matmul_int8(X, 64, S, W, S, Y, 32, 0, 32, 64, sffn.SFFN_BF16, None, 0, None) == sffn.SFFN_OK
     assert lib.sffn_quantize_tokens(None, 64, None, None, 0, 64, None) == sffn.SFFN_OK
     assert experts(lib, T=0) == sffn.SFFN_OK
 
 
 def test_matmul_int8_refuses(lib):
-    assert lib.sffn_matmul_int8(X, 72, S, W, S, Y, 32, 4, 32, 72, sffn.SFFN_BF16, None) == sffn.SFFN_ERR_ARG
-    assert lib.sffn_matmul_int8(X, 64, None, W, S, Y, 32, 4, 32, 64, sffn.SFFN_BF16, None) == sffn.SFFN_ERR_ARG
+    assert lib.sffn_matmul_int8(X, 72, S, W, S, Y, 32, 4, 32, 72, sffn.SFFN_BF16, None, 0, None) == sffn.SFFN_ERR_ARG
+    assert lib.sffn_matmul_int8(X, 64, None, W, S, Y, 32, 4, 32, 64, sffn.SFFN_BF16, None, 0, None) == sffn.SFFN_ERR_ARG
 
 
 def experts(lib, **bad):
@@ -118,6 +123,9 @@ def test_workspace_sizes(lib):
     assert sffn.sffn_route_workspace(1, 64, 8) == 0
     assert sffn.sffn_route_workspace(16384, 256, 8) > 0
     assert sffn.sffn_route_workspace(16384, 2000, 8) == 0
+    assert sffn.sffn_grouped_workspace(64, 64, 1024, 512, 4, sffn.SFFN_I8) == 0
+    assert sffn.sffn_grouped_workspace(8192, 8192, 1024, 512, 4, sffn.SFFN_BF16) == 0
+    assert sffn.sffn_grouped_workspace(8192, 8192, 1024, 512, 4, sffn.SFFN_I8) >= 2 * 512 * (8192 + 4 * 1024)
     assert sffn.sffn_experts_workspace(1, 8, 2560, 1024) >= 4 * 8 * 1024
     assert sffn.sffn_experts_workspace(0, 8, 2560, 1024) == 0
     # sizes pass 32 bits
