@@ -6,6 +6,8 @@
 // unit's gate z = W1_e[i] . x_t, and only a live unit's row of W3_e is read;
 // the down product then gathers the live units' rows of W2_e^T.  Both passes
 // are reads of weight rows (bf16, fp32 sums; h stays fp32).
+#include <cstdlib>
+
 #include "common.cuh"
 #include "ops.h"
 
@@ -117,6 +119,18 @@ __global__ void __launch_bounds__(EC_THREADS) experts_combine_kernel(const Exper
       make_uint2(pack_bf16x2_rn(sum.x, sum.y), pack_bf16x2_rn(sum.z, sum.w));
 }
 
+// xg[r] = x[rows[r] / k]: a grouped copy of the tokens, one block a row.
+__global__ void __launch_bounds__(128) experts_gather_kernel(const ExpertsArgs a, uint16_t* __restrict__ xg) {
+  const int r = blockIdx.x;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int i = a.rows[r];
+  if (i < 0 || i / a.k >= a.T) return;
+  const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.x) + (size_t)(i / a.k) * a.ldx);
+  uint4* dst = reinterpret_cast<uint4*>(xg + (size_t)r * a.D);
+  for (int c = threadIdx.x; c < a.D / 8; c += 128) dst[c] = __ldg(src + c);
+}
+
 size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
 
 // Few choices: the gate-first passes above; more: the grouped products on the tensor cores.
@@ -127,7 +141,8 @@ bool few(int T, int k) { return (long long)T * k <= 64; }
 size_t experts_workspace(int T, int k, int D, int H) {
   const size_t R = (size_t)T * k;
   if (few(T, k)) return sizeof(float) * R * H;
-  return round_up(2 * R * round_up(H, 8), 256) + sizeof(float) * R * D;  // h, then the choices' products
+  // h, then the choices' products (and before them, in the same place, the grouped tokens)
+  return round_up(2 * R * round_up(H, 8), 256) + sizeof(float) * R * D;
 }
 
 cudaError_t launch_experts(const ExpertsArgs& a, cudaStream_t s) {
@@ -157,6 +172,14 @@ cudaError_t launch_experts(const ExpertsArgs& a, cudaStream_t s) {
   up.K = a.D;
   up.E = a.E;
   up.act = a.act;
+  if (!std::getenv("SFFN_GATHER4")) {
+    uint16_t* xg = reinterpret_cast<uint16_t*>(o);
+    if ((e = ops_launch(experts_gather_kernel, dim3((unsigned)R), 128, 0, s, 1, a, xg)) != cudaSuccess) return e;
+    up.x = xg;
+    up.ldx = a.D;
+    up.index = nullptr;
+    up.XR = R;
+  }
   if ((e = launch_gmm(up, s)) != cudaSuccess) return e;
   GmmArgs down;
   down.x = a.workspace;

@@ -39,10 +39,10 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn();  // ffn_tc.cu
 
 namespace {
 
-constexpr int TG_EPI_WARP0 = 4;   // warps 4..7: epilogue (TMEM lane quarter = warp % 4)
+constexpr int TG_EPI_WARP0 = 4;   // warps 4..11 (int8: 4..7): epilogue (TMEM lane quarter = warp % 4)
 constexpr int TG_CONV_WARP0 = 8;  // warps 8..23: int8 -> fp16
 constexpr int TG_CONV_WARPS = 16;
-constexpr int TG_THREADS = 256, TG_THREADS_I8 = 32 * (TG_CONV_WARP0 + TG_CONV_WARPS);
+constexpr int TG_THREADS = 384, TG_THREADS_I8 = 32 * (TG_CONV_WARP0 + TG_CONV_WARPS);
 constexpr uint64_t TG_TIMEOUT_NS = 250000000ull;
 constexpr size_t TG_SMEM = 227 * 1024;
 // what a kernel multiplies: bf16; bf16 gate and up together; int8 codes widened in flight; fp16 copies of codes
@@ -268,6 +268,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
     gmm_tc_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mW3,
                   const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mXb, const TgArgs p) {
   constexpr bool GATED = MODE == TG_GATED, I8 = MODE == TG_I8, F16 = MODE == TG_I8 || MODE == TG_F16;
+  constexpr int EW = I8 ? 4 : 8;  // epilogue warps
   extern __shared__ uint8_t smraw[];
   uint8_t* sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
   constexpr uint32_t AB = 128u * 128u;  // one A region: 128 rows x 128 bytes
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&accf[b], 1);
-      mbar_init(&acce[b], 4 * CTAS);
+      mbar_init(&acce[b], EW * CTAS);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -522,22 +523,41 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
       it0 += p.KC;
       rt0 += KCH;
     }
-  } else if (warp >= TG_EPI_WARP0 && warp < TG_EPI_WARP0 + 4) {
+  } else if (warp >= TG_EPI_WARP0 && warp < TG_EPI_WARP0 + EW) {
     // ---------------------------------------------------------------- epilogue: lane = one row of w
+    // Warp ew empties TMEM lanes 32 (ew % 4) .., and of the 32-column pieces every EW / 4-th.
     const int ew = warp - TG_EPI_WARP0;
     uint32_t tl = 0;
     for (int t = first; t < total; t += step, ++tl) {
       const Tile q = tile_at<CTAS>(p, s_off, s_pre, t);
       const uint32_t b = tl & 1;
-      const int n = q.mt * 128 * CTAS + n0r + 32 * ew + lane;
+      const int n = q.mt * 128 * CTAS + n0r + 32 * (ew & 3) + lane;
+      const bool nok = n < p.g.N;
       if (!__all_sync(0xffffffffu, tg_wait<false>(&accf[b], (tl >> 1) & 1, abort_flag, p.err))) break;
       tc_fence_after();
-      const uint32_t ta = tmem + b * (uint32_t)((GATED ? 2 : 1) * p.NT) + ((uint32_t)(32 * ew) << 16);
-      const float sw = F16 && n < p.g.N ? p.g.sw[(size_t)q.e * p.g.N + n] : 0.f;
+      const uint32_t ta = tmem + b * (uint32_t)((GATED ? 2 : 1) * p.NT) + ((uint32_t)(32 * (ew & 3)) << 16);
+      const float sw = F16 && nok ? p.g.sw[(size_t)q.e * p.g.N + n] : 0.f;
       const int rows = q.r1 - q.r0;
-      for (int c0 = 0; c0 < rows; c0 += 32) {
+      for (int c0 = 32 * (ew >> 2); c0 < rows; c0 += 32 * (EW / 4)) {
         uint32_t v[32];
         tmem_ld32(ta + c0, v);
+        // lane j looks up where row j of the piece goes (-1: past the group) and its scale
+        int to = -1;
+        float sx = 0.f;
+        {
+          const int r = q.r0 + c0 + lane;
+          if (r < q.r1) {
+            to = p.g.out_index ? p.g.out_index[r] : r;
+            if (F16) {
+              int src = r;
+              if (p.g.index) {
+                const int i = p.g.index[r];
+                src = i >= 0 && i / p.g.index_div < p.g.XR ? i / p.g.index_div : -1;
+              }
+              sx = src >= 0 ? p.g.sx[src] : 0.f;
+            }
+          }
+        }
         if constexpr (GATED) {
           uint32_t u[32];
           tmem_ld32(ta + p.NT + c0, u);
@@ -548,37 +568,45 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
         } else {
           tmem_ld_wait();
         }
-        const int m = min(32, rows - c0);
-        if (n < p.g.N) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            if (j >= m) break;
-            const int r = q.r0 + c0 + j;
-            float f = __uint_as_float(v[j]);
-            if (F16) {
-              int src = r;
-              if (p.g.index) {
-                const int i = p.g.index[r];
-                src = i >= 0 && i / p.g.index_div < p.g.XR ? i / p.g.index_div : -1;
-              }
-              f = f * (src >= 0 ? p.g.sx[src] : 0.f) * sw;
-            }
-            const size_t at = (size_t)(p.g.out_index ? p.g.out_index[r] : r) * p.g.ldy + n;
-            if (p.g.y_f32)
-              reinterpret_cast<float*>(p.g.y)[at] = f;
+        if (c0 + 32 * (EW / 4) >= rows) {  // this warp has read its last columns
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (CTAS == 2)
+              arrive_remote(cluster_map(smem_u32(&acce[b]), 0));
             else
-              reinterpret_cast<__nv_bfloat16*>(p.g.y)[at] = __float2bfloat16_rn(f);
+              mbar_arrive(&acce[b]);
           }
         }
-        __syncwarp();
+        if (p.g.y_f32) {
+          float* y = reinterpret_cast<float*>(p.g.y) + n;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const int row = __shfl_sync(0xffffffffu, to, j);
+            float f = __uint_as_float(v[j]);
+            if (F16) f = f * __shfl_sync(0xffffffffu, sx, j) * sw;
+            if (nok && row >= 0) y[(uint64_t)(uint32_t)row * (uint64_t)p.g.ldy] = f;
+          }
+        } else {
+          __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(p.g.y) + n;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const int row = __shfl_sync(0xffffffffu, to, j);
+            float f = __uint_as_float(v[j]);
+            if (F16) f = f * __shfl_sync(0xffffffffu, sx, j) * sw;
+            if (nok && row >= 0) y[(uint64_t)(uint32_t)row * (uint64_t)p.g.ldy] = __float2bfloat16_rn(f);
+          }
+        }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (CTAS == 2)
-          arrive_remote(cluster_map(smem_u32(&acce[b]), 0));
-        else
-          mbar_arrive(&acce[b]);
+      if (32 * (ew >> 2) >= rows) {  // no columns for this warp
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (CTAS == 2)
+            arrive_remote(cluster_map(smem_u32(&acce[b]), 0));
+          else
+            mbar_arrive(&acce[b]);
+        }
       }
     }
   }
