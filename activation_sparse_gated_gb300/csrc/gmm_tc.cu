@@ -58,6 +58,7 @@ struct TgArgs {
   int S;       // operand stages
   int SR;      // raw stages (int8)
   int cols;    // TMEM columns allocated
+  int nacc;    // accumulators: 2, or 1 where one takes all of TMEM (the epilogue is not hidden then)
   int* err;
 };
 
@@ -438,7 +439,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
         const Tile q = tile_at<CTAS>(p, s_off, s_pre, t);
         const uint32_t idesc = (F16 ? 1u << 4 : (1u << 4) | (1u << 7) | (1u << 10)) | ((KN ? 1u : 0u) << 15) |
                                ((uint32_t)(q.n >> 3) << 17) | ((uint32_t)(128 * CTAS >> 4) << 24);
-        const uint32_t b = tl & 1, use = tl >> 1;
+        const uint32_t b = p.nacc == 2 ? tl & 1 : 0, use = p.nacc == 2 ? tl >> 1 : tl;
         if (use > 0 && !__all_sync(0xffffffffu, tg_wait<CTAS == 2>(&acce[b], (use - 1) & 1, abort_flag, p.err))) break;
         tc_fence_after();
         const uint32_t d = tmem + b * (uint32_t)((GATED ? 2 : 1) * p.NT);
@@ -530,10 +531,10 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
     uint32_t tl = 0;
     for (int t = first; t < total; t += step, ++tl) {
       const Tile q = tile_at<CTAS>(p, s_off, s_pre, t);
-      const uint32_t b = tl & 1;
+      const uint32_t b = p.nacc == 2 ? tl & 1 : 0, use = p.nacc == 2 ? tl >> 1 : tl;
       const int n = q.mt * 128 * CTAS + n0r + 32 * (ew & 3) + lane;
       const bool nok = n < p.g.N;
-      if (!__all_sync(0xffffffffu, tg_wait<false>(&accf[b], (tl >> 1) & 1, abort_flag, p.err))) break;
+      if (!__all_sync(0xffffffffu, tg_wait<false>(&accf[b], use & 1, abort_flag, p.err))) break;
       tc_fence_after();
       const uint32_t ta = tmem + b * (uint32_t)((GATED ? 2 : 1) * p.NT) + ((uint32_t)(32 * (ew & 3)) << 16);
       const float sw = F16 && nok ? p.g.sw[(size_t)q.e * p.g.N + n] : 0.f;
@@ -693,7 +694,8 @@ cudaError_t launch_gmm_tc(const GmmArgs& a, int ctas, int nt, cudaStream_t s) {
   p.S = a.i8 ? 4 : std::min(16, slots());
   p.SR = a.i8 ? std::min(12, slots() - 4) : 0;
   int cols = 32;
-  while (cols < 2 * (gated ? 2 : 1) * p.NT) cols <<= 1;
+  p.nacc = 2 * (gated ? 2 : 1) * p.NT <= 512 ? 2 : 1;
+  while (cols < p.nacc * (gated ? 2 : 1) * p.NT) cols <<= 1;
   p.cols = cols;
   p.bxr = std::min(ntl, 32);
   CUtensorMap mW, mW3, mX, mXb;
@@ -758,7 +760,7 @@ size_t gmm_workspace(int R, int XR, int N, int K, int E, int i8) {
 cudaError_t launch_gmm(const GmmArgs& a, cudaStream_t s) {
   if (const char* v = std::getenv("SFFN_GMM_TUNE")) {
     int c = 0, n = 0;
-    if (std::sscanf(v, "%d,%d", &c, &n) == 2 && c > 0) return launch_gmm_tc(a, c, a.w3 ? std::min(128, n) : n, s);
+    if (std::sscanf(v, "%d,%d", &c, &n) == 2 && c > 0) return launch_gmm_tc(a, c, n, s);
     return launch_gmm_rows(a, s);
   }
   const int busy = std::min(a.E, a.R);
@@ -776,7 +778,7 @@ cudaError_t launch_gmm(const GmmArgs& a, cudaStream_t s) {
     b.f16 = 1;
     return launch_gmm_tc(b, 2, 256, s);
   }
-  if (a.w3) return launch_gmm_tc(a, a.R >= 96 * busy ? 2 : 1, 128, s);
+  if (a.w3) return a.R >= 128 * busy ? launch_gmm_tc(a, 2, 256, s) : launch_gmm_tc(a, 1, 128, s);
   if (a.R < 16 || (a.i8 && a.R <= 4 * busy)) return launch_gmm_rows(a, s);
   if (a.R >= 96 * busy) return launch_gmm_tc(a, 2, 256, s);
   return launch_gmm_tc(a, 1, 128, s);
