@@ -47,6 +47,9 @@ constexpr uint64_t TG_TIMEOUT_NS = 250000000ull;
 constexpr size_t TG_SMEM = 227 * 1024;
 // what a kernel multiplies: bf16; bf16 gate and up together; int8 codes widened in flight; fp16 copies of codes
 enum { TG_BF16, TG_GATED, TG_I8, TG_F16 };
+// the epilogue's shared scratch of a warp: 16 rows of 32 words, 4 words apart (no bank conflicts either way)
+constexpr int TG_EPI_PITCH = 36;
+constexpr uint32_t TG_EPI_BYTES = 16 * TG_EPI_PITCH * 4;
 constexpr int TG_G = 8;           // weight tiles of one raster group
 
 struct TgArgs {
@@ -58,6 +61,7 @@ struct TgArgs {
   int S;       // operand stages
   int SR;      // raw stages (int8)
   int cols;    // TMEM columns allocated
+  int vec;     // rows of y take 16-byte stores: y, ldy and N are multiples of that
   int nacc;    // accumulators: 2, or 1 where one takes all of TMEM (the epilogue is not hidden then)
   int* err;
 };
@@ -230,6 +234,9 @@ __device__ __forceinline__ void widen4(uint32_t v, uint32_t* out) {
 __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
+__device__ __forceinline__ void sts4(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ uint4 lds16a(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
@@ -276,8 +283,9 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
   const uint32_t NTl = (uint32_t)p.NT / CTAS;
   const uint32_t bb = (NTl + 7) / 8 * 1024u;                 // B region
   const uint32_t st_bytes = (GATED ? 2 : 1) * AB + bb;       // operand stage
-  const uint32_t raw0 = (uint32_t)p.S * st_bytes;            // raw stages (int8) follow
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + raw0 + (I8 ? (uint32_t)p.SR * st_bytes : 0u));
+  const uint32_t raw0 = (uint32_t)p.S * st_bytes;
+  // then the raw stages (int8) or the epilogue's scratch, then the barriers
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + raw0 + (I8 ? (uint32_t)p.SR * st_bytes : 8u * TG_EPI_BYTES));
   uint64_t* full = bars;
   uint64_t* empty = full + p.S;
   uint64_t* rfull = empty + p.S;
@@ -579,23 +587,75 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
               mbar_arrive(&acce[b]);
           }
         }
-        if (p.g.y_f32) {
-          float* y = reinterpret_cast<float*>(p.g.y) + n;
+        if (!I8 && p.vec) {
+          // through this warp's shared scratch, so that a store carries 16 bytes of a row a lane
+          const uint32_t buf = smb + raw0 + (uint32_t)ew * TG_EPI_BYTES;
+          const int nc = q.mt * 128 * CTAS + n0r + 32 * (ew & 3);  // the warp's first column of y
+          if (p.g.y_f32) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const int row = __shfl_sync(0xffffffffu, to, j);
-            float f = __uint_as_float(v[j]);
-            if (F16) f = f * __shfl_sync(0xffffffffu, sx, j) * sw;
-            if (nok && row >= 0) y[(uint64_t)(uint32_t)row * (uint64_t)p.g.ldy] = f;
+            for (int h = 0; h < 2; ++h) {  // 16 rows x 32 columns
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                float f = __uint_as_float(v[16 * h + j]);
+                if (F16) f = f * __shfl_sync(0xffffffffu, sx, 16 * h + j) * sw;
+                sts4(buf + (uint32_t)(j * TG_EPI_PITCH + lane) * 4u, __float_as_uint(f));
+              }
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int j = 4 * i + (lane >> 3), c = 4 * (lane & 7);
+                const int row = __shfl_sync(0xffffffffu, to, 16 * h + j);
+                const uint4 d = lds16a(buf + (uint32_t)(j * TG_EPI_PITCH + c) * 4u);
+                if (row >= 0 && nc + c < p.g.N)
+                  *reinterpret_cast<uint4*>(reinterpret_cast<float*>(p.g.y) + (uint64_t)(uint32_t)row * (uint64_t)p.g.ldy +
+                                            nc + c) = d;
+              }
+              __syncwarp();
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {  // rows 2 j and 2 j + 1 in one word
+              float f0 = __uint_as_float(v[2 * j]), f1 = __uint_as_float(v[2 * j + 1]);
+              if (F16) {
+                f0 = f0 * __shfl_sync(0xffffffffu, sx, 2 * j) * sw;
+                f1 = f1 * __shfl_sync(0xffffffffu, sx, 2 * j + 1) * sw;
+              }
+              sts4(buf + (uint32_t)(j * TG_EPI_PITCH + lane) * 4u, pack_bf16x2_rn(f0, f1));
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int j = 8 * i + (lane >> 2), c = 8 * (lane & 3);
+              const uint32_t at = buf + (uint32_t)(j * TG_EPI_PITCH + c) * 4u;
+              const uint4 d = lds16a(at), e = lds16a(at + 16);
+              const int ra = __shfl_sync(0xffffffffu, to, 2 * j), rb = __shfl_sync(0xffffffffu, to, 2 * j + 1);
+              __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(p.g.y) + nc + c;
+              if (nc + c < p.g.N) {
+                if (ra >= 0)
+                  *reinterpret_cast<uint4*>(y + (uint64_t)(uint32_t)ra * (uint64_t)p.g.ldy) =
+                      make_uint4(__byte_perm(d.x, d.y, 0x5410), __byte_perm(d.z, d.w, 0x5410),
+                                 __byte_perm(e.x, e.y, 0x5410), __byte_perm(e.z, e.w, 0x5410));
+                if (rb >= 0)
+                  *reinterpret_cast<uint4*>(y + (uint64_t)(uint32_t)rb * (uint64_t)p.g.ldy) =
+                      make_uint4(__byte_perm(d.x, d.y, 0x7632), __byte_perm(d.z, d.w, 0x7632),
+                                 __byte_perm(e.x, e.y, 0x7632), __byte_perm(e.z, e.w, 0x7632));
+              }
+            }
+            __syncwarp();
           }
         } else {
-          __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(p.g.y) + n;
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             const int row = __shfl_sync(0xffffffffu, to, j);
             float f = __uint_as_float(v[j]);
             if (F16) f = f * __shfl_sync(0xffffffffu, sx, j) * sw;
-            if (nok && row >= 0) y[(uint64_t)(uint32_t)row * (uint64_t)p.g.ldy] = __float2bfloat16_rn(f);
+            if (nok && row >= 0) {
+              const uint64_t at = (uint64_t)(uint32_t)row * (uint64_t)p.g.ldy + n;
+              if (p.g.y_f32)
+                reinterpret_cast<float*>(p.g.y)[at] = f;
+              else
+                reinterpret_cast<__nv_bfloat16*>(p.g.y)[at] = __float2bfloat16_rn(f);
+            }
           }
         }
       }
@@ -684,7 +744,9 @@ cudaError_t launch_gmm_tc(const GmmArgs& a, int ctas, int nt, cudaStream_t s) {
   const bool gated = a.w3 != nullptr;
   cudaError_t e = ops_error_word(&p.err);
   if (e != cudaSuccess) return e;
-  const size_t fixed = 1024 + 8 * (2 * 16 + 2 * 16 + 4) + 8 + sizeof(int) * 2 * (size_t)(a.E + 1) + 64;
+  const size_t yb = a.y_f32 ? 4 : 2;
+  p.vec = ((uintptr_t)a.y & 15) == 0 && a.ldy * yb % 16 == 0 && a.N * yb % 16 == 0;
+  const size_t fixed = (a.i8 ? 0 : 8 * TG_EPI_BYTES) + 1024 + 8 * (2 * 16 + 2 * 16 + 4) + 8 + sizeof(int) * 2 * (size_t)(a.E + 1) + 64;
   auto stage_bytes = [&] { return (gated ? 2u : 1u) * 16384u + (uint32_t)(p.NT / ctas + 7) / 8 * 1024u; };
   auto slots = [&] { return (int)((TG_SMEM - fixed) / stage_bytes()); };
   // int8: the converters' four groups need four operand stages and three raw ones
