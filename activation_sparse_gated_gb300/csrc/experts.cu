@@ -6,91 +6,186 @@
 // unit's gate z = W1_e[i] . x_t, and only a live unit's row of W3_e is read;
 // the down product then gathers the live units' rows of W2_e^T.  Both passes
 // are reads of weight rows (bf16, fp32 sums; h stays fp32).
+#include <algorithm>
 #include <cstdlib>
 
 #include "common.cuh"
 #include "ops.h"
+#include "tc.cuh"
 
 namespace sffn {
 namespace {
 
+// Gate and up of few tokens: h[p, i] = A(W1_e[i] . x_t) (W3_e[i] . x_t) for the
+// choices p = (t, j) of expert e.  blockIdx.y is the y-th busy expert; a warp
+// takes one hidden unit and TM of the expert's rows together, so W1 is read
+// once per TM rows and W3 only where a row keeps the unit.
 constexpr int EG_WARPS = 8;
-
+template <int TM>
 __global__ void __launch_bounds__(32 * EG_WARPS) experts_gate_kernel(const ExpertsArgs a, float* __restrict__ h) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int p = blockIdx.y, t = p / a.k;
   pdl_launch_dependents();
-  pdl_wait();
   const int i = blockIdx.x * EG_WARPS + warp;
-  if (i >= a.H) return;
-  const int e = a.ids[p];
-  float out = 0.f;
-  if (e >= 0 && e < a.E) {
-    const size_t off = ((size_t)e * a.H + i) * a.D;
-    const uint4* w1 = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.W1) + off);
-    const uint4* w3 = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.W3) + off);
-    const uint4* x = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.x) + (size_t)t * a.ldx);
-    const int n = a.D / 8;
-    auto dot = [&](const uint4* w) {
-      float2 acc = make_float2(0.f, 0.f);
-#pragma unroll 4
-      for (int k = lane; k < n; k += 32) {
-        float u[8], v[8];
-        Elt<bf16_tag>::unpack(__ldg(w + k), u);
-        Elt<bf16_tag>::unpack(__ldg(x + k), v);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          ffma2(acc, make_float2(u[2 * j], u[2 * j + 1]), make_float2(v[2 * j], v[2 * j + 1]));
-      }
-      return warp_sum(acc.x + acc.y);
-    };
-    const float g = activation(a.act, dot(w1));
-    if (g != 0.f) out = g * dot(w3);
-  }
-  if (lane == 0) h[(size_t)p * a.H + i] = out;
-}
-
-// y[t, 8 columns a lane] = sum over the token's choices and live units.
-constexpr int ED_WARPS = 8;
-__global__ void __launch_bounds__(32 * ED_WARPS) experts_down_kernel(const ExpertsArgs a, const float* __restrict__ h) {
-  __shared__ float s_sum[ED_WARPS][32][9];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = blockIdx.y;
-  pdl_launch_dependents();
   pdl_wait();
-  const int n = (blockIdx.x * 32 + lane) * 8;
-  float2 acc[4] = {};
-  for (int j = 0; j < a.k; ++j) {
-    const int p = t * a.k + j, e = a.ids[p];
-    const float w = a.weights[p];
-    if (e < 0 || e >= a.E || w == 0.f) continue;
-    const uint16_t* w2 = reinterpret_cast<const uint16_t*>(a.W2t) + (size_t)e * a.H * a.D;
-    for (int i0 = warp * 32; i0 < a.H; i0 += 32 * ED_WARPS) {
-      const float hv = i0 + lane < a.H ? h[(size_t)p * a.H + i0 + lane] * w : 0.f;
-      uint32_t live = __ballot_sync(0xffffffffu, hv != 0.f);
-      while (live) {
-        const int b = __ffs(live) - 1;
-        live &= live - 1;
-        const float c = __shfl_sync(0xffffffffu, hv, b);
-        if (n < a.D) {
-          float v[8];
-          Elt<bf16_tag>::unpack(__ldg(reinterpret_cast<const uint4*>(w2 + (size_t)(i0 + b) * a.D + n)), v);
+  if (i >= a.H) return;
+  const int P = a.T * a.k;
+  int e = -1, r0 = 0, r1 = 0, left = blockIdx.y;
+  for (int e0 = 0; e0 < a.E && e < 0; e0 += 32) {
+    int b = 0, c = 0;
+    if (e0 + lane < a.E) {
+      b = min(max(a.offsets[e0 + lane], 0), P);
+      c = min(max(a.offsets[e0 + lane + 1], b), P);
+    }
+    const uint32_t busy = __ballot_sync(0xffffffffu, c > b);
+    const int n = __popc(busy);
+    if (left < n) {
+      const int at = __fns(busy, 0, left + 1);
+      e = e0 + at;
+      r0 = __shfl_sync(0xffffffffu, b, at);
+      r1 = __shfl_sync(0xffffffffu, c, at);
+    }
+    left -= n;
+  }
+  if (e < 0) return;
+  const size_t off = ((size_t)e * a.H + i) * a.D;
+  const uint4* w1 = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.W1) + off);
+  const uint4* w3 = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.W3) + off);
+  const int n = a.D / 8;
+  for (int c0 = r0; c0 < r1; c0 += TM) {
+    const uint4* x[TM];
+    int p[TM];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) ffma2(acc[q], make_float2(v[2 * q], v[2 * q + 1]), make_float2(c, c));
+    for (int t = 0; t < TM; ++t) {
+      p[t] = c0 + t < r1 ? a.rows[c0 + t] : -1;
+      if (p[t] >= P) p[t] = -1;
+      x[t] = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.x) + (size_t)(max(p[t], 0) / a.k) * a.ldx);
+    }
+    auto dot = [&](const uint4* w, float (&out)[TM]) {
+      float2 acc[TM] = {};
+#pragma unroll(TM == 1 ? 5 : 2)
+      for (int k = lane; k < n; k += 32) {
+        float u[8];
+        Elt<bf16_tag>::unpack(__ldg(w + k), u);
+#pragma unroll
+        for (int t = 0; t < TM; ++t) {
+          float v[8];
+          Elt<bf16_tag>::unpack(__ldg(x[t] + k), v);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            ffma2(acc[t], make_float2(u[2 * j], u[2 * j + 1]), make_float2(v[2 * j], v[2 * j + 1]));
         }
       }
+#pragma unroll
+      for (int t = 0; t < TM; ++t) out[t] = warp_sum(acc[t].x + acc[t].y);
+    };
+    float g[TM], u[TM];
+    dot(w1, g);
+    bool live = false;
+#pragma unroll
+    for (int t = 0; t < TM; ++t) {
+      g[t] = activation(a.act, g[t]);
+      u[t] = 0.f;
+      live = live || (p[t] >= 0 && g[t] != 0.f);
     }
+    if (live) dot(w3, u);
+#pragma unroll
+    for (int t = 0; t < TM; ++t)
+      if (lane == t && p[t] >= 0) h[(size_t)p[t] * a.H + i] = g[t] != 0.f ? g[t] * u[t] : 0.f;
   }
+}
+
+// y[t, 256 columns] = sum over the token's choices and their live units of
+// (w h) W2^T[unit].  A cluster of ED_SPLIT blocks cuts the k H units; a warp
+// lists the live ones of its share (ballots), then gathers their row segments
+// four at a time, 16 bytes a lane; sums go over the warps in shared memory and
+// over the blocks through distributed shared memory, in a fixed order.
+constexpr int ED_WARPS = 16;
+constexpr int ED_SPLIT = 8;
+constexpr int ED_LIST = 128;  // units a warp lists before it gathers
+__global__ void __launch_bounds__(32 * ED_WARPS) experts_down_kernel(const ExpertsArgs a, const float* __restrict__ h) {
+  __shared__ float s_sum[ED_WARPS][256 + 4];
+  __shared__ float s_c[ED_WARPS][ED_LIST];
+  __shared__ int s_u[ED_WARPS][ED_LIST];  // row of W2^T: expert * H + unit (in rows, checked against 31 bits)
+  __shared__ float s_part[256];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = blockIdx.y;
+  const int rank = blockIdx.x % ED_SPLIT, n = (blockIdx.x / ED_SPLIT) * 256 + lane * 8;
+  pdl_launch_dependents();
+  pdl_wait();
+  float2 acc[4] = {};
+  const uint16_t* w2 = reinterpret_cast<const uint16_t*>(a.W2t) + n;
+  const int seg = (a.H + 31) / 32, segs = seg * a.k;  // 32-unit pieces of the token's choices
+  const int s0 = (int)((long long)segs * (rank * ED_WARPS + warp) / (ED_SPLIT * ED_WARPS));
+  const int s1 = (int)((long long)segs * (rank * ED_WARPS + warp + 1) / (ED_SPLIT * ED_WARPS));
+  int count = 0;
+  auto gather = [&] {
+    __syncwarp();
+    if (n < a.D) {
+      int i = 0;
+      for (; i + 4 <= count; i += 4) {
+        uint4 v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = __ldg(reinterpret_cast<const uint4*>(w2 + (size_t)s_u[warp][i + q] * a.D));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float f[8];
+          Elt<bf16_tag>::unpack(v[q], f);
+          const float c = s_c[warp][i + q];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) ffma2(acc[j], make_float2(f[2 * j], f[2 * j + 1]), make_float2(c, c));
+        }
+      }
+      for (; i < count; ++i) {
+        float f[8];
+        Elt<bf16_tag>::unpack(__ldg(reinterpret_cast<const uint4*>(w2 + (size_t)s_u[warp][i] * a.D)), f);
+        const float c = s_c[warp][i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ffma2(acc[j], make_float2(f[2 * j], f[2 * j + 1]), make_float2(c, c));
+      }
+    }
+    __syncwarp();
+    count = 0;
+  };
+  for (int s = s0; s < s1; ++s) {
+    const int j = s / seg, u = (s - j * seg) * 32 + lane, p = t * a.k + j, e = a.ids[p];
+    const float w = e >= 0 && e < a.E ? a.weights[p] : 0.f;
+    if (w == 0.f) continue;
+    const float c = u < a.H ? h[(size_t)p * a.H + u] * w : 0.f;
+    const uint32_t live = __ballot_sync(0xffffffffu, c != 0.f);
+    if (count + __popc(live) > ED_LIST) gather();
+    if (c != 0.f) {
+      const int at = count + __popc(live & ((1u << lane) - 1));
+      s_c[warp][at] = c;
+      s_u[warp][at] = e * a.H + u;
+    }
+    count += __popc(live);
+  }
+  gather();
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    s_sum[warp][lane][2 * q] = acc[q].x;
-    s_sum[warp][lane][2 * q + 1] = acc[q].y;
+    s_sum[warp][lane * 8 + 2 * q] = acc[q].x;
+    s_sum[warp][lane * 8 + 2 * q + 1] = acc[q].y;
   }
   __syncthreads();
-  const int l = threadIdx.x >> 3, j = threadIdx.x & 7, nn = (blockIdx.x * 32 + l) * 8 + j;
-  float v = 0.f;
+  if (threadIdx.x < 256) {
+    float v = 0.f;
 #pragma unroll
-  for (int q = 0; q < ED_WARPS; ++q) v += s_sum[q][l][j];
-  if (nn < a.D) reinterpret_cast<__nv_bfloat16*>(a.y)[(size_t)t * a.D + nn] = __float2bfloat16_rn(v);
+    for (int q = 0; q < ED_WARPS; ++q) v += s_sum[q][threadIdx.x];
+    s_part[threadIdx.x] = v;
+  }
+  cluster_sync_all();
+  constexpr int SHARE = 256 / ED_SPLIT;
+  const int c = rank * SHARE + (int)threadIdx.x, col = (blockIdx.x / ED_SPLIT) * 256 + c;
+  if (threadIdx.x < SHARE && col < a.D) {
+    const uint32_t at = smem_u32(&s_part[c]);
+    float v[ED_SPLIT], sum = 0.f;
+#pragma unroll
+    for (int q = 0; q < ED_SPLIT; ++q)
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[q]) : "r"(cluster_map(at, (uint32_t)q)) : "memory");
+#pragma unroll
+    for (int q = 0; q < ED_SPLIT; ++q) sum += v[q];
+    reinterpret_cast<__nv_bfloat16*>(a.y)[(size_t)t * a.D + col] = __float2bfloat16_rn(sum);
+  }
+  cluster_sync_all();  // the partial sums stay until every block has read them
 }
 
 // y[t] = sum_j weights[t, j] o[t k + j] in the order of the places; a place
@@ -134,7 +229,10 @@ __global__ void __launch_bounds__(128) experts_gather_kernel(const ExpertsArgs a
 size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
 
 // Few choices: the gate-first passes above; more: the grouped products on the tensor cores.
-bool few(int T, int k) { return (long long)T * k <= 64; }
+bool few(int T, int k) {
+  const char* v = std::getenv("SFFN_FEW");
+  return (long long)T * k <= (v ? std::atoi(v) : 64);
+}
 
 }  // namespace
 
@@ -149,10 +247,12 @@ cudaError_t launch_experts(const ExpertsArgs& a, cudaStream_t s) {
   cudaError_t e;
   if (few(a.T, a.k)) {
     float* h = static_cast<float*>(a.workspace);
-    if ((e = ops_launch(experts_gate_kernel, dim3((a.H + EG_WARPS - 1) / EG_WARPS, a.T * a.k), 32 * EG_WARPS, 0, s, 1, a,
-                        h)) != cudaSuccess)
-      return e;
-    return ops_launch(experts_down_kernel, dim3((a.D + 255) / 256, a.T), 32 * ED_WARPS, 0, s, 1, a, (const float*)h);
+    const dim3 grid((unsigned)((a.H + EG_WARPS - 1) / EG_WARPS), (unsigned)std::min(a.E, a.T * a.k));
+    e = a.T == 1 ? ops_launch(experts_gate_kernel<1>, grid, 32 * EG_WARPS, 0, s, 1, a, h)
+                 : ops_launch(experts_gate_kernel<4>, grid, 32 * EG_WARPS, 0, s, 1, a, h);
+    if (e != cudaSuccess) return e;
+    return ops_launch(experts_down_kernel, dim3((unsigned)((a.D + 255) / 256 * ED_SPLIT), (unsigned)a.T), 32 * ED_WARPS, 0,
+                      s, ED_SPLIT, a, (const float*)h);
   }
   const int R = a.T * a.k, Hp = (int)round_up(a.H, 8);
   float* o = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + round_up(2 * (size_t)R * Hp, 256));

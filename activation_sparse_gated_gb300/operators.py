@@ -9,6 +9,7 @@ requires a gradient is refused while gradients are recorded.
 """
 from __future__ import annotations
 
+from functools import lru_cache
 from typing import NamedTuple
 
 import torch
@@ -29,7 +30,12 @@ class Routing(NamedTuple):
     rows: torch.Tensor
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # no stream object in between
+
+
 def _raw(device):
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 
@@ -39,6 +45,9 @@ def _done(rc):
 
 
 def _operand(name, t, dtypes, dim, device=None):
+    if (isinstance(t, torch.Tensor) and t.ndim == dim and t.dtype in dtypes and t.is_cuda
+            and (device is None or t.device == device) and not t.requires_grad):
+        return
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
     if t.dim() != dim:
@@ -51,6 +60,22 @@ def _operand(name, t, dtypes, dim, device=None):
         raise ValueError(f"{name} is on {t.device}, not {device}")
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name} requires a gradient: the operators have none")
+
+
+# scratch sizes depend on the arguments alone
+@lru_cache(maxsize=4096)
+def _route_bytes(T, E, k):
+    return load().sffn_route_workspace(T, E, k)
+
+
+@lru_cache(maxsize=4096)
+def _grouped_bytes(R, XR, N, K, E):
+    return load().sffn_grouped_workspace(R, XR, N, K, E, SFFN_I8)
+
+
+@lru_cache(maxsize=4096)
+def _experts_bytes(T, k, D, H):
+    return load().sffn_experts_workspace(T, k, D, H)
 
 
 def _pitch(name, t):
@@ -77,18 +102,17 @@ def route(logits, k: int, score: str = "softmax", normalize: bool = True, stream
     T, E = logits.shape
     if not 1 <= k <= E:
         raise ValueError(f"k={k} outside 1..{E}")
-    device, lib, n = logits.device, load(), T * k
-    ld = _pitch("logits", logits)
-    buf = torch.empty(3 * n + E + 1, dtype=torch.int32, device=device)
-    weights, ids, rows, offsets = buf.split((n, n, n, E + 1))
-    weights, ids = weights.view(torch.float32).view(T, k), ids.view(T, k)
-    nb = lib.sffn_route_workspace(T, E, k)
-    ws = torch.empty(nb, dtype=torch.uint8, device=device) if nb else None
+    device = logits.device
+    weights = torch.empty((T, k), dtype=torch.float32, device=device)
+    ids = torch.empty((T, k), dtype=torch.int32, device=device)
+    offsets = torch.empty(E + 1, dtype=torch.int32, device=device)
+    rows = torch.empty(T * k, dtype=torch.int32, device=device)
+    ws, nb = _scratch(_route_bytes(T, E, k), device)
     flags = (SFFN_ROUTE_SIGMOID if score == "sigmoid" else 0) | (SFFN_ROUTE_NORMALIZE if normalize else 0)
-    at = buf.data_ptr()
-    _done(lib.sffn_route(logits.data_ptr(), ld, at, at + 4 * n, at + 12 * n, at + 8 * n, T, E, k,
-                         SFFN_F32 if logits.dtype == torch.float32 else SFFN_BF16, flags,
-                         ws.data_ptr() if nb else None, nb, _raw(device)))
+    _done(load().sffn_route(logits.data_ptr(), _pitch("logits", logits), weights.data_ptr(), ids.data_ptr(),
+                            offsets.data_ptr(), rows.data_ptr(), T, E, k,
+                            SFFN_F32 if logits.dtype == torch.float32 else SFFN_BF16, flags, nb and ws.data_ptr(), nb,
+                            _raw(device)))
     return Routing(weights, ids, offsets, rows)
 
 
@@ -140,10 +164,9 @@ def matmul_int8(xq, sx, wq, sw, dtype="bf16", out=None, stream=None):
     for name, t in (("wq", wq), ("sx", sx), ("sw", sw)):
         _dense(name, t)
     y, code, ldy = _result(out, dtype, (T, N), device)
-    lib = load()
-    ws, nb = _scratch(lib.sffn_grouped_workspace(T, T, N, K, 1, SFFN_I8), device)
-    _done(lib.sffn_matmul_int8(xq.data_ptr(), _pitch("xq", xq), sx.data_ptr(), wq.data_ptr(), sw.data_ptr(),
-                               y.data_ptr(), ldy, T, N, K, code, nb and ws.data_ptr(), nb, _raw(device)))
+    ws, nb = _scratch(_grouped_bytes(T, T, N, K, 1), device)
+    _done(load().sffn_matmul_int8(xq.data_ptr(), _pitch("xq", xq), sx.data_ptr(), wq.data_ptr(), sw.data_ptr(),
+                                  y.data_ptr(), ldy, T, N, K, code, nb and ws.data_ptr(), nb, _raw(device)))
     return y
 
 
@@ -184,9 +207,8 @@ def grouped_matmul(x, w, offsets, sx=None, sw=None, index=None, index_div: int =
     elif sx is not None or sw is not None:
         raise ValueError("scales go with int8 operands")
     y, code, ldy = _result(out, dtype, (R, N), device)
-    lib = load()
-    ws, nb = _scratch(lib.sffn_grouped_workspace(R, XR, N, K, E, SFFN_I8) if i8 else 0, device)
-    _done(lib.sffn_grouped_matmul(
+    ws, nb = _scratch(_grouped_bytes(R, XR, N, K, E) if i8 else 0, device)
+    _done(load().sffn_grouped_matmul(
         x.data_ptr(), _pitch("x", x), sx.data_ptr() if i8 else None, w.data_ptr(), sw.data_ptr() if i8 else None,
         offsets.data_ptr(), index.data_ptr() if index is not None else None, index_div, y.data_ptr(), ldy, R, XR, N, K,
         E, SFFN_I8 if i8 else SFFN_BF16, code, SFFN_W_KN if transposed else 0,
@@ -226,12 +248,10 @@ def experts_forward(x, routing: Routing, W1, W3, W2t, act: str = "relu", out=Non
         if tuple(out.shape) != (T, D):
             raise ValueError(f"out has shape {tuple(out.shape)}, not {(T, D)}")
         _dense("out", out)
-    lib = load()
-    nb = lib.sffn_experts_workspace(T, k, D, H)
-    ws = torch.empty(nb, dtype=torch.uint8, device=device)
-    _done(lib.sffn_experts_forward(
+    ws, nb = _scratch(_experts_bytes(T, k, D, H), device)
+    _done(load().sffn_experts_forward(
         x.data_ptr(), _pitch("x", x), weights.data_ptr(), ids.data_ptr(), offsets.data_ptr(), rows.data_ptr(),
-        W1.data_ptr(), W3.data_ptr(), W2t.data_ptr(), out.data_ptr(), T, E, k, D, H, _ACT[act], ws.data_ptr(), nb,
+        W1.data_ptr(), W3.data_ptr(), W2t.data_ptr(), out.data_ptr(), T, E, k, D, H, _ACT[act], nb and ws.data_ptr(), nb,
         _raw(device)))
     return out
 

@@ -392,7 +392,7 @@ def check_experts(x, routing, W1, W3, W2t, act, y):
 
 @pytest.mark.parametrize("T,E,k,D,H", [(1, 1, 1, 8, 1), (1, 8, 2, 128, 100), (1, 64, 8, 2560, 1024), (2, 4, 3, 264, 65),
                                        (5, 16, 4, 384, 130), (33, 8, 2, 520, 200), (64, 64, 8, 256, 96),
-                                       (200, 6, 2, 384, 257), (513, 5, 3, 256, 128), (300, 128, 4, 136, 72)])
+                                       (20, 2, 2, 136, 90), (2, 8, 8, 64, 2600), (200, 6, 2, 384, 257), (513, 5, 3, 256, 128), (300, 128, 4, 136, 72)])
 @pytest.mark.parametrize("act", ["relu", "rsp", "silu"])
 def test_experts_forward(T, E, k, D, H, act):
     g = gen(T + D + H)
