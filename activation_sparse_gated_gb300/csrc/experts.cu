@@ -17,69 +17,101 @@ namespace sffn {
 namespace {
 
 // Gate and up of few tokens: h[p, i] = A(W1_e[i] . x_t) (W3_e[i] . x_t) for the
-// choices p = (t, j) of expert e.  blockIdx.y is the y-th busy expert; a warp
-// takes one hidden unit and TM of the expert's rows together, so W1 is read
-// once per TM rows and W3 only where a row keeps the unit.
+// choices p = (t, j) of expert e.  blockIdx.y is a choice (one token: its
+// choices are its experts) or the y-th busy expert; a warp takes one hidden
+// unit and TM of the expert's rows together, so W1 is read once per TM rows and
+// W3 only where a row keeps the unit.  EG_U pieces of a weight row are
+// requested before the first is used; the rows of x sit in shared memory
+// (STAGED) unless they are too long for it.
 constexpr int EG_WARPS = 8;
-template <int TM>
+constexpr int EG_U = 5;
+constexpr size_t EG_STAGE = 40 * 1024;  // most bytes of staged x a block
+
+template <int TM, bool STAGED>
 __global__ void __launch_bounds__(32 * EG_WARPS) experts_gate_kernel(const ExpertsArgs a, float* __restrict__ h) {
+  extern __shared__ uint4 s_x[];  // [TM][D / 8]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_launch_dependents();
   const int i = blockIdx.x * EG_WARPS + warp;
+  const int P = a.T * a.k, n = a.D / 8;
+  pdl_launch_dependents();
   pdl_wait();
-  if (i >= a.H) return;
-  const int P = a.T * a.k;
-  int e = -1, r0 = 0, r1 = 0, left = blockIdx.y;
-  for (int e0 = 0; e0 < a.E && e < 0; e0 += 32) {
-    int b = 0, c = 0;
-    if (e0 + lane < a.E) {
-      b = min(max(a.offsets[e0 + lane], 0), P);
-      c = min(max(a.offsets[e0 + lane + 1], b), P);
+  int e = -1, r0 = 0, r1 = 0;
+  if (TM == 1) {
+    e = a.ids[blockIdx.y];
+    r1 = 1;
+    if (e >= a.E) e = -1;
+  } else {
+    int left = blockIdx.y;
+    for (int e0 = 0; e0 < a.E && e < 0; e0 += 32) {
+      int b = 0, c = 0;
+      if (e0 + lane < a.E) {
+        b = min(max(a.offsets[e0 + lane], 0), P);
+        c = min(max(a.offsets[e0 + lane + 1], b), P);
+      }
+      const uint32_t busy = __ballot_sync(0xffffffffu, c > b);
+      const int m = __popc(busy);
+      if (left < m) {
+        const int at = __fns(busy, 0, left + 1);
+        e = e0 + at;
+        r0 = __shfl_sync(0xffffffffu, b, at);
+        r1 = __shfl_sync(0xffffffffu, c, at);
+      }
+      left -= m;
     }
-    const uint32_t busy = __ballot_sync(0xffffffffu, c > b);
-    const int n = __popc(busy);
-    if (left < n) {
-      const int at = __fns(busy, 0, left + 1);
-      e = e0 + at;
-      r0 = __shfl_sync(0xffffffffu, b, at);
-      r1 = __shfl_sync(0xffffffffu, c, at);
-    }
-    left -= n;
   }
-  if (e < 0) return;
-  const size_t off = ((size_t)e * a.H + i) * a.D;
+  if (e < 0) return;  // the whole block
+  const size_t off = ((size_t)e * a.H + min(i, a.H - 1)) * a.D;
   const uint4* w1 = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.W1) + off);
   const uint4* w3 = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.W3) + off);
-  const int n = a.D / 8;
   for (int c0 = r0; c0 < r1; c0 += TM) {
-    const uint4* x[TM];
     int p[TM];
+    const uint4* x[TM];
 #pragma unroll
     for (int t = 0; t < TM; ++t) {
-      p[t] = c0 + t < r1 ? a.rows[c0 + t] : -1;
+      p[t] = TM == 1 ? (int)blockIdx.y : c0 + t < r1 ? a.rows[c0 + t] : -1;
       if (p[t] >= P) p[t] = -1;
       x[t] = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.x) + (size_t)(max(p[t], 0) / a.k) * a.ldx);
     }
-    auto dot = [&](const uint4* w, float (&out)[TM]) {
+    uint4 w[EG_U];
+#pragma unroll
+    for (int q = 0; q < EG_U; ++q)  // the first pieces of W1 travel while x is staged
+      w[q] = lane + 32 * q < n ? __ldg(w1 + lane + 32 * q) : make_uint4(0, 0, 0, 0);
+    if (STAGED) {
+      __syncthreads();
+#pragma unroll
+      for (int t = 0; t < TM; ++t)
+        for (int k = threadIdx.x; k < n; k += 32 * EG_WARPS) s_x[t * n + k] = __ldg(x[t] + k);
+      __syncthreads();
+    }
+    auto dot = [&](const uint4* wp, bool loaded, float (&out)[TM]) {
       float2 acc[TM] = {};
-#pragma unroll(TM == 1 ? 5 : 2)
-      for (int k = lane; k < n; k += 32) {
-        float u[8];
-        Elt<bf16_tag>::unpack(__ldg(w + k), u);
+      for (int k0 = lane; k0 < n; k0 += 32 * EG_U) {
+        if (!loaded || k0 != lane) {
 #pragma unroll
-        for (int t = 0; t < TM; ++t) {
-          float v[8];
-          Elt<bf16_tag>::unpack(__ldg(x[t] + k), v);
+          for (int q = 0; q < EG_U; ++q) w[q] = k0 + 32 * q < n ? __ldg(wp + k0 + 32 * q) : make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            ffma2(acc[t], make_float2(u[2 * j], u[2 * j + 1]), make_float2(v[2 * j], v[2 * j + 1]));
+        for (int q = 0; q < EG_U; ++q) {
+          const int k = k0 + 32 * q;
+          if (k < n) {
+            float u[8];
+            Elt<bf16_tag>::unpack(w[q], u);
+#pragma unroll
+            for (int t = 0; t < TM; ++t) {
+              float v[8];
+              Elt<bf16_tag>::unpack(STAGED ? lds16(s_x + t * n + k) : __ldg(x[t] + k), v);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                ffma2(acc[t], make_float2(u[2 * j], u[2 * j + 1]), make_float2(v[2 * j], v[2 * j + 1]));
+            }
+          }
         }
       }
 #pragma unroll
       for (int t = 0; t < TM; ++t) out[t] = warp_sum(acc[t].x + acc[t].y);
     };
     float g[TM], u[TM];
-    dot(w1, g);
+    dot(w1, true, g);
     bool live = false;
 #pragma unroll
     for (int t = 0; t < TM; ++t) {
@@ -87,10 +119,10 @@ __global__ void __launch_bounds__(32 * EG_WARPS) experts_gate_kernel(const Exper
       u[t] = 0.f;
       live = live || (p[t] >= 0 && g[t] != 0.f);
     }
-    if (live) dot(w3, u);
+    if (live && i < a.H) dot(w3, false, u);
 #pragma unroll
     for (int t = 0; t < TM; ++t)
-      if (lane == t && p[t] >= 0) h[(size_t)p[t] * a.H + i] = g[t] != 0.f ? g[t] * u[t] : 0.f;
+      if (lane == t && p[t] >= 0 && i < a.H) h[(size_t)p[t] * a.H + i] = g[t] != 0.f ? g[t] * u[t] : 0.f;
   }
 }
 
@@ -247,9 +279,14 @@ cudaError_t launch_experts(const ExpertsArgs& a, cudaStream_t s) {
   cudaError_t e;
   if (few(a.T, a.k)) {
     float* h = static_cast<float*>(a.workspace);
-    const dim3 grid((unsigned)((a.H + EG_WARPS - 1) / EG_WARPS), (unsigned)std::min(a.E, a.T * a.k));
-    e = a.T == 1 ? ops_launch(experts_gate_kernel<1>, grid, 32 * EG_WARPS, 0, s, 1, a, h)
-                 : ops_launch(experts_gate_kernel<4>, grid, 32 * EG_WARPS, 0, s, 1, a, h);
+    const dim3 grid((unsigned)((a.H + EG_WARPS - 1) / EG_WARPS), (unsigned)(a.T == 1 ? a.k : std::min(a.E, a.T * a.k)));
+    const size_t row = 2 * (size_t)a.D;
+    if (a.T == 1)
+      e = row <= EG_STAGE ? ops_launch(experts_gate_kernel<1, true>, grid, 32 * EG_WARPS, row, s, 1, a, h)
+                          : ops_launch(experts_gate_kernel<1, false>, grid, 32 * EG_WARPS, 0, s, 1, a, h);
+    else
+      e = 4 * row <= EG_STAGE ? ops_launch(experts_gate_kernel<4, true>, grid, 32 * EG_WARPS, 4 * row, s, 1, a, h)
+                              : ops_launch(experts_gate_kernel<4, false>, grid, 32 * EG_WARPS, 0, s, 1, a, h);
     if (e != cudaSuccess) return e;
     return ops_launch(experts_down_kernel, dim3((unsigned)((a.D + 255) / 256 * ED_SPLIT), (unsigned)a.T), 32 * ED_WARPS, 0,
                       s, ED_SPLIT, a, (const float*)h);

@@ -6,8 +6,11 @@
 //
 // Bound by memory: 2 bytes read and 1 written per value.  One block per token
 // keeps the token in registers between the maximum and the codes, so it is
-// read once; the quotient is the correctly rounded division, which a product
-// with 1 / s is not.
+// read once.  The code of a value is decided by the correctly rounded quotient,
+// which costs more than the memory; a product with 1 / s is off by at most a
+// few units in the last place, below 1e-4 for quotients up to 127, so it gives
+// the same code unless it lies that near a half, and only then is the quotient
+// taken.
 #include "common.cuh"
 #include "ops.h"
 
@@ -17,6 +20,16 @@ namespace {
 __device__ __forceinline__ int code_of(float v, float s) {
   const int q = __float2int_rn(__fdiv_rn(v, s));
   return q > 127 ? 127 : q < -127 ? -127 : q;
+}
+
+// The codes of two packed bf16 values by the product; *far is raised to the
+// largest distance of a product from its code.
+__device__ __forceinline__ uint32_t fast_codes(uint32_t w, float inv, float* far) {
+  constexpr float ROUND = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, to even
+  const float a = __uint_as_float(w << 16) * inv, b = __uint_as_float(w & 0xffff0000u) * inv;
+  const float ra = a + ROUND, rb = b + ROUND;
+  *far = fmaxf(*far, fmaxf(fabsf(a - (ra - ROUND)), fabsf(b - (rb - ROUND))));
+  return __byte_perm(__float_as_uint(ra), __float_as_uint(rb), 0x0040) & 0xffffu;
 }
 
 // NT threads, V 16-byte pieces a thread in registers, or (V = 0) one value at a
@@ -59,6 +72,8 @@ __global__ void __launch_bounds__(NT) quantize_tokens_kernel(const uint16_t* __r
   const float s = bad ? __uint_as_float(0x7fc00000u) : __fdiv_rn(__uint_as_float(m), 127.f);
   if (tid == 0) sc[t] = s;
   const bool zero = bad || s == 0.f;
+  const float inv = __fdiv_rn(1.f, s);
+  const bool tiny = !zero && !(s > 1e-30f && s < 1e30f);
   if constexpr (V > 0) {
     const int n = K / 8;
 #pragma unroll
@@ -67,7 +82,13 @@ __global__ void __launch_bounds__(NT) quantize_tokens_kernel(const uint16_t* __r
       if (at >= n) continue;
       const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
       uint32_t o[2] = {0, 0};
+      float far = 0.f;
       if (!zero) {
+        o[0] = fast_codes(w[0], inv, &far) | (fast_codes(w[1], inv, &far) << 16);
+        o[1] = fast_codes(w[2], inv, &far) | (fast_codes(w[3], inv, &far) << 16);
+      }
+      if (!(far < 0.4999f) || tiny) {  // near a half (or 1 / s is no number): by the quotients
+        o[0] = o[1] = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t lo = (uint32_t)code_of(__uint_as_float(w[j] << 16), s) & 0xffu;
@@ -92,13 +113,13 @@ cudaError_t go(const void* x, long long ld, int8_t* q, float* sc, int T, int K, 
 
 cudaError_t launch_quantize_tokens(const void* x, long long ld, int8_t* q, float* sc, int T, int K, cudaStream_t s) {
   const bool vec = K % 8 == 0 && ld % 8 == 0 && ((uintptr_t)x & 15) == 0 && ((uintptr_t)q & 7) == 0;
-  if (!vec || K > 256 * 8 * 8) return go<256, 0>(x, ld, q, sc, T, K, s);
+  if (!vec || K > 512 * 4 * 8) return go<256, 0>(x, ld, q, sc, T, K, s);
   const int n = K / 8;
   if (n <= 128) return go<128, 1>(x, ld, q, sc, T, K, s);
   if (n <= 256) return go<256, 1>(x, ld, q, sc, T, K, s);
   if (n <= 512) return go<256, 2>(x, ld, q, sc, T, K, s);
   if (n <= 1024) return go<256, 4>(x, ld, q, sc, T, K, s);
-  return go<256, 8>(x, ld, q, sc, T, K, s);
+  return go<512, 4>(x, ld, q, sc, T, K, s);
 }
 
 }  // namespace sffn

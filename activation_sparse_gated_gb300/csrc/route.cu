@@ -11,20 +11,22 @@
 // One warp takes a token: the logits sit in registers (E / 32 a lane) as
 // order-preserving integer keys, and a choice is one warp-wide maximum of the
 // keys and one minimum of the indexes that hold it (redux, no shuffle trees).
-// The sort is exact integer work, so its result does not depend on timing:
-// blocks own consecutive tokens, count their choices per expert, and a second
-// kernel adds the counts of the blocks before it.  Up to ROUTE_ONE choices one
-// block does both.
+// The sort is exact integer work, so its result does not depend on timing: a
+// cluster of blocks owns a chunk of consecutive tokens (16 a block, one a warp:
+// the choice is a chain of dependent steps, so it wants warps) and counts its
+// choices per expert, and a second kernel adds the counts of the chunks before
+// its own.  Up to ROUTE_ONE choices one block does both.
 #include "common.cuh"
 #include "ops.h"
+#include "tc.cuh"
 
 namespace sffn {
 namespace {
 
 constexpr int ROUTE_WARPS = 16;
 constexpr int ROUTE_THREADS = 32 * ROUTE_WARPS;
-constexpr int ROUTE_ONE = 2048;   // choices that one block sorts by itself
-constexpr int ROUTE_BLOCKS = 128; // most blocks of the two-kernel form
+constexpr int ROUTE_ONE = 512;    // choices that one block sorts by itself
+constexpr int ROUTE_CHUNKS = 128; // most chunks of the two-kernel form
 
 // Larger float <-> larger key; NaN and -inf share the key 0 (closed).
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -194,33 +196,52 @@ __global__ void __launch_bounds__(ROUTE_THREADS) route_one_kernel(const RouteArg
 }
 
 template <int L>
-__global__ void __launch_bounds__(ROUTE_THREADS) route_choose_kernel(const RouteArgs a, int per) {
+__global__ void __launch_bounds__(ROUTE_THREADS) route_choose_kernel(const RouteArgs a, int per, int split) {
   extern __shared__ int sm[];
   pdl_launch_dependents();
   pdl_wait();
-  const int t0 = min(a.T, (int)blockIdx.x * per), t1 = min(a.T, t0 + per);
+  const int chunk = blockIdx.x / split, rank = blockIdx.x % split, sub = (per + split - 1) / split;
+  const int c1 = min(a.T, chunk * per + per), t0 = min(c1, chunk * per + rank * sub), t1 = min(c1, t0 + sub);
   choose_block<L>(a, t0, t1, sm);
-  for (int e = threadIdx.x; e < a.E; e += ROUTE_THREADS) a.hist[(size_t)blockIdx.x * a.E + e] = sm[e];
+  if (split > 1) cluster_sync_all();
+  for (int e = rank * ROUTE_THREADS + threadIdx.x; e < a.E; e += split * ROUTE_THREADS) {
+    int v = sm[e];
+    if (split > 1) {
+      v = 0;
+      const uint32_t at = smem_u32(sm + e);
+      for (int q = 0; q < split; ++q) {
+        int w;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(w) : "r"(cluster_map(at, (uint32_t)q)) : "memory");
+        v += w;
+      }
+    }
+    a.hist[(size_t)chunk * a.E + e] = v;
+  }
+  if (split > 1) cluster_sync_all();  // the counts stay until every block has read them
 }
 
 __global__ void __launch_bounds__(ROUTE_THREADS) route_group_kernel(const RouteArgs a, int per, int nb, int warps) {
   extern __shared__ int sm[];
   int* s_base = sm;
   int* s_w = s_base + a.E + 1;
-  int* s_mine = s_w + ROUTE_WARPS;  // [E] choices of the blocks before this one
+  int* s_mine = s_w + ROUTE_WARPS;  // [E] choices of the chunks before this one
   int* s_cnt = s_mine + a.E;
+  for (int e = threadIdx.x; e < a.E; e += ROUTE_THREADS) s_mine[e] = s_base[e] = 0;
   pdl_launch_dependents();
   pdl_wait();
-  for (int e = threadIdx.x; e < a.E; e += ROUTE_THREADS) {
+  __syncthreads();
+  // several threads an expert where there are few: each sums every `stride`-th chunk
+  const int cols = min((a.E + 31) / 32 * 32, ROUTE_THREADS), stride = ROUTE_THREADS / cols, first = threadIdx.x / cols;
+  for (int e = threadIdx.x % cols; e < a.E && first < stride; e += cols) {
     int before = 0, total = 0;
-#pragma unroll 8
-    for (int b = 0; b < nb; ++b) {
+#pragma unroll 16
+    for (int b = first; b < nb; b += stride) {
       const int v = a.hist[(size_t)b * a.E + e];
       if (b < (int)blockIdx.x) before += v;
       total += v;
     }
-    s_mine[e] = before;
-    s_base[e] = total;
+    atomicAdd(&s_mine[e], before);
+    atomicAdd(&s_base[e], total);
   }
   __syncthreads();
   exclusive_scan(s_base, a.E, s_w);
@@ -242,8 +263,8 @@ int scatter_warps(int E, int fixed_ints) {
   return w < 1 ? 1 : w > ROUTE_WARPS ? ROUTE_WARPS : w;
 }
 
-int route_blocks(int T, int* per) {
-  *per = (T + ROUTE_BLOCKS - 1) / ROUTE_BLOCKS;
+int route_chunks(int T, int* per) {
+  *per = (T + ROUTE_CHUNKS - 1) / ROUTE_CHUNKS;
   if (*per < ROUTE_WARPS) *per = ROUTE_WARPS;
   return (T + *per - 1) / *per;
 }
@@ -255,8 +276,10 @@ cudaError_t route_l(const RouteArgs& a, cudaStream_t s) {
     return ops_launch(route_one_kernel<L>, dim3(1), ROUTE_THREADS, sizeof(int) * (fixed + warps * a.E), s, 1, a, warps);
   }
   int per;
-  const int nb = route_blocks(a.T, &per);
-  cudaError_t e = ops_launch(route_choose_kernel<L>, dim3(nb), ROUTE_THREADS, sizeof(int) * a.E, s, 1, a, per);
+  const int nb = route_chunks(a.T, &per);
+  const int split = per > 4 * ROUTE_WARPS ? 8 : per > 2 * ROUTE_WARPS ? 4 : per > ROUTE_WARPS ? 2 : 1;
+  cudaError_t e = ops_launch(route_choose_kernel<L>, dim3(nb * split), ROUTE_THREADS, sizeof(int) * a.E, s, split, a, per,
+                             split);
   if (e != cudaSuccess) return e;
   const int fixed = 2 * a.E + 1 + ROUTE_WARPS, warps = scatter_warps(a.E, fixed);
   return ops_launch(route_group_kernel, dim3(nb), ROUTE_THREADS, sizeof(int) * (fixed + warps * a.E), s, 1, a, per, nb,
@@ -268,7 +291,7 @@ cudaError_t route_l(const RouteArgs& a, cudaStream_t s) {
 size_t route_workspace(int T, int E, int k) {
   if ((long long)T * k <= ROUTE_ONE) return 0;
   int per;
-  return sizeof(int) * (size_t)route_blocks(T, &per) * E;
+  return sizeof(int) * (size_t)route_chunks(T, &per) * E;
 }
 
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t s) {

@@ -10,7 +10,6 @@ requires a gradient is refused while gradients are recorded.
 from __future__ import annotations
 
 from functools import lru_cache
-from typing import NamedTuple
 
 import torch
 
@@ -22,12 +21,53 @@ _OUT = {"bf16": (torch.bfloat16, SFFN_BF16), "f32": (torch.float32, SFFN_F32),
         torch.bfloat16: (torch.bfloat16, SFFN_BF16), torch.float32: (torch.float32, SFFN_F32)}
 
 
-class Routing(NamedTuple):
-    """``route``'s result: weights [T, k] fp32, ids [T, k], offsets [E + 1] and rows [T * k] (int32)."""
-    weights: torch.Tensor
-    ids: torch.Tensor
-    offsets: torch.Tensor
-    rows: torch.Tensor
+class Routing:
+    """``route``'s result: weights [T, k] fp32, ids [T, k], offsets [E + 1] and rows [T * k] (int32), in one buffer
+    whose views are made when they are asked for; iterates in that order.  ``Routing.of`` takes four tensors of a
+    caller's own."""
+
+    __slots__ = ("T", "E", "k", "buf", "_views")
+
+    def __init__(self, buf, T, E, k, views=None):
+        self.buf, self.T, self.E, self.k, self._views = buf, T, E, k, views
+
+    @classmethod
+    def of(cls, weights, ids, offsets, rows):
+        _operand("weights", weights, (torch.float32,), 2)
+        device = weights.device
+        for name, t, dim in (("ids", ids, 2), ("offsets", offsets, 1), ("rows", rows, 1)):
+            _operand(name, t, (torch.int32,), dim, device)
+        for name, t in (("weights", weights), ("ids", ids), ("offsets", offsets), ("rows", rows)):
+            _dense(name, t)
+        T, k = weights.shape
+        if ids.shape != weights.shape or rows.shape[0] != T * k:
+            raise ValueError("the routing's tensors are of other tokens or choices")
+        return cls(None, T, offsets.shape[0] - 1, k, (weights, ids, offsets, rows))
+
+    def _all(self):
+        if self._views is None:
+            n, T, k, b = self.T * self.k, self.T, self.k, self.buf
+            self._views = (b[:n].view(torch.float32).view(T, k), b.as_strided((T, k), (k, 1), n),
+                           b.as_strided((self.E + 1,), (1,), 3 * n), b.as_strided((n,), (1,), 2 * n))
+        return self._views
+
+    weights = property(lambda self: self._all()[0])
+    ids = property(lambda self: self._all()[1])
+    offsets = property(lambda self: self._all()[2])
+    rows = property(lambda self: self._all()[3])
+
+    def __iter__(self):
+        return iter(self._all())
+
+    def _pointers(self):
+        if self.buf is not None:
+            at, n = self.buf.data_ptr(), 4 * self.T * self.k
+            return at, at + n, at + 3 * n, at + 2 * n
+        return tuple(t.data_ptr() for t in self._views)
+
+    @property
+    def device(self):
+        return (self._views[0] if self.buf is None else self.buf).device
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # no stream object in between
@@ -103,17 +143,15 @@ def route(logits, k: int, score: str = "softmax", normalize: bool = True, stream
     if not 1 <= k <= E:
         raise ValueError(f"k={k} outside 1..{E}")
     device = logits.device
-    weights = torch.empty((T, k), dtype=torch.float32, device=device)
-    ids = torch.empty((T, k), dtype=torch.int32, device=device)
-    offsets = torch.empty(E + 1, dtype=torch.int32, device=device)
-    rows = torch.empty(T * k, dtype=torch.int32, device=device)
+    n = T * k
+    buf = torch.empty(3 * n + E + 1, dtype=torch.int32, device=device)
     ws, nb = _scratch(_route_bytes(T, E, k), device)
     flags = (SFFN_ROUTE_SIGMOID if score == "sigmoid" else 0) | (SFFN_ROUTE_NORMALIZE if normalize else 0)
-    _done(load().sffn_route(logits.data_ptr(), _pitch("logits", logits), weights.data_ptr(), ids.data_ptr(),
-                            offsets.data_ptr(), rows.data_ptr(), T, E, k,
+    at = buf.data_ptr()
+    _done(load().sffn_route(logits.data_ptr(), _pitch("logits", logits), at, at + 4 * n, at + 12 * n, at + 8 * n, T, E, k,
                             SFFN_F32 if logits.dtype == torch.float32 else SFFN_BF16, flags, nb and ws.data_ptr(), nb,
                             _raw(device)))
-    return Routing(weights, ids, offsets, rows)
+    return Routing(buf, T, E, k)
 
 
 def quantize_tokens(x, stream=None):
@@ -216,9 +254,9 @@ def grouped_matmul(x, w, offsets, sx=None, sw=None, index=None, index_div: int =
     return y
 
 
-def experts_forward(x, routing: Routing, W1, W3, W2t, act: str = "relu", out=None, stream=None):
-    """y[t] = sum_j weights[t, j] W2_e (A(W1_e x_t) * (W3_e x_t)) over the routing's choices e = ids[t, j]; x [T, D],
-    W1, W3 and W2t (W2 transposed) [E, H, D], all bf16."""
+def experts_forward(x, routing, W1, W3, W2t, act: str = "relu", out=None, stream=None):
+    """y[t] = sum_j weights[t, j] W2_e (A(W1_e x_t) * (W3_e x_t)) over the choices e = ids[t, j] of ``route``'s result (or of
+    its four tensors); x [T, D], W1, W3 and W2t (W2 transposed) [E, H, D], all bf16."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return experts_forward(x, routing, W1, W3, W2t, act, out)
@@ -233,14 +271,13 @@ def experts_forward(x, routing: Routing, W1, W3, W2t, act: str = "relu", out=Non
             raise ValueError(f"{name} {tuple(t.shape)} does not go with x {tuple(x.shape)} and W1 {tuple(W1.shape)}")
         _dense(name, t)
     E, H = W1.shape[0], W1.shape[1]
-    weights, ids, offsets, rows = routing
-    for name, t, dtype, dim in (("weights", weights, torch.float32, 2), ("ids", ids, torch.int32, 2),
-                                ("offsets", offsets, torch.int32, 1), ("rows", rows, torch.int32, 1)):
-        _operand(name, t, (dtype,), dim, device)
-        _dense(name, t)
-    k = weights.shape[1]
-    if weights.shape[0] != T or ids.shape != weights.shape or rows.shape[0] != T * k or offsets.shape[0] != E + 1:
-        raise ValueError("the routing is of other tokens or experts")
+    if not isinstance(routing, Routing):
+        routing = Routing.of(*routing)
+    k = routing.k
+    if routing.T != T or routing.E != E:
+        raise ValueError(f"the routing is of {routing.T} tokens and {routing.E} experts, not {T} and {E}")
+    if routing.device != device:
+        raise ValueError(f"the routing is on {routing.device}, not {device}")
     if out is None:
         out = torch.empty((T, D), dtype=torch.bfloat16, device=device)
     else:
@@ -250,9 +287,8 @@ def experts_forward(x, routing: Routing, W1, W3, W2t, act: str = "relu", out=Non
         _dense("out", out)
     ws, nb = _scratch(_experts_bytes(T, k, D, H), device)
     _done(load().sffn_experts_forward(
-        x.data_ptr(), _pitch("x", x), weights.data_ptr(), ids.data_ptr(), offsets.data_ptr(), rows.data_ptr(),
-        W1.data_ptr(), W3.data_ptr(), W2t.data_ptr(), out.data_ptr(), T, E, k, D, H, _ACT[act], nb and ws.data_ptr(), nb,
-        _raw(device)))
+        x.data_ptr(), _pitch("x", x), *routing._pointers(), W1.data_ptr(), W3.data_ptr(), W2t.data_ptr(),
+        out.data_ptr(), T, E, k, D, H, _ACT[act], nb and ws.data_ptr(), nb, _raw(device)))
     return out
 
 

@@ -390,7 +390,7 @@ def check_experts(x, routing, W1, W3, W2t, act, y):
     close(y, ref, bound)
 
 
-@pytest.mark.parametrize("T,E,k,D,H", [(1, 1, 1, 8, 1), (1, 8, 2, 128, 100), (1, 64, 8, 2560, 1024), (2, 4, 3, 264, 65),
+@pytest.mark.parametrize("T,E,k,D,H", [(1, 1, 1, 8, 1), (1, 8, 2, 128, 100), (1, 64, 8, 2560, 1024), (2, 4, 3, 264, 65), (1, 4, 2, 22000, 20), (3, 4, 2, 6000, 24),
                                        (5, 16, 4, 384, 130), (33, 8, 2, 520, 200), (64, 64, 8, 256, 96),
                                        (20, 2, 2, 136, 90), (2, 8, 8, 64, 2600), (200, 6, 2, 384, 257), (513, 5, 3, 256, 128), (300, 128, 4, 136, 72)])
 @pytest.mark.parametrize("act", ["relu", "rsp", "silu"])
@@ -423,6 +423,7 @@ def test_experts_closed_tokens_strides_and_streams(T):
     y = sffn.experts_forward(x, routing, W1, W3, W2t)
     assert (y[1] == 0).all()
     check_experts(x.contiguous(), routing, W1, W3, W2t, "relu", y)
+    assert torch.equal(sffn.experts_forward(x, tuple(routing), W1, W3, W2t), y)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     r2 = sffn.route(z, k, stream=side)
