@@ -19,26 +19,92 @@ namespace {
 // Gate and up of few tokens: h[p, i] = A(W1_e[i] . x_t) (W3_e[i] . x_t) for the
 // choices p = (t, j) of expert e.  blockIdx.y is a choice (one token: its
 // choices are its experts) or the y-th busy expert; a warp takes one hidden
-// unit and TM of the expert's rows together, so W1 is read once per TM rows and
+// unit and up to EG_ROWS of the expert's rows together, so W1 is read once for them and
 // W3 only where a row keeps the unit.  EG_U pieces of a weight row are
 // requested before the first is used; the rows of x sit in shared memory
 // (STAGED) unless they are too long for it.
 constexpr int EG_WARPS = 8;
 constexpr int EG_U = 5;
+constexpr int EG_ROWS = 4;
 constexpr size_t EG_STAGE = 40 * 1024;  // most bytes of staged x a block
 
+// The unit's TM rows from c0 on: rows past r1 are computed on row c0's token and not stored.
 template <int TM, bool STAGED>
+__device__ __forceinline__ void gate_rows(const ExpertsArgs& a, float* __restrict__ h, uint4* s_x, const uint4* w1,
+                                          const uint4* w3, int i, int c0, int r1, bool by_choice) {
+  const int lane = threadIdx.x & 31, P = a.T * a.k, n = a.D / 8;
+  int p[TM];
+  const uint4* x[TM];
+#pragma unroll
+  for (int t = 0; t < TM; ++t) {
+    p[t] = by_choice ? c0 : c0 + t < r1 ? a.rows[c0 + t] : -1;
+    if (p[t] >= P) p[t] = -1;
+    x[t] = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.x) + (size_t)(max(p[t], 0) / a.k) * a.ldx);
+  }
+  uint4 w[EG_U];
+#pragma unroll
+  for (int q = 0; q < EG_U; ++q)  // the first pieces of W1 travel while x is staged
+    w[q] = lane + 32 * q < n ? __ldg(w1 + lane + 32 * q) : make_uint4(0, 0, 0, 0);
+  if (STAGED) {
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < TM; ++t)
+      for (int k = threadIdx.x; k < n; k += 32 * EG_WARPS) s_x[t * n + k] = __ldg(x[t] + k);
+    __syncthreads();
+  }
+  auto dot = [&](const uint4* wp, bool loaded, float (&out)[TM]) {
+    float2 acc[TM] = {};
+    for (int k0 = lane; k0 < n; k0 += 32 * EG_U) {
+      if (!loaded || k0 != lane) {
+#pragma unroll
+        for (int q = 0; q < EG_U; ++q) w[q] = k0 + 32 * q < n ? __ldg(wp + k0 + 32 * q) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int q = 0; q < EG_U; ++q) {
+        const int k = k0 + 32 * q;
+        if (k < n) {
+          float u[8];
+          Elt<bf16_tag>::unpack(w[q], u);
+#pragma unroll
+          for (int t = 0; t < TM; ++t) {
+            float v[8];
+            Elt<bf16_tag>::unpack(STAGED ? lds16(s_x + t * n + k) : __ldg(x[t] + k), v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              ffma2(acc[t], make_float2(u[2 * j], u[2 * j + 1]), make_float2(v[2 * j], v[2 * j + 1]));
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < TM; ++t) out[t] = warp_sum(acc[t].x + acc[t].y);
+  };
+  float g[TM], u[TM];
+  dot(w1, true, g);
+  bool live = false;
+#pragma unroll
+  for (int t = 0; t < TM; ++t) {
+    g[t] = activation(a.act, g[t]);
+    u[t] = 0.f;
+    live = live || (p[t] >= 0 && g[t] != 0.f);
+  }
+  if (live && i < a.H) dot(w3, false, u);
+#pragma unroll
+  for (int t = 0; t < TM; ++t)
+    if (lane == t && p[t] >= 0 && i < a.H) h[(size_t)p[t] * a.H + i] = g[t] != 0.f ? g[t] * u[t] : 0.f;
+}
+
+template <bool ONE, bool STAGED>
 __global__ void __launch_bounds__(32 * EG_WARPS) experts_gate_kernel(const ExpertsArgs a, float* __restrict__ h) {
-  extern __shared__ uint4 s_x[];  // [TM][D / 8]
+  extern __shared__ uint4 s_x[];  // [ONE ? 1 : EG_ROWS][D / 8]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int i = blockIdx.x * EG_WARPS + warp;
-  const int P = a.T * a.k, n = a.D / 8;
+  const int P = a.T * a.k;
   pdl_launch_dependents();
   pdl_wait();
   int e = -1, r0 = 0, r1 = 0;
-  if (TM == 1) {
+  if (ONE) {
     e = a.ids[blockIdx.y];
-    r1 = 1;
     if (e >= a.E) e = -1;
   } else {
     int left = blockIdx.y;
@@ -63,66 +129,14 @@ __global__ void __launch_bounds__(32 * EG_WARPS) experts_gate_kernel(const Exper
   const size_t off = ((size_t)e * a.H + min(i, a.H - 1)) * a.D;
   const uint4* w1 = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.W1) + off);
   const uint4* w3 = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.W3) + off);
-  for (int c0 = r0; c0 < r1; c0 += TM) {
-    int p[TM];
-    const uint4* x[TM];
-#pragma unroll
-    for (int t = 0; t < TM; ++t) {
-      p[t] = TM == 1 ? (int)blockIdx.y : c0 + t < r1 ? a.rows[c0 + t] : -1;
-      if (p[t] >= P) p[t] = -1;
-      x[t] = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.x) + (size_t)(max(p[t], 0) / a.k) * a.ldx);
+  if (ONE) {
+    gate_rows<1, STAGED>(a, h, s_x, w1, w3, i, (int)blockIdx.y, 0, true);
+  } else {
+    for (int c0 = r0; c0 < r1; c0 += EG_ROWS) {
+      if (r1 - c0 == 1) gate_rows<1, STAGED>(a, h, s_x, w1, w3, i, c0, r1, false);
+      else if (r1 - c0 == 2) gate_rows<2, STAGED>(a, h, s_x, w1, w3, i, c0, r1, false);
+      else gate_rows<EG_ROWS, STAGED>(a, h, s_x, w1, w3, i, c0, r1, false);
     }
-    uint4 w[EG_U];
-#pragma unroll
-    for (int q = 0; q < EG_U; ++q)  // the first pieces of W1 travel while x is staged
-      w[q] = lane + 32 * q < n ? __ldg(w1 + lane + 32 * q) : make_uint4(0, 0, 0, 0);
-    if (STAGED) {
-      __syncthreads();
-#pragma unroll
-      for (int t = 0; t < TM; ++t)
-        for (int k = threadIdx.x; k < n; k += 32 * EG_WARPS) s_x[t * n + k] = __ldg(x[t] + k);
-      __syncthreads();
-    }
-    auto dot = [&](const uint4* wp, bool loaded, float (&out)[TM]) {
-      float2 acc[TM] = {};
-      for (int k0 = lane; k0 < n; k0 += 32 * EG_U) {
-        if (!loaded || k0 != lane) {
-#pragma unroll
-          for (int q = 0; q < EG_U; ++q) w[q] = k0 + 32 * q < n ? __ldg(wp + k0 + 32 * q) : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int q = 0; q < EG_U; ++q) {
-          const int k = k0 + 32 * q;
-          if (k < n) {
-            float u[8];
-            Elt<bf16_tag>::unpack(w[q], u);
-#pragma unroll
-            for (int t = 0; t < TM; ++t) {
-              float v[8];
-              Elt<bf16_tag>::unpack(STAGED ? lds16(s_x + t * n + k) : __ldg(x[t] + k), v);
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                ffma2(acc[t], make_float2(u[2 * j], u[2 * j + 1]), make_float2(v[2 * j], v[2 * j + 1]));
-            }
-          }
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < TM; ++t) out[t] = warp_sum(acc[t].x + acc[t].y);
-    };
-    float g[TM], u[TM];
-    dot(w1, true, g);
-    bool live = false;
-#pragma unroll
-    for (int t = 0; t < TM; ++t) {
-      g[t] = activation(a.act, g[t]);
-      u[t] = 0.f;
-      live = live || (p[t] >= 0 && g[t] != 0.f);
-    }
-    if (live && i < a.H) dot(w3, false, u);
-#pragma unroll
-    for (int t = 0; t < TM; ++t)
-      if (lane == t && p[t] >= 0 && i < a.H) h[(size_t)p[t] * a.H + i] = g[t] != 0.f ? g[t] * u[t] : 0.f;
   }
 }
 
@@ -282,11 +296,11 @@ cudaError_t launch_experts(const ExpertsArgs& a, cudaStream_t s) {
     const dim3 grid((unsigned)((a.H + EG_WARPS - 1) / EG_WARPS), (unsigned)(a.T == 1 ? a.k : std::min(a.E, a.T * a.k)));
     const size_t row = 2 * (size_t)a.D;
     if (a.T == 1)
-      e = row <= EG_STAGE ? ops_launch(experts_gate_kernel<1, true>, grid, 32 * EG_WARPS, row, s, 1, a, h)
-                          : ops_launch(experts_gate_kernel<1, false>, grid, 32 * EG_WARPS, 0, s, 1, a, h);
+      e = row <= EG_STAGE ? ops_launch(experts_gate_kernel<true, true>, grid, 32 * EG_WARPS, row, s, 1, a, h)
+                          : ops_launch(experts_gate_kernel<true, false>, grid, 32 * EG_WARPS, 0, s, 1, a, h);
     else
-      e = 4 * row <= EG_STAGE ? ops_launch(experts_gate_kernel<4, true>, grid, 32 * EG_WARPS, 4 * row, s, 1, a, h)
-                              : ops_launch(experts_gate_kernel<4, false>, grid, 32 * EG_WARPS, 0, s, 1, a, h);
+      e = EG_ROWS * row <= EG_STAGE ? ops_launch(experts_gate_kernel<false, true>, grid, 32 * EG_WARPS, EG_ROWS * row, s, 1, a, h)
+                              : ops_launch(experts_gate_kernel<false, false>, grid, 32 * EG_WARPS, 0, s, 1, a, h);
     if (e != cudaSuccess) return e;
     return ops_launch(experts_down_kernel, dim3((unsigned)((a.D + 255) / 256 * ED_SPLIT), (unsigned)a.T), 32 * ED_WARPS, 0,
                       s, ED_SPLIT, a, (const float*)h);

@@ -49,6 +49,7 @@ constexpr size_t TG_SMEM = 227 * 1024;
 enum { TG_BF16, TG_GATED, TG_I8, TG_F16 };
 // the epilogue's shared scratch of a warp: 16 rows of 32 words, 4 words apart (no bank conflicts either way)
 constexpr int TG_EPI_PITCH = 36;
+constexpr int TG_PART = 132;  // words between the rows of a partial tile
 constexpr uint32_t TG_EPI_BYTES = 16 * TG_EPI_PITCH * 4;
 constexpr int TG_G = 8;           // weight tiles of one raster group
 
@@ -60,6 +61,7 @@ struct TgArgs {
   int KC;      // 64-wide K chunks
   int S;       // operand stages
   int SR;      // raw stages (int8)
+  int ks;      // blocks of a cluster that cut K between them (1: no cut)
   int cols;    // TMEM columns allocated
   int vec;     // rows of y take 16-byte stores: y, ldy and N are multiples of that
   int nacc;    // accumulators: 2, or 1 where one takes all of TMEM (the epilogue is not hidden then)
@@ -292,12 +294,18 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
   uint64_t* rempty = rfull + p.SR;
   uint64_t* accf = rempty + p.SR;  // [2]
   uint64_t* acce = accf + 2;       // [2]
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(acce + 2);
+  uint64_t* partf = acce + 2;      // K cut: every block's partial tile is in its shared memory,
+  uint64_t* partd = partf + 1;     // and every block has read its share of them
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(partd + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   int* s_off = reinterpret_cast<int*>(tslot + 2);  // [E + 1]
   int* s_pre = s_off + p.g.E + 1;                  // [E + 1]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = CTAS == 2 ? cluster_rank() : 0;
+  const int ks = CTAS == 1 && !GATED ? p.ks : 1;
+  const int kr = ks > 1 ? (int)cluster_rank() : 0;  // this block's share of K: chunks [cb, ce), whole pairs of them
+  const int KP = (p.KC + 1) / 2, cb = 2 * (int)((long long)KP * kr / ks);
+  const int ce = min(p.KC, 2 * (int)((long long)KP * (kr + 1) / ks));
 
   if (tid == 0) {
     for (int s = 0; s < p.S; ++s) {
@@ -312,6 +320,8 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
       mbar_init(&accf[b], 1);
       mbar_init(&acce[b], EW * CTAS);
     }
+    mbar_init(partf, EW * ks);
+    mbar_init(partd, EW * ks);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_map(&mW);
@@ -356,12 +366,12 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (CTAS == 2) cluster_sync_all();  // the other block's barriers exist before anything arrives on them
+  if (CTAS == 2 || ks > 1) cluster_sync_all();  // the other blocks' barriers exist before anything arrives on them
   tc_fence_after();
   const uint32_t tmem = *tslot;
   if (tid == 0) pdl_launch_dependents();
   const int total = s_pre[p.g.E];
-  const int first = blockIdx.x / CTAS, step = gridDim.x / CTAS;
+  const int first = blockIdx.x / (CTAS * ks), step = gridDim.x / (CTAS * ks);
   const uint32_t smb = smem_u32(sm);
   const int n0r = 128 * (int)rank;  // this block's rows inside a weight tile
 
@@ -370,7 +380,8 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
     const bool xside = warp == 3;
     uint64_t* fb = I8 ? rfull : full;
     uint64_t* eb = I8 ? rempty : empty;
-    const int S = I8 ? p.SR : p.S, KCH = I8 ? (p.g.K + 127) / 128 : p.KC, KW = I8 ? 128 : 64;
+    const int S = I8 ? p.SR : p.S, KW = I8 ? 128 : 64;
+    const int kb = I8 ? cb / 2 : cb, ke = I8 ? (ce + 1) / 2 : ce;
     const uint32_t base = I8 ? smb + raw0 : smb;
     uint32_t it = 0, s = 0, par = 1;  // par: parity of the wait for stage s (a fresh barrier passes parity 1)
     bool ok = true;
@@ -396,7 +407,11 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
             gy[h][j] = src;
           }
       }
-      for (int c = 0; c < KCH; ++c, ++it) {
+      if (ks > 1 && t != first) {  // the stages held the last tile's partial sums
+        if (!__all_sync(0xffffffffu, tg_wait<true>(partd, (uint32_t)((t - first) / step - 1) & 1, abort_flag, p.err))) break;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+      for (int c = kb; c < ke; ++c, ++it) {
         if (!__all_sync(0xffffffffu, tg_wait<false>(&eb[s], par, abort_flag, p.err))) {
           ok = false;
           break;
@@ -451,7 +466,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
         if (use > 0 && !__all_sync(0xffffffffu, tg_wait<CTAS == 2>(&acce[b], (use - 1) & 1, abort_flag, p.err))) break;
         tc_fence_after();
         const uint32_t d = tmem + b * (uint32_t)((GATED ? 2 : 1) * p.NT);
-        for (int c = 0; c < p.KC; ++c) {
+        for (int c = cb; c < ce; ++c) {
           if (!__all_sync(0xffffffffu, tg_wait<I8 && CTAS == 2>(&full[s], par, abort_flag, p.err))) {
             ok = false;
             break;
@@ -463,8 +478,8 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const uint64_t ak = ad + (KN ? (k * 2048) >> 4 : 2 * k);
-            tg_mma<CTAS>(d, ak, bd + 2 * k, idesc, c > 0 || k > 0, one);
-            if (GATED) tg_mma<CTAS>(d + p.NT, ak + (AB >> 4), bd + 2 * k, idesc, c > 0 || k > 0, one);
+            tg_mma<CTAS>(d, ak, bd + 2 * k, idesc, c > cb || k > 0, one);
+            if (GATED) tg_mma<CTAS>(d + p.NT, ak + (AB >> 4), bd + 2 * k, idesc, c > cb || k > 0, one);
           }
           tg_commit<CTAS>(&empty[s], one);
           if (++s == (uint32_t)p.S) {
@@ -481,13 +496,12 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
     // Four groups of four warps take every fourth chunk each: a chunk's chain of load, widen, store, fence and
     // arrival is longer than its MMAs, four of them overlap.
     const int cg = (warp - TG_CONV_WARP0) >> 2, cw = warp & 3, row8 = lane & 7, cj = lane >> 3;
-    const int KCH = (p.g.K + 127) / 128;
     uint32_t it0 = 0, rt0 = 0;  // chunks and raw stages of the tiles before
     bool ok = true;
     for (int t = first; t < total && ok; t += step) {
       const Tile q = tile_at<CTAS>(p, s_off, s_pre, t);
       const int groups = 16 + q.n / CTAS / 8;  // 8-row groups: A, then B (both regions are dense)
-      for (int c = (int)((cg - it0) & 3u); c < p.KC; c += 4) {
+      for (int c = (int)((cg - it0) & 3u); c < ce - cb; c += 4) {  // cb is even: halves are as in the whole sum
         const uint32_t it = it0 + c, rt = rt0 + (c >> 1), s = it % p.S, rs = rt % p.SR;
         const int half = c & 1;
         // A parity wait must not run two phases ahead.  With four stages a group meets every phase of its stage's
@@ -526,11 +540,11 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
           else
             mbar_arrive(&full[s]);
           mbar_arrive(&rempty[rs]);
-          if (half == 0 && c == p.KC - 1) mbar_arrive(&rempty[rs]);  // no second half: its arrival as well
+          if (half == 0 && c == ce - cb - 1) mbar_arrive(&rempty[rs]);  // no second half: its arrival as well
         }
       }
-      it0 += p.KC;
-      rt0 += KCH;
+      it0 += ce - cb;
+      rt0 += (ce - cb + 1) / 2;
     }
   } else if (warp >= TG_EPI_WARP0 && warp < TG_EPI_WARP0 + EW) {
     // ---------------------------------------------------------------- epilogue: lane = one row of w
@@ -547,6 +561,65 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
       const uint32_t ta = tmem + b * (uint32_t)((GATED ? 2 : 1) * p.NT) + ((uint32_t)(32 * (ew & 3)) << 16);
       const float sw = F16 && nok ? p.g.sw[(size_t)q.e * p.g.N + n] : 0.f;
       const int rows = q.r1 - q.r0;
+      if (CTAS == 1 && !GATED && ks > 1) {
+        // K is cut over the cluster: every block leaves its partial tile, [row of x][128 rows of w], in the stages
+        // (their copies and MMAs are done, and the producers wait for `partd`); then each sums its share of the
+        // rows over the blocks in their order, so the result does not depend on timing.
+        for (int c0 = 32 * (ew >> 2); c0 < rows; c0 += 32 * (EW / 4)) {
+          uint32_t v[32];
+          tmem_ld32(ta + c0, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (c0 + j < rows) sts4(smb + (uint32_t)((c0 + j) * TG_PART + 32 * (ew & 3) + lane) * 4u, v[j]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acce[b]);
+        if (lane < ks) arrive_remote(cluster_map(smem_u32(partf), (uint32_t)lane));
+        if (!__all_sync(0xffffffffu, tg_wait<true>(partf, tl & 1, abort_flag, p.err))) break;
+        const int t0 = (int)((long long)rows * kr / ks), t1 = (int)((long long)rows * (kr + 1) / ks);
+        const int nc = q.mt * 128 + 4 * lane;
+        float s4[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s4[i] = F16 && nc + i < p.g.N ? p.g.sw[(size_t)q.e * p.g.N + nc + i] : 1.f;
+        for (int r = t0 + ew; r < t1; r += EW) {
+          const uint32_t at = smb + (uint32_t)(r * TG_PART + 4 * lane) * 4u;
+          float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int k = 0; k < ks; ++k) {
+            const float4 v = ld_cluster_f4(cluster_map(at, (uint32_t)k));
+            sum.x += v.x;
+            sum.y += v.y;
+            sum.z += v.z;
+            sum.w += v.w;
+          }
+          const int gr = q.r0 + r;
+          float f[4] = {sum.x, sum.y, sum.z, sum.w};
+          if (F16) {
+            int src = gr;
+            if (p.g.index) {
+              const int i = p.g.index[gr];
+              src = i >= 0 && i / p.g.index_div < p.g.XR ? i / p.g.index_div : -1;
+            }
+            const float sx = src >= 0 ? p.g.sx[src] : 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = f[i] * sx * s4[i];
+          }
+          const uint64_t o = (uint64_t)(uint32_t)(p.g.out_index ? p.g.out_index[gr] : gr) * (uint64_t)p.g.ldy + nc;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (nc + i < p.g.N) {
+              if (p.g.y_f32)
+                reinterpret_cast<float*>(p.g.y)[o + i] = f[i];
+              else
+                reinterpret_cast<__nv_bfloat16*>(p.g.y)[o + i] = __float2bfloat16_rn(f[i]);
+            }
+        }
+        __syncwarp();
+        if (lane < ks) arrive_remote(cluster_map(smem_u32(partd), (uint32_t)lane));
+        if (t + step < total && !__all_sync(0xffffffffu, tg_wait<true>(partd, tl & 1, abort_flag, p.err))) break;
+        continue;
+      }
       for (int c0 = 32 * (ew >> 2); c0 < rows; c0 += 32 * (EW / 4)) {
         uint32_t v[32];
         tmem_ld32(ta + c0, v);
@@ -673,7 +746,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (CTAS == 2) cluster_sync_all();  // no block leaves while the other may still signal its barriers
+  if (CTAS == 2 || ks > 1) cluster_sync_all();  // no block leaves while another may still signal its barriers
   tc_fence_after();
   if (warp == 2) tg_dealloc<CTAS>(tmem, (uint32_t)p.cols);
 }
@@ -701,36 +774,50 @@ bool encode_w(CUtensorMap* m, const void* w, const GmmArgs& a) {
 
 template <int CTAS, int MODE, bool KN>
 cudaError_t tg_go(const CUtensorMap& mW, const CUtensorMap& mW3, const CUtensorMap& mX, const CUtensorMap& mXb,
-                  const TgArgs& p, size_t smem, int sms, cudaStream_t s) {
+                  TgArgs p, size_t smem, int sms, cudaStream_t s) {
   auto kernel = gmm_tc_kernel<CTAS, MODE, KN>;
   constexpr int threads = MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS;
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
-  static int clusters = 0;
+  static int clusters[9] = {};  // clusters that fit at once, by their blocks (a pair, or the cut of K)
   std::call_once(once, [&] {
     attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TG_SMEM);
-    clusters = sms / CTAS;
-    if (attr == cudaSuccess && CTAS == 2) {  // pairs that fit at once
+    clusters[1] = sms;
+    for (int c = 2; attr == cudaSuccess && c <= (CTAS == 2 ? 2 : 8); ++c) {
       cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3((unsigned)(sms / 2 * 2));
+      cfg.gridDim = dim3((unsigned)(sms / c * c));
       cfg.blockDim = dim3(threads);
       cfg.dynamicSmemBytes = TG_SMEM;
       cudaLaunchAttribute at[1];
       at[0].id = cudaLaunchAttributeClusterDimension;
-      at[0].val.clusterDim.x = 2;
+      at[0].val.clusterDim.x = (unsigned)c;
       at[0].val.clusterDim.y = 1;
       at[0].val.clusterDim.z = 1;
       cfg.attrs = at;
       cfg.numAttrs = 1;
       int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0) clusters = std::min(clusters, n);
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0) clusters[c] = std::min(sms / c, n);
     }
+    (void)cudaGetLastError();
   });
   if (attr != cudaSuccess) return attr;
   const GmmArgs& a = p.g;
   const long long most = (long long)p.MT * ((long long)a.R / p.NT + std::min(a.E, a.R));  // tiles at most
-  const int n = (int)std::min<long long>(clusters, std::max(1ll, most));
-  return ops_launch(kernel, dim3((unsigned)(n * CTAS)), threads, smem, s, CTAS, mW, mW3, mX, mXb, p);
+  int c = CTAS;
+  if (CTAS == 1 && MODE != TG_GATED) {
+    // Fewer tiles than half the SMs (as far as sizes tell: groups of equal length): a cluster cuts K, as often as the
+    // tiles' clusters fit at once.  A cut costs a tile's exchange, about two microseconds, so a share keeps 4 pairs of
+    // chunks at least.
+    const int busy = std::min(a.E, a.R);
+    const long long tiles = (long long)p.MT * busy * (((a.R + busy - 1) / busy + p.NT - 1) / p.NT);
+    const int most_cut = std::getenv("SFFN_KS") ? std::atoi(std::getenv("SFFN_KS")) : 8;
+    for (int k = 2; k <= std::min(most_cut, (p.KC + 1) / 8); ++k)
+      if (clusters[k] >= tiles) c = k;
+  }
+  p.ks = CTAS == 1 ? c : 1;
+  if (clusters[c] < 1) return cudaErrorInvalidConfiguration;
+  const int n = (int)std::min<long long>(clusters[c], std::max(1ll, most));
+  return ops_launch(kernel, dim3((unsigned)(n * c)), threads, smem, s, c, mW, mW3, mX, mXb, p);
 }
 
 }  // namespace
@@ -746,7 +833,7 @@ cudaError_t launch_gmm_tc(const GmmArgs& a, int ctas, int nt, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const size_t yb = a.y_f32 ? 4 : 2;
   p.vec = ((uintptr_t)a.y & 15) == 0 && a.ldy * yb % 16 == 0 && a.N * yb % 16 == 0;
-  const size_t fixed = (a.i8 ? 0 : 8 * TG_EPI_BYTES) + 1024 + 8 * (2 * 16 + 2 * 16 + 4) + 8 + sizeof(int) * 2 * (size_t)(a.E + 1) + 64;
+  const size_t fixed = (a.i8 ? 0 : 8 * TG_EPI_BYTES) + 1024 + 8 * (2 * 16 + 2 * 16 + 6) + 8 + sizeof(int) * 2 * (size_t)(a.E + 1) + 64;
   auto stage_bytes = [&] { return (gated ? 2u : 1u) * 16384u + (uint32_t)(p.NT / ctas + 7) / 8 * 1024u; };
   auto slots = [&] { return (int)((TG_SMEM - fixed) / stage_bytes()); };
   // int8: the converters' four groups need four operand stages and three raw ones
@@ -812,8 +899,9 @@ __global__ void __launch_bounds__(256) widen_kernel(const uint8_t* __restrict__ 
 
 // Rows per expert from which fp16 copies pay.
 constexpr int TG_WIDE_ROWS = 768;
+int wide_rows() { const char* v = std::getenv("SFFN_WIDE"); return v ? std::atoi(v) : TG_WIDE_ROWS; }
 
-bool wide(int R, int E, int i8) { return i8 && R / E >= TG_WIDE_ROWS; }
+bool wide(int R, int E, int i8) { return i8 && R / E >= wide_rows(); }
 
 size_t gmm_workspace(int R, int XR, int N, int K, int E, int i8) {
   return wide(R, E, i8) ? 2 * ((size_t)XR * K + (size_t)E * N * K) : 0;

@@ -46,9 +46,9 @@ class Routing:
 
     def _all(self):
         if self._views is None:
-            n, T, k, b = self.T * self.k, self.T, self.k, self.buf
-            self._views = (b[:n].view(torch.float32).view(T, k), b.as_strided((T, k), (k, 1), n),
-                           b.as_strided((self.E + 1,), (1,), 3 * n), b.as_strided((n,), (1,), 2 * n))
+            n, shape = self.T * self.k, (self.T, self.k)
+            weights, ids, rows, offsets = self.buf.split((n, n, n, self.E + 1))
+            self._views = weights.view(torch.float32).view(shape), ids.view(shape), offsets, rows
         return self._views
 
     weights = property(lambda self: self._all()[0])

@@ -293,6 +293,23 @@ def test_grouped_matmul_int8_long_groups():
         close(y[r], ref, 3 * 2.0 ** -24 * ref.abs() + int8_bound(xe, w[e], scale))
 
 
+@pytest.mark.parametrize("counts", [[20, 0, 33], [130], [17, 64, 300]], ids=str)
+@pytest.mark.parametrize("transposed", [False, True])
+def test_grouped_matmul_few_tiles_long_sums(counts, transposed):
+    """Few tiles and a long sum: blocks of a cluster cut K between them."""
+    g, R, E, N, K = gen(71), sum(counts), len(counts), 264, 3000
+    x = torch.randn(R, K, generator=g, device=DEV).to(BF)
+    w = torch.randn(E, N, K, generator=g, device=DEV).to(BF)
+    off = offsets_of(counts)
+    y = sffn.grouped_matmul(x, w.transpose(1, 2).contiguous() if transposed else w, off, transposed=transposed, dtype="f32")
+    z = sffn.grouped_matmul(x, w.transpose(1, 2).contiguous() if transposed else w, off, transposed=transposed, dtype="f32")
+    assert torch.equal(y, z)
+    b = off.tolist()
+    for e in range(E):
+        xe, we = x[b[e]:b[e + 1]].double(), w[e].double()
+        close(y[b[e]:b[e + 1]], xe @ we.T, K * 2.0 ** -23 * (xe.abs() @ we.abs().T))
+
+
 @pytest.mark.parametrize("E", [200, 1000])
 def test_grouped_matmul_many_experts(E):
     """Tables of many groups, most of them empty or short."""
