@@ -21,53 +21,17 @@ _OUT = {"bf16": (torch.bfloat16, SFFN_BF16), "f32": (torch.float32, SFFN_F32),
         torch.bfloat16: (torch.bfloat16, SFFN_BF16), torch.float32: (torch.float32, SFFN_F32)}
 
 
-class Routing:
-    """``route``'s result: weights [T, k] fp32, ids [T, k], offsets [E + 1] and rows [T * k] (int32), in one buffer
-    whose views are made when they are asked for; iterates in that order.  ``Routing.of`` takes four tensors of a
-    caller's own."""
+class Routing(tuple):
+    """``route``'s result, the four tensors weights [T, k] fp32, ids [T, k], offsets [E + 1] and rows [T * k] (int32)."""
 
-    __slots__ = ("T", "E", "k", "buf", "_views")
+    weights = property(lambda self: self[0])
+    ids = property(lambda self: self[1])
+    offsets = property(lambda self: self[2])
+    rows = property(lambda self: self[3])
 
-    def __init__(self, buf, T, E, k, views=None):
-        self.buf, self.T, self.E, self.k, self._views = buf, T, E, k, views
 
-    @classmethod
-    def of(cls, weights, ids, offsets, rows):
-        _operand("weights", weights, (torch.float32,), 2)
-        device = weights.device
-        for name, t, dim in (("ids", ids, 2), ("offsets", offsets, 1), ("rows", rows, 1)):
-            _operand(name, t, (torch.int32,), dim, device)
-        for name, t in (("weights", weights), ("ids", ids), ("offsets", offsets), ("rows", rows)):
-            _dense(name, t)
-        T, k = weights.shape
-        if ids.shape != weights.shape or rows.shape[0] != T * k:
-            raise ValueError("the routing's tensors are of other tokens or choices")
-        return cls(None, T, offsets.shape[0] - 1, k, (weights, ids, offsets, rows))
-
-    def _all(self):
-        if self._views is None:
-            n, shape = self.T * self.k, (self.T, self.k)
-            weights, ids, rows, offsets = self.buf.split((n, n, n, self.E + 1))
-            self._views = weights.view(torch.float32).view(shape), ids.view(shape), offsets, rows
-        return self._views
-
-    weights = property(lambda self: self._all()[0])
-    ids = property(lambda self: self._all()[1])
-    offsets = property(lambda self: self._all()[2])
-    rows = property(lambda self: self._all()[3])
-
-    def __iter__(self):
-        return iter(self._all())
-
-    def _pointers(self):
-        if self.buf is not None:
-            at, n = self.buf.data_ptr(), 4 * self.T * self.k
-            return at, at + n, at + 3 * n, at + 2 * n
-        return tuple(t.data_ptr() for t in self._views)
-
-    @property
-    def device(self):
-        return (self._views[0] if self.buf is None else self.buf).device
+class _Routed(Routing):
+    """A routing that ``route`` made: its tensors are known to fit each other."""
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # no stream object in between
@@ -143,15 +107,17 @@ def route(logits, k: int, score: str = "softmax", normalize: bool = True, stream
     if not 1 <= k <= E:
         raise ValueError(f"k={k} outside 1..{E}")
     device = logits.device
-    n = T * k
-    buf = torch.empty(3 * n + E + 1, dtype=torch.int32, device=device)
+    weights = torch.empty((T, k), dtype=torch.float32, device=device)
+    ids = torch.empty((T, k), dtype=torch.int32, device=device)
+    offsets = torch.empty(E + 1, dtype=torch.int32, device=device)
+    rows = torch.empty(T * k, dtype=torch.int32, device=device)
     ws, nb = _scratch(_route_bytes(T, E, k), device)
     flags = (SFFN_ROUTE_SIGMOID if score == "sigmoid" else 0) | (SFFN_ROUTE_NORMALIZE if normalize else 0)
-    at = buf.data_ptr()
-    _done(load().sffn_route(logits.data_ptr(), _pitch("logits", logits), at, at + 4 * n, at + 12 * n, at + 8 * n, T, E, k,
+    _done(load().sffn_route(logits.data_ptr(), _pitch("logits", logits), weights.data_ptr(), ids.data_ptr(),
+                            offsets.data_ptr(), rows.data_ptr(), T, E, k,
                             SFFN_F32 if logits.dtype == torch.float32 else SFFN_BF16, flags, nb and ws.data_ptr(), nb,
                             _raw(device)))
-    return Routing(buf, T, E, k)
+    return _Routed((weights, ids, offsets, rows))
 
 
 def quantize_tokens(x, stream=None):
@@ -265,19 +231,29 @@ def experts_forward(x, routing, W1, W3, W2t, act: str = "relu", out=None, stream
     if act not in _ACT:
         raise ValueError(f"act {act!r} is none of {', '.join(_ACT)}")
     T, D = x.shape
+    shape = W1.shape
     for name, t in (("W1", W1), ("W3", W3), ("W2t", W2t)):
         _operand(name, t, (torch.bfloat16,), 3, device)
-        if t.shape != W1.shape or t.shape[2] != D:
-            raise ValueError(f"{name} {tuple(t.shape)} does not go with x {tuple(x.shape)} and W1 {tuple(W1.shape)}")
-        _dense(name, t)
-    E, H = W1.shape[0], W1.shape[1]
-    if not isinstance(routing, Routing):
-        routing = Routing.of(*routing)
-    k = routing.k
-    if routing.T != T or routing.E != E:
-        raise ValueError(f"the routing is of {routing.T} tokens and {routing.E} experts, not {T} and {E}")
-    if routing.device != device:
-        raise ValueError(f"the routing is on {routing.device}, not {device}")
+        if t.shape != shape or shape[2] != D:
+            raise ValueError(f"{name} {tuple(t.shape)} does not go with x {tuple(x.shape)} and W1 {tuple(shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    E, H = shape[0], shape[1]
+    weights, ids, offsets, rows = routing
+    if type(routing) is not _Routed:
+        _operand("weights", weights, (torch.float32,), 2, device)
+        _operand("ids", ids, (torch.int32,), 2, device)
+        _operand("offsets", offsets, (torch.int32,), 1, device)
+        _operand("rows", rows, (torch.int32,), 1, device)
+        for name, t in (("weights", weights), ("ids", ids), ("offsets", offsets), ("rows", rows)):
+            _dense(name, t)
+        if ids.shape != weights.shape or rows.shape[0] != weights.numel():
+            raise ValueError("the routing's tensors are of other tokens or choices")
+    elif weights.device != device:
+        raise ValueError(f"the routing is on {weights.device}, not {device}")
+    k = weights.shape[1]
+    if weights.shape[0] != T or offsets.shape[0] != E + 1:
+        raise ValueError(f"the routing is of {weights.shape[0]} tokens and {offsets.shape[0] - 1} experts, not {T} and {E}")
     if out is None:
         out = torch.empty((T, D), dtype=torch.bfloat16, device=device)
     else:
@@ -287,8 +263,9 @@ def experts_forward(x, routing, W1, W3, W2t, act: str = "relu", out=None, stream
         _dense("out", out)
     ws, nb = _scratch(_experts_bytes(T, k, D, H), device)
     _done(load().sffn_experts_forward(
-        x.data_ptr(), _pitch("x", x), *routing._pointers(), W1.data_ptr(), W3.data_ptr(), W2t.data_ptr(),
-        out.data_ptr(), T, E, k, D, H, _ACT[act], nb and ws.data_ptr(), nb, _raw(device)))
+        x.data_ptr(), _pitch("x", x), weights.data_ptr(), ids.data_ptr(), offsets.data_ptr(), rows.data_ptr(),
+        W1.data_ptr(), W3.data_ptr(), W2t.data_ptr(), out.data_ptr(), T, E, k, D, H, _ACT[act], nb and ws.data_ptr(), nb,
+        _raw(device)))
     return out
 
 
