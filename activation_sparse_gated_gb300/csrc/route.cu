@@ -9,10 +9,10 @@
 // for every grouped row, the choice token * k + place that it serves.
 //
 // One warp takes a token: the logits sit in registers (E / 32 a lane) as
-// order-preserving integer keys, and a choice is one warp-wide maximum of the
-// keys and one minimum of the indexes that hold it (redux, no shuffle trees).
+// order-preserving integer keys that each lane sorts, and a choice is one or
+// two warp-wide maxima over the lanes' firsts (redux, no shuffle trees).
 // The sort is exact integer work, so its result does not depend on timing: a
-// cluster of blocks owns a chunk of consecutive tokens (16 a block, one a warp:
+// cluster of blocks owns a chunk of consecutive tokens (a token or two a warp:
 // the choice is a chain of dependent steps, so it wants warps) and counts its
 // choices per expert, and a second kernel adds the counts of the chunks before
 // its own.  Up to ROUTE_ONE choices one block does both.
@@ -41,49 +41,129 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 // exp(v - m) for v <= m, with equal infinities counting as equal
 __device__ __forceinline__ float exp_below(float v, float m) { return v == m ? 1.f : expf(v - m); }
 
-// One token by one warp: lane j < k ends up with choice j.  L: logits a lane.
-template <int L>
-__device__ __forceinline__ int choose(const RouteArgs& a, int t, int lane) {
-  uint32_t key[L];
-  const size_t base = (size_t)t * a.ld;
+// A lane's logits e = lane + 32 i as keys, sorted once (up to 8 of them); then a round looks at the lanes' firsts alone and the
+// winner's list moves up.  hi orders, lo says which: the larger lo is the lower index.
+//   bf16 (and E <= 65535): value and index fit one word, so a round is one redux;
+//   fp32: the value, then the index among the lanes that hold it.
+template <int L, bool BF16>
+struct Keys {
+  uint32_t hi[L], lo[BF16 ? 1 : L];
+
+  __device__ __forceinline__ void load(const RouteArgs& a, size_t base, int lane) {
 #pragma unroll
-  for (int i = 0; i < L; ++i) {
-    const int e = lane + 32 * i;
-    float v = -INFINITY;
-    if (e < a.E)
-      v = a.bf16 ? __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(a.logits)[base + e] << 16)
+    for (int i = 0; i < L; ++i) {
+      const int e = lane + 32 * i;
+      float v = -INFINITY;
+      if (e < a.E)
+        v = BF16 ? __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(a.logits)[base + e] << 16)
                  : reinterpret_cast<const float*>(a.logits)[base + e];
-    key[i] = order_key(v);
-  }
-  uint32_t ck = 0;
-  int ce = -1;
-  float all = 0.f, m = 0.f;
-  for (int j = 0; j < a.k; ++j) {
-    uint32_t best = 0;
-#pragma unroll
-    for (int i = 0; i < L; ++i) best = max(best, key[i]);
-    best = __reduce_max_sync(0xffffffffu, best);
-    if (best == 0) break;  // no open expert is left
-    uint32_t at = 0xffffffffu;
-#pragma unroll
-    for (int i = L - 1; i >= 0; --i)
-      if (key[i] == best) at = (uint32_t)(lane + 32 * i);
-    at = __reduce_min_sync(0xffffffffu, at);
-    if (j == 0) {
-      m = key_value(best);
-      if (!a.sigmoid && !a.normalize) {  // the sum over every open expert
-#pragma unroll
-        for (int i = 0; i < L; ++i)
-          if (key[i]) all += exp_below(key_value(key[i]), m);
-        all = warp_sum(all);
+      hi[i] = order_key(v);
+      if (BF16) {
+        if (hi[i]) hi[i] = (hi[i] & 0xffff0000u) | (uint32_t)(0xffff - e);  // a bf16 value's low half is all ones or zeros
+      } else {
+        lo[i] = ~(uint32_t)e;
       }
     }
+  }
+  __device__ __forceinline__ void order(int i, int j) {  // the larger first
+    if (BF16) {
+      const uint32_t x = max(hi[i], hi[j]);
+      hi[j] = min(hi[i], hi[j]);
+      hi[i] = x;
+    } else {
+      const bool sw = hi[j] > hi[i] || (hi[j] == hi[i] && lo[j] > lo[i]);
+      const uint32_t h = hi[i], l = lo[i];
+      hi[i] = sw ? hi[j] : h;
+      lo[i] = sw ? lo[j] : l;
+      hi[j] = sw ? h : hi[j];
+      lo[j] = sw ? l : lo[j];
+    }
+  }
+  static constexpr bool SORTED = L <= 8;  // longer lists look for their first in every round
+  __device__ __forceinline__ void sort() {  // odd-even transposition
+    if (!SORTED) return;
+#pragma unroll
+    for (int r = 0; r < L; ++r)
+#pragma unroll
+      for (int i = 0; i + 1 < L; ++i)
+        if (((i ^ r) & 1) == 0) order(i, i + 1);
+  }
+  __device__ __forceinline__ void pop() {
+#pragma unroll
+    for (int i = 0; i + 1 < L; ++i) {
+      hi[i] = hi[i + 1];
+      if (!BF16) lo[i] = lo[i + 1];
+    }
+    hi[L - 1] = 0;
+  }
+  // the largest key of the warp (0: none is open), and its index; the lane that holds it drops it
+  __device__ __forceinline__ uint32_t next(int* e) {
+    uint32_t top = hi[0];
+    if (!SORTED) {
+#pragma unroll
+      for (int i = 1; i < L; ++i) top = max(top, hi[i]);
+    }
+    const uint32_t best = __reduce_max_sync(0xffffffffu, top);
+    if (best == 0) return 0;
+    if (BF16) {
+      if (SORTED) {
+        if (top == best) pop();
+      } else {
+#pragma unroll
+        for (int i = 0; i < L; ++i) hi[i] = hi[i] == best ? 0u : hi[i];
+      }
+      *e = 0xffff - (int)(best & 0xffffu);
+      // the low half of the value: zeros, or ones where the key is complemented (a negative value)
+      return (best & 0x80000000u) ? best & 0xffff0000u : best | 0xffffu;
+    }
+    uint32_t mine = top == best ? lo[0] : 0u;
+    if (!SORTED) {
+      mine = 0;
+#pragma unroll
+      for (int i = L - 1; i >= 0; --i)
+        if (hi[i] == best) mine = lo[i];  // the lowest index last
+    }
+    const uint32_t at = __reduce_max_sync(0xffffffffu, mine);
+    if (SORTED) {
+      if (top == best && mine == at) pop();
+    } else {
+#pragma unroll
+      for (int i = 0; i < L; ++i) hi[i] = lo[i] == at ? 0u : hi[i];
+    }
+    *e = (int)~at;
+    return best;
+  }
+};
+
+// One token by one warp: lane j < k ends up with choice j, and returns it.  L: logits a lane.
+template <int L, bool BF16>
+__device__ __forceinline__ int choose(const RouteArgs& a, int t, int lane) {
+  Keys<L, BF16> keys;
+  keys.load(a, (size_t)t * a.ld, lane);
+  float all = 0.f, m = 0.f;
+  if (!a.sigmoid && !a.normalize) {  // the sum over every open expert
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < L; ++i) top = max(top, keys.hi[i]);
+    top = __reduce_max_sync(0xffffffffu, top);
+    auto value = [](uint32_t k) { return key_value(!BF16 ? k : (k & 0x80000000u) ? k & 0xffff0000u : k | 0xffffu); };
+    const float mx = value(top);
 #pragma unroll
     for (int i = 0; i < L; ++i)
-      if (at == (uint32_t)(lane + 32 * i)) key[i] = 0;
+      if (keys.hi[i]) all += exp_below(value(keys.hi[i]), mx);
+    all = warp_sum(all);
+  }
+  keys.sort();
+  uint32_t ck = 0;
+  int ce = -1;
+  for (int j = 0; j < a.k; ++j) {
+    int e = 0;
+    const uint32_t best = keys.next(&e);
+    if (best == 0) break;  // no open expert is left
+    if (j == 0) m = key_value(best);
     if (lane == j) {
       ck = best;
-      ce = (int)at;
+      ce = e;
     }
   }
   float w = 0.f;
@@ -99,13 +179,13 @@ __device__ __forceinline__ int choose(const RouteArgs& a, int t, int lane) {
 }
 
 // Tokens [t0, t1) of this block: choices, then counts per expert in s_hist.
-template <int L>
+template <int L, bool BF16>
 __device__ __forceinline__ void choose_block(const RouteArgs& a, int t0, int t1, int* s_hist) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int e = threadIdx.x; e < a.E; e += ROUTE_THREADS) s_hist[e] = 0;
   __syncthreads();
   for (int t = t0 + warp; t < t1; t += ROUTE_WARPS) {
-    const int e = choose<L>(a, t, lane);
+    const int e = choose<L, BF16>(a, t, lane);
     if (lane < a.k && e >= 0) atomicAdd(&s_hist[e], 1);
   }
   __syncthreads();
@@ -179,7 +259,7 @@ __device__ __forceinline__ void exclusive_scan(int* s_v, int E, int* s_w) {
   __syncthreads();
 }
 
-template <int L>
+template <int L, bool BF16>
 __global__ void __launch_bounds__(ROUTE_THREADS) route_one_kernel(const RouteArgs a, int warps) {
   extern __shared__ int sm[];
   int* s_base = sm;               // [E + 1]
@@ -187,7 +267,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS) route_one_kernel(const RouteArg
   int* s_cnt = s_w + ROUTE_WARPS; // [warps][E]
   pdl_launch_dependents();
   pdl_wait();
-  choose_block<L>(a, 0, a.T, s_base);
+  choose_block<L, BF16>(a, 0, a.T, s_base);
   exclusive_scan(s_base, a.E, s_w);
   for (int e = threadIdx.x; e <= a.E; e += ROUTE_THREADS) a.offsets[e] = s_base[e];
   const int total = s_base[a.E];
@@ -195,14 +275,14 @@ __global__ void __launch_bounds__(ROUTE_THREADS) route_one_kernel(const RouteArg
   scatter_block(a, 0, a.T, s_base, s_cnt, warps);
 }
 
-template <int L>
+template <int L, bool BF16>
 __global__ void __launch_bounds__(ROUTE_THREADS) route_choose_kernel(const RouteArgs a, int per, int split) {
   extern __shared__ int sm[];
   pdl_launch_dependents();
   pdl_wait();
   const int chunk = blockIdx.x / split, rank = blockIdx.x % split, sub = (per + split - 1) / split;
   const int c1 = min(a.T, chunk * per + per), t0 = min(c1, chunk * per + rank * sub), t1 = min(c1, t0 + sub);
-  choose_block<L>(a, t0, t1, sm);
+  choose_block<L, BF16>(a, t0, t1, sm);
   if (split > 1) cluster_sync_all();
   for (int e = rank * ROUTE_THREADS + threadIdx.x; e < a.E; e += split * ROUTE_THREADS) {
     int v = sm[e];
@@ -269,21 +349,26 @@ int route_chunks(int T, int* per) {
   return (T + *per - 1) / *per;
 }
 
-template <int L>
-cudaError_t route_l(const RouteArgs& a, cudaStream_t s) {
+template <int L, bool BF16>
+cudaError_t route_lt(const RouteArgs& a, cudaStream_t s) {
   if ((long long)a.T * a.k <= ROUTE_ONE) {
     const int fixed = a.E + 1 + ROUTE_WARPS, warps = scatter_warps(a.E, fixed);
-    return ops_launch(route_one_kernel<L>, dim3(1), ROUTE_THREADS, sizeof(int) * (fixed + warps * a.E), s, 1, a, warps);
+    return ops_launch(route_one_kernel<L, BF16>, dim3(1), ROUTE_THREADS, sizeof(int) * (fixed + warps * a.E), s, 1, a, warps);
   }
   int per;
   const int nb = route_chunks(a.T, &per);
-  const int split = per > 4 * ROUTE_WARPS ? 8 : per > 2 * ROUTE_WARPS ? 4 : per > ROUTE_WARPS ? 2 : 1;
-  cudaError_t e = ops_launch(route_choose_kernel<L>, dim3(nb * split), ROUTE_THREADS, sizeof(int) * a.E, s, split, a, per,
+  const int split = per > 8 * ROUTE_WARPS ? 8 : per > 4 * ROUTE_WARPS ? 4 : per > 2 * ROUTE_WARPS ? 2 : 1;
+  cudaError_t e = ops_launch(route_choose_kernel<L, BF16>, dim3(nb * split), ROUTE_THREADS, sizeof(int) * a.E, s, split, a, per,
                              split);
   if (e != cudaSuccess) return e;
   const int fixed = 2 * a.E + 1 + ROUTE_WARPS, warps = scatter_warps(a.E, fixed);
   return ops_launch(route_group_kernel, dim3(nb), ROUTE_THREADS, sizeof(int) * (fixed + warps * a.E), s, 1, a, per, nb,
                     warps);
+}
+
+template <int L>
+cudaError_t route_l(const RouteArgs& a, cudaStream_t s) {
+  return a.bf16 ? route_lt<L, true>(a, s) : route_lt<L, false>(a, s);
 }
 
 }  // namespace
