@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(32 * GR_WARPS) gmm_rows_kernel(const GmmArgs a
           if (I8) v = v * (src[t] >= 0 ? a.sx[src[t]] : 0.f) * a.sw[(size_t)e * a.N + n];
         }
     if (row >= 0) {
-      const size_t at = (size_t)(a.out_index ? a.out_index[row] : row) * a.ldy + n;
+      const size_t at = (size_t)row * a.ldy + n;
       if (a.y_f32)
         reinterpret_cast<float*>(a.y)[at] = v;
       else
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(32 * GK_WARPS) gmm_rows_kn_kernel(const GmmArg
 #pragma unroll
     for (int q = 0; q < GK_WARPS; ++q) v += s_sum[q][l][j];
     if (nn < a.N) {
-      const size_t at = (size_t)(a.out_index ? a.out_index[r] : r) * a.ldy + nn;
+      const size_t at = (size_t)r * a.ldy + nn;
       if (a.y_f32)
         reinterpret_cast<float*>(a.y)[at] = v;
       else

@@ -36,7 +36,6 @@ struct GmmArgs {
   const float* sw = nullptr;      // int8: [E, N]
   const int* offsets = nullptr;   // [E + 1]
   const int* index = nullptr;     // source row of row r is index[r] / index_div
-  const int* out_index = nullptr; // row r is stored at y row out_index[r]
   int index_div = 1;
   void* y = nullptr;
   long long ldx = 0, ldy = 0;
