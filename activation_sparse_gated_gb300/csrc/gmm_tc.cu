@@ -61,7 +61,6 @@ struct TgArgs {
   int KC;      // 64-wide K chunks
   int S;       // operand stages
   int SR;      // raw stages (int8)
-  int G;    // raster
   int ks;      // blocks of a cluster that cut K between them (1: no cut)
   int cols;    // TMEM columns allocated
   int vec;     // rows of y take 16-byte stores: y, ldy and N are multiples of that
@@ -266,8 +265,8 @@ __device__ __forceinline__ Tile tile_at(const TgArgs& p, const int* s_off, const
   constexpr int Q = 16 * CTAS;
   const int per = ((m + tt - 1) / tt + Q - 1) / Q * Q;
   const int i = t - s_pre[lo];
-  const int g = i / (p.G * tt), rest = i - g * p.G * tt, gm = min(p.G, p.MT - g * p.G);
-  q.mt = g * p.G + rest % gm;
+  const int g = i / (TG_G * tt), rest = i - g * TG_G * tt, gm = min(TG_G, p.MT - g * TG_G);
+  q.mt = g * TG_G + rest % gm;
   q.r0 = s_off[lo] + (rest / gm) * per;
   q.r1 = min(s_off[lo + 1], q.r0 + per);
   q.n = (q.r1 - q.r0 + Q - 1) / Q * Q;
@@ -816,7 +815,7 @@ cudaError_t tg_go(const CUtensorMap& mW, const CUtensorMap& mW3, const CUtensorM
       if (clusters[k] >= tiles) c = k;
   }
   p.ks = CTAS == 1 ? c : 1;
-  p.G = std::getenv("SFFN_G") ? std::atoi(std::getenv("SFFN_G")) : 8;
+
   if (clusters[c] < 1) return cudaErrorInvalidConfiguration;
   const int n = (int)std::min<long long>(clusters[c], std::max(1ll, most));
   return ops_launch(kernel, dim3((unsigned)(n * c)), threads, smem, s, c, mW, mW3, mX, mXb, p);
