@@ -83,13 +83,15 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
 // Bounded wait; PAIR: it also sees what threads of the pair's other block released.
 template <bool PAIR>
 __device__ __forceinline__ bool tg_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
-  if (PAIR ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
+  uint64_t t0 = 0;  // the clock is read only after many tries: reading it costs more than most waits
   for (uint32_t i = 1;; ++i) {
     if (PAIR ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
     if ((i & 63u) == 0) {
       if (*abort) return false;
-      if (globaltimer_ns() - t0 > TG_TIMEOUT_NS) {
+      const uint64_t t = globaltimer_ns();
+      if (t0 == 0) {
+        t0 = t;
+      } else if (t - t0 > TG_TIMEOUT_NS) {
         *abort = 1;
         atomicOr(err, DEV_ERR_TIMEOUT);
         return false;
