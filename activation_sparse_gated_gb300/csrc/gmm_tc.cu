@@ -498,19 +498,43 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
     // Four groups of four warps take every fourth chunk each: a chunk's chain of load, widen, store, fence and
     // arrival is longer than its MMAs, four of them overlap.
     const int cg = (warp - TG_CONV_WARP0) >> 2, cw = warp & 3, row8 = lane & 7, cj = lane >> 3;
-    uint32_t it0 = 0, rt0 = 0;  // chunks and raw stages of the tiles before
+    // Stages and their phases are counted up, never divided for: a division costs as much as the widening.
+    const int n = ce - cb, nr = (n + 1) / 2;  // chunks and raw stages of a tile
+    uint32_t s = 0, epar = 1;                 // stage of the next chunk; parity of the wait for it (fresh: passes)
+    uint32_t rs = 0, rpar = 0;                // raw stage of the next chunk, parity of its wait
+    int skip = cg;                            // chunks to go on to the group's next one
     bool ok = true;
+    auto forward = [&](int chunks, int raws) {
+      s += chunks;
+      while (s >= (uint32_t)p.S) {
+        s -= p.S;
+        epar ^= 1;
+      }
+      rs += raws;
+      while (rs >= (uint32_t)p.SR) {
+        rs -= p.SR;
+        rpar ^= 1;
+      }
+    };
     for (int t = first; t < total && ok; t += step) {
       const Tile q = tile_at<CTAS>(p, s_off, s_pre, t);
       const int groups = 16 + q.n / CTAS / 8;  // 8-row groups: A, then B (both regions are dense)
-      for (int c = (int)((cg - it0) & 3u); c < ce - cb; c += 4) {  // cb is even: halves are as in the whole sum
-        const uint32_t it = it0 + c, rt = rt0 + (c >> 1), s = it % p.S, rs = rt % p.SR;
+      int c = 0;
+      for (;;) {
+        if (c + skip >= n) {  // the next chunk is in a later tile
+          forward(n - c, nr - (c >> 1));
+          skip -= n - c;
+          break;
+        }
+        forward(skip, ((c + skip) >> 1) - (c >> 1));  // cb is even: halves are as in the whole sum
+        c += skip;
+        skip = 4;
         const int half = c & 1;
         // A parity wait must not run two phases ahead.  With four stages a group meets every phase of its stage's
         // `empty`; that wait shows that chunk it - 4 and all before it are multiplied, so of the raw stage every
         // phase before this one is over (its last chunk is at most 2 (rt - SR) + 1 <= it - 4 for SR >= 3).
-        ok = it < (uint32_t)p.S || tg_wait<false>(&empty[s], (it / p.S - 1) & 1, abort_flag, p.err);
-        if (ok) ok = tg_wait<false>(&rfull[rs], (rt / p.SR) & 1, abort_flag, p.err);
+        ok = tg_wait<false>(&empty[s], epar, abort_flag, p.err);
+        if (ok) ok = tg_wait<false>(&rfull[rs], rpar, abort_flag, p.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t src = smb + raw0 + rs * st_bytes + (uint32_t)row8 * 128u + ((uint32_t)((half * 4 + cj) ^ row8) << 4);
@@ -542,11 +566,9 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
           else
             mbar_arrive(&full[s]);
           mbar_arrive(&rempty[rs]);
-          if (half == 0 && c == ce - cb - 1) mbar_arrive(&rempty[rs]);  // no second half: its arrival as well
+          if (half == 0 && c == n - 1) mbar_arrive(&rempty[rs]);  // no second half: its arrival as well
         }
       }
-      it0 += ce - cb;
-      rt0 += (ce - cb + 1) / 2;
     }
   } else if (warp >= TG_EPI_WARP0 && warp < TG_EPI_WARP0 + EW) {
     // ---------------------------------------------------------------- epilogue: lane = one row of w
