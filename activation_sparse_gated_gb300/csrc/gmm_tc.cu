@@ -158,40 +158,41 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-// The MMA warp stays converged, so that descriptors live in uniform registers;
-// `one` (lane 0) issues.
+// True in one lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t v;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(v));
+  return v != 0;
+}
+
+// Operand descriptors travel as their low words: the high words are the same for every stage.
 template <int CTAS>
-__device__ __forceinline__ void tg_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc, uint32_t one) {
+__device__ __forceinline__ void tg_mma(uint32_t d, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi,
+                                       uint32_t idesc, uint32_t acc) {
   if constexpr (CTAS == 2)
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(one)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %6, 0;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(acc)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(one)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %6, 0;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(acc)
         : "memory");
 }
 
-// Arrive on `bar` (in both blocks of a pair) when the MMAs issued so far are done.
+// Arrive on `bar` (in both blocks of a pair) when the MMAs this thread issued so far are done.
 template <int CTAS>
-__device__ __forceinline__ void tg_commit(uint64_t* bar, uint32_t one) {
+__device__ __forceinline__ void tg_commit(uint32_t bar) {
   if constexpr (CTAS == 2)
     asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
-        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::
-            "r"(smem_u32(bar)),
-        "h"((uint16_t)3), "r"(one)
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
         : "memory");
   else
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
-        "r"(one)
-        : "memory");
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 template <int CTAS>
@@ -456,9 +457,14 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer (first block of a pair)
+    // The warp stays converged; one lane issues a chunk's MMAs and their commit together.  A chunk costs the warp's
+    // issue about as much as its MMAs cost the tensor cores, so the loop holds nothing but 32-bit adds.
     if (rank == 0) {
-      const uint32_t one = lane == 0 ? 1u : 0u;
-      uint32_t s = 0, par = 0, tl = 0;
+      const uint32_t st0 = (smb >> 4) & 0x3fffu;  // (in a cluster an address holds the block's rank above its offset)
+      uint32_t s = 0, par = 0, tl = 0, st = st0;   // st: the stage's address in 16-byte units
+      const uint32_t st16 = st_bytes >> 4, eb = smem_u32(empty);
+      const uint32_t hi = (uint32_t)(smem_desc(0, 0, 1024, SMEM_LAYOUT_SW128) >> 32);
+      const uint32_t alo0 = (KN ? AB / 2 : 16) >> 4 << 16, blo0 = 1u << 16;  // the leading byte offset
       bool ok = true;
       for (int t = first; t < total && ok; t += step, ++tl) {
         const Tile q = tile_at<CTAS>(p, s_off, s_pre, t);
@@ -468,28 +474,32 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
         if (use > 0 && !__all_sync(0xffffffffu, tg_wait<CTAS == 2>(&acce[b], (use - 1) & 1, abort_flag, p.err))) break;
         tc_fence_after();
         const uint32_t d = tmem + b * (uint32_t)((GATED ? 2 : 1) * p.NT);
+        uint32_t acc = 0;
         for (int c = cb; c < ce; ++c) {
-          if (!__all_sync(0xffffffffu, tg_wait<I8 && CTAS == 2>(&full[s], par, abort_flag, p.err))) {
+          if (!__all_sync(0xffffffffu, tg_wait<I8 && CTAS == 2>(full + s, par, abort_flag, p.err))) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t st = smb + s * st_bytes;
-          const uint64_t ad = KN ? smem_desc(st, AB / 2, 1024, SMEM_LAYOUT_SW128) : smem_desc(st, 16, 1024, SMEM_LAYOUT_SW128);
-          const uint64_t bd = smem_desc(st + (GATED ? 2 : 1) * AB, 16, 1024, SMEM_LAYOUT_SW128);
+          const uint32_t al = alo0 + st, bl = blo0 + st + ((GATED ? 2 : 1) * AB >> 4);
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint64_t ak = ad + (KN ? (k * 2048) >> 4 : 2 * k);
-            tg_mma<CTAS>(d, ak, bd + 2 * k, idesc, c > cb || k > 0, one);
-            if (GATED) tg_mma<CTAS>(d + p.NT, ak + (AB >> 4), bd + 2 * k, idesc, c > cb || k > 0, one);
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t ak = al + (KN ? (k * 2048) >> 4 : 2 * k);
+              tg_mma<CTAS>(d, ak, hi, bl + 2 * k, hi, idesc, k == 0 ? acc : 1u);
+              if (GATED) tg_mma<CTAS>(d + p.NT, ak + (AB >> 4), hi, bl + 2 * k, hi, idesc, k == 0 ? acc : 1u);
+            }
+            tg_commit<CTAS>(eb + 8 * s);
           }
-          tg_commit<CTAS>(&empty[s], one);
+          acc = 1;
+          st += st16;
           if (++s == (uint32_t)p.S) {
             s = 0;
             par ^= 1;
+            st = st0;
           }
         }
-        if (ok) tg_commit<CTAS>(&accf[b], one);
+        if (ok && elect_one()) tg_commit<CTAS>(smem_u32(&accf[b]));
       }
     }
     __syncwarp();
