@@ -280,6 +280,7 @@ template <int CTAS, int MODE, bool KN>
 __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
     gmm_tc_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mW3,
                   const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mXb, const TgArgs p) {
+  static_assert(MODE != TG_I8 || CTAS == 1, "the converters arrive on their own block's barriers");
   constexpr bool GATED = MODE == TG_GATED, I8 = MODE == TG_I8, F16 = MODE == TG_I8 || MODE == TG_F16;
   constexpr int EW = I8 ? 4 : 8;  // epilogue warps
   extern __shared__ uint8_t smraw[];
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
 
   if (tid == 0) {
     for (int s = 0; s < p.S; ++s) {
-      mbar_init(&full[s], I8 ? 4 * CTAS : 1);
+      mbar_init(&full[s], I8 ? 4 : 1);
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < p.SR; ++s) {
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
       const int xr = q.r0 + (int)rank * nl;  // this block's rows of x
       const bool big = nl > p.bxr;           // one copy of the whole region, or one small box
       const uint32_t xbytes = p.g.index ? (uint32_t)nl * 128u : (big ? NTl : (uint32_t)p.bxr) * 128u;
-      const uint32_t tx = ((GATED ? 2 : 1) * AB + xbytes) * (I8 ? 1 : CTAS);
+      const uint32_t tx = ((GATED ? 2 : 1) * AB + xbytes) * CTAS;
       int gy[2][4];
       if (xside && p.g.index) {
 #pragma unroll
@@ -420,26 +421,26 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
           break;
         }
         const uint32_t st = base + s * st_bytes;
-        // a pair's 16-bit stages complete on the first block's barrier
-        const uint32_t bar = CTAS == 2 && !I8 ? cluster_map(smem_u32(&fb[s]), 0) : smem_u32(&fb[s]);
+        // a pair's stages complete on the first block's barrier
+        const uint32_t bar = CTAS == 2 ? cluster_map(smem_u32(&fb[s]), 0) : smem_u32(&fb[s]);
         if (!xside) {
           if (lane == 0) {
-            if (I8 || rank == 0) mbar_arrive_expect_tx(&fb[s], tx);
+            if (rank == 0) mbar_arrive_expect_tx(&fb[s], tx);
             if constexpr (KN) {
-              tma_w3d<I8 ? 1 : CTAS>(st, &mW, nb, c * KW, q.e, bar);
-              tma_w3d<I8 ? 1 : CTAS>(st + AB / 2, &mW, nb + 64, c * KW, q.e, bar);
+              tma_w3d<CTAS>(st, &mW, nb, c * KW, q.e, bar);
+              tma_w3d<CTAS>(st + AB / 2, &mW, nb + 64, c * KW, q.e, bar);
             } else {
-              tma_w3d<I8 ? 1 : CTAS>(st, &mW, c * KW, nb, q.e, bar);
+              tma_w3d<CTAS>(st, &mW, c * KW, nb, q.e, bar);
             }
-            if (GATED) tma_w3d<I8 ? 1 : CTAS>(st + AB, &mW3, c * KW, nb, q.e, bar);
+            if (GATED) tma_w3d<CTAS>(st + AB, &mW3, c * KW, nb, q.e, bar);
           }
         } else {
           const uint32_t bst = st + (GATED ? 2 : 1) * AB;
           if (p.g.index) {
-            if (lane < nl / 4) tma_gather4<I8 ? 1 : CTAS>(bst + lane * 512u, &mX, c * KW, gy[0], bar);
-            if (lane + 32 < nl / 4) tma_gather4<I8 ? 1 : CTAS>(bst + (lane + 32) * 512u, &mX, c * KW, gy[1], bar);
+            if (lane < nl / 4) tma_gather4<CTAS>(bst + lane * 512u, &mX, c * KW, gy[0], bar);
+            if (lane + 32 < nl / 4) tma_gather4<CTAS>(bst + (lane + 32) * 512u, &mX, c * KW, gy[1], bar);
           } else if (lane == 0) {
-            tma_x2d<I8 ? 1 : CTAS>(bst, big ? &mXb : &mX, c * KW, xr, bar);
+            tma_x2d<CTAS>(bst, big ? &mXb : &mX, c * KW, xr, bar);
           }
         }
         if (++s == (uint32_t)S) {
@@ -449,7 +450,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
       }
     }
     // after a failed wait copies may still be in flight: let them land before the block ends
-    if (!ok && lane == 0 && (I8 || rank == 0))
+    if (!ok && lane == 0 && rank == 0)
       for (int i = 0; i < S && (uint32_t)i < it; ++i) {
         const uint32_t use = (it - 1 - i) / S;
         mbar_wait_drain(&fb[i], use & 1, TG_TIMEOUT_NS);
@@ -476,7 +477,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
         const uint32_t d = tmem + b * (uint32_t)((GATED ? 2 : 1) * p.NT);
         uint32_t acc = 0;
         for (int c = cb; c < ce; ++c) {
-          if (!__all_sync(0xffffffffu, tg_wait<I8 && CTAS == 2>(full + s, par, abort_flag, p.err))) {
+          if (!__all_sync(0xffffffffu, tg_wait<false>(full + s, par, abort_flag, p.err))) {
             ok = false;
             break;
           }
@@ -571,10 +572,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-          if (CTAS == 2)
-            arrive_remote(cluster_map(smem_u32(&full[s]), 0));
-          else
-            mbar_arrive(&full[s]);
+          mbar_arrive(&full[s]);
           mbar_arrive(&rempty[rs]);
           if (half == 0 && c == n - 1) mbar_arrive(&rempty[rs]);  // no second half: its arrival as well
         }
@@ -844,8 +842,7 @@ cudaError_t tg_go(const CUtensorMap& mW, const CUtensorMap& mW3, const CUtensorM
     // chunks at least.
     const int busy = std::min(a.E, a.R);
     const long long tiles = (long long)p.MT * busy * (((a.R + busy - 1) / busy + p.NT - 1) / p.NT);
-    const int most_cut = std::getenv("SFFN_KS") ? std::atoi(std::getenv("SFFN_KS")) : 8;
-    for (int k = 2; k <= std::min(most_cut, (p.KC + 1) / 8); ++k)
+    for (int k = 2; k <= std::min(8, (p.KC + 1) / 8); ++k)
       if (clusters[k] >= tiles) c = k;
   }
   p.ks = CTAS == 1 ? c : 1;
@@ -895,8 +892,7 @@ cudaError_t launch_gmm_tc(const GmmArgs& a, int ctas, int nt, cudaStream_t s) {
   const size_t smem = fixed + (size_t)(p.S + p.SR) * st;
   const int sms = ops_num_sms();
   if (a.i8)
-    return ctas == 2 ? tg_go<2, TG_I8, false>(mW, mW3, mX, mXb, p, smem, sms, s)
-                     : tg_go<1, TG_I8, false>(mW, mW3, mX, mXb, p, smem, sms, s);
+    return tg_go<1, TG_I8, false>(mW, mW3, mX, mXb, p, smem, sms, s);
   if (a.f16) return tg_go<2, TG_F16, false>(mW, mW3, mX, mXb, p, smem, sms, s);
   if (gated)
     return ctas == 2 ? tg_go<2, TG_GATED, false>(mW, mW3, mX, mXb, p, smem, sms, s)
@@ -932,20 +928,21 @@ __global__ void __launch_bounds__(256) widen_kernel(const uint8_t* __restrict__ 
   }
 }
 
-// Rows per expert from which fp16 copies pay.
-constexpr int TG_WIDE_ROWS = 768;
-int wide_rows() { const char* v = std::getenv("SFFN_WIDE"); return v ? std::atoi(v) : TG_WIDE_ROWS; }
+// Rows per expert from which fp16 copies of the codes, made once, pay for 256-row pair tiles (us, N = 14336, K = 4096,
+// widened in flight / copies: 640 rows 91 / 98, 768 rows 110 / 103, 2048 rows 248 / 159).
+constexpr int TG_WIDE_ROWS = 704;
 
-bool wide(int R, int E, int i8) { return i8 && R / E >= wide_rows(); }
+bool wide(int R, int E, int i8) { return i8 && R / E >= TG_WIDE_ROWS; }
 
 size_t gmm_workspace(int R, int XR, int N, int K, int E, int i8) {
   return wide(R, E, i8) ? 2 * ((size_t)XR * K + (size_t)E * N * K) : 0;
 }
 
 cudaError_t launch_gmm(const GmmArgs& a, cudaStream_t s) {
-  if (const char* v = std::getenv("SFFN_GMM_TUNE")) {
+  const char* tune = std::getenv("SFFN_GMM_TUNE");
+  if (tune) {
     int c = 0, n = 0;
-    if (std::sscanf(v, "%d,%d", &c, &n) == 2 && c > 0) return launch_gmm_tc(a, c, n, s);
+    if (std::sscanf(tune, "%d,%d", &c, &n) == 2 && c > 0) return launch_gmm_tc(a, c, n, s);
     return launch_gmm_rows(a, s);
   }
   const int busy = std::min(a.E, a.R);
@@ -964,9 +961,11 @@ cudaError_t launch_gmm(const GmmArgs& a, cudaStream_t s) {
     return launch_gmm_tc(b, 2, 256, s);
   }
   if (a.w3) return a.R >= 128 * busy ? launch_gmm_tc(a, 2, 256, s) : launch_gmm_tc(a, 1, 128, s);
-  if (a.R < 16 || (a.i8 && a.R <= 4 * busy)) return launch_gmm_rows(a, s);
-  if (a.R >= 96 * busy) return launch_gmm_tc(a, 2, 256, s);
-  return launch_gmm_tc(a, 1, 128, s);
+  if (a.i8) return a.R <= std::max(a.E, 4) ? launch_gmm_rows(a, s) : launch_gmm_tc(a, 1, 128, s);
+  // A pair's 256 x 256 tiles from 96 rows a group on, where they fill the SMs (us, 128 x 128 / pair tiles; 64 experts, N =
+  // 1024, K = 2560: 64 rows each 63 / 65, 96 72 / 68, 256 102 / 83; one, N = K = 4096: 256 rows 17 / 24, 512 19 / 24).
+  const long long pairs = (long long)((a.N + 255) / 256) * busy * (((a.R + busy - 1) / busy + 255) / 256);
+  return a.R >= 96 * busy && 2 * pairs >= ops_num_sms() ? launch_gmm_tc(a, 2, 256, s) : launch_gmm_tc(a, 1, 128, s);
 }
 
 }  // namespace sffn
