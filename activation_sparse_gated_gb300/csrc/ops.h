@@ -19,6 +19,7 @@ struct RouteArgs {
   float* weights;
   int *ids, *offsets, *rows, *hist;
   int T, E, k, bf16, sigmoid, normalize;
+  int vec;  // rows of logits are 16-byte aligned
 };
 size_t route_workspace(int T, int E, int k);
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t s);

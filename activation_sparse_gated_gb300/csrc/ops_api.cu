@@ -114,6 +114,7 @@ int sffn_route(const void* logits, long long ld, float* weights, int* ids, int* 
   a.bf16 = dtype == SFFN_BF16;
   a.sigmoid = (flags & SFFN_ROUTE_SIGMOID) != 0;
   a.normalize = (flags & SFFN_ROUTE_NORMALIZE) != 0;
+  a.vec = !misaligned(logits, 16) && ld * (a.bf16 ? 2 : 4) % 16 == 0;
   const cudaError_t e = launch_route(a, s);
   return e == cudaSuccess ? SFFN_OK : cuda_fail("sffn_route", e);
 }

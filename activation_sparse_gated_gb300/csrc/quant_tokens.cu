@@ -11,6 +11,8 @@
 // few units in the last place, below 1e-4 for quotients up to 127, so it gives
 // the same code unless it lies that near a half, and only then is the quotient
 // taken.
+#include <algorithm>
+
 #include "common.cuh"
 #include "ops.h"
 
@@ -33,80 +35,90 @@ __device__ __forceinline__ uint32_t fast_codes(uint32_t w, float inv, float* far
 }
 
 // NT threads, V 16-byte pieces a thread in registers, or (V = 0) one value at a
-// time from memory twice (rows that are not 16-byte aligned, or longer).
+// time from memory twice (rows that are not 16-byte aligned, or longer).  A
+// block walks tokens gridDim.x apart and requests the next one's pieces before
+// it works on this one's.
 template <int NT, int V>
 __global__ void __launch_bounds__(NT) quantize_tokens_kernel(const uint16_t* __restrict__ x, long long ld,
                                                              int8_t* __restrict__ q, float* __restrict__ sc, int T,
                                                              int K) {
-  __shared__ uint32_t s_max[NT / 32];
-  const int tid = threadIdx.x, t = blockIdx.x;
+  __shared__ uint32_t s_max[2][NT / 32];
+  const int tid = threadIdx.x, n = K / 8;
   pdl_launch_dependents();
   pdl_wait();
-  const uint16_t* row = x + (size_t)t * ld;
-  int8_t* out = q + (size_t)t * K;
-  uint4 c[V > 0 ? V : 1];
-  uint32_t m = 0;  // the largest |x| as bits: ordered like the values, NaN above infinity
-  if constexpr (V > 0) {
-    const int n = K / 8;
+  uint4 c[V > 0 ? V : 1], next[V > 0 ? V : 1];
+  auto load = [&](int t, uint4* to) {
+    const uint4* row = reinterpret_cast<const uint4*>(x + (size_t)t * ld);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int at = tid + i * NT;
-      c[i] = at < n ? reinterpret_cast<const uint4*>(row)[at] : make_uint4(0, 0, 0, 0);
+      to[i] = at < n ? __ldcs(row + at) : make_uint4(0, 0, 0, 0);
     }
+  };
+  if constexpr (V > 0) load(blockIdx.x, next);
+  int turn = 0;
+  for (int t = blockIdx.x; t < T; t += gridDim.x, turn ^= 1) {
+    const uint16_t* row = x + (size_t)t * ld;
+    int8_t* out = q + (size_t)t * K;
+    uint32_t m = 0;  // the largest |x| as bits: ordered like the values, NaN above infinity
+    if constexpr (V > 0) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+      for (int i = 0; i < V; ++i) c[i] = next[i];
+      if (t + gridDim.x < T) load(t + gridDim.x, next);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) m = max(m, max((w[j] << 16) & 0x7fffffffu, w[j] & 0x7fff0000u));
-    }
-  } else {
-    for (int i = tid; i < K; i += NT) m = max(m, ((uint32_t)row[i] << 16) & 0x7fffffffu);
-  }
-  m = __reduce_max_sync(0xffffffffu, m);
-  if ((tid & 31) == 0) s_max[tid >> 5] = m;
-  __syncthreads();
-  m = s_max[0];
+      for (int i = 0; i < V; ++i) {
+        const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
 #pragma unroll
-  for (int w = 1; w < NT / 32; ++w) m = max(m, s_max[w]);
-  const bool bad = m >= 0x7f800000u;
-  const float s = bad ? __uint_as_float(0x7fc00000u) : __fdiv_rn(__uint_as_float(m), 127.f);
-  if (tid == 0) sc[t] = s;
-  const bool zero = bad || s == 0.f;
-  const float inv = __fdiv_rn(1.f, s);
-  const bool tiny = !zero && !(s > 1e-30f && s < 1e30f);
-  if constexpr (V > 0) {
-    const int n = K / 8;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int at = tid + i * NT;
-      if (at >= n) continue;
-      const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
-      uint32_t o[2] = {0, 0};
-      float far = 0.f;
-      if (!zero) {
-        o[0] = fast_codes(w[0], inv, &far) | (fast_codes(w[1], inv, &far) << 16);
-        o[1] = fast_codes(w[2], inv, &far) | (fast_codes(w[3], inv, &far) << 16);
+        for (int j = 0; j < 4; ++j) m = max(m, max((w[j] << 16) & 0x7fffffffu, w[j] & 0x7fff0000u));
       }
-      if (!(far < 0.4999f) || tiny) {  // near a half (or 1 / s is no number): by the quotients
-        o[0] = o[1] = 0;
+    } else {
+      for (int i = tid; i < K; i += NT) m = max(m, ((uint32_t)row[i] << 16) & 0x7fffffffu);
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((tid & 31) == 0) s_max[turn][tid >> 5] = m;
+    __syncthreads();
+    m = s_max[turn][0];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t lo = (uint32_t)code_of(__uint_as_float(w[j] << 16), s) & 0xffu;
-          const uint32_t hi = (uint32_t)code_of(__uint_as_float(w[j] & 0xffff0000u), s) & 0xffu;
-          o[j >> 1] |= (lo | (hi << 8)) << (16 * (j & 1));
+    for (int w = 1; w < NT / 32; ++w) m = max(m, s_max[turn][w]);
+    const bool bad = m >= 0x7f800000u;
+    const float s = bad ? __uint_as_float(0x7fc00000u) : __fdiv_rn(__uint_as_float(m), 127.f);
+    if (tid == 0) sc[t] = s;
+    const bool zero = bad || s == 0.f;
+    const float inv = __fdiv_rn(1.f, s);
+    const bool tiny = !zero && !(s > 1e-30f && s < 1e30f);
+    if constexpr (V > 0) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int at = tid + i * NT;
+        if (at >= n) continue;
+        const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+        uint32_t o[2] = {0, 0};
+        float far = 0.f;
+        if (!zero) {
+          o[0] = fast_codes(w[0], inv, &far) | (fast_codes(w[1], inv, &far) << 16);
+          o[1] = fast_codes(w[2], inv, &far) | (fast_codes(w[3], inv, &far) << 16);
         }
+        if (!(far < 0.4999f) || tiny) {  // near a half (or 1 / s is no number): by the quotients
+          o[0] = o[1] = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t lo = (uint32_t)code_of(__uint_as_float(w[j] << 16), s) & 0xffu;
+            const uint32_t hi = (uint32_t)code_of(__uint_as_float(w[j] & 0xffff0000u), s) & 0xffu;
+            o[j >> 1] |= (lo | (hi << 8)) << (16 * (j & 1));
+          }
+        }
+        __stcs(reinterpret_cast<uint2*>(out) + at, make_uint2(o[0], o[1]));
       }
-      reinterpret_cast<uint2*>(out)[at] = make_uint2(o[0], o[1]);
+    } else {
+      for (int i = tid; i < K; i += NT)
+        out[i] = zero ? 0 : (int8_t)code_of(__uint_as_float((uint32_t)row[i] << 16), s);
     }
-  } else {
-    for (int i = tid; i < K; i += NT)
-      out[i] = zero ? 0 : (int8_t)code_of(__uint_as_float((uint32_t)row[i] << 16), s);
   }
 }
 
 template <int NT, int V>
 cudaError_t go(const void* x, long long ld, int8_t* q, float* sc, int T, int K, cudaStream_t s) {
-  return ops_launch(quantize_tokens_kernel<NT, V>, dim3((unsigned)T), NT, 0, s, 1, (const uint16_t*)x, ld, q, sc, T, K);
+  return ops_launch(quantize_tokens_kernel<NT, V>, dim3((unsigned)std::min(T, 2048 / NT * ops_num_sms())), NT, 0, s, 1, (const uint16_t*)x, ld, q, sc, T, K);
 }
 
 }  // namespace

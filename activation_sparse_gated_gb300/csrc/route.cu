@@ -41,7 +41,7 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 // exp(v - m) for v <= m, with equal infinities counting as equal
 __device__ __forceinline__ float exp_below(float v, float m) { return v == m ? 1.f : expf(v - m); }
 
-// A lane's logits e = lane + 32 i as keys, sorted once (up to 8 of them); then a round looks at the lanes' firsts alone and the
+// A lane's logits as keys, sorted once (up to 8 of them); then a round looks at the lanes' firsts alone and the
 // winner's list moves up.  hi orders, lo says which: the larger lo is the lower index.
 //   bf16 (and E <= 65535): value and index fit one word, so a round is one redux;
 //   fp32: the value, then the index among the lanes that hold it.
@@ -49,19 +49,49 @@ template <int L, bool BF16>
 struct Keys {
   uint32_t hi[L], lo[BF16 ? 1 : L];
 
+  // A lane holds V neighbouring logits at a time, one load of them where rows are aligned to it (a.vec).
+  static constexpr int V = L < (BF16 ? 8 : 4) ? L : (BF16 ? 8 : 4);
+
   __device__ __forceinline__ void load(const RouteArgs& a, size_t base, int lane) {
+    constexpr int EB = BF16 ? 2 : 4;
+    const uint8_t* row = reinterpret_cast<const uint8_t*>(a.logits) + base * EB;
 #pragma unroll
-    for (int i = 0; i < L; ++i) {
-      const int e = lane + 32 * i;
-      float v = -INFINITY;
-      if (e < a.E)
-        v = BF16 ? __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(a.logits)[base + e] << 16)
-                 : reinterpret_cast<const float*>(a.logits)[base + e];
-      hi[i] = order_key(v);
-      if (BF16) {
-        if (hi[i]) hi[i] = (hi[i] & 0xffff0000u) | (uint32_t)(0xffff - e);  // a bf16 value's low half is all ones or zeros
-      } else {
-        lo[i] = ~(uint32_t)e;
+    for (int c = 0; c < L / V; ++c) {
+      const int e0 = (c * 32 + lane) * V;
+      uint32_t raw[V * EB >= 4 ? V * EB / 4 : 1] = {};
+      const bool one = a.vec && e0 + V <= a.E;
+      if (one) {
+        if constexpr (V * EB == 16) {
+          const uint4 v = *reinterpret_cast<const uint4*>(row + (size_t)e0 * EB);
+          raw[0] = v.x;
+          raw[1] = v.y;
+          raw[2] = v.z;
+          raw[3] = v.w;
+        } else if constexpr (V * EB == 8) {
+          const uint2 v = *reinterpret_cast<const uint2*>(row + (size_t)e0 * EB);
+          raw[0] = v.x;
+          raw[1] = v.y;
+        } else if constexpr (V * EB == 4) {
+          raw[0] = *reinterpret_cast<const uint32_t*>(row + (size_t)e0 * EB);
+        } else {
+          raw[0] = *reinterpret_cast<const uint16_t*>(row + (size_t)e0 * EB);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int i = c * V + j, e = e0 + j;
+        float v = -INFINITY;
+        if (one)
+          v = BF16 ? __uint_as_float((j & 1) ? raw[j / 2] & 0xffff0000u : raw[j / 2] << 16) : __uint_as_float(raw[BF16 ? 0 : j]);
+        else if (e < a.E)
+          v = BF16 ? __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(row)[e] << 16)
+                   : reinterpret_cast<const float*>(row)[e];
+        hi[i] = order_key(v);
+        if (BF16) {
+          if (hi[i]) hi[i] = (hi[i] & 0xffff0000u) | (uint32_t)(0xffff - e);  // a bf16 value's low half is all ones or zeros
+        } else {
+          lo[i] = ~(uint32_t)e;
+        }
       }
     }
   }
