@@ -126,15 +126,15 @@ struct Keys {
     }
     hi[L - 1] = 0;
   }
-  // the largest key of the warp (0: none is open), and its index; the lane that holds it drops it
-  __device__ __forceinline__ uint32_t next(int* e) {
+  // The largest key of the warp (0: none is open) and, for fp32, the low word that says whose it is; the lane that
+  // holds it drops it.
+  __device__ __forceinline__ uint32_t next(uint32_t* low) {
     uint32_t top = hi[0];
     if (!SORTED) {
 #pragma unroll
       for (int i = 1; i < L; ++i) top = max(top, hi[i]);
     }
     const uint32_t best = __reduce_max_sync(0xffffffffu, top);
-    if (best == 0) return 0;
     if (BF16) {
       if (SORTED) {
         if (top == best) pop();
@@ -142,16 +142,14 @@ struct Keys {
 #pragma unroll
         for (int i = 0; i < L; ++i) hi[i] = hi[i] == best ? 0u : hi[i];
       }
-      *e = 0xffff - (int)(best & 0xffffu);
-      // the low half of the value: zeros, or ones where the key is complemented (a negative value)
-      return (best & 0x80000000u) ? best & 0xffff0000u : best | 0xffffu;
+      return best;
     }
     uint32_t mine = top == best ? lo[0] : 0u;
     if (!SORTED) {
       mine = 0;
 #pragma unroll
       for (int i = L - 1; i >= 0; --i)
-        if (hi[i] == best) mine = lo[i];  // the lowest index last
+        if (hi[i] == best) mine = max(mine, lo[i]);
     }
     const uint32_t at = __reduce_max_sync(0xffffffffu, mine);
     if (SORTED) {
@@ -160,8 +158,15 @@ struct Keys {
 #pragma unroll
       for (int i = 0; i < L; ++i) hi[i] = lo[i] == at ? 0u : hi[i];
     }
-    *e = (int)~at;
+    *low = at;
     return best;
+  }
+  // a bf16 key's low half holds the index: the value's was zeros, or ones where the key is complemented (negative)
+  static __device__ __forceinline__ float value(uint32_t key) {
+    return key_value(!BF16 ? key : (key & 0x80000000u) ? key & 0xffff0000u : key | 0xffffu);
+  }
+  static __device__ __forceinline__ int index(uint32_t key, uint32_t low) {
+    return BF16 ? 0xffff - (int)(key & 0xffffu) : (int)~low;
   }
 };
 
@@ -170,34 +175,32 @@ template <int L, bool BF16>
 __device__ __forceinline__ int choose(const RouteArgs& a, int t, int lane) {
   Keys<L, BF16> keys;
   keys.load(a, (size_t)t * a.ld, lane);
-  float all = 0.f, m = 0.f;
+  float all = 0.f;
   if (!a.sigmoid && !a.normalize) {  // the sum over every open expert
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < L; ++i) top = max(top, keys.hi[i]);
-    top = __reduce_max_sync(0xffffffffu, top);
-    auto value = [](uint32_t k) { return key_value(!BF16 ? k : (k & 0x80000000u) ? k & 0xffff0000u : k | 0xffffu); };
-    const float mx = value(top);
+    const float mx = keys.value(__reduce_max_sync(0xffffffffu, top));
 #pragma unroll
     for (int i = 0; i < L; ++i)
-      if (keys.hi[i]) all += exp_below(value(keys.hi[i]), mx);
+      if (keys.hi[i]) all += exp_below(keys.value(keys.hi[i]), mx);
     all = warp_sum(all);
   }
   keys.sort();
-  uint32_t ck = 0;
-  int ce = -1;
+  uint32_t ck = 0, cl = 0;
   for (int j = 0; j < a.k; ++j) {
-    int e = 0;
-    const uint32_t best = keys.next(&e);
+    uint32_t low = 0;
+    const uint32_t best = keys.next(&low);
     if (best == 0) break;  // no open expert is left
-    if (j == 0) m = key_value(best);
     if (lane == j) {
       ck = best;
-      ce = e;
+      cl = low;
     }
   }
+  const int ce = ck ? keys.index(ck, cl) : -1;
+  const float m = keys.value(__shfl_sync(0xffffffffu, ck, 0)), v = keys.value(ck);
   float w = 0.f;
-  if (ce >= 0) w = a.sigmoid ? 1.f / (1.f + expf(-key_value(ck))) : exp_below(key_value(ck), m);
+  if (ce >= 0) w = a.sigmoid ? 1.f / (1.f + expf(-v)) : exp_below(v, m);
   float total = 1.f;
   if (a.normalize) total = warp_sum(w);
   else if (!a.sigmoid) total = all;
@@ -223,22 +226,29 @@ __device__ __forceinline__ void choose_block(const RouteArgs& a, int t0, int t1,
 
 // Grouped rows of this block's choices, given s_base[e] = the row of its first
 // choice of expert e.  Warps take consecutive spans of choices; s_cnt[w][e]
-// counts span w, and the spans before a warp's own give its first row.
+// (zero before) counts span w, and the spans before a warp's own give its first
+// row.
 __device__ __forceinline__ void scatter_block(const RouteArgs& a, int t0, int t1, const int* s_base, int* s_cnt,
                                               int warps) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int p0 = t0 * a.k, n = (t1 - t0) * a.k;
   const int span = ((n + warps - 1) / warps + 31) / 32 * 32;
-  for (int i = threadIdx.x; i < warps * a.E; i += ROUTE_THREADS) s_cnt[i] = 0;
-  __syncthreads();
   const int b = min(n, warp * span), c = warp < warps ? min(n, b + span) : b;
-  for (int i = b + lane; i < c; i += 32) {
+  constexpr int KEEP = 4;  // the span's first choices stay in registers
+  int kept[KEEP];
+#pragma unroll
+  for (int q = 0; q < KEEP; ++q) kept[q] = b + 32 * q + lane < c ? a.ids[p0 + b + 32 * q + lane] : -1;
+#pragma unroll
+  for (int q = 0; q < KEEP; ++q)
+    if (kept[q] >= 0) atomicAdd(&s_cnt[warp * a.E + kept[q]], 1);
+  for (int i = b + 32 * KEEP + lane; i < c; i += 32) {
     const int e = a.ids[p0 + i];
     if (e >= 0) atomicAdd(&s_cnt[warp * a.E + e], 1);
   }
   __syncthreads();
   for (int e = threadIdx.x; e < a.E; e += ROUTE_THREADS) {
     int at = s_base[e];
+#pragma unroll 4
     for (int w = 0; w < warps; ++w) {
       const int v = s_cnt[w * a.E + e];
       s_cnt[w * a.E + e] = at;
@@ -246,19 +256,17 @@ __device__ __forceinline__ void scatter_block(const RouteArgs& a, int t0, int t1
     }
   }
   __syncthreads();
-  for (int i0 = b; i0 < c; i0 += 32) {
-    const int i = i0 + lane;
-    const int e = i < c ? a.ids[p0 + i] : -1;
+  auto place = [&](int i0, int e) {
     const uint32_t same = __match_any_sync(0xffffffffu, e);
-    if (e >= 0) {
-      const int rank = __popc(same & ((1u << lane) - 1));
-      const int at = s_cnt[warp * a.E + e] + rank;
-      a.rows[at] = p0 + i;
-    }
+    if (e >= 0) a.rows[s_cnt[warp * a.E + e] + __popc(same & ((1u << lane) - 1))] = p0 + i0 + lane;
     __syncwarp();
     if (e >= 0 && (same >> lane) == 1u) s_cnt[warp * a.E + e] += __popc(same);  // the last lane of its expert
     __syncwarp();
-  }
+  };
+#pragma unroll
+  for (int q = 0; q < KEEP; ++q)
+    if (b + 32 * q < c) place(b + 32 * q, kept[q]);
+  for (int i0 = b + 32 * KEEP; i0 < c; i0 += 32) place(i0, i0 + lane < c ? a.ids[p0 + i0 + lane] : -1);
 }
 
 // Exclusive sums of s_v[0 .. E) into s_v, the total in s_v[E] (whole block).
@@ -295,6 +303,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS) route_one_kernel(const RouteArg
   int* s_base = sm;               // [E + 1]
   int* s_w = s_base + a.E + 1;    // [ROUTE_WARPS]
   int* s_cnt = s_w + ROUTE_WARPS; // [warps][E]
+  for (int i = threadIdx.x; i < warps * a.E; i += ROUTE_THREADS) s_cnt[i] = 0;
   pdl_launch_dependents();
   pdl_wait();
   choose_block<L, BF16>(a, 0, a.T, s_base);
@@ -337,18 +346,24 @@ __global__ void __launch_bounds__(ROUTE_THREADS) route_group_kernel(const RouteA
   int* s_mine = s_w + ROUTE_WARPS;  // [E] choices of the chunks before this one
   int* s_cnt = s_mine + a.E;
   for (int e = threadIdx.x; e < a.E; e += ROUTE_THREADS) s_mine[e] = s_base[e] = 0;
+  for (int i = threadIdx.x; i < warps * a.E; i += ROUTE_THREADS) s_cnt[i] = 0;
   pdl_launch_dependents();
   pdl_wait();
   __syncthreads();
   // several threads an expert where there are few: each sums every `stride`-th chunk
-  const int cols = min((a.E + 31) / 32 * 32, ROUTE_THREADS), stride = ROUTE_THREADS / cols, first = threadIdx.x / cols;
-  for (int e = threadIdx.x % cols; e < a.E && first < stride; e += cols) {
+  const int cols = min((a.E + 31) / 32 * 32, ROUTE_THREADS), stride = ROUTE_THREADS / cols, from = threadIdx.x / cols;
+  for (int e = threadIdx.x % cols; e < a.E && from < stride; e += cols) {
     int before = 0, total = 0;
-#pragma unroll 16
-    for (int b = first; b < nb; b += stride) {
-      const int v = a.hist[(size_t)b * a.E + e];
-      if (b < (int)blockIdx.x) before += v;
-      total += v;
+    constexpr int B = 32;  // counts in flight
+    for (int b0 = from; b0 < nb; b0 += B * stride) {
+      int v[B];
+#pragma unroll
+      for (int i = 0; i < B; ++i) v[i] = b0 + i * stride < nb ? a.hist[(size_t)(b0 + i * stride) * a.E + e] : 0;
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        if (b0 + i * stride < (int)blockIdx.x) before += v[i];
+        total += v[i];
+      }
     }
     atomicAdd(&s_mine[e], before);
     atomicAdd(&s_base[e], total);
