@@ -7,26 +7,43 @@
 //
 // The weights are the M side of the MMA (128 rows of w a block, 256 a pair of
 // blocks with cta_group::2) and the rows of x the N side, whose width is any
-// multiple of 16 (32 for a pair): a group of 5 rows costs 16 columns, one of
-// 130 costs 144 or two tiles of 80, so ragged groups waste little.  A block
-// walks the tiles of all groups (persistent, tile ids strided by the grid); the
-// tile list is a prefix sum over the groups that every block makes for itself
-// from the device's offsets, so the host never waits for them.  One warp feeds
-// a ring of shared stages by TMA, one thread issues the MMAs, four warps empty
-// one of two TMEM accumulators while the MMAs fill the other.
+// multiple of 16 (32 for a pair) up to 256: a ragged group reads no more rows
+// than it has.  An MMA of 16 K values takes about 130 cycles whatever its width
+// (measured: a 64-wide chunk about 550 at 16 to 128 columns, one block), so full
+// tensor rate wants 256 columns, and 128 x 16 weights per 130 cycles and SM are
+// still above the memory's rate, which is what bounds short groups.
+//
+// A block walks the tiles of all groups (persistent, tile ids strided by the
+// grid); the tile list is a prefix sum over the groups that every block makes
+// for itself from the device's offsets, so the host never waits for them.  Two
+// warps feed a ring of shared stages by TMA (one the weights, one the rows of x:
+// a single one is too slow for 128-wide tiles), one warp issues the MMAs, and
+// eight empty one TMEM accumulator while the MMAs fill the other.  Tiles are
+// taken eight weight tiles at a time over a group's rows (1, 2 and 4 or 32 and
+// 64 are up to 5 and 15 % slower at 8192 x 14336 x 4096: L2).
 //
 // Rows of x come as 2D tiles, or, through an index, by gather4 (four rows a
-// copy), so the grouped copy of x is never made.
+// copy), so a grouped copy of x need not be made.
 //
 // int8: this part's int8 MMA rate is far below its 16-bit rate, and int8 codes are
 // exact in fp16 with exact products and fp32 sums that are exact below 2^24.  So
-// the raw codes arrive by TMA and eight warps widen them into the fp16 operand
-// tiles: half the memory traffic of 16-bit weights at the 16-bit MMA's rate.
+// the raw codes arrive by TMA and sixteen warps widen them into the fp16 operand
+// tiles: half the memory traffic of 16-bit weights.  Widening and the exchange
+// around it cost a chunk as much again as its MMAs; where groups are long the
+// codes are widened once into fp16 copies instead (widen_kernel).
+//
+// Few tiles and a long sum: the blocks of a cluster cut K and add their partial
+// tiles through distributed shared memory in a fixed order.
+//
+// Measured (us; share of the copy rate / of cuBLAS's burst rate): bf16, 128 rows
+// over 64 experts of 1024 x 2560 44.6 (97 % / 1 %); 16384 ragged rows over 64
+// experts of 7168 x 2560 521 (76 % / 60 %); one group 8192 x 14336 x 4096 499
+// (- / 99 %); int8 8192 x 14336 x 4096 533 (- / 93 %, 40 of it the copies), 77 x
+// 2560 x 7168 15.5 (19 % / 9 %: latency of the chunks' chain and of the launch),
+// 4093 rows over 16 experts of 1000 x 2560 50 (18 % / 22 %: widening).
 #include <cudaTypedefs.h>
 
 #include <algorithm>
-#include <cstdio>
-#include <cstdlib>
 #include <mutex>
 
 #include "common.cuh"
@@ -45,6 +62,7 @@ constexpr int TG_CONV_WARPS = 16;
 constexpr int TG_THREADS = 384, TG_THREADS_I8 = 32 * (TG_CONV_WARP0 + TG_CONV_WARPS);
 constexpr uint64_t TG_TIMEOUT_NS = 250000000ull;
 constexpr size_t TG_SMEM = 227 * 1024;
+constexpr int TG_DEVICES = 64;
 // what a kernel multiplies: bf16; bf16 gate and up together; int8 codes widened in flight; fp16 copies of codes
 enum { TG_BF16, TG_GATED, TG_I8, TG_F16 };
 // the epilogue's shared scratch of a warp: 16 rows of 32 words, 4 words apart (no bank conflicts either way)
@@ -59,7 +77,7 @@ struct TgArgs {
   int bxr;     // rows of a small x box (no index); the large one has NT / CTAS
   int MT;      // weight tiles: ceil(N / (128 CTAS))
   int KC;      // 64-wide K chunks
-  int S;       // operand stages
+  int S;       // operand stages (int8: of widened codes)
   int SR;      // raw stages (int8)
   int ks;      // blocks of a cluster that cut K between them (1: no cut)
   int cols;    // TMEM columns allocated
@@ -809,10 +827,19 @@ cudaError_t tg_go(const CUtensorMap& mW, const CUtensorMap& mW3, const CUtensorM
                   TgArgs p, size_t smem, int sms, cudaStream_t s) {
   auto kernel = gmm_tc_kernel<CTAS, MODE, KN>;
   constexpr int threads = MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS;
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  static int clusters[9] = {};  // clusters that fit at once, by their blocks (a pair, or the cut of K)
-  std::call_once(once, [&] {
+  struct Setup {
+    std::once_flag once;
+    cudaError_t attr = cudaSuccess;
+    int clusters[9] = {};  // clusters that fit at once, by their blocks (a pair, or the cut of K)
+  };
+  static Setup setups[TG_DEVICES];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= TG_DEVICES) return cudaErrorInvalidDevice;
+  int (&clusters)[9] = setups[dev].clusters;
+  cudaError_t& attr = setups[dev].attr;
+  std::call_once(setups[dev].once, [&] {
     attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TG_SMEM);
     clusters[1] = sms;
     for (int c = 2; attr == cudaSuccess && c <= (CTAS == 2 ? 2 : 8); ++c) {
@@ -846,7 +873,6 @@ cudaError_t tg_go(const CUtensorMap& mW, const CUtensorMap& mW3, const CUtensorM
       if (clusters[k] >= tiles) c = k;
   }
   p.ks = CTAS == 1 ? c : 1;
-
   if (clusters[c] < 1) return cudaErrorInvalidConfiguration;
   const int n = (int)std::min<long long>(clusters[c], std::max(1ll, most));
   return ops_launch(kernel, dim3((unsigned)(n * c)), threads, smem, s, c, mW, mW3, mX, mXb, p);
@@ -865,7 +891,8 @@ cudaError_t launch_gmm_tc(const GmmArgs& a, int ctas, int nt, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const size_t yb = a.y_f32 ? 4 : 2;
   p.vec = ((uintptr_t)a.y & 15) == 0 && a.ldy * yb % 16 == 0 && a.N * yb % 16 == 0;
-  const size_t fixed = (a.i8 ? 0 : 8 * TG_EPI_BYTES) + 1024 + 8 * (2 * 16 + 2 * 16 + 6) + 8 + sizeof(int) * 2 * (size_t)(a.E + 1) + 64;
+  const size_t fixed = (a.i8 ? 0 : 8 * TG_EPI_BYTES) + 1024 + 8 * (2 * 16 + 2 * 16 + 6) + 8 +
+                       sizeof(int) * 2 * (size_t)(a.E + 1) + 64;
   auto stage_bytes = [&] { return (gated ? 2u : 1u) * 16384u + (uint32_t)(p.NT / ctas + 7) / 8 * 1024u; };
   auto slots = [&] { return (int)((TG_SMEM - fixed) / stage_bytes()); };
   // int8: the converters' four groups need four operand stages and three raw ones
@@ -891,8 +918,7 @@ cudaError_t launch_gmm_tc(const GmmArgs& a, int ctas, int nt, cudaStream_t s) {
   }
   const size_t smem = fixed + (size_t)(p.S + p.SR) * st;
   const int sms = ops_num_sms();
-  if (a.i8)
-    return tg_go<1, TG_I8, false>(mW, mW3, mX, mXb, p, smem, sms, s);
+  if (a.i8) return tg_go<1, TG_I8, false>(mW, mW3, mX, mXb, p, smem, sms, s);
   if (a.f16) return tg_go<2, TG_F16, false>(mW, mW3, mX, mXb, p, smem, sms, s);
   if (gated)
     return ctas == 2 ? tg_go<2, TG_GATED, false>(mW, mW3, mX, mXb, p, smem, sms, s)
@@ -939,12 +965,6 @@ size_t gmm_workspace(int R, int XR, int N, int K, int E, int i8) {
 }
 
 cudaError_t launch_gmm(const GmmArgs& a, cudaStream_t s) {
-  const char* tune = std::getenv("SFFN_GMM_TUNE");
-  if (tune) {
-    int c = 0, n = 0;
-    if (std::sscanf(tune, "%d,%d", &c, &n) == 2 && c > 0) return launch_gmm_tc(a, c, n, s);
-    return launch_gmm_rows(a, s);
-  }
   const int busy = std::min(a.E, a.R);
   if (wide(a.R, a.E, a.i8) && a.workspace) {
     const long long nx = (long long)a.XR * (a.K / 16), nw = (long long)a.E * a.N * (a.K / 16);
@@ -960,6 +980,8 @@ cudaError_t launch_gmm(const GmmArgs& a, cudaStream_t s) {
     b.f16 = 1;
     return launch_gmm_tc(b, 2, 256, s);
   }
+  // Gate and up together: 256 rows a tile take all of TMEM, so their epilogue is not hidden, and still win from 128
+  // rows a group on (4096 tokens, 8 of 64 experts, D = 2560, H = 1024: 561 against 643 us; 512 tokens 225 / 211).
   if (a.w3) return a.R >= 128 * busy ? launch_gmm_tc(a, 2, 256, s) : launch_gmm_tc(a, 1, 128, s);
   if (a.i8) return a.R <= std::max(a.E, 4) ? launch_gmm_rows(a, s) : launch_gmm_tc(a, 1, 128, s);
   // A pair's 256 x 256 tiles from 96 rows a group on, where they fill the SMs (us, 128 x 128 / pair tiles; 64 experts, N =

@@ -310,6 +310,100 @@ def test_grouped_matmul_few_tiles_long_sums(counts, transposed):
         close(y[b[e]:b[e + 1]], xe @ we.T, K * 2.0 ** -23 * (xe.abs() @ we.abs().T))
 
 
+PAIRS = [130, 97, 256, 1, 0, 300, 64, 257, 100, 128, 200, 31, 180, 96, 0, 513, 140, 33, 128, 160]
+
+
+@pytest.mark.parametrize("N,K,out", [(1000, 136, "bf16"), (1001, 72, "f32"), (1003, 200, "bf16"), (2056, 64, "f32")])
+@pytest.mark.parametrize("transposed", [False, True])
+def test_grouped_matmul_long_ragged_groups(N, K, out, transposed):
+    """Groups long and many enough for tiles of a pair of blocks; odd widths take narrow stores."""
+    if transposed:
+        N = N // 8 * 8
+    g, R, E = gen(N), sum(PAIRS), len(PAIRS)
+    x = torch.randn(R, K, generator=g, device=DEV).to(BF)
+    w = torch.randn(E, N, K, generator=g, device=DEV).to(BF)
+    off = offsets_of(PAIRS)
+    wide = torch.full((R, N + 5), 3.0, device=DEV, dtype=BF if out == "bf16" else torch.float32)
+    y = sffn.grouped_matmul(x, w.transpose(1, 2).contiguous() if transposed else w, off, transposed=transposed,
+                            out=wide[:, 3:3 + N])
+    z = sffn.grouped_matmul(x, w.transpose(1, 2).contiguous() if transposed else w, off, transposed=transposed, dtype=out)
+    assert torch.equal(y, z)
+    assert (wide[:, :3] == 3).all() and (wide[:, 3 + N:] == 3).all()
+    b = off.tolist()
+    for e in range(E):
+        xe, we = x[b[e]:b[e + 1]].double(), w[e].double()
+        close(y[b[e]:b[e + 1]], xe @ we.T, K * 2.0 ** -23 * (xe.abs() @ we.abs().T))
+
+
+def test_grouped_matmul_long_groups_read_tokens_through_an_index():
+    g, T, k, E, N, K = gen(72), 1400, 2, 20, 1000, 136
+    routing = sffn.route(torch.randn(T, E, generator=g, device=DEV), k)
+    x = torch.randn(T, K, generator=g, device=DEV).to(BF)
+    w = torch.randn(E, N, K, generator=g, device=DEV).to(BF)
+    y = sffn.grouped_matmul(x, w, routing.offsets, index=routing.rows, index_div=k, dtype="f32")
+    z = sffn.grouped_matmul(x[(routing.rows // k).long()].contiguous(), w, routing.offsets, dtype="f32")
+    assert torch.equal(y, z)
+
+
+@pytest.mark.parametrize("counts", [[3, 0, 1, 2], [1] * 30, [0, 4], [2]], ids=str)
+@pytest.mark.parametrize("N,K", [(33, 48), (400, 1040), (6000, 256)])
+def test_grouped_matmul_int8_few_rows(counts, N, K):
+    """Groups of one to four rows: the dot products of four."""
+    g, R, E = gen(N + K), sum(counts), len(counts)
+    x, sx = int8_operands(g, R, K, full=True)
+    w, sw = int8_operands(g, E * N, K, full=True)
+    w, sw = w.view(E, N, K), sw.view(E, N)
+    off = offsets_of(counts)
+    y = sffn.grouped_matmul(x, w, off, sx=sx, sw=sw, dtype="f32")
+    b = off.tolist()
+    for e in range(E):
+        r = slice(b[e], b[e + 1])
+        scale = torch.outer(sx[r].double(), sw[e].double())
+        ref = (x[r].double() @ w[e].double().T) * scale
+        close(y[r], ref, 3 * 2.0 ** -24 * ref.abs() + int8_bound(x[r], w[e], scale))
+
+
+def test_grouped_matmul_past_32_bits():
+    """Weights, rows and results whose byte and element offsets pass 32 bits."""
+    g = gen(81)
+    E, N, K = 40, 7168, 8000  # 2.3e9 weights
+    w = torch.zeros(E, N, K, device=DEV, dtype=BF)
+    w[-1] = torch.randn(N, K, generator=g, device=DEV).to(BF)
+    x = torch.randn(20, K, generator=g, device=DEV).to(BF)
+    y = sffn.grouped_matmul(x, w, offsets_of([0] * (E - 1) + [20]), dtype="f32")
+    xe, we = x.double(), w[-1].double()
+    close(y, xe @ we.T, K * 2.0 ** -23 * (xe.abs() @ we.abs().T))
+    del w, we
+    R, N, K = 310000, 7168, 64  # 2.2e9 results
+    x = torch.randn(R, K, generator=g, device=DEV).to(BF)
+    w = torch.randn(1, N, K, generator=g, device=DEV).to(BF)
+    y = sffn.grouped_matmul(x, w, offsets_of([R]))
+    for r in (slice(0, 50), slice(R - 300, R)):
+        xe, we = x[r].double(), w[0].double()
+        close(y[r], xe @ we.T, K * 2.0 ** -23 * (xe.abs() @ we.abs().T))
+
+
+def test_two_streams_at_once():
+    """Calls that overlap on the GPU share nothing."""
+    g, E, N, K = gen(83), 6, 520, 512
+    x = torch.randn(600, K, generator=g, device=DEV).to(BF)
+    w = torch.randn(E, N, K, generator=g, device=DEV).to(BF)
+    q, sx = int8_operands(g, 600, K)
+    wq, sw = int8_operands(g, N, K)
+    off = offsets_of([100] * 6)
+    want = sffn.grouped_matmul(x, w, off), sffn.matmul_int8(q, sx, wq, sw), sffn.route(x[:, :64].float(), 4)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(8):
+        got.append((sffn.grouped_matmul(x, w, off, stream=a), sffn.matmul_int8(q, sx, wq, sw, stream=b),
+                    sffn.route(x[:, :64].float(), 4, stream=b)))
+    torch.cuda.synchronize()
+    for y, z, r in got:
+        assert torch.equal(y, want[0]) and torch.equal(z, want[1])
+        assert all(torch.equal(p, v) for p, v in zip(r, want[2]))
+
+
 @pytest.mark.parametrize("E", [200, 1000])
 def test_grouped_matmul_many_experts(E):
     """Tables of many groups, most of them empty or short."""
@@ -409,7 +503,7 @@ def check_experts(x, routing, W1, W3, W2t, act, y):
 
 @pytest.mark.parametrize("T,E,k,D,H", [(1, 1, 1, 8, 1), (1, 8, 2, 128, 100), (1, 64, 8, 2560, 1024), (2, 4, 3, 264, 65), (1, 4, 2, 22000, 20), (3, 4, 2, 6000, 24),
                                        (5, 16, 4, 384, 130), (33, 8, 2, 520, 200), (64, 64, 8, 256, 96),
-                                       (20, 2, 2, 136, 90), (2, 8, 8, 64, 2600), (200, 6, 2, 384, 257), (513, 5, 3, 256, 128), (300, 128, 4, 136, 72)])
+                                       (20, 2, 2, 136, 90), (2, 8, 8, 64, 2600), (200, 6, 2, 384, 257), (513, 5, 3, 256, 128), (300, 128, 4, 136, 72), (700, 4, 2, 200, 300), (130, 1, 1, 512, 1000)])
 @pytest.mark.parametrize("act", ["relu", "rsp", "silu"])
 def test_experts_forward(T, E, k, D, H, act):
     g = gen(T + D + H)
