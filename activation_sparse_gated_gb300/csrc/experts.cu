@@ -289,22 +289,23 @@ __global__ void __launch_bounds__(32 * EX_WARPS) experts_gather_kernel(const Exp
 
 size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
 
-// Few choices: the gate-first passes above; more: the grouped products on the tensor cores (k = 8 of 64 experts, D =
-// 2560, H = 1024, ReLU at 90 %: 85 against 121 us at 8 tokens, 139 against 145 at 16, 295 against 168 at 32).
-bool few(int T, int k) { return (long long)T * k <= 128; }
+// Up to two choices an expert: the gate-first passes above; more: the grouped products on the tensor cores (us, passes
+// / products, ReLU at 90 %, D = 2560, H = 1024: 8 of 64 experts 50 / 83 at 4 tokens, 79 / 101 at 8, 134 / 129 at 16; 2 of
+// 8 experts 31 / 38 at 8 tokens, 51 / 40 at 16; D = H = 4096, 4 of 16 experts 192 / 213 at 8, 328 / 256 at 16).
+bool few(int T, int k, int E) { return (long long)T * k <= 2ll * E; }
 
 }  // namespace
 
 size_t experts_workspace(int T, int k, int D, int H) {
   const size_t R = (size_t)T * k;
-  if (few(T, k)) return sizeof(float) * R * H;
   // h, the rows' products (before them, in the same place, the grouped tokens), and the choices' rows
-  return round_up(2 * R * round_up(H, 8), 256) + round_up(sizeof(float) * R * D, 256) + sizeof(int) * R;
+  const size_t products = round_up(2 * R * round_up(H, 8), 256) + round_up(sizeof(float) * R * D, 256) + sizeof(int) * R;
+  return std::max(products, sizeof(float) * R * H);  // the gate-first passes: h in fp32
 }
 
 cudaError_t launch_experts(const ExpertsArgs& a, cudaStream_t s) {
   cudaError_t e;
-  if (few(a.T, a.k)) {
+  if (few(a.T, a.k, a.E)) {
     float* h = static_cast<float*>(a.workspace);
     const dim3 grid((unsigned)((a.H + EG_WARPS - 1) / EG_WARPS), (unsigned)(a.T == 1 ? a.k : std::min(a.E, a.T * a.k)));
     const size_t row = 2 * (size_t)a.D;

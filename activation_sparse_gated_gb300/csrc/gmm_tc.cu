@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
   int* s_pre = s_off + p.g.E + 1;                  // [E + 1]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = CTAS == 2 ? cluster_rank() : 0;
-  const int ks = CTAS == 1 && !GATED ? p.ks : 1;
+  const int ks = CTAS == 1 ? p.ks : 1;
   const int kr = ks > 1 ? (int)cluster_rank() : 0;  // this block's share of K: chunks [cb, ce), whole pairs of them
   const int KP = (p.KC + 1) / 2, cb = 2 * (int)((long long)KP * kr / ks);
   const int ce = min(p.KC, 2 * (int)((long long)KP * (kr + 1) / ks));
@@ -611,17 +611,21 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
       const uint32_t ta = tmem + b * (uint32_t)((GATED ? 2 : 1) * p.NT) + ((uint32_t)(32 * (ew & 3)) << 16);
       const float sw = F16 && nok ? p.g.sw[(size_t)q.e * p.g.N + n] : 0.f;
       const int rows = q.r1 - q.r0;
-      if (CTAS == 1 && !GATED && ks > 1) {
+      if (CTAS == 1 && ks > 1) {
         // K is cut over the cluster: every block leaves its partial tile, [row of x][128 rows of w], in the stages
         // (their copies and MMAs are done, and the producers wait for `partd`); then each sums its share of the
-        // rows over the blocks in their order, so the result does not depend on timing.
+        // rows over the blocks in their order, so the result does not depend on timing.  Gate and up: two tiles.
+        const uint32_t up = (uint32_t)(p.NT * TG_PART) * 4u;
         for (int c0 = 32 * (ew >> 2); c0 < rows; c0 += 32 * (EW / 4)) {
-          uint32_t v[32];
-          tmem_ld32(ta + c0, v);
-          tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (c0 + j < rows) sts4(smb + (uint32_t)((c0 + j) * TG_PART + 32 * (ew & 3) + lane) * 4u, v[j]);
+          for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+            uint32_t v[32];
+            tmem_ld32(ta + h * p.NT + c0, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c0 + j < rows) sts4(smb + h * up + (uint32_t)((c0 + j) * TG_PART + 32 * (ew & 3) + lane) * 4u, v[j]);
+          }
         }
         tc_fence_before();
         __syncwarp();
@@ -635,16 +639,25 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
         for (int i = 0; i < 4; ++i) s4[i] = F16 && nc + i < p.g.N ? p.g.sw[(size_t)q.e * p.g.N + nc + i] : 1.f;
         for (int r = t0 + ew; r < t1; r += EW) {
           const uint32_t at = smb + (uint32_t)(r * TG_PART + 4 * lane) * 4u;
-          float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int k = 0; k < ks; ++k) {
-            const float4 v = ld_cluster_f4(cluster_map(at, (uint32_t)k));
-            sum.x += v.x;
-            sum.y += v.y;
-            sum.z += v.z;
-            sum.w += v.w;
+          auto sum_of = [&](uint32_t where, float (&f)[4]) {
+            f[0] = f[1] = f[2] = f[3] = 0.f;
+            for (int k = 0; k < ks; ++k) {
+              const float4 v = ld_cluster_f4(cluster_map(where, (uint32_t)k));
+              f[0] += v.x;
+              f[1] += v.y;
+              f[2] += v.z;
+              f[3] += v.w;
+            }
+          };
+          float f[4];
+          sum_of(at, f);
+          if (GATED) {
+            float u[4];
+            sum_of(at + up, u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = activation(p.g.act, f[i]) * u[i];
           }
           const int gr = q.r0 + r;
-          float f[4] = {sum.x, sum.y, sum.z, sum.w};
           if (F16) {
             int src = gr;
             if (p.g.index) {
@@ -863,7 +876,7 @@ cudaError_t tg_go(const CUtensorMap& mW, const CUtensorMap& mW3, const CUtensorM
   const GmmArgs& a = p.g;
   const long long most = (long long)p.MT * ((long long)a.R / p.NT + std::min(a.E, a.R));  // tiles at most
   int c = CTAS;
-  if (CTAS == 1 && MODE != TG_GATED) {
+  if (CTAS == 1) {
     // Fewer tiles than half the SMs (as far as sizes tell: groups of equal length): a cluster cuts K, as often as the
     // tiles' clusters fit at once.  A cut costs a tile's exchange, about two microseconds, so a share keeps 4 pairs of
     // chunks at least.

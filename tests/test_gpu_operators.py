@@ -503,7 +503,7 @@ def check_experts(x, routing, W1, W3, W2t, act, y):
 
 @pytest.mark.parametrize("T,E,k,D,H", [(1, 1, 1, 8, 1), (1, 8, 2, 128, 100), (1, 64, 8, 2560, 1024), (2, 4, 3, 264, 65), (1, 4, 2, 22000, 20), (3, 4, 2, 6000, 24),
                                        (5, 16, 4, 384, 130), (33, 8, 2, 520, 200), (64, 64, 8, 256, 96),
-                                       (20, 2, 2, 136, 90), (2, 8, 8, 64, 2600), (200, 6, 2, 384, 257), (513, 5, 3, 256, 128), (300, 128, 4, 136, 72), (700, 4, 2, 200, 300), (130, 1, 1, 512, 1000)])
+                                       (20, 2, 2, 136, 90), (2, 8, 8, 64, 2600), (200, 6, 2, 384, 257), (513, 5, 3, 256, 128), (300, 128, 4, 136, 72), (40, 4, 2, 2048, 200), (24, 2, 2, 256, 4000), (700, 4, 2, 200, 300), (130, 1, 1, 512, 1000)])
 @pytest.mark.parametrize("act", ["relu", "rsp", "silu"])
 def test_experts_forward(T, E, k, D, H, act):
     g = gen(T + D + H)
