@@ -872,6 +872,44 @@ PROFILE_CASES = {
 }
 
 
+# the mixture-of-experts and 8-bit operators (no handle): --batch is their tokens or rows
+OPERATOR_CASES = ("op-experts", "op-grouped", "op-int8", "op-quantize", "op-route")
+
+
+def run_operator_case(args):
+    """`--calls` calls of one operator on inputs of about a layer's size for a profiler capture: 16 experts of D = 2560,
+    H = 1024 with 4 choices a token, an int8 product 7168 x 2560, token codes of 14336 values, a router over 256."""
+    import torch
+    import activation_sparse_gated_gb300 as sffn
+    g = torch.Generator(device="cuda").manual_seed(5)
+    T, D, H, E, k = args.batch, 2560, 1024, 16, 4
+    randn = lambda *shape: torch.randn(*shape, generator=g, device="cuda")  # noqa: E731
+    if args.profile_case == "op-route":
+        z = randn(T, 256).to(torch.bfloat16)
+        call = lambda: sffn.route(z, 8, score="sigmoid")  # noqa: E731
+    elif args.profile_case == "op-quantize":
+        x = randn(T, 14336).to(torch.bfloat16)
+        call = lambda: sffn.quantize_tokens(x)  # noqa: E731
+    elif args.profile_case == "op-int8":
+        (wq, sw), (xq, sx) = (sffn.quantize_tokens(randn(n, D).to(torch.bfloat16)) for n in (7168, T))
+        call = lambda: sffn.matmul_int8(xq, sx, wq, sw)  # noqa: E731
+    elif args.profile_case == "op-grouped":
+        x, w = randn(T, D).to(torch.bfloat16), randn(E, H, D).to(torch.bfloat16)
+        offsets = torch.tensor([T * i // E for i in range(E + 1)], dtype=torch.int32, device="cuda")
+        call = lambda: sffn.grouped_matmul(x, w, offsets)  # noqa: E731
+    else:
+        W1, W3 = ((randn(E, H, D) * D ** -0.5).to(torch.bfloat16) for _ in range(2))
+        W2t = (randn(E, H, D) * H ** -0.5).to(torch.bfloat16)
+        x = randn(T, D).to(torch.bfloat16)
+        x[:, -1], W1[:, :, -1] = 1, -1.28125
+        routing = sffn.route(randn(T, E), k)
+        call = lambda: sffn.experts_forward(x, routing, W1, W3, W2t)  # noqa: E731
+    for _ in range(args.calls):
+        call()
+        sffn.sffn_check()
+    print(f"profile case {args.profile_case}: {args.calls} calls of {T} tokens", flush=True)
+
+
 def run_profile_case(args):
     """A short forward loop for profiler captures: ONE full-size layer of the named
     workload, `--calls` forwards of `--batch` tokens, each followed by a
@@ -881,6 +919,8 @@ def run_profile_case(args):
     import torch
     from activation_sparse_gated_gb300 import synthetic as syn
     import activation_sparse_gated_gb300 as sffn
+    if args.profile_case in OPERATOR_CASES:
+        return run_operator_case(args)
     name, gate = PROFILE_CASES[args.profile_case]
     lw = syn.workload_layers(name, sets=1, gate=gate, **({} if args.sparsity is None else {"s": args.sparsity}))[0]
     dtype = {"int8": "int8", "int4": "int4", "bf16": "bf16", "f32": "f32"}.get(args.dtype or "", lw.dtype)
@@ -909,7 +949,7 @@ def build_parser() -> argparse.ArgumentParser:
     ap.add_argument("--cpu-budget", type=float, default=12.0, help="seconds of CPU oracle work")
     ap.add_argument("--sweep", action="store_true",
                     help="the D=4096 sparsity x batch sweep (both gates, one JSON line per point) instead of the step")
-    ap.add_argument("--profile-case", choices=sorted(PROFILE_CASES), default=None,
+    ap.add_argument("--profile-case", choices=sorted(PROFILE_CASES) + list(OPERATOR_CASES), default=None,
                     help="run a short forward loop on one layer of this workload for a profiler capture (no timing)")
     ap.add_argument("--calls", type=int, default=8, help="--profile-case: forwards to run")
     ap.add_argument("--batch", type=int, default=1, help="--profile-case: tokens per forward")
