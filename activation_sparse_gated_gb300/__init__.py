@@ -43,7 +43,7 @@ EXPORTS = ("sffn_create", "sffn_create_ex", "sffn_set_live_threshold", "sffn_set
            "sffn_last_error", "sffn_version", "sffn_debug_timeout_probe", "sffn_forward_noalloc",
            "sffn_set_weights_int8", "sffn_get_weights_int8",
            "sffn_route_workspace", "sffn_route", "sffn_quantize_tokens", "sffn_matmul_int8", "sffn_grouped_matmul",
-           "sffn_grouped_workspace",            "sffn_experts_workspace", "sffn_experts_forward", "sffn_check")
+           "sffn_grouped_workspace", "sffn_experts_workspace", "sffn_experts_forward", "sffn_check")
 
 _lib = None
 
