@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(32 * ED_WARPS) experts_down_kernel(const Exper
 constexpr int EC_THREADS = 256;
 __global__ void __launch_bounds__(EC_THREADS) experts_combine_kernel(const ExpertsArgs a, const float* __restrict__ o,
                                                                      const int* __restrict__ slot) {
-  const int t = blockIdx.y, c = (blockIdx.x * EC_THREADS + threadIdx.x) * 4;
+  const int t = blockIdx.x, c = (blockIdx.y * EC_THREADS + threadIdx.x) * 4;
   pdl_launch_dependents();
   pdl_wait();
   if (c >= a.D) return;
@@ -358,8 +358,8 @@ cudaError_t launch_experts(const ExpertsArgs& a, cudaStream_t s) {
   down.K = a.H;
   down.E = a.E;
   if ((e = launch_gmm(down, s)) != cudaSuccess) return e;
-  return ops_launch(experts_combine_kernel, dim3((a.D + 4 * EC_THREADS - 1) / (4 * EC_THREADS), a.T), EC_THREADS, 0, s, 1,
-                    a, (const float*)o, (const int*)slot);
+  return ops_launch(experts_combine_kernel, dim3((unsigned)a.T, (unsigned)((a.D + 4 * EC_THREADS - 1) / (4 * EC_THREADS))),
+                    EC_THREADS, 0, s, 1, a, (const float*)o, (const int*)slot);
 }
 
 }  // namespace sffn

@@ -34,11 +34,15 @@ class _Routed(Routing):
     """A routing that ``route`` made: its tensors are known to fit each other."""
 
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # no stream object in between
+# no stream object in between, where torch offers it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _raw(device):
-    if _raw_stream is not None and device.index is not None:
+    if device.index != _get_device():
+        raise ValueError(f"the tensors are on {device}, which is not the current device")
+    if _raw_stream is not None:
         return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 

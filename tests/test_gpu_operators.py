@@ -543,6 +543,15 @@ def test_experts_closed_tokens_strides_and_streams(T):
     assert torch.equal(y, y2)
 
 
+def test_experts_many_tokens():
+    """More tokens than a grid's second dimension holds."""
+    g, T, E, k, D, H = gen(33), 70000, 3, 2, 64, 40
+    x = torch.randn(T, D, generator=g, device=DEV).to(BF)
+    W1, W3, W2t = ((torch.randn(E, H, D, generator=g, device=DEV) * 0.2).to(BF) for _ in range(3))
+    routing = sffn.route(torch.randn(T, E, generator=g, device=DEV), k)
+    check_experts(x, routing, W1, W3, W2t, "silu", sffn.experts_forward(x, routing, W1, W3, W2t, act="silu"))
+
+
 def test_moe_layer_and_graph_capture():
     g, T, E, k, D, H = gen(31), 40, 8, 2, 256, 160
     x = torch.randn(T, D, generator=g, device=DEV).to(BF)
