@@ -2,6 +2,8 @@
 
 nvcc compiles each translation unit for sm_103a (one -gencode, -lineinfo) in
 parallel, then links a shared library with the CUDA runtime linked statically.
+``build_torch_calls`` compiles binding/torch_calls.cpp (host code, against the
+installed PyTorch's headers) -> _torch_calls.so, the tensor operators' calls.
 """
 from __future__ import annotations
 
@@ -75,5 +77,39 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
     return lib
 
 
+# the tensor operators' calls, a CPython module against the installed PyTorch
+TORCH_CALLS_SRC = os.path.join(PKG, "binding", "torch_calls.cpp")
+TORCH_CALLS = os.path.join(PKG, "_torch_calls.so")
+
+
+def build_torch_calls(force: bool = False) -> str:
+    """Compile _torch_calls.so next to the package (a few seconds)."""
+    deps = [TORCH_CALLS_SRC, os.path.abspath(__file__), *glob.glob(os.path.join(INCLUDE, "*.h"))]
+    if not force and os.path.exists(TORCH_CALLS) and \
+            all(os.path.getmtime(p) <= os.path.getmtime(TORCH_CALLS) for p in deps):
+        return TORCH_CALLS
+    import importlib.util
+    import sysconfig
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("PyTorch is not installed")
+    torch_dir = os.path.dirname(spec.origin)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    tmp = TORCH_CALLS + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I", INCLUDE,
+           "-isystem", os.path.join(torch_dir, "include"),
+           "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"],
+           TORCH_CALLS_SRC, "-o", tmp, "-L", os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode:
+        sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+        raise RuntimeError("the host compiler failed on torch_calls.cpp")
+    os.replace(tmp, TORCH_CALLS)
+    return TORCH_CALLS
+
+
 if __name__ == "__main__":
+    print(build_torch_calls(force="--force" in sys.argv))
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv, debug="--debug" in sys.argv))

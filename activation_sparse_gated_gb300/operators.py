@@ -6,17 +6,25 @@ and pass pointers.  ``stream`` is a torch stream (default: the current one);
 tensors used on another stream than their own are the caller's to order, as
 with any torch operation.  Nothing here is differentiable, and a tensor that
 requires a gradient is refused while gradients are recorded.
+
+The ordinary call (fresh outputs, the current stream) goes through
+``_torch_calls`` (binding/torch_calls.cpp), which checks, allocates and calls the
+library in one step and answers None for whatever it does not take; the code
+here then does the same and names what is wrong.
 """
 from __future__ import annotations
 
+import ctypes
+import os
 from functools import lru_cache
 
 import torch
 
-from . import (SFFN_ACT_RELU, SFFN_ACT_RSP, SFFN_ACT_SILU, SFFN_BF16, SFFN_F32, SFFN_I8, SFFN_OK,
+from . import (LIB_PATH, SFFN_ACT_RELU, SFFN_ACT_RSP, SFFN_ACT_SILU, SFFN_BF16, SFFN_F32, SFFN_I8, SFFN_OK,
                SFFN_ROUTE_NORMALIZE, SFFN_ROUTE_SIGMOID, SFFN_W_KN, SffnError, load, sffn_last_error, sffn_strerror)
 
 _ACT = {"relu": SFFN_ACT_RELU, "rsp": SFFN_ACT_RSP, "silu": SFFN_ACT_SILU}
+_SCORE = {"softmax": 0, "sigmoid": SFFN_ROUTE_SIGMOID}
 _OUT = {"bf16": (torch.bfloat16, SFFN_BF16), "f32": (torch.float32, SFFN_F32),
         torch.bfloat16: (torch.bfloat16, SFFN_BF16), torch.float32: (torch.float32, SFFN_F32)}
 
@@ -30,8 +38,14 @@ class Routing(tuple):
     rows = property(lambda self: self[3])
 
 
-class _Routed(Routing):
-    """A routing that ``route`` made: its tensors are known to fit each other."""
+try:
+    from . import _torch_calls as _calls
+except ImportError:  # not built: the same calls, slower
+    _calls = None
+if _calls is not None and os.path.exists(LIB_PATH):
+    _calls.bind(*(ctypes.cast(getattr(load(), name), ctypes.c_void_p).value for name in (
+        "sffn_route_workspace", "sffn_route", "sffn_quantize_tokens", "sffn_grouped_workspace", "sffn_matmul_int8",
+        "sffn_grouped_matmul", "sffn_experts_workspace", "sffn_experts_forward")))
 
 
 # no stream object in between, where torch offers it
@@ -101,6 +115,10 @@ def _dense(name, t):
 
 def route(logits, k: int, score: str = "softmax", normalize: bool = True, stream=None) -> Routing:
     """The k largest of each token's logits [T, E] (fp32 or bf16), their weights and their grouping by expert."""
+    if stream is None and _calls is not None and score in _SCORE:
+        r = _calls.route(logits, k, _SCORE[score] | (SFFN_ROUTE_NORMALIZE if normalize else 0))
+        if r is not None:
+            return Routing(r)
     if stream is not None:
         with torch.cuda.stream(stream):
             return route(logits, k, score, normalize)
@@ -121,11 +139,15 @@ def route(logits, k: int, score: str = "softmax", normalize: bool = True, stream
                             offsets.data_ptr(), rows.data_ptr(), T, E, k,
                             SFFN_F32 if logits.dtype == torch.float32 else SFFN_BF16, flags, nb and ws.data_ptr(), nb,
                             _raw(device)))
-    return _Routed((weights, ids, offsets, rows))
+    return Routing((weights, ids, offsets, rows))
 
 
 def quantize_tokens(x, stream=None):
     """(codes int8 [T, K], scales fp32 [T]) of bf16 tokens x [T, K]."""
+    if stream is None and _calls is not None:
+        r = _calls.quantize_tokens(x)
+        if r is not None:
+            return r
     if stream is not None:
         with torch.cuda.stream(stream):
             return quantize_tokens(x)
@@ -155,6 +177,10 @@ def _result(out, dtype, shape, device):
 
 def matmul_int8(xq, sx, wq, sw, dtype="bf16", out=None, stream=None):
     """y[t, n] = sx[t] sw[n] sum_k xq[t, k] wq[n, k]; codes xq [T, K], wq [N, K], y of ``dtype`` (or ``out``'s)."""
+    if stream is None and out is None and _calls is not None and dtype in _OUT:
+        y = _calls.matmul_int8(xq, sx, wq, sw, _OUT[dtype][1] == SFFN_F32)
+        if y is not None:
+            return y
     if stream is not None:
         with torch.cuda.stream(stream):
             return matmul_int8(xq, sx, wq, sw, dtype, out)
@@ -183,6 +209,11 @@ def grouped_matmul(x, w, offsets, sx=None, sw=None, index=None, index_div: int =
     """Row r of expert e (offsets[e] <= r < offsets[e + 1]) of y is w[e] @ x[r]; with ``index``, w[e] @ x[index[r] //
     index_div].  bf16 x [rows, K] and w [E, N, K] ([E, K, N] with ``transposed``), or int8 codes with their scales sx
     [rows] and sw [E, N].  Rows past offsets[E] are not written."""
+    if stream is None and out is None and _calls is not None and dtype in _OUT:
+        y = _calls.grouped_matmul(x, w, offsets, sx, sw, index, index_div, bool(transposed),
+                                  _OUT[dtype][1] == SFFN_F32)
+        if y is not None:
+            return y
     if stream is not None:
         with torch.cuda.stream(stream):
             return grouped_matmul(x, w, offsets, sx, sw, index, index_div, transposed, dtype, out)
@@ -227,6 +258,10 @@ def grouped_matmul(x, w, offsets, sx=None, sw=None, index=None, index_div: int =
 def experts_forward(x, routing, W1, W3, W2t, act: str = "relu", out=None, stream=None):
     """y[t] = sum_j weights[t, j] W2_e (A(W1_e x_t) * (W3_e x_t)) over the choices e = ids[t, j] of ``route``'s result (or of
     its four tensors); x [T, D], W1, W3 and W2t (W2 transposed) [E, H, D], all bf16."""
+    if stream is None and out is None and _calls is not None and act in _ACT:
+        y = _calls.experts_forward(x, routing, W1, W3, W2t, _ACT[act])
+        if y is not None:
+            return y
     if stream is not None:
         with torch.cuda.stream(stream):
             return experts_forward(x, routing, W1, W3, W2t, act, out)
@@ -244,17 +279,14 @@ def experts_forward(x, routing, W1, W3, W2t, act: str = "relu", out=None, stream
             raise ValueError(f"{name} must be contiguous")
     E, H = shape[0], shape[1]
     weights, ids, offsets, rows = routing
-    if type(routing) is not _Routed:
-        _operand("weights", weights, (torch.float32,), 2, device)
-        _operand("ids", ids, (torch.int32,), 2, device)
-        _operand("offsets", offsets, (torch.int32,), 1, device)
-        _operand("rows", rows, (torch.int32,), 1, device)
-        for name, t in (("weights", weights), ("ids", ids), ("offsets", offsets), ("rows", rows)):
-            _dense(name, t)
-        if ids.shape != weights.shape or rows.shape[0] != weights.numel():
-            raise ValueError("the routing's tensors are of other tokens or choices")
-    elif weights.device != device:
-        raise ValueError(f"the routing is on {weights.device}, not {device}")
+    _operand("weights", weights, (torch.float32,), 2, device)
+    _operand("ids", ids, (torch.int32,), 2, device)
+    _operand("offsets", offsets, (torch.int32,), 1, device)
+    _operand("rows", rows, (torch.int32,), 1, device)
+    for name, t in (("weights", weights), ("ids", ids), ("offsets", offsets), ("rows", rows)):
+        _dense(name, t)
+    if ids.shape != weights.shape or rows.shape[0] != weights.numel():
+        raise ValueError("the routing's tensors are of other tokens or choices")
     k = weights.shape[1]
     if weights.shape[0] != T or offsets.shape[0] != E + 1:
         raise ValueError(f"the routing is of {weights.shape[0]} tokens and {offsets.shape[0] - 1} experts, not {T} and {E}")

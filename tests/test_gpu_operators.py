@@ -593,6 +593,42 @@ def test_int8_linear_of_quantised_tokens():
     close(y, ref, bound * (1 + 2.0 ** -7))
 
 
+def test_calls_with_and_without_the_native_module(monkeypatch):
+    """The calls' one-step form and the wrappers' own give the same results and take the same cases."""
+    from activation_sparse_gated_gb300 import operators
+    assert operators._calls is not None
+    g, T, E, k, D, H = gen(91), 30, 6, 2, 128, 72
+    big = torch.randn(T, 2 * D, generator=g, device=DEV).to(BF)
+    x = big[:, 8:8 + D]
+    W1, W3, W2t = (torch.randn(E, H, D, generator=g, device=DEV).to(BF) for _ in range(3))
+    z = torch.randn(T, 2 * E, generator=g, device=DEV)[:, :E]
+    q, sx = int8_operands(g, T, D)
+    wq, sw = int8_operands(g, E * H, D)
+
+    def calls():
+        r = sffn.route(z, k, score="sigmoid", normalize=False)
+        y = [*r, *sffn.quantize_tokens(x), sffn.matmul_int8(q, sx, wq, sw), sffn.matmul_int8(q, sx, wq, sw, dtype="f32")]
+        y += [sffn.grouped_matmul(x, W1, r.offsets, index=r.rows, index_div=k),
+              sffn.grouped_matmul(x[:0], W1, offsets_of([0] * E), dtype=torch.float32),
+              sffn.grouped_matmul(q, wq.view(E, H, D), r.offsets, sx=sx, sw=sw.view(E, H), index=r.rows, index_div=k),
+              sffn.grouped_matmul(x[:, :H], W2t, offsets_of([5] * E), transposed=1),
+              sffn.experts_forward(x, r, W1, W3, W2t, act="silu")]
+        return y
+
+    one = calls()
+    monkeypatch.setattr(operators, "_calls", None)
+    two = calls()
+    assert len(one) == len(two)
+    for a, b in zip(one, two):
+        assert a.shape == b.shape and a.dtype == b.dtype and torch.equal(a, b)
+    monkeypatch.undo()
+    with pytest.raises((ValueError, sffn.SffnError)):
+        sffn.route(z, 10 ** 30)
+    with torch.no_grad():
+        w = torch.nn.Parameter(W1.clone())
+        assert torch.equal(sffn.grouped_matmul(x, w, offsets_of([5] * E)), sffn.grouped_matmul(x, W1, offsets_of([5] * E)))
+
+
 def test_wrappers_refuse_on_the_gpu():
     x, w = torch.zeros(4, 64, dtype=BF, device=DEV), torch.zeros(2, 8, 64, dtype=BF, device=DEV)
     off = offsets_of([2, 2])

@@ -132,6 +132,28 @@ def test_workspace_sizes(lib):
     assert sffn.sffn_experts_workspace(1 << 20, 8, 4096, 14336) > 1 << 33
 
 
+def test_native_calls_build_load_and_decline(lib):
+    """The one-step calls load against the installed PyTorch, and answer None for what they do not take."""
+    torch = pytest.importorskip("torch")
+    libbuild.build_torch_calls()
+    import importlib.util
+    spec = importlib.util.spec_from_file_location("_torch_calls", libbuild.TORCH_CALLS)
+    calls = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(calls)
+    z = torch.zeros(4, 8)
+    x, w = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(2, 8, 64, dtype=torch.bfloat16)
+    off = torch.zeros(3, dtype=torch.int32)
+    assert calls.route(z, 2, 0) is None and calls.route(None, 2, 0) is None and calls.route(z) is None
+    assert calls.quantize_tokens(x) is None and calls.quantize_tokens(7) is None
+    assert calls.matmul_int8(x, z, x, z, False) is None
+    assert calls.grouped_matmul(x, w, off, None, None, None, 1, False, False) is None
+    assert calls.experts_forward(x, (z, off, off, off), w, w, w, 0) is None
+    with pytest.raises(TypeError):
+        calls.bind(1, 2)
+    with pytest.raises(ValueError):
+        calls.bind(*[0] * 8)
+
+
 def test_tensor_wrappers_refuse():
     torch = pytest.importorskip("torch")
     z, x = torch.zeros(4, 8), torch.zeros(4, 64, dtype=torch.bfloat16)
