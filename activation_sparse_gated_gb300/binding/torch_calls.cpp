@@ -15,7 +15,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -64,7 +64,7 @@ bool pitch(const Tensor& t, int64_t* ld) {
 bool fits(int64_t v) { return v >= 0 && v <= INT32_MAX; }
 
 Tensor make(at::IntArrayRef shape, at::ScalarType type, int device) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, (c10::DeviceIndex)device)));
+  return at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, (c10::DeviceIndex)device), std::nullopt);
 }
 
 // The tensors' device if it is the current one, else -1; its current stream.
