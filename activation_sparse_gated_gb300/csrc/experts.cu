@@ -142,10 +142,11 @@ __global__ void __launch_bounds__(32 * EG_WARPS) experts_gate_kernel(const Exper
 // y[t, 256 columns] = sum over the token's choices and their live units of
 // (w h) W2^T[unit].  A cluster of ED_SPLIT blocks cuts the k H units; a warp
 // lists the live ones of its share (ballots), then gathers their row segments
-// four at a time, 16 bytes a lane; sums go over the warps in shared memory and
+// eight at a time, 16 bytes a lane; sums go over the warps in shared memory and
 // over the blocks through distributed shared memory, in a fixed order.
 constexpr int ED_WARPS = 16;
 constexpr int ED_SPLIT = 8;
+constexpr int ED_ROWS = 8;    // row segments in flight a lane
 constexpr int ED_LIST = 128;  // units a warp lists before it gathers
 __global__ void __launch_bounds__(32 * ED_WARPS) experts_down_kernel(const ExpertsArgs a, const float* __restrict__ h) {
   __shared__ float s_sum[ED_WARPS][256 + 4];
@@ -165,44 +166,51 @@ __global__ void __launch_bounds__(32 * ED_WARPS) experts_down_kernel(const Exper
   auto gather = [&] {
     __syncwarp();
     if (n < a.D) {
-      int i = 0;
-      for (; i + 4 <= count; i += 4) {
-        uint4 v[4];
+      for (int i = 0; i < count; i += ED_ROWS) {
+        uint4 v[ED_ROWS];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = __ldg(reinterpret_cast<const uint4*>(w2 + (size_t)s_u[warp][i + q] * a.D));
+        for (int q = 0; q < ED_ROWS; ++q)
+          if (i + q < count) v[q] = __ldg(reinterpret_cast<const uint4*>(w2 + (size_t)s_u[warp][i + q] * a.D));
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float f[8];
-          Elt<bf16_tag>::unpack(v[q], f);
-          const float c = s_c[warp][i + q];
+        for (int q = 0; q < ED_ROWS; ++q)
+          if (i + q < count) {
+            float f[8];
+            Elt<bf16_tag>::unpack(v[q], f);
+            const float c = s_c[warp][i + q];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) ffma2(acc[j], make_float2(f[2 * j], f[2 * j + 1]), make_float2(c, c));
-        }
-      }
-      for (; i < count; ++i) {
-        float f[8];
-        Elt<bf16_tag>::unpack(__ldg(reinterpret_cast<const uint4*>(w2 + (size_t)s_u[warp][i] * a.D)), f);
-        const float c = s_c[warp][i];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) ffma2(acc[j], make_float2(f[2 * j], f[2 * j + 1]), make_float2(c, c));
+            for (int j = 0; j < 4; ++j) ffma2(acc[j], make_float2(f[2 * j], f[2 * j + 1]), make_float2(c, c));
+          }
       }
     }
     __syncwarp();
     count = 0;
   };
-  for (int s = s0; s < s1; ++s) {
-    const int j = s / seg, u = (s - j * seg) * 32 + lane, p = t * a.k + j, e = a.ids[p];
-    const float w = e >= 0 && e < a.E ? a.weights[p] : 0.f;
-    if (w == 0.f) continue;
-    const float c = u < a.H ? h[(size_t)p * a.H + u] * w : 0.f;
-    const uint32_t live = __ballot_sync(0xffffffffu, c != 0.f);
-    if (count + __popc(live) > ED_LIST) gather();
-    if (c != 0.f) {
-      const int at = count + __popc(live & ((1u << lane) - 1));
-      s_c[warp][at] = c;
-      s_u[warp][at] = e * a.H + u;
+  constexpr int AHEAD = 2;  // pieces whose expert, weight and units are loaded together
+  for (int s = s0; s < s1; s += AHEAD) {
+    int e[AHEAD], u[AHEAD];
+    float w[AHEAD], hv[AHEAD];
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q) {
+      const int at = min(s + q, s1 - 1), j = at / seg, p = t * a.k + j;
+      u[q] = (at - j * seg) * 32 + lane;
+      e[q] = a.ids[p];
+      w[q] = a.weights[p];
+      hv[q] = u[q] < a.H ? h[(size_t)p * a.H + u[q]] : 0.f;
     }
-    count += __popc(live);
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q) {
+      // (a choice that is not taken has no h: what was read for it is not used)
+      const bool on = s + q < s1 && e[q] >= 0 && e[q] < a.E && w[q] != 0.f && u[q] < a.H;
+      const float c = on ? hv[q] * w[q] : 0.f;
+      const uint32_t live = __ballot_sync(0xffffffffu, c != 0.f);
+      if (count + __popc(live) > ED_LIST) gather();
+      if (c != 0.f) {
+        const int at = count + __popc(live & ((1u << lane) - 1));
+        s_c[warp][at] = c;
+        s_u[warp][at] = e[q] * a.H + u[q];
+      }
+      count += __popc(live);
+    }
   }
   gather();
 #pragma unroll

@@ -314,6 +314,31 @@ __global__ void __launch_bounds__(ROUTE_THREADS) route_one_kernel(const RouteArg
   scatter_block(a, 0, a.T, s_base, s_cnt, warps);
 }
 
+// One token by one warp, with no shared memory and no barrier: its choices are
+// different experts, so a choice's row is the number of choices below it.
+template <int L, bool BF16>
+__global__ void __launch_bounds__(32) route_token_kernel(const RouteArgs a) {
+  const int lane = threadIdx.x;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int mine = choose<L, BF16>(a, 0, lane);  // lane j < k: choice j, or -1
+  int rank = 0;
+  for (int j = 0; j < a.k; ++j) {
+    const int e = __shfl_sync(0xffffffffu, mine, j);
+    rank += e >= 0 && e < mine;
+  }
+  if (lane < a.k) a.rows[mine >= 0 ? rank : lane] = mine >= 0 ? lane : -1;  // places without an expert are the last
+  for (int e0 = 0; e0 <= a.E; e0 += 32) {
+    const int e = e0 + lane;
+    int below = 0;
+    for (int j = 0; j < a.k; ++j) {
+      const int c = __shfl_sync(0xffffffffu, mine, j);
+      below += c >= 0 && c < e;
+    }
+    if (e <= a.E) a.offsets[e] = below;
+  }
+}
+
 template <int L, bool BF16>
 __global__ void __launch_bounds__(ROUTE_THREADS) route_choose_kernel(const RouteArgs a, int per, int split) {
   extern __shared__ int sm[];
@@ -396,6 +421,7 @@ int route_chunks(int T, int* per) {
 
 template <int L, bool BF16>
 cudaError_t route_lt(const RouteArgs& a, cudaStream_t s) {
+  if (a.T == 1) return ops_launch(route_token_kernel<L, BF16>, dim3(1), 32, 0, s, 1, a);
   if ((long long)a.T * a.k <= ROUTE_ONE) {
     const int fixed = a.E + 1 + ROUTE_WARPS, warps = scatter_warps(a.E, fixed);
     return ops_launch(route_one_kernel<L, BF16>, dim3(1), ROUTE_THREADS, sizeof(int) * (fixed + warps * a.E), s, 1, a, warps);
