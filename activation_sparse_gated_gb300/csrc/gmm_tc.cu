@@ -351,6 +351,13 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
     if (GATED) tma_prefetch_map(&mW3);
   }
   if (warp == 2) tg_alloc<CTAS>(tslot, (uint32_t)p.cols);
+  // what needs nothing of the kernel before this one comes before the wait for it
+  tc_fence_before();
+  __syncthreads();
+  if (CTAS == 2 || ks > 1) cluster_sync_all();  // the other blocks' barriers exist before anything arrives on them
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  if (tid == 0) pdl_launch_dependents();
   pdl_wait();  // the offsets, x and the index come from earlier kernels
   if (warp == 3) {  // group bounds and the prefix sum of their tiles
     // bounds that go back or past the end are cut: a group starts where the ones before it ended at the latest
@@ -386,12 +393,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
       last = __shfl_sync(0xffffffffu, hi, 31);
     }
   }
-  tc_fence_before();
   __syncthreads();
-  if (CTAS == 2 || ks > 1) cluster_sync_all();  // the other blocks' barriers exist before anything arrives on them
-  tc_fence_after();
-  const uint32_t tmem = *tslot;
-  if (tid == 0) pdl_launch_dependents();
   const int total = s_pre[p.g.E];
   const int first = blockIdx.x / (CTAS * ks), step = gridDim.x / (CTAS * ks);
   const uint32_t smb = smem_u32(sm);
@@ -640,14 +642,19 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
         for (int r = t0 + ew; r < t1; r += EW) {
           const uint32_t at = smb + (uint32_t)(r * TG_PART + 4 * lane) * 4u;
           auto sum_of = [&](uint32_t where, float (&f)[4]) {
+            float4 v[8];  // every block's part in flight together, added in their order
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (k < ks) v[k] = ld_cluster_f4(cluster_map(where, (uint32_t)k));
             f[0] = f[1] = f[2] = f[3] = 0.f;
-            for (int k = 0; k < ks; ++k) {
-              const float4 v = ld_cluster_f4(cluster_map(where, (uint32_t)k));
-              f[0] += v.x;
-              f[1] += v.y;
-              f[2] += v.z;
-              f[3] += v.w;
-            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (k < ks) {
+                f[0] += v[k].x;
+                f[1] += v[k].y;
+                f[2] += v[k].z;
+                f[3] += v[k].w;
+              }
           };
           float f[4];
           sum_of(at, f);
