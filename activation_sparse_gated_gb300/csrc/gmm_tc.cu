@@ -39,7 +39,7 @@
 // over 64 experts of 1024 x 2560 44.6 (97 % / 1 %); 16384 ragged rows over 64
 // experts of 7168 x 2560 521 (76 % / 60 %); one group 8192 x 14336 x 4096 499
 // (- / 99 %); int8 8192 x 14336 x 4096 533 (- / 93 %, 40 of it the copies), 77 x
-// 2560 x 7168 15.5 (19 % / 9 %: latency of the chunks' chain and of the launch),
+// 2560 x 7168 14.8 (20 % / 9 %: latency of the chunks' chain and of the launch),
 // 4093 rows over 16 experts of 1000 x 2560 50 (18 % / 22 %: widening).
 #include <cudaTypedefs.h>
 
@@ -292,6 +292,15 @@ __device__ __forceinline__ Tile tile_at(const TgArgs& p, const int* s_off, const
   q.r1 = min(s_off[lo + 1], q.r0 + per);
   q.n = (q.r1 - q.r0 + Q - 1) / Q * Q;
   return q;
+}
+
+// activation() with the device's fast exponential and quotient.  Gate and up leave no room for a second accumulator, so
+// this stands between two tiles' MMAs (4096 tokens, 8 of 64 experts, D = 2560, H = 1024, R-S+ 540 us with the
+// precise ones, 521 so; SiLU 531 / 523).  Its relative error is below 2^-15 wherever the result is a normal number; the
+// product with the up value is then rounded to bf16 (2^-9).
+__device__ __forceinline__ float gate_act(int act, float z) {
+  if (act != ACT_SILU && !(z > 0.f)) return 0.f;
+  return act == 0 ? z : __fdividef(z, 1.f + __expf(-z));
 }
 
 template <int CTAS, int MODE, bool KN>
@@ -662,7 +671,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
             float u[4];
             sum_of(at + up, u);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = activation(p.g.act, f[i]) * u[i];
+            for (int i = 0; i < 4; ++i) f[i] = gate_act(p.g.act, f[i]) * u[i];
           }
           const int gr = q.r0 + r;
           if (F16) {
@@ -714,9 +723,14 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
           uint32_t u[32];
           tmem_ld32(ta + p.NT + c0, u);
           tmem_ld_wait();
+          if (p.g.act == 0) {  // hoisted: as a branch of each value ReLU pays for the others
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            v[j] = __float_as_uint(activation(p.g.act, __uint_as_float(v[j])) * __uint_as_float(u[j]));
+            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(gate_act(0, __uint_as_float(v[j])) * __uint_as_float(u[j]));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              v[j] = __float_as_uint(gate_act(p.g.act, __uint_as_float(v[j])) * __uint_as_float(u[j]));
+          }
         } else {
           tmem_ld_wait();
         }
