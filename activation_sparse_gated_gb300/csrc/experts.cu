@@ -6,6 +6,13 @@
 // unit's gate z = W1_e[i] . x_t, and only a live unit's row of W3_e is read;
 // the down product then gathers the live units' rows of W2_e^T.  Both passes
 // are reads of weight rows (bf16, fp32 sums; h stays fp32).
+//
+// Measured: one token, 8 of 64 experts, D = 2560, H = 1024, ReLU at 90 %: 20 us
+// with its router (50 MB, 37 % of the copy rate): loads that wait for the
+// choice, for the gate, for the live units, one after the other.  Many tokens
+// are products on the tensor cores (4096 tokens 484 us): gate and up 227, down
+// 148 (its fp32 rows are 335 MB; 127 with rows of bf16), combination 62, the
+// grouped copy of x 31, the router 15.
 #include <algorithm>
 
 #include "common.cuh"

