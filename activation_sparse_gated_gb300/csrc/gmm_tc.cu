@@ -8,10 +8,10 @@
 // The weights are the M side of the MMA (128 rows of w a block, 256 a pair of
 // blocks with cta_group::2) and the rows of x the N side, whose width is any
 // multiple of 16 (32 for a pair) up to 256: a ragged group reads no more rows
-// than it has.  An MMA of 16 K values takes about 130 cycles whatever its width
-// (measured: a 64-wide chunk about 550 at 16 to 128 columns, one block), so full
-// tensor rate wants 256 columns, and 128 x 16 weights per 130 cycles and SM are
-// still above the memory's rate, which is what bounds short groups.
+// than it has.  An MMA of 16 K values takes N / 2 cycles from 96 columns on and 49
+// below (measured, one block, operands in shared memory): full tensor rate from
+// 128 columns on, 256 halve the traffic of w; and 128 x 16 weights per 49 cycles
+// and SM are above the memory's rate, which is what bounds short groups.
 //
 // A block walks the tiles of all groups (persistent, tile ids strided by the
 // grid); the tile list is a prefix sum over the groups that every block makes
@@ -27,10 +27,13 @@
 //
 // int8: this part's int8 MMA rate is far below its 16-bit rate, and int8 codes are
 // exact in fp16 with exact products and fp32 sums that are exact below 2^24.  So
-// the raw codes arrive by TMA and sixteen warps widen them into the fp16 operand
-// tiles: half the memory traffic of 16-bit weights.  Widening and the exchange
-// around it cost a chunk as much again as its MMAs; where groups are long the
-// codes are widened once into fp16 copies instead (widen_kernel).
+// the raw codes arrive by TMA, 128 a row, and sixteen warps widen them: half the
+// memory traffic of 16-bit weights.  The widened w goes to TMEM (an MMA takes its
+// A operand from there), the widened x to shared memory, which at 128 x 128 is
+// busy with copies, loads, stores and the MMAs' reads of x for four cycles in
+// five.  64 codes of a 128 x 128 tile take 0.28 us, 0.19 without the widening,
+// 0.13 the MMAs.  Where groups are long the codes are widened once into fp16
+// copies instead (widen_kernel).
 //
 // Few tiles and a long sum: the blocks of a cluster cut K and add their partial
 // tiles through distributed shared memory in a fixed order.
@@ -39,8 +42,9 @@
 // over 64 experts of 1024 x 2560 44.6 (97 % / 1 %); 16384 ragged rows over 64
 // experts of 7168 x 2560 521 (76 % / 60 %); one group 8192 x 14336 x 4096 499
 // (- / 99 %); int8 8192 x 14336 x 4096 533 (- / 93 %, 40 of it the copies), 77 x
-// 2560 x 7168 14.8 (20 % / 9 %: latency of the chunks' chain and of the launch),
-// 4093 rows over 16 experts of 1000 x 2560 50 (18 % / 22 %: widening).
+// 2560 x 7168 14.4 (20 % / 10 %: latency of the chunks' chain and of the launch),
+// 4093 rows over 16 experts of 1000 x 2560 43 (20 % / 25 %: widening; 50 with
+// w widened in shared memory, a value a store and 64 codes a stage).
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -58,7 +62,7 @@ namespace {
 
 constexpr int TG_EPI_WARP0 = 4;   // warps 4..11 (int8: 4..7): epilogue (TMEM lane quarter = warp % 4)
 constexpr int TG_CONV_WARP0 = 8;  // warps 8..23: int8 -> fp16
-constexpr int TG_CONV_WARPS = 16;
+constexpr int TG_CONV_WARPS = 16, TG_CONV_GROUPS = 2;
 constexpr int TG_THREADS = 384, TG_THREADS_I8 = 32 * (TG_CONV_WARP0 + TG_CONV_WARPS);
 constexpr uint64_t TG_TIMEOUT_NS = 250000000ull;
 constexpr size_t TG_SMEM = 227 * 1024;
@@ -79,6 +83,7 @@ struct TgArgs {
   int KC;      // 64-wide K chunks
   int S;       // operand stages (int8: of widened codes)
   int SR;      // raw stages (int8)
+  int wcol;    // int8: first TMEM column of the widened weights
   int ks;      // blocks of a cluster that cut K between them (1: no cut)
   int cols;    // TMEM columns allocated
   int vec;     // rows of y take 16-byte stores: y, ldy and N are multiples of that
@@ -201,6 +206,16 @@ __device__ __forceinline__ void tg_mma(uint32_t d, uint32_t alo, uint32_t ahi, u
         : "memory");
 }
 
+// The same with A in TMEM: lane = row, a column = two values of K.
+__device__ __forceinline__ void tg_mma_t(uint32_t d, uint32_t a, uint32_t blo, uint32_t bhi, uint32_t idesc,
+                                         uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(blo), "r"(bhi), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
 // Arrive on `bar` (in both blocks of a pair) when the MMAs this thread issued so far are done.
 template <int CTAS>
 __device__ __forceinline__ void tg_commit(uint32_t bar) {
@@ -229,6 +244,16 @@ __device__ __forceinline__ void tg_dealloc(uint32_t taddr, uint32_t ncols) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
   else
     tmem_dealloc(taddr, ncols);
+}
+
+// 16 consecutive columns of this thread's lane, written; not waited for.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 
 // 32 consecutive fp32 columns of this thread's lane, not waited for.
@@ -315,10 +340,11 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
   constexpr uint32_t AB = 128u * 128u;  // one A region: 128 rows x 128 bytes
   const uint32_t NTl = (uint32_t)p.NT / CTAS;
   const uint32_t bb = (NTl + 7) / 8 * 1024u;                 // B region
-  const uint32_t st_bytes = (GATED ? 2 : 1) * AB + bb;       // operand stage
+  // an operand stage; int8: 128 codes of x widened (two 64-wide tiles; the weights' are in TMEM), a raw stage both's
+  const uint32_t st_bytes = I8 ? 2 * bb : (GATED ? 2 : 1) * AB + bb, raw_bytes = AB + bb;
   const uint32_t raw0 = (uint32_t)p.S * st_bytes;
-  // then the raw stages (int8) or the epilogue's scratch, then the barriers
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + raw0 + (I8 ? (uint32_t)p.SR * st_bytes : 8u * TG_EPI_BYTES));
+  const uint32_t epi0 = raw0 + (I8 ? (uint32_t)p.SR * raw_bytes : 0u);  // the epilogue's scratch, then the barriers
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + epi0 + EW * TG_EPI_BYTES);
   uint64_t* full = bars;
   uint64_t* empty = full + p.S;
   uint64_t* rfull = empty + p.S;
@@ -340,12 +366,12 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
 
   if (tid == 0) {
     for (int s = 0; s < p.S; ++s) {
-      mbar_init(&full[s], I8 ? 4 : 1);
+      mbar_init(&full[s], I8 ? TG_CONV_WARPS / TG_CONV_GROUPS : 1);
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < p.SR; ++s) {
       mbar_init(&rfull[s], 1);
-      mbar_init(&rempty[s], 8);  // four warps, two halves
+      mbar_init(&rempty[s], TG_CONV_WARPS / TG_CONV_GROUPS);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&accf[b], 1);
@@ -415,7 +441,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
     uint64_t* eb = I8 ? rempty : empty;
     const int S = I8 ? p.SR : p.S, KW = I8 ? 128 : 64;
     const int kb = I8 ? cb / 2 : cb, ke = I8 ? (ce + 1) / 2 : ce;
-    const uint32_t base = I8 ? smb + raw0 : smb;
+    const uint32_t base = I8 ? smb + raw0 : smb, stage = I8 ? raw_bytes : st_bytes;
     uint32_t it = 0, s = 0, par = 1;  // par: parity of the wait for stage s (a fresh barrier passes parity 1)
     bool ok = true;
     for (int t = first; t < total && ok; t += step) {
@@ -449,7 +475,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
           ok = false;
           break;
         }
-        const uint32_t st = base + s * st_bytes;
+        const uint32_t st = base + s * stage;
         // a pair's stages complete on the first block's barrier
         const uint32_t bar = CTAS == 2 ? cluster_map(smem_u32(&fb[s]), 0) : smem_u32(&fb[s]);
         if (!xside) {
@@ -487,8 +513,8 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer (first block of a pair)
-    // The warp stays converged; one lane issues a chunk's MMAs and their commit together.  A chunk costs the warp's
-    // issue about as much as its MMAs cost the tensor cores, so the loop holds nothing but 32-bit adds.
+    // The warp stays converged; one lane issues a stage's MMAs and their commit together.  Up to 64 columns the issue
+    // is what an MMA costs, so the loop holds nothing but 32-bit adds.
     if (rank == 0) {
       const uint32_t st0 = (smb >> 4) & 0x3fffu;  // (in a cluster an address holds the block's rank above its offset)
       uint32_t s = 0, par = 0, tl = 0, st = st0;   // st: the stage's address in 16-byte units
@@ -505,16 +531,22 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
         tc_fence_after();
         const uint32_t d = tmem + b * (uint32_t)((GATED ? 2 : 1) * p.NT);
         uint32_t acc = 0;
-        for (int c = cb; c < ce; ++c) {
+        for (int c = I8 ? cb / 2 : cb; c < (I8 ? (ce + 1) / 2 : ce); ++c) {
           if (!__all_sync(0xffffffffu, tg_wait<false>(full + s, par, abort_flag, p.err))) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t al = alo0 + st, bl = blo0 + st + ((GATED ? 2 : 1) * AB >> 4);
+          const uint32_t al = alo0 + st, bl = blo0 + st + ((I8 ? 0 : GATED ? 2 : 1) * AB >> 4);
           if (elect_one()) {
+            if constexpr (I8) {
+              const uint32_t at = tmem + (uint32_t)p.wcol + 64u * s;  // the stage's weights
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+              for (int k = 0; k < 8; ++k)
+                tg_mma_t(d, at + 8 * k, bl + (k >> 2) * (bb >> 4) + 2 * (k & 3), hi, idesc, k == 0 ? acc : 1u);
+            }
+#pragma unroll
+            for (int k = 0; k < (I8 ? 0 : 4); ++k) {
               const uint32_t ak = al + (KN ? (k * 2048) >> 4 : 2 * k);
               tg_mma<CTAS>(d, ak, hi, bl + 2 * k, hi, idesc, k == 0 ? acc : 1u);
               if (GATED) tg_mma<CTAS>(d + p.NT, ak + (AB >> 4), hi, bl + 2 * k, hi, idesc, k == 0 ? acc : 1u);
@@ -535,22 +567,22 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
     __syncwarp();
   } else if (I8 && warp >= TG_CONV_WARP0) {
     // ---------------------------------------------------------------- int8 -> fp16 operand tiles
-    // Four groups of four warps take every fourth chunk each: a chunk's chain of load, widen, store, fence and
-    // arrival is longer than its MMAs, four of them overlap.
-    const int cg = (warp - TG_CONV_WARP0) >> 2, cw = warp & 3, row8 = lane & 7, cj = lane >> 3;
+    // Two groups of eight warps take every other raw stage of 128 codes each, a warp 64 of them.
+    const int cg = (warp - TG_CONV_WARP0) >> 3, half = (warp - TG_CONV_WARP0) >> 2 & 1, cw = warp & 3;
+    const int row8 = lane & 7, cj = lane >> 3;
     // Stages and their phases are counted up, never divided for: a division costs as much as the widening.
-    const int n = ce - cb, nr = (n + 1) / 2;  // chunks and raw stages of a tile
-    uint32_t s = 0, epar = 1;                 // stage of the next chunk; parity of the wait for it (fresh: passes)
-    uint32_t rs = 0, rpar = 0;                // raw stage of the next chunk, parity of its wait
-    int skip = cg;                            // chunks to go on to the group's next one
+    const int n = (ce + 1) / 2 - cb / 2;  // raw stages of a tile
+    uint32_t s = 0, epar = 1;             // operand stage of the next one; parity of the wait for it (fresh: passes)
+    uint32_t rs = 0, rpar = 0;            // its raw stage, parity of its wait
+    int skip = cg;                        // raw stages to go on to the group's next one
     bool ok = true;
-    auto forward = [&](int chunks, int raws) {
-      s += chunks;
+    auto forward = [&](int by) {
+      s += by;
       while (s >= (uint32_t)p.S) {
         s -= p.S;
         epar ^= 1;
       }
-      rs += raws;
+      rs += by;
       while (rs >= (uint32_t)p.SR) {
         rs -= p.SR;
         rpar ^= 1;
@@ -558,27 +590,47 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
     };
     for (int t = first; t < total && ok; t += step) {
       const Tile q = tile_at<CTAS>(p, s_off, s_pre, t);
-      const int groups = 16 + q.n / CTAS / 8;  // 8-row groups: A, then B (both regions are dense)
+      const int groups = q.n / 8;  // 8-row groups of x
       int c = 0;
       for (;;) {
-        if (c + skip >= n) {  // the next chunk is in a later tile
-          forward(n - c, nr - (c >> 1));
+        if (c + skip >= n) {  // the next one is in a later tile
+          forward(n - c);
           skip -= n - c;
           break;
         }
-        forward(skip, ((c + skip) >> 1) - (c >> 1));  // cb is even: halves are as in the whole sum
+        forward(skip);
         c += skip;
-        skip = 4;
-        const int half = c & 1;
-        // A parity wait must not run two phases ahead.  With four stages a group meets every phase of its stage's
-        // `empty`; that wait shows that chunk it - 4 and all before it are multiplied, so of the raw stage every
-        // phase before this one is over (its last chunk is at most 2 (rt - SR) + 1 <= it - 4 for SR >= 3).
+        skip = TG_CONV_GROUPS;
+        // A parity wait must not run two phases ahead.  The group's last wait for `empty`, two raw stages ago, showed
+        // that stage it - 2 - S was multiplied, so with S >= 2 the phase before this one (it - 2 S) is over; this wait
+        // shows that it - S and all before are, so with SR >= S the raw stage's phase before this one is over, too.
         ok = tg_wait<false>(&empty[s], epar, abort_flag, p.err);
         if (ok) ok = tg_wait<false>(&rfull[rs], rpar, abort_flag, p.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint32_t src = smb + raw0 + rs * st_bytes + (uint32_t)row8 * 128u + ((uint32_t)((half * 4 + cj) ^ row8) << 4);
-        const uint32_t dst = smb + s * st_bytes + (uint32_t)row8 * 128u;
+        const uint32_t rw = smb + raw0 + rs * raw_bytes;
+        {  // weights: a lane's row, 64 codes, into its TMEM lane
+          tc_fence_after();
+          const uint32_t src = rw + (uint32_t)(32 * cw + lane) * 128u;
+          uint4 v[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = lds16a(src + ((uint32_t)((half * 4 + j) ^ row8) << 4));
+          const uint32_t at = tmem + (uint32_t)p.wcol + 64u * s + 32u * half + ((uint32_t)(32 * cw) << 16);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t o[16];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              widen4(v[2 * h + j].x, o + 8 * j);
+              widen4(v[2 * h + j].y, o + 8 * j + 2);
+              widen4(v[2 * h + j].z, o + 8 * j + 4);
+              widen4(v[2 * h + j].w, o + 8 * j + 6);
+            }
+            tmem_st16(at + 16 * h, o);
+          }
+        }
+        const uint32_t src = rw + AB + (uint32_t)row8 * 128u + ((uint32_t)((half * 4 + cj) ^ row8) << 4);
+        const uint32_t dst = smb + s * st_bytes + half * bb + (uint32_t)row8 * 128u;
         const uint32_t d0 = dst + ((uint32_t)((2 * cj) ^ row8) << 4), d1 = dst + ((uint32_t)((2 * cj + 1) ^ row8) << 4);
         for (int g0 = cw; g0 < groups; g0 += 16) {
           uint4 v[4];
@@ -598,12 +650,13 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
               sts16(d1 + off, o[4], o[5], o[6], o[7]);
             }
         }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&full[s]);
           mbar_arrive(&rempty[rs]);
-          if (half == 0 && c == n - 1) mbar_arrive(&rempty[rs]);  // no second half: its arrival as well
         }
       }
     }
@@ -744,9 +797,9 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
               mbar_arrive(&acce[b]);
           }
         }
-        if (!I8 && p.vec) {
+        if (p.vec) {
           // through this warp's shared scratch, so that a store carries 16 bytes of a row a lane
-          const uint32_t buf = smb + raw0 + (uint32_t)ew * TG_EPI_BYTES;
+          const uint32_t buf = smb + epi0 + (uint32_t)ew * TG_EPI_BYTES;
           const int nc = q.mt * 128 * CTAS + n0r + 32 * (ew & 3);  // the warp's first column of y
           if (p.g.y_f32) {
 #pragma unroll
@@ -925,19 +978,22 @@ cudaError_t launch_gmm_tc(const GmmArgs& a, int ctas, int nt, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const size_t yb = a.y_f32 ? 4 : 2;
   p.vec = ((uintptr_t)a.y & 15) == 0 && a.ldy * yb % 16 == 0 && a.N * yb % 16 == 0;
-  const size_t fixed = (a.i8 ? 0 : 8 * TG_EPI_BYTES) + 1024 + 8 * (2 * 16 + 2 * 16 + 6) + 8 +
+  const size_t fixed = (a.i8 ? 4 : 8) * TG_EPI_BYTES + 1024 + 8 * (2 * 16 + 2 * 16 + 6) + 8 +
                        sizeof(int) * 2 * (size_t)(a.E + 1) + 64;
-  auto stage_bytes = [&] { return (gated ? 2u : 1u) * 16384u + (uint32_t)(p.NT / ctas + 7) / 8 * 1024u; };
-  auto slots = [&] { return (int)((TG_SMEM - fixed) / stage_bytes()); };
-  // int8: the converters' four groups need four operand stages and three raw ones
-  while (a.i8 && slots() < 7) p.NT >>= 1;
+  const int room = (int)(TG_SMEM - fixed);
+  auto b_bytes = [&] { return (p.NT / ctas + 7) / 8 * 1024; };
+  // int8: three operand stages (two are 10 to 15 % slower) and as many raw ones at least (see the converters' waits)
+  constexpr int least = 3;
+  while (a.i8 && room < 2 * least * b_bytes() + least * (16384 + b_bytes())) p.NT >>= 1;
   const int ntl = p.NT / ctas;
-  const uint32_t st = stage_bytes();
-  p.S = a.i8 ? 4 : std::min(16, slots());
-  p.SR = a.i8 ? std::min(12, slots() - 4) : 0;
+  const int st = a.i8 ? 2 * b_bytes() : (gated ? 2 : 1) * 16384 + b_bytes(), raw = a.i8 ? 16384 + b_bytes() : 0;
+  p.S = a.i8 ? least : std::min(16, room / st);
+  p.SR = a.i8 ? std::min(12, (room - p.S * st) / raw) : 0;
+  const int wide = (gated ? 2 : 1) * p.NT, wcols = a.i8 ? 64 * p.S : 0;  // TMEM columns: an accumulator, the weights
+  p.nacc = 2 * wide + wcols <= 512 ? 2 : 1;
+  p.wcol = p.nacc * wide;
   int cols = 32;
-  p.nacc = 2 * (gated ? 2 : 1) * p.NT <= 512 ? 2 : 1;
-  while (cols < p.nacc * (gated ? 2 : 1) * p.NT) cols <<= 1;
+  while (cols < p.wcol + wcols) cols <<= 1;
   p.cols = cols;
   p.bxr = std::min(ntl, 32);
   CUtensorMap mW, mW3, mX, mXb;
@@ -950,7 +1006,7 @@ cudaError_t launch_gmm_tc(const GmmArgs& a, int ctas, int nt, cudaStream_t s) {
     if (!encode(&mX, a.x, 2, dims, strides, box, a.i8 != 0) || !encode(&mXb, a.x, 2, dims, strides, boxb, a.i8 != 0))
       return cudaErrorInvalidValue;
   }
-  const size_t smem = fixed + (size_t)(p.S + p.SR) * st;
+  const size_t smem = fixed + (size_t)p.S * st + (size_t)p.SR * raw;
   const int sms = ops_num_sms();
   if (a.i8) return tg_go<1, TG_I8, false>(mW, mW3, mX, mXb, p, smem, sms, s);
   if (a.f16) return tg_go<2, TG_F16, false>(mW, mW3, mX, mXb, p, smem, sms, s);
@@ -989,8 +1045,9 @@ __global__ void __launch_bounds__(256) widen_kernel(const uint8_t* __restrict__ 
 }
 
 // Rows per expert from which fp16 copies of the codes, made once, pay for 256-row pair tiles (us, N = 14336, K = 4096,
-// widened in flight / copies: 640 rows 91 / 98, 768 rows 110 / 103, 2048 rows 248 / 159).
-constexpr int TG_WIDE_ROWS = 704;
+// widened in flight / copies: 640 rows 81 / 97, 768 97 / 103, 900 113 / 102, 2048 221 / 161; 16 experts of 1000 x 2560:
+// 768 rows each 82 / 94, 1024 106 / 111).
+constexpr int TG_WIDE_ROWS = 832;
 
 bool wide(int R, int E, int i8) { return i8 && R / E >= TG_WIDE_ROWS; }
 

@@ -174,6 +174,14 @@ def test_matmul_int8(T, N, K, out):
     close(y, ref, 3 * 2.0 ** -24 * ref.abs() + int8_bound(xq, wq, scale))
 
 
+@pytest.mark.parametrize("T,N", [(700, 4001), (800, 4000), (310, 9000)])
+@pytest.mark.parametrize("K", [16, 144, 272, 448, 1104])
+def test_matmul_int8_several_tiles_a_block(T, N, K):
+    """More tiles than blocks, each of an odd or even number of stages: the stages' phases run on from tile to tile."""
+    test_matmul_int8(T, N, K, "bf16")
+    test_matmul_int8(T, N, K, "f32")
+
+
 def test_matmul_int8_strides_zero_scales_and_out():
     g = gen(11)
     big, sx = int8_operands(g, 40, 512)
