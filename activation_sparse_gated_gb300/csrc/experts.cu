@@ -355,6 +355,7 @@ cudaError_t launch_experts(const ExpertsArgs& a, cudaStream_t s) {
   up.XR = R;
   up.N = a.H;
   up.K = a.D;
+  up.NY = Hp;
   up.E = a.E;
   up.act = a.act;
   if ((e = launch_gmm(up, s)) != cudaSuccess) return e;

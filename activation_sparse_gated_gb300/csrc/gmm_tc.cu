@@ -816,7 +816,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
                 const int j = 4 * i + (lane >> 3), c = 4 * (lane & 7);
                 const int row = __shfl_sync(0xffffffffu, to, 16 * h + j);
                 const uint4 d = lds16a(buf + (uint32_t)(j * TG_EPI_PITCH + c) * 4u);
-                if (row >= 0 && nc + c < p.g.N)
+                if (row >= 0 && nc + c < p.g.NY)
                   *reinterpret_cast<uint4*>(reinterpret_cast<float*>(p.g.y) + (uint64_t)(uint32_t)row * (uint64_t)p.g.ldy +
                                             nc + c) = d;
               }
@@ -840,7 +840,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
               const uint4 d = lds16a(at), e = lds16a(at + 16);
               const int ra = __shfl_sync(0xffffffffu, to, 2 * j), rb = __shfl_sync(0xffffffffu, to, 2 * j + 1);
               __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(p.g.y) + nc + c;
-              if (nc + c < p.g.N) {
+              if (nc + c < p.g.NY) {
                 if (ra >= 0)
                   *reinterpret_cast<uint4*>(y + (uint64_t)(uint32_t)ra * (uint64_t)p.g.ldy) =
                       make_uint4(__byte_perm(d.x, d.y, 0x5410), __byte_perm(d.z, d.w, 0x5410),
@@ -977,7 +977,8 @@ cudaError_t launch_gmm_tc(const GmmArgs& a, int ctas, int nt, cudaStream_t s) {
   cudaError_t e = ops_error_word(&p.err);
   if (e != cudaSuccess) return e;
   const size_t yb = a.y_f32 ? 4 : 2;
-  p.vec = ((uintptr_t)a.y & 15) == 0 && a.ldy * yb % 16 == 0 && a.N * yb % 16 == 0;
+  p.g.NY = std::max(a.N, a.NY);
+  p.vec = ((uintptr_t)a.y & 15) == 0 && a.ldy * yb % 16 == 0 && p.g.NY * yb % 16 == 0;
   const size_t fixed = (a.i8 ? 4 : 8) * TG_EPI_BYTES + 1024 + 8 * (2 * 16 + 2 * 16 + 6) + 8 +
                        sizeof(int) * 2 * (size_t)(a.E + 1) + 64;
   const int room = (int)(TG_SMEM - fixed);
@@ -1044,12 +1045,24 @@ __global__ void __launch_bounds__(256) widen_kernel(const uint8_t* __restrict__ 
   }
 }
 
-// Rows per expert from which fp16 copies of the codes, made once, pay for 256-row pair tiles (us, N = 14336, K = 4096,
-// widened in flight / copies: 640 rows 81 / 97, 768 97 / 103, 900 113 / 102, 2048 221 / 161; 16 experts of 1000 x 2560:
-// 768 rows each 82 / 94, 1024 106 / 111).
+// fp16 copies of the codes, made once, against widening in flight: copies let 256 x 256 pair tiles run at full tensor
+// rate, so a round of tiles over the SMs, 0.28 us per 64 codes either way, does four times the work on two SMs; they
+// cost a launch and an exposed epilogue, 5 us, and three bytes of traffic a code.  (us, in flight / copies, K = 4096:
+// 1024 rows, N = 14336 116 / 103; 2048 rows, N = 512 22 / 31, 1024 25 / 34, 2048 42 / 37, 14336 221 / 161; 8192 rows, N =
+// 16 25 / 47, 512 45 / 50, 1024 81 / 69; 16 experts of 1000 x 2560: 1024 rows each 106 / 111, 1536 145 / 145.)
+// Below TG_WIDE_ROWS an expert they never pay (768 rows, N = 14336: 97 / 103), and no workspace is asked for.
 constexpr int TG_WIDE_ROWS = 832;
 
 bool wide(int R, int E, int i8) { return i8 && R / E >= TG_WIDE_ROWS; }
+
+bool copies_pay(const GmmArgs& a) {
+  const long long rows = a.R / a.E, sms = ops_num_sms();
+  const long long small = (long long)a.E * ((a.N + 127) / 128) * ((rows + 127) / 128);
+  const long long pairs = (long long)a.E * ((a.N + 255) / 256) * ((rows + 255) / 256);
+  const long long rounds = (small + sms - 1) / sms - (2 * pairs + sms - 1) / sms;
+  const long long codes = ((long long)a.XR + (long long)a.E * a.N) * a.K;
+  return rounds * ((a.K + 63) / 64) * 280 > 5000 + codes / 2000;  // ns
+}
 
 size_t gmm_workspace(int R, int XR, int N, int K, int E, int i8) {
   return wide(R, E, i8) ? 2 * ((size_t)XR * K + (size_t)E * N * K) : 0;
@@ -1057,7 +1070,7 @@ size_t gmm_workspace(int R, int XR, int N, int K, int E, int i8) {
 
 cudaError_t launch_gmm(const GmmArgs& a, cudaStream_t s) {
   const int busy = std::min(a.E, a.R);
-  if (wide(a.R, a.E, a.i8) && a.workspace) {
+  if (wide(a.R, a.E, a.i8) && a.workspace && copies_pay(a)) {
     const long long nx = (long long)a.XR * (a.K / 16), nw = (long long)a.E * a.N * (a.K / 16);
     const int grid = (int)std::min<long long>((nx + nw + 255) / 256, 8ll * ops_num_sms());
     const cudaError_t e = ops_launch(widen_kernel, dim3((unsigned)grid), 256, 0, s, 1, (const uint8_t*)a.x, a.ldx,
@@ -1071,14 +1084,15 @@ cudaError_t launch_gmm(const GmmArgs& a, cudaStream_t s) {
     b.f16 = 1;
     return launch_gmm_tc(b, 2, 256, s);
   }
-  // Gate and up together: 256 rows a tile take all of TMEM, so their epilogue is not hidden, and still win from 128
-  // rows a group on (4096 tokens, 8 of 64 experts, D = 2560, H = 1024: 561 against 643 us; 512 tokens 225 / 211).
-  if (a.w3) return a.R >= 128 * busy ? launch_gmm_tc(a, 2, 256, s) : launch_gmm_tc(a, 1, 128, s);
   if (a.i8) return a.R <= std::max(a.E, 4) ? launch_gmm_rows(a, s) : launch_gmm_tc(a, 1, 128, s);
   // A pair's 256 x 256 tiles from 96 rows a group on, where they fill the SMs (us, 128 x 128 / pair tiles; 64 experts, N =
   // 1024, K = 2560: 64 rows each 63 / 65, 96 72 / 68, 256 102 / 83; one, N = K = 4096: 256 rows 17 / 24, 512 19 / 24).
   const long long pairs = (long long)((a.N + 255) / 256) * busy * (((a.R + busy - 1) / busy + 255) / 256);
-  return a.R >= 96 * busy && 2 * pairs >= ops_num_sms() ? launch_gmm_tc(a, 2, 256, s) : launch_gmm_tc(a, 1, 128, s);
+  const bool fill = 2 * pairs >= ops_num_sms();
+  // Gate and up together: 256 rows a tile take all of TMEM, so their epilogue is not hidden, and still win from 128
+  // rows a group on (4096 tokens, 8 of 64 experts, D = 2560, H = 1024: 561 against 643 us; 512 tokens 225 / 211).
+  if (a.w3) return a.R >= 128 * busy && fill ? launch_gmm_tc(a, 2, 256, s) : launch_gmm_tc(a, 1, 128, s);
+  return a.R >= 96 * busy && fill ? launch_gmm_tc(a, 2, 256, s) : launch_gmm_tc(a, 1, 128, s);
 }
 
 }  // namespace sffn

@@ -42,6 +42,7 @@ struct GmmArgs {
   long long ldx = 0, ldy = 0;
   int R = 0, XR = 0, N = 0, K = 0, E = 1;  // XR: rows of x
   int i8 = 0, y_f32 = 0, kn = 0, act = 0;
+  int NY = 0;                     // columns of y that may be written (past N: zeros), if more than N
   int f16 = 0;                    // x and w are fp16 copies of int8 codes (with their scales)
   void* workspace = nullptr;      // gmm_workspace() bytes
 };

@@ -46,24 +46,40 @@ __device__ __forceinline__ uint32_t fast_codes(uint32_t w0, uint32_t w1, float2 
 }
 
 // NT threads, V 16-byte pieces a thread in registers, or (V = 0) one value at a
-// time from memory twice (rows that are not 16-byte aligned, or longer).  A
+// time from memory twice (strides that align with nothing, or longer rows).  A
 // block walks tokens gridDim.x apart and requests the next one's pieces before
 // it works on this one's.
-template <int NT, int V>
+//
+// SHIFT: rows that start anywhere, K odd for instance, where x and q are aligned
+// as wholes and x's and q's rows start at the same place in a piece of eight.
+// Pieces are those of the whole tensors; a row's first and last one may belong
+// to its neighbours in part: their values count as zeros and their codes are
+// not written.  (4346 tokens of 9668: XXX us, one value at a time 64.)
+template <int NT, int V, bool SHIFT>
 __global__ void __launch_bounds__(NT) quantize_tokens_kernel(const uint16_t* __restrict__ x, long long ld,
                                                              int8_t* __restrict__ q, float* __restrict__ sc, int T,
                                                              int K) {
   __shared__ uint32_t s_max[2][NT / 32];
-  const int tid = threadIdx.x, n = K / 8;
+  const int tid = threadIdx.x;
   pdl_launch_dependents();
   pdl_wait();
   uint4 c[V > 0 ? V : 1], next[V > 0 ? V : 1];
   auto load = [&](int t, uint4* to) {
-    const uint4* row = reinterpret_cast<const uint4*>(x + (size_t)t * ld);
+    const size_t start = (size_t)t * ld;
+    const int ph = SHIFT ? (int)(start & 7) : 0, n = SHIFT ? (ph + K + 7) / 8 : K / 8;
+    const uint4* row = reinterpret_cast<const uint4*>(x + (start - ph));
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int at = tid + i * NT;
-      to[i] = at < n ? __ldcs(row + at) : make_uint4(0, 0, 0, 0);
+      const int at = tid + i * NT, lo = 8 * at - ph;  // lo: the piece's first value in the row
+      if (SHIFT && at < n && (lo < 0 || lo + 8 > K)) {
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (lo + j >= 0 && lo + j < K) w[j >> 1] |= (uint32_t)x[start + lo + j] << (16 * (j & 1));
+        to[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+        to[i] = at < n ? __ldcs(row + at) : make_uint4(0, 0, 0, 0);
+      }
     }
   };
   if constexpr (V > 0) load(blockIdx.x, next);
@@ -71,6 +87,7 @@ __global__ void __launch_bounds__(NT) quantize_tokens_kernel(const uint16_t* __r
   for (int t = blockIdx.x; t < T; t += gridDim.x, turn ^= 1) {
     const uint16_t* row = x + (size_t)t * ld;
     int8_t* out = q + (size_t)t * K;
+    const int ph = SHIFT ? (int)((size_t)t * K & 7) : 0, n = SHIFT ? (ph + K + 7) / 8 : K / 8;
     uint32_t m = 0;  // the largest |x| as bits: ordered like the values, NaN above infinity
     if constexpr (V > 0) {
 #pragma unroll
@@ -118,7 +135,14 @@ __global__ void __launch_bounds__(NT) quantize_tokens_kernel(const uint16_t* __r
             o[j >> 1] |= (lo | (hi << 8)) << (16 * (j & 1));
           }
         }
-        __stcs(reinterpret_cast<uint2*>(out) + at, make_uint2(o[0], o[1]));
+        const int lo = 8 * at - ph;
+        if (SHIFT && (lo < 0 || lo + 8 > K)) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (lo + j >= 0 && lo + j < K) out[lo + j] = (int8_t)(o[j >> 2] >> (8 * (j & 3)));
+        } else {
+          __stcs(reinterpret_cast<uint2*>(out + lo), make_uint2(o[0], o[1]));
+        }
       }
     } else {
       for (int i = tid; i < K; i += NT)
@@ -127,16 +151,25 @@ __global__ void __launch_bounds__(NT) quantize_tokens_kernel(const uint16_t* __r
   }
 }
 
-template <int NT, int V>
+template <int NT, int V, bool SHIFT = false>
 cudaError_t go(const void* x, long long ld, int8_t* q, float* sc, int T, int K, cudaStream_t s) {
-  return ops_launch(quantize_tokens_kernel<NT, V>, dim3((unsigned)std::min(T, 2048 / NT * ops_num_sms())), NT, 0, s, 1, (const uint16_t*)x, ld, q, sc, T, K);
+  return ops_launch(quantize_tokens_kernel<NT, V, SHIFT>, dim3((unsigned)std::min(T, 2048 / NT * ops_num_sms())), NT, 0, s, 1, (const uint16_t*)x, ld, q, sc, T, K);
 }
 
 }  // namespace
 
 cudaError_t launch_quantize_tokens(const void* x, long long ld, int8_t* q, float* sc, int T, int K, cudaStream_t s) {
-  const bool vec = K % 8 == 0 && ld % 8 == 0 && ((uintptr_t)x & 15) == 0 && ((uintptr_t)q & 7) == 0;
-  if (!vec || K > 512 * 4 * 8) return go<256, 0>(x, ld, q, sc, T, K, s);
+  const bool aligned = ((uintptr_t)x & 15) == 0 && ((uintptr_t)q & 7) == 0;
+  const int most = K % 8 ? (K + 14) / 8 : K / 8;  // pieces of a row
+  if (!aligned || (T > 1 && (ld - K) % 8 != 0) || most > 512 * 4) return go<256, 0>(x, ld, q, sc, T, K, s);
+  if (K % 8 != 0) {
+    const int n = most;
+    if (n <= 128) return go<128, 1, true>(x, ld, q, sc, T, K, s);
+    if (n <= 256) return go<256, 1, true>(x, ld, q, sc, T, K, s);
+    if (n <= 512) return go<256, 2, true>(x, ld, q, sc, T, K, s);
+    if (n <= 1024) return go<256, 4, true>(x, ld, q, sc, T, K, s);
+    return go<512, 4, true>(x, ld, q, sc, T, K, s);
+  }
   const int n = K / 8;
   if (n <= 128) return go<128, 1>(x, ld, q, sc, T, K, s);
   if (n <= 256) return go<256, 1>(x, ld, q, sc, T, K, s);

@@ -132,6 +132,28 @@ def test_quantize_tokens(T, K):
     assert (q.cpu().numpy() == code).all()
 
 
+@pytest.mark.parametrize("T", [1, 2, 9, 700])
+@pytest.mark.parametrize("K,pad", [(1, 0), (3, 0), (7, 8), (9, 0), (15, 16), (1001, 0), (1019, 8), (2047, 0), (4095, 5),
+                                   (8193, 0), (8196, 64), (11577, 0), (16370, 0), (16383, 0), (16384, 0)])
+def test_quantize_rows_that_start_anywhere(T, K, pad):
+    """Rows of odd lengths next to rows of NaN and infinities, which must not reach them, and codes next to codes."""
+    wide = torch.randn(T, K + pad, generator=gen(T + K), device=DEV).to(BF)
+    x = wide[:, :K]
+    wide[:, K:] = math.inf
+    for r, v in ((1, math.nan), (4, math.inf), (6, 0.0)):
+        x[r:r + 1] = v
+    q, s = sffn.quantize_tokens(x)
+    for r in range(T):
+        if r in (1, 4):
+            assert torch.isnan(s[r]) and (q[r] == 0).all()
+    xc = x.float().cpu().numpy()
+    xc[[r for r in (1, 4) if r < T]] = 0
+    sc = abs(xc).max(1) / xc.dtype.type(127)
+    code = (xc / (sc + (sc == 0))[:, None]).round().clip(-127, 127)
+    assert (torch.nan_to_num(s).cpu().numpy() == sc).all()
+    assert (q.cpu().numpy() == code).all()
+
+
 def test_quantize_special_values_and_strides():
     x = torch.randn(6, 512, generator=gen(3), device=DEV).to(BF)
     x[1, 3], x[2, 5], x[3, 7] = math.nan, math.inf, -math.inf
@@ -277,6 +299,30 @@ def test_grouped_matmul_int8_reads_tokens_through_an_index():
     y = sffn.grouped_matmul(x, w, routing.offsets, sx=sx, sw=sw, index=routing.rows, index_div=k, dtype="f32")
     z = sffn.grouped_matmul(x[src].contiguous(), w, routing.offsets, sx=sx[src].contiguous(), sw=sw, dtype="f32")
     assert torch.equal(y, z)
+
+
+@pytest.mark.parametrize("T,N,K", [(2048, 2048, 4096), (2100, 3001, 2064), (3000, 5001, 1040)])
+def test_matmul_int8_copies(T, N, K):
+    """Enough tiles for the fp16 copies of the codes."""
+    test_matmul_int8(T, N, K, "bf16")
+    test_matmul_int8(T, N, K, "f32")
+
+
+@pytest.mark.parametrize("k,index", [(1, False), (2, True)])
+def test_grouped_matmul_int8_copies(k, index):
+    g, T, E, N, K = gen(63), 1800 // k, 2, 6000, 2064
+    R, rows = T * k, torch.randperm(T * k, generator=torch.Generator().manual_seed(3)).to(DEV, torch.int32)
+    x, sx = int8_operands(g, T if index else R, K, full=True)
+    w, sw = int8_operands(g, E * N, K)
+    offsets = torch.tensor([0, R // 3, R], dtype=torch.int32, device=DEV)
+    y = sffn.grouped_matmul(x, w.view(E, N, K), offsets, sx, sw.view(E, N), index=rows if index else None,
+                            index_div=k, dtype="f32")
+    src = (rows // k).long() if index else torch.arange(R, device=DEV)
+    xq, s = x[src], sx[src]
+    for e, (a, b) in enumerate(((0, R // 3), (R // 3, R))):
+        scale = torch.outer(s[a:b].double(), sw.view(E, N)[e].double())
+        ref = (xq[a:b].double() @ w.view(E, N, K)[e].double().T) * scale
+        close(y[a:b], ref, 3 * 2.0 ** -24 * ref.abs() + int8_bound(xq[a:b], w.view(E, N, K)[e], scale))
 
 
 def test_grouped_matmul_int8_long_groups():
