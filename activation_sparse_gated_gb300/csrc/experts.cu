@@ -307,7 +307,16 @@ size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
 // Up to two choices an expert: the gate-first passes above; more: the grouped products on the tensor cores (us, passes
 // / products, ReLU at 90 %, D = 2560, H = 1024: 8 of 64 experts 50 / 83 at 4 tokens, 79 / 101 at 8, 134 / 129 at 16; 2 of
 // 8 experts 31 / 38 at 8 tokens, 51 / 40 at 16; D = H = 4096, 4 of 16 experts 192 / 213 at 8, 328 / 256 at 16).
-bool few(int T, int k, int E) { return (long long)T * k <= 2ll * E; }
+//
+// The passes cost by the unit, the products by the byte: with SiLU, where every unit is live, products from 12288 units of
+// all choices on (H = 1500, D = 320: 16 choices 38 / 32, 8 23 / 23; D = 4096, H = 2048: 5 choices 68 / 69, 8 92 / 85), and
+// else from 100 D units on (ReLU, H = 1500, D = 320: 32 choices 34 / 34, 80 65 / 39; D = 640: 37 / 42, 68 / 54; D = 1024:
+// 44 / 56, 79 / 71; D = 2560: 73 / 113, 140 / 143).
+bool few(const ExpertsArgs& a) {
+  const long long choices = (long long)a.T * a.k, units = choices * a.H;
+  if (choices > 2ll * a.E) return false;
+  return units <= (a.act == ACT_SILU ? 12288 : 100ll * a.D);
+}
 
 }  // namespace
 
@@ -320,7 +329,7 @@ size_t experts_workspace(int T, int k, int D, int H) {
 
 cudaError_t launch_experts(const ExpertsArgs& a, cudaStream_t s) {
   cudaError_t e;
-  if (few(a.T, a.k, a.E)) {
+  if (few(a)) {
     float* h = static_cast<float*>(a.workspace);
     const dim3 grid((unsigned)((a.H + EG_WARPS - 1) / EG_WARPS), (unsigned)(a.T == 1 ? a.k : std::min(a.E, a.T * a.k)));
     const size_t row = 2 * (size_t)a.D;

@@ -54,7 +54,7 @@ __device__ __forceinline__ uint32_t fast_codes(uint32_t w0, uint32_t w1, float2 
 // as wholes and x's and q's rows start at the same place in a piece of eight.
 // Pieces are those of the whole tensors; a row's first and last one may belong
 // to its neighbours in part: their values count as zeros and their codes are
-// not written.  (4346 tokens of 9668: XXX us, one value at a time 64.)
+// not written.  (4346 tokens of 9668: 37 us, one value at a time 64; 9672 28.)
 template <int NT, int V, bool SHIFT>
 __global__ void __launch_bounds__(NT) quantize_tokens_kernel(const uint16_t* __restrict__ x, long long ld,
                                                              int8_t* __restrict__ q, float* __restrict__ sc, int T,
