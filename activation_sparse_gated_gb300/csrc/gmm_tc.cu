@@ -755,22 +755,16 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
       for (int c0 = 32 * (ew >> 2); c0 < rows; c0 += 32 * (EW / 4)) {
         uint32_t v[32];
         tmem_ld32(ta + c0, v);
-        // lane j looks up where row j of the piece goes (-1: past the group) and its scale
-        int to = -1;
-        float sx = 0.f;
-        {
-          const int r = q.r0 + c0 + lane;
-          if (r < q.r1) {
-            to = r;
-            if (F16) {
-              int src = r;
-              if (p.g.index) {
-                const int i = p.g.index[r];
-                src = i >= 0 && i / p.g.index_div < p.g.XR ? i / p.g.index_div : -1;
-              }
-              sx = src >= 0 ? p.g.sx[src] : 0.f;
-            }
+        const int left = min(rows - c0, 32);  // rows of this piece, r0 + c0 on
+        const uint64_t y0 = (uint64_t)(uint32_t)(q.r0 + c0) * (uint64_t)p.g.ldy;
+        float sx = 0.f;  // lane j: the scale of row j
+        if (F16 && lane < left) {
+          int src = q.r0 + c0 + lane;
+          if (p.g.index) {
+            const int i = p.g.index[src];
+            src = i >= 0 && i / p.g.index_div < p.g.XR ? i / p.g.index_div : -1;
           }
+          sx = src >= 0 ? p.g.sx[src] : 0.f;
         }
         if constexpr (GATED) {
           uint32_t u[32];
@@ -814,11 +808,10 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int j = 4 * i + (lane >> 3), c = 4 * (lane & 7);
-                const int row = __shfl_sync(0xffffffffu, to, 16 * h + j);
                 const uint4 d = lds16a(buf + (uint32_t)(j * TG_EPI_PITCH + c) * 4u);
-                if (row >= 0 && nc + c < p.g.NY)
-                  *reinterpret_cast<uint4*>(reinterpret_cast<float*>(p.g.y) + (uint64_t)(uint32_t)row * (uint64_t)p.g.ldy +
-                                            nc + c) = d;
+                if (16 * h + j < left && nc + c < p.g.NY)
+                  *reinterpret_cast<uint4*>(reinterpret_cast<float*>(p.g.y) + y0 +
+                                            (uint64_t)(16 * h + j) * (uint64_t)p.g.ldy + nc + c) = d;
               }
               __syncwarp();
             }
@@ -838,15 +831,14 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
               const int j = 8 * i + (lane >> 2), c = 8 * (lane & 3);
               const uint32_t at = buf + (uint32_t)(j * TG_EPI_PITCH + c) * 4u;
               const uint4 d = lds16a(at), e = lds16a(at + 16);
-              const int ra = __shfl_sync(0xffffffffu, to, 2 * j), rb = __shfl_sync(0xffffffffu, to, 2 * j + 1);
-              __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(p.g.y) + nc + c;
+              __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(p.g.y) + y0 + (uint64_t)(2 * j) * (uint64_t)p.g.ldy + nc + c;
               if (nc + c < p.g.NY) {
-                if (ra >= 0)
-                  *reinterpret_cast<uint4*>(y + (uint64_t)(uint32_t)ra * (uint64_t)p.g.ldy) =
+                if (2 * j < left)
+                  *reinterpret_cast<uint4*>(y) =
                       make_uint4(__byte_perm(d.x, d.y, 0x5410), __byte_perm(d.z, d.w, 0x5410),
                                  __byte_perm(e.x, e.y, 0x5410), __byte_perm(e.z, e.w, 0x5410));
-                if (rb >= 0)
-                  *reinterpret_cast<uint4*>(y + (uint64_t)(uint32_t)rb * (uint64_t)p.g.ldy) =
+                if (2 * j + 1 < left)
+                  *reinterpret_cast<uint4*>(y + p.g.ldy) =
                       make_uint4(__byte_perm(d.x, d.y, 0x7632), __byte_perm(d.z, d.w, 0x7632),
                                  __byte_perm(e.x, e.y, 0x7632), __byte_perm(e.z, e.w, 0x7632));
               }
@@ -854,18 +846,20 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
             __syncwarp();
           }
         } else {
+          const uint32_t size = p.g.y_f32 ? 4 : 2;
+          uint8_t* to = reinterpret_cast<uint8_t*>(p.g.y) + (y0 + n) * size;
+          const uint64_t pitch = (uint64_t)p.g.ldy * size;
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
-            const int row = __shfl_sync(0xffffffffu, to, j);
             float f = __uint_as_float(v[j]);
             if (F16) f = f * __shfl_sync(0xffffffffu, sx, j) * sw;
-            if (nok && row >= 0) {
-              const uint64_t at = (uint64_t)(uint32_t)row * (uint64_t)p.g.ldy + n;
+            if (nok && j < left) {
               if (p.g.y_f32)
-                reinterpret_cast<float*>(p.g.y)[at] = f;
+                *reinterpret_cast<float*>(to) = f;
               else
-                reinterpret_cast<__nv_bfloat16*>(p.g.y)[at] = __float2bfloat16_rn(f);
+                *reinterpret_cast<__nv_bfloat16*>(to) = __float2bfloat16_rn(f);
             }
+            to += pitch;
           }
         }
       }
@@ -1086,13 +1080,14 @@ cudaError_t launch_gmm(const GmmArgs& a, cudaStream_t s) {
   }
   if (a.i8) return a.R <= std::max(a.E, 4) ? launch_gmm_rows(a, s) : launch_gmm_tc(a, 1, 128, s);
   // A pair's 256 x 256 tiles from 96 rows a group on, where they fill the SMs (us, 128 x 128 / pair tiles; 64 experts, N =
-  // 1024, K = 2560: 64 rows each 63 / 65, 96 72 / 68, 256 102 / 83; one, N = K = 4096: 256 rows 17 / 24, 512 19 / 24).
+  // 1024, K = 2560: 64 rows each 63 / 65, 96 72 / 68, 256 102 / 83; one, N = K = 4096: 256 rows 17 / 24, 512 19 / 24)
+  // and N fills more than one of the pair's blocks (16384 rows, 16 experts, N = 100, K = 2560: 21 / 25).
   const long long pairs = (long long)((a.N + 255) / 256) * busy * (((a.R + busy - 1) / busy + 255) / 256);
   const bool fill = 2 * pairs >= ops_num_sms();
   // Gate and up together: 256 rows a tile take all of TMEM, so their epilogue is not hidden, and still win from 128
   // rows a group on (4096 tokens, 8 of 64 experts, D = 2560, H = 1024: 561 against 643 us; 512 tokens 225 / 211).
-  if (a.w3) return a.R >= 128 * busy && fill ? launch_gmm_tc(a, 2, 256, s) : launch_gmm_tc(a, 1, 128, s);
-  return a.R >= 96 * busy && fill ? launch_gmm_tc(a, 2, 256, s) : launch_gmm_tc(a, 1, 128, s);
+  if (a.w3) return a.R >= 128 * busy && fill && a.N > 128 ? launch_gmm_tc(a, 2, 256, s) : launch_gmm_tc(a, 1, 128, s);
+  return a.R >= 96 * busy && fill && a.N > 128 ? launch_gmm_tc(a, 2, 256, s) : launch_gmm_tc(a, 1, 128, s);
 }
 
 }  // namespace sffn
