@@ -15,7 +15,7 @@
 // cluster of blocks owns a chunk of consecutive tokens (a token or two a warp:
 // the choice is a chain of dependent steps, so it wants warps) and counts its
 // choices per expert, and a second kernel adds the counts of the chunks before
-// its own.  Up to ROUTE_ONE choices one block does both.
+// its own.  A few choices are one block's work altogether.
 //
 // Measured (us): one token, 8 of 64 experts, 6.4 a call, 2.9 in a graph (a chain
 // of dependent steps, next to nothing is read); 16384 tokens, 8 of 256 experts,
@@ -30,7 +30,9 @@ namespace {
 
 constexpr int ROUTE_WARPS = 16;
 constexpr int ROUTE_THREADS = 32 * ROUTE_WARPS;
-constexpr int ROUTE_ONE = 512;    // choices that one block sorts by itself
+// Choices that one block sorts by itself, of so many tokens at most (us, one block / two kernels, 2 of 8 experts: 64 tokens
+// 6.7 / 9.4, 128 8.8 / 9.3, 256 15.2 / 9.4; 8 of 64: 64 tokens 7.4 / 9.3; 8 of 256: 48 8.6 / 9.8, 64 10.6 / 9.6).
+constexpr int ROUTE_ONE = 512, ROUTE_ONE_TOKENS = 128;
 constexpr int ROUTE_CHUNKS = 128; // most chunks of the two-kernel form
 
 // Larger float <-> larger key; NaN and -inf share the key 0 (closed).
@@ -418,6 +420,8 @@ int scatter_warps(int E, int fixed_ints) {
   return w < 1 ? 1 : w > ROUTE_WARPS ? ROUTE_WARPS : w;
 }
 
+bool one_block(int T, int k) { return T <= ROUTE_ONE_TOKENS && (long long)T * k <= ROUTE_ONE; }
+
 int route_chunks(int T, int* per) {
   *per = (T + ROUTE_CHUNKS - 1) / ROUTE_CHUNKS;
   if (*per < ROUTE_WARPS) *per = ROUTE_WARPS;
@@ -427,7 +431,7 @@ int route_chunks(int T, int* per) {
 template <int L, bool BF16>
 cudaError_t route_lt(const RouteArgs& a, cudaStream_t s) {
   if (a.T == 1) return ops_launch(route_token_kernel<L, BF16>, dim3(1), 32, 0, s, 1, a);
-  if ((long long)a.T * a.k <= ROUTE_ONE) {
+  if (one_block(a.T, a.k)) {
     const int fixed = a.E + 1 + ROUTE_WARPS, warps = scatter_warps(a.E, fixed);
     return ops_launch(route_one_kernel<L, BF16>, dim3(1), ROUTE_THREADS, sizeof(int) * (fixed + warps * a.E), s, 1, a, warps);
   }
@@ -450,7 +454,7 @@ cudaError_t route_l(const RouteArgs& a, cudaStream_t s) {
 }  // namespace
 
 size_t route_workspace(int T, int E, int k) {
-  if ((long long)T * k <= ROUTE_ONE) return 0;
+  if (one_block(T, k)) return 0;
   int per;
   return sizeof(int) * (size_t)route_chunks(T, &per) * E;
 }
