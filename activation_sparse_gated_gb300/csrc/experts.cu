@@ -90,7 +90,7 @@ __device__ __forceinline__ void gate_rows(const ExpertsArgs& a, float* __restric
   bool live = false;
 #pragma unroll
   for (int t = 0; t < TM; ++t) {
-    g[t] = activation(a.act, g[t]);
+    g[t] = g[t] != g[t] ? g[t] : activation(a.act, g[t]);  // a NaN gate is live: its token must come out as NaN
     u[t] = 0.f;
     live = live || (p[t] >= 0 && g[t] != 0.f);
   }

@@ -418,8 +418,11 @@ int sffn_grouped_matmul(const void* x, long long ldx, const float* sx, const voi
  * for the same T, E, k; W1, W3 are [E, H, D] and W2t is W2 transposed, [E, H, D]
  * (row i of expert e is column i of W2_e), dense; x [T, D] (row pitch ldx), y
  * [T, D] dense, fully written: a token without an open expert gets 0, a choice
- * of weight 0 adds nothing.  D % 8 == 0, any H >= 1.  x, W1, W3, W2t and y are
- * 16-byte aligned and y overlaps none of them; the workspace holds
+ * of weight 0 adds nothing.  A unit whose gate A(W1_e x_t) is 0 is dead and adds
+ * exactly 0, also where its up value is infinite or NaN; a NaN gate is live, so a
+ * token that holds a NaN comes out as NaN.  (Weights are taken to be finite: not
+ * every form reads those of a dead unit.)  D % 8 == 0, any H >= 1.  x, W1, W3,
+ * W2t and y are 16-byte aligned and y overlaps none of them; the workspace holds
  * sffn_experts_workspace(T, k, D, H) bytes.
  */
 size_t sffn_experts_workspace(int T, int k, int D, int H);

@@ -700,3 +700,44 @@ def test_wrappers_refuse_on_the_gpu():
         sffn.grouped_matmul(x[:, :60], w[:, :, :60].contiguous(), off)
     with pytest.raises(sffn.SffnError, match="overlap"):
         sffn.grouped_matmul(x, w, off, out=x[:, :8])
+
+
+# ------------------------------------------------------------------ values that are no numbers, and values at the types' ends
+
+
+# one token; few tokens (staged, too long to stage); products of one block, with K cut over a cluster, of pairs of blocks
+FORMS = [(1, 8, 2, 128, 100), (5, 16, 4, 384, 130), (3, 4, 2, 6000, 24), (33, 8, 2, 520, 200), (64, 4, 2, 2560, 130),
+         (4000, 8, 2, 264, 600)]
+
+
+@pytest.mark.parametrize("T,E,k,D,H", FORMS)
+@pytest.mark.parametrize("act", ["relu", "rsp", "silu"])
+def test_experts_nan_stays_visible_and_with_its_token(T, E, k, D, H, act):
+    """A token that holds a NaN comes out as NaN, however many tokens there are, and leaves the others as they are."""
+    g = gen(T + D)
+    x = torch.randn(T, D, generator=g, device=DEV).to(BF)
+    W1, W3, W2t = ((torch.randn(E, H, D, generator=g, device=DEV) * 0.05).to(BF) for _ in range(3))
+    routing = sffn.route(torch.randn(T, E, generator=g, device=DEV), k)
+    clean = sffn.experts_forward(x, routing, W1, W3, W2t, act=act)
+    at = T // 2
+    x[at, D // 3] = math.nan
+    y = sffn.experts_forward(x, routing, W1, W3, W2t, act=act)
+    assert torch.isnan(y[at]).all()
+    keep = [t for t in range(T) if t != at]
+    assert torch.isfinite(clean).all() and torch.equal(y[keep], clean[keep])
+
+
+@pytest.mark.parametrize("T,E,k,D,H", FORMS)
+@pytest.mark.parametrize("act", ["relu", "rsp", "silu"])
+def test_experts_dead_unit_adds_nothing(T, E, k, D, H, act):
+    """A unit whose gate is 0 adds exactly 0, also where its up value overflows to infinity."""
+    g = gen(T + H)
+    x = (torch.rand(T, D, generator=g, device=DEV) + 0.5).to(BF)
+    W1, W3, W2t = ((torch.randn(E, H, D, generator=g, device=DEV) * 0.05).to(BF) for _ in range(3))
+    W1[:, 3] = -1000.0  # SiLU of less than -100 is 0 in fp32
+    W3[:, 3] = 0
+    routing = sffn.route(torch.randn(T, E, generator=g, device=DEV), k)
+    clean = sffn.experts_forward(x, routing, W1, W3, W2t, act=act)
+    W3[:, 3] = 3e38
+    assert torch.equal(sffn.experts_forward(x, routing, W1, W3, W2t, act=act), clean)
+    assert torch.isfinite(clean).all()
