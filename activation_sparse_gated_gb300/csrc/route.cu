@@ -4,7 +4,9 @@
 // are closed experts and are never chosen), their weights
 //   softmax   w_j = exp(z_j - m) / sum_i exp(z_i - m), i over the chosen
 //             (normalised) or over all E
-//   sigmoid   w_j = 1 / (1 + exp(-z_j)), over their sum when normalised,
+//   sigmoid   w_j = 1 / (1 + exp(-z_j)), over their sum when normalised (where
+//             the largest z_j, m, is below 0, both times 1 + exp(-m): fp32 holds
+//             no sigmoid below about -88, but their ratios it does),
 // and a stable counting sort of the T k choices by expert: offsets[E + 1] and,
 // for every grouped row, the choice token * k + place that it serves.
 //
@@ -44,6 +46,10 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
+
+// Below this a sigmoid is 0 in binary64 as well (exp(-745.2) rounds to 0): a token whose largest logit lies there, at a
+// mask of the type's lowest value say, keeps weights of 0.
+constexpr float SIGMOID_LOWEST = -745.f;
 
 // exp(v - m) for v <= m, with equal infinities counting as equal
 __device__ __forceinline__ float exp_below(float v, float m) { return v == m ? 1.f : expf(v - m); }
@@ -207,7 +213,14 @@ __device__ __forceinline__ int choose(const RouteArgs& a, int t, int lane) {
   const int ce = ck ? keys.index(ck, cl) : -1;
   const float m = keys.value(__shfl_sync(0xffffffffu, ck, 0)), v = keys.value(ck);
   float w = 0.f;
-  if (ce >= 0) w = a.sigmoid ? 1.f / (1.f + expf(-v)) : exp_below(v, m);
+  if (ce >= 0) {
+    if (!a.sigmoid)
+      w = exp_below(v, m);
+    else if (a.normalize && m < 0.f && m > SIGMOID_LOWEST)
+      w = exp_below(v, m) * (1.f + expf(m)) / (1.f + expf(v));
+    else
+      w = 1.f / (1.f + expf(-v));
+  }
   float total = 1.f;
   if (a.normalize) total = warp_sum(w);
   else if (!a.sigmoid) total = all;

@@ -355,7 +355,9 @@ enum { SFFN_I8 = 4 };
  *   weights [T, k] fp32: exp(z_j - m) / sum exp(z_i - m), summed over all open
  *     experts, or over the chosen ones with SFFN_ROUTE_NORMALIZE;
  *     SFFN_ROUTE_SIGMOID: 1 / (1 + exp(-z_j)), over the chosen ones' sum with
- *     SFFN_ROUTE_NORMALIZE.  0 for a place without an open expert.
+ *     SFFN_ROUTE_NORMALIZE (the ratios hold also where fp32 has no number for the
+ *     sigmoids themselves; a token whose largest logit is below -745, where
+ *     binary64 has none either, gets 0).  0 for a place without an open expert.
  *   ids [T, k]: the chosen experts, -1 for a place without an open expert.
  *   offsets [E + 1], rows [T * k]: the choices in order of (expert, token,
  *     place): grouped row r of expert e, offsets[e] <= r < offsets[e + 1], is

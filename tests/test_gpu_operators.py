@@ -741,3 +741,28 @@ def test_experts_dead_unit_adds_nothing(T, E, k, D, H, act):
     W3[:, 3] = 3e38
     assert torch.equal(sffn.experts_forward(x, routing, W1, W3, W2t, act=act), clean)
     assert torch.isfinite(clean).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF], ids=str)
+@pytest.mark.parametrize("T,E,k", [(1, 8, 8), (5, 48, 6), (700, 48, 6), (300, 300, 8)])
+def test_route_normalised_sigmoid_of_very_negative_logits(T, E, k, dtype):
+    """The ratio of two sigmoids is an ordinary number where both are too small for fp32."""
+    z = -85 - 115 * torch.rand(T, E, generator=gen(T + E), device=DEV)
+    z[0] = -90.0
+    if T > 3:
+        z[1] = -86 - 3 * torch.rand(E, generator=gen(1), device=DEV)  # sigmoids at fp32's smallest normal number
+        z[2] -= 3e4
+        z[3] = -math.inf
+        z[3, 4] = -1e30
+        z[4] *= 3.4
+    z = z.to(dtype)
+    w, ids, _, _ = sffn.route(z, k, score="sigmoid", normalize=True)
+    v = torch.sort(-z.double().cpu(), dim=1, stable=True).values[:, :k].neg()
+    ls = torch.nn.functional.logsigmoid(v)
+    ref = torch.exp(ls - torch.logsumexp(ls, 1, keepdim=True))
+    ref[v[:, 0] < -745] = 0  # sigmoids that binary64 does not hold either: as good as masked
+    # the difference of two logits is rounded once, which exp turns into that share of its result (below 1e-37 past a
+    # difference of 88); exp itself 2 steps each, and a product, a quotient and sums of k terms
+    tol = 88 * 2.0 ** -24 + (k + 16) * 2.0 ** -23
+    torch.testing.assert_close(w.double().cpu(), ref, rtol=tol, atol=1e-37)
+    assert ids[0].tolist() == list(range(k))
