@@ -382,7 +382,11 @@ int sffn_quantize_tokens(const void* x, long long ldx, int8_t* q, float* scales,
 /*
  * y[t, n] = sx[t] sw[n] sum_k xq[t, k] wq[n, k]: int8 codes xq [T, K] (row
  * pitch ldx) and wq [N, K] with one scale per token and per output channel;
- * y [T, N] (row pitch ldy) bf16 or f32.  K % 16 == 0, ldx % 16 == 0, xq and wq
+ * y [T, N] (row pitch ldy) bf16 or f32.  The sum is exact while its partial sums
+ * stay below 2^24.  Past that the form that takes the call shows: the dot products
+ * of few rows (up to four, or as many as there are experts) sum in int32 and round
+ * once, the tensor cores add in fp32, 16 products a step, and may lose 17 * 2^-23
+ * of the running sum in each.  K % 16 == 0, ldx % 16 == 0, xq and wq
  * 16-byte aligned.  The workspace holds sffn_grouped_workspace(T, T, N, K, 1,
  * SFFN_I8) bytes (0 for short batches: NULL is fine).
  */

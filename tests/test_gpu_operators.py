@@ -766,3 +766,45 @@ def test_route_normalised_sigmoid_of_very_negative_logits(T, E, k, dtype):
     tol = 88 * 2.0 ** -24 + (k + 16) * 2.0 ** -23
     torch.testing.assert_close(w.double().cpu(), ref, rtol=tol, atol=1e-37)
     assert ids[0].tolist() == list(range(k))
+
+
+def largest_partial_sum(xq, wq):
+    """The largest magnitude that a sum of consecutive products can have: at most twice the largest prefix's."""
+    most = 0
+    for row in xq:
+        most = max(most, (row.long() * wq.long()).cumsum(1).abs().max().item())
+    return 2 * most
+
+
+@pytest.mark.parametrize("T,N,K", [(3, 90, 65536), (4, 300, 14336), (5, 90, 65536), (40, 90, 65536), (130, 200, 14336),
+                                   (300, 130, 4096)])
+def test_matmul_int8_is_exact_below_2_24(T, N, K):
+    """Every partial sum is an integer below 2^24, so nothing but the scales is rounded, however long the sum."""
+    g = gen(T + K)
+    xq, sx = int8_operands(g, T, K)
+    wq, sw = int8_operands(g, N, K)
+    assert largest_partial_sum(xq, wq) < 2 ** 24
+    ref = (xq.double() @ wq.double().T) * torch.outer(sx.double(), sw.double())
+    close(sffn.matmul_int8(xq, sx, wq, sw, dtype="f32"), ref, 2 * 2.0 ** -24 * ref.abs())
+    off = torch.tensor([0, T // 2, T], dtype=torch.int32, device=DEV)
+    y = sffn.grouped_matmul(xq, wq.expand(2, N, K).contiguous(), off, sx=sx, sw=sw.expand(2, N).contiguous(), dtype="f32")
+    close(y, ref, 2 * 2.0 ** -24 * ref.abs())
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 64, 65536), (4, 64, 2048), (4, 64, 14336), (4, 64, 65536), (5, 64, 2048),
+                                   (5, 64, 14336), (5, 64, 65536), (130, 200, 14336), (300, 130, 65536),
+                                   (2048, 2048, 4096), (2100, 3001, 14336)])
+def test_matmul_int8_sums_past_2_24(T, N, K):
+    """Codes of one sign, so that every sum passes 2^24.  Up to four rows sum in int32 and round once; the tensor cores
+    add 16 products and the running sum at a time in fp32, each of the 17 terms cut to the last place of the largest.
+    The running sum grows evenly, so n = K / 16 steps lose less than 17 * 2^-23 * (n + 1) / 2 of the sum, and blocks that
+    share K join at most eight parts."""
+    g = gen(T + K)
+    xq = torch.randint(100, 128, (T, K), generator=g, device=DEV, dtype=torch.int8)
+    wq = torch.randint(100, 128, (N, K), generator=g, device=DEV, dtype=torch.int8)
+    sx, sw = (torch.rand(n, generator=g, device=DEV) + 0.5 for n in (T, N))
+    total = xq.double() @ wq.double().T
+    assert total.min() > 2 ** 24
+    ref = total * torch.outer(sx.double(), sw.double())
+    share = 2.0 ** -24 if T <= 4 else 17 * 2.0 ** -23 * (K / 16 + 1) / 2 + 8 * 2.0 ** -23
+    close(sffn.matmul_int8(xq, sx, wq, sw, dtype="f32"), ref, (share * 1.01 + 3 * 2.0 ** -24) * ref)
