@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(NT) quantize_tokens_kernel(const uint16_t* __r
   pdl_launch_dependents();
   pdl_wait();
   uint4 c[V > 0 ? V : 1], next[V > 0 ? V : 1];
-  auto load = [&](int t, uint4* to) {
+  auto load = [&](uint32_t t, uint4* to) {
     const size_t start = (size_t)t * ld;
     const int ph = SHIFT ? (int)(start & 7) : 0, n = SHIFT ? (ph + K + 7) / 8 : K / 8;
     const uint4* row = reinterpret_cast<const uint4*>(x + (start - ph));
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(NT) quantize_tokens_kernel(const uint16_t* __r
   };
   if constexpr (V > 0) load(blockIdx.x, next);
   int turn = 0;
-  for (int t = blockIdx.x; t < T; t += gridDim.x, turn ^= 1) {
+  for (uint32_t t = blockIdx.x; t < (uint32_t)T; t += gridDim.x, turn ^= 1) {  // (unsigned: t may pass 2^31 at the end)
     const uint16_t* row = x + (size_t)t * ld;
     int8_t* out = q + (size_t)t * K;
     const int ph = SHIFT ? (int)((size_t)t * K & 7) : 0, n = SHIFT ? (ph + K + 7) / 8 : K / 8;
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(NT) quantize_tokens_kernel(const uint16_t* __r
     if constexpr (V > 0) {
 #pragma unroll
       for (int i = 0; i < V; ++i) c[i] = next[i];
-      if (t + gridDim.x < T) load(t + gridDim.x, next);
+      if (t + gridDim.x < (uint32_t)T) load(t + gridDim.x, next);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};

@@ -808,3 +808,13 @@ def test_matmul_int8_sums_past_2_24(T, N, K):
     ref = total * torch.outer(sx.double(), sw.double())
     share = 2.0 ** -24 if T <= 4 else 17 * 2.0 ** -23 * (K / 16 + 1) / 2 + 8 * 2.0 ** -23
     close(sffn.matmul_int8(xq, sx, wq, sw, dtype="f32"), ref, (share * 1.01 + 3 * 2.0 ** -24) * ref)
+
+
+def test_quantize_as_many_tokens_as_an_int_counts():
+    """The last tokens' numbers are within a step of 2^31: a block's next token must not turn negative."""
+    T = 2 ** 31 - 100
+    x = torch.ones(T, 1, device=DEV, dtype=BF)
+    x[-3:, 0] = torch.tensor([0.0, -254.0, 2.0], dtype=BF, device=DEV)
+    q, s = sffn.quantize_tokens(x)
+    assert s[-3:].tolist() == [0.0, 2.0, torch.tensor(2.0).div(127).item()] and q[-3:, 0].tolist() == [0, -127, 127]
+    assert (q[:-3] == 127).all() and (s[:-3] == torch.tensor(1.0, device=DEV).div(127)).all()
