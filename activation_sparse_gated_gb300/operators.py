@@ -15,6 +15,7 @@ here then does the same and names what is wrong.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from functools import lru_cache
 
@@ -320,7 +321,10 @@ class MoEFFN:
         self.k, self.act, self.score, self.normalize = k, act, score, normalize
 
     def route(self, x):
-        return route(x.float() @ self.Wr.T, self.k, self.score, self.normalize)
+        # a NaN logit closes an expert, and with all of them closed a corrupted token would come out as 0: it counts as 0
+        # instead, so that the token has experts, which keep its NaN
+        z = (x.float() @ self.Wr.T).nan_to_num_(nan=0.0, posinf=math.inf, neginf=-math.inf)
+        return route(z, self.k, self.score, self.normalize)
 
     def forward(self, x):
         return experts_forward(x, self.route(x), self.W1, self.W3, self.W2t, self.act)

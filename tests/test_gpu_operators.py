@@ -818,3 +818,19 @@ def test_quantize_as_many_tokens_as_an_int_counts():
     q, s = sffn.quantize_tokens(x)
     assert s[-3:].tolist() == [0.0, 2.0, torch.tensor(2.0).div(127).item()] and q[-3:, 0].tolist() == [0, -127, 127]
     assert (q[:-3] == 127).all() and (s[:-3] == torch.tensor(1.0, device=DEV).div(127)).all()
+
+
+@pytest.mark.parametrize("T", [1, 5, 300])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_moe_keeps_a_corrupted_token_visible(T, bad):
+    g, E, D, H = gen(T), 6, 128, 200
+    x = torch.randn(T, D, generator=g, device=DEV).to(BF)
+    Wr = torch.randn(E, D, generator=g, device=DEV)
+    W1, W3, W2 = (torch.randn(E, a, b, generator=g, device=DEV).to(BF) for a, b in ((H, D), (H, D), (D, H)))
+    moe = sffn.MoEFFN(Wr, W1, W3, W2, 2)
+    clean = moe(x)
+    x[T // 2, 7] = bad
+    y = moe(x)
+    assert not torch.isfinite(y[T // 2]).any()
+    keep = [t for t in range(T) if t != T // 2]
+    assert torch.equal(y[keep], clean[keep]) and torch.isfinite(clean).all()
