@@ -15,7 +15,6 @@ here then does the same and names what is wrong.
 from __future__ import annotations
 
 import ctypes
-import math
 import os
 from functools import lru_cache
 
@@ -306,12 +305,23 @@ def experts_forward(x, routing, W1, W3, W2t, act: str = "relu", out=None, stream
     return out
 
 
+def _parts(w):
+    """w as the sum of bf16 matrices [parts, *w.shape]: 8 of its bits each, so one holds bf16, two fp16 and three fp32."""
+    parts, rest = [], w.float()
+    for _ in range({torch.bfloat16: 1, torch.float16: 2}.get(w.dtype, 3)):
+        parts.append(rest.to(torch.bfloat16))
+        rest = rest - parts[-1].float()
+    return torch.stack(parts)
+
+
 class MoEFFN:
     """A mixture of gated experts behind its router, ``y = moe(x)`` for x [T, D] bf16.
 
-    ``Wr`` [E, D] is the router's matrix (its logits are an fp32 product by torch), W1, W3 [E, H, D] and
-    W2 [E, D, H] the experts' weights; W2 is laid out once as [E, H, D], so that a live unit's column is
-    one contiguous row.  ``k`` choices a token, ``score`` and ``normalize`` as in :func:`route`.
+    ``Wr`` [E, D] is the router's matrix, W1, W3 [E, H, D] and W2 [E, D, H] the experts' weights.  Wr and W2 are laid out
+    once, when the layer is made: W2 as [E, H, D], so that a live unit's column is one contiguous row, and Wr as bf16
+    parts whose sum it is, for :func:`grouped_matmul`: the logits are sums in fp32 of all of Wr's bits, whatever
+    precision the process allows its matrix products.  ``k`` choices a token, ``score`` and ``normalize`` as in
+    :func:`route`.  A token that holds a NaN or an infinity does not come out finite.
     """
 
     def __init__(self, Wr, W1, W3, W2, k: int, act: str = "relu", score: str = "softmax", normalize: bool = True):
@@ -319,12 +329,18 @@ class MoEFFN:
         self.W1, self.W3 = W1.contiguous(), W3.contiguous()
         self.W2t = W2.transpose(1, 2).contiguous()
         self.k, self.act, self.score, self.normalize = k, act, score, normalize
+        parts = _parts(Wr)
+        self._shape = tuple(parts.shape[:2])
+        self._parts = parts.reshape(1, -1, Wr.shape[1])  # one group of parts * E rows
+        self._all = torch.tensor([0, 2 ** 31 - 1], dtype=torch.int32, device=Wr.device)  # its rows, however many
 
     def route(self, x):
-        # a NaN logit closes an expert, and with all of them closed a corrupted token would come out as 0: it counts as 0
-        # instead, so that the token has experts, which keep its NaN
-        z = (x.float() @ self.Wr.T).nan_to_num_(nan=0.0, posinf=math.inf, neginf=-math.inf)
-        return route(z, self.k, self.score, self.normalize)
+        z = grouped_matmul(x, self._parts, self._all, dtype="f32")
+        if self._shape[0] > 1:
+            z = z.view(-1, *self._shape).sum(1)
+        # a logit of NaN or -inf closes an expert, and with all of them closed a corrupted token would come out as 0: it
+        # counts as 0, so that the token has experts, which keep its NaN
+        return route(z.nan_to_num_(0.0, 0.0, 0.0), self.k, self.score, self.normalize)
 
     def forward(self, x):
         return experts_forward(x, self.route(x), self.W1, self.W3, self.W2t, self.act)

@@ -834,3 +834,44 @@ def test_moe_keeps_a_corrupted_token_visible(T, bad):
     assert not torch.isfinite(y[T // 2]).any()
     keep = [t for t in range(T) if t != T // 2]
     assert torch.equal(y[keep], clean[keep]) and torch.isfinite(clean).all()
+
+
+@pytest.mark.parametrize("tf32", [False, True])
+@pytest.mark.parametrize("T", [1, 7, 300])
+def test_moe_choice_does_not_follow_the_tf32_switch(T, tf32):
+    """Experts whose logits differ by less than TF32 resolves are told apart, whatever the process-wide switch says."""
+    g, E, D, H = gen(T), 4, 256, 64
+    x = (torch.rand(T, D, generator=g, device=DEV) + 0.5).to(BF)
+    Wr = (1 + torch.arange(E, device=DEV) * 2.0 ** -13)[:, None].expand(E, D).contiguous()  # TF32 steps by 2^-10
+    W1, W3 = (torch.randn(E, H, D, generator=g, device=DEV).to(BF) for _ in range(2))
+    # an fp32 logit is off by D steps of 2^-23 at most, 2^-15 of its sum: a quarter of the gaps
+    moe = sffn.MoEFFN(Wr, W1, W3, W3.transpose(1, 2), 2)
+    before = torch.backends.cuda.matmul.allow_tf32
+    torch.backends.cuda.matmul.allow_tf32 = tf32
+    try:
+        ids = moe.route(x).ids
+    finally:
+        torch.backends.cuda.matmul.allow_tf32 = before
+    assert ids.tolist() == [[E - 1, E - 2]] * T
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, BF], ids=str)
+@pytest.mark.parametrize("T,E,D", [(0, 5, 64), (1, 64, 2560), (9, 7, 72), (400, 100, 1032)])
+def test_moe_router_product(T, E, D, dtype):
+    """The layer's weights against the softmax in 64 bits of all of Wr's bits."""
+    g = gen(T + D)
+    x = torch.randn(T, 2 * D, generator=g, device=DEV).to(BF)[:, 8:8 + D]
+    Wr = (torch.randn(E, D, generator=g, device=DEV) * 0.1).to(dtype)
+    W = torch.zeros(E, 8, D, device=DEV, dtype=BF)
+    weights, ids, _, _ = sffn.MoEFFN(Wr, W, W, W.transpose(1, 2), E if E < 32 else 32, normalize=False).route(x)
+    z, mag = x.double() @ Wr.double().T, x.double().abs() @ Wr.double().abs().T
+    # D steps of the product and three of the parts' sum, on logits; exp turns twice the largest into a share, and adds
+    # two steps of its own and those of a sum of E terms and a quotient
+    dz = (D + 4) * 2.0 ** -23 * mag.amax(1, keepdim=True)
+    p = torch.softmax(z, 1)
+    picked = p.gather(1, ids.long())
+    tol = picked * (2.1 * dz + (E + 8) * 2.0 ** -23)
+    assert ((weights.double() - picked).abs() <= tol).all()
+    # the chosen are the largest, as far as the logits' bounds tell them apart
+    left = z.scatter(1, ids.long(), -math.inf).amax(1, keepdim=True)
+    assert (z.gather(1, ids.long()) + 2 * dz >= left).all()
