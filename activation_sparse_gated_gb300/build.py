@@ -8,9 +8,11 @@ installed PyTorch's headers) -> _torch_calls.so, the tensor operators' calls.
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -82,18 +84,26 @@ TORCH_CALLS_SRC = os.path.join(PKG, "binding", "torch_calls.cpp")
 TORCH_CALLS = os.path.join(PKG, "_torch_calls.so")
 
 
-def build_torch_calls(force: bool = False) -> str:
-    """Compile _torch_calls.so next to the package (a few seconds)."""
+def _torch_dir():
+    """The installed PyTorch's directory; None without one that has CUDA.  (It is not imported.)"""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        return None
+    d = os.path.dirname(spec.origin)
+    return d if os.path.exists(os.path.join(d, "lib", "libtorch_cuda.so")) else None
+
+
+def build_torch_calls(force: bool = False):
+    """Compile _torch_calls.so next to the package (a few seconds).  Without a PyTorch that has CUDA there is nothing to
+    build it against: None, and the tensor operators go without it."""
+    torch_dir = _torch_dir()
+    if torch_dir is None:
+        sys.stderr.write("no PyTorch with CUDA: torch_calls.cpp is not built\n")
+        return None
     deps = [TORCH_CALLS_SRC, os.path.abspath(__file__), *glob.glob(os.path.join(INCLUDE, "*.h"))]
     if not force and os.path.exists(TORCH_CALLS) and \
             all(os.path.getmtime(p) <= os.path.getmtime(TORCH_CALLS) for p in deps):
         return TORCH_CALLS
-    import importlib.util
-    import sysconfig
-    spec = importlib.util.find_spec("torch")
-    if spec is None:
-        raise RuntimeError("PyTorch is not installed")
-    torch_dir = os.path.dirname(spec.origin)
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     tmp = TORCH_CALLS + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I", INCLUDE,
@@ -110,6 +120,10 @@ def build_torch_calls(force: bool = False) -> str:
     return TORCH_CALLS
 
 
+def main(argv) -> None:
+    print(build(force="--force" in argv, verbose="-v" in argv, debug="--debug" in argv))  # needs no PyTorch
+    print(build_torch_calls(force="--force" in argv))
+
+
 if __name__ == "__main__":
-    print(build_torch_calls(force="--force" in sys.argv))
-    print(build(force="--force" in sys.argv, verbose="-v" in sys.argv, debug="--debug" in sys.argv))
+    main(sys.argv)

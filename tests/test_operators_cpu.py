@@ -167,3 +167,39 @@ def test_tensor_wrappers_refuse():
         sffn.route(z[0], 2)
     with pytest.raises(AttributeError):
         sffn.no_such_operator
+
+
+def fake_torch(monkeypatch, root, version, libs):
+    """What build.py sees of an installed PyTorch of that version with those libraries."""
+    d = root / version / "torch"
+    (d / "lib").mkdir(parents=True)
+    (d / "__init__.py").write_text("")
+    (d / "version.py").write_text(f"from typing import Optional\n__version__ = '{version}'\ncuda = '13.0'\n")
+    for name in libs:
+        (d / "lib" / name).write_text("")
+    import importlib.util
+    spec = importlib.util.spec_from_file_location("torch", str(d / "__init__.py"))
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: spec if name == "torch" else None)
+
+
+def test_build_without_a_cuda_pytorch(monkeypatch, tmp_path):
+    """The C library needs no PyTorch: without one, or with one for CPUs, the calls' module is left out."""
+    import importlib.util
+    with monkeypatch.context() as m:
+        m.setattr(importlib.util, "find_spec", lambda name, *a: None)
+        assert libbuild.build_torch_calls(force=True) is None
+    fake_torch(monkeypatch, tmp_path, "2.11.0+cpu", ["libtorch_cpu.so"])
+    assert libbuild.build_torch_calls(force=True) is None
+
+
+def test_a_failed_module_leaves_the_library_built(monkeypatch):
+    made = []
+
+    def fail(force=False):
+        raise RuntimeError("no compiler")
+
+    monkeypatch.setattr(libbuild, "build", lambda **k: made.append("lib"))
+    monkeypatch.setattr(libbuild, "build_torch_calls", fail)
+    with pytest.raises(RuntimeError):
+        libbuild.main([])
+    assert made == ["lib"]
