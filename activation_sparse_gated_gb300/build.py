@@ -3,13 +3,14 @@
 nvcc compiles each translation unit for sm_103a (one -gencode, -lineinfo) in
 parallel, then links a shared library with the CUDA runtime linked statically.
 ``build_torch_calls`` compiles binding/torch_calls.cpp (host code, against the
-installed PyTorch's headers) -> _torch_calls.so, the tensor operators' calls.
+installed PyTorch's headers) -> _torch_calls.*.so, the tensor operators' calls.
 """
 from __future__ import annotations
 
 import glob
 import importlib.util
 import os
+import re
 import subprocess
 import sys
 import sysconfig
@@ -81,7 +82,19 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
 
 # the tensor operators' calls, a CPython module against the installed PyTorch
 TORCH_CALLS_SRC = os.path.join(PKG, "binding", "torch_calls.cpp")
-TORCH_CALLS = os.path.join(PKG, "_torch_calls.so")
+
+
+def torch_calls_path() -> str:
+    """Where the module for this Python and the installed PyTorch is.  It reads tensors by the layout in that PyTorch's
+    headers, so its name holds both versions and another's is never loaded."""
+    version, spec = "none", importlib.util.find_spec("torch")
+    if spec is not None and spec.origin:
+        with open(os.path.join(os.path.dirname(spec.origin), "version.py")) as f:
+            version = re.search(r"^__version__ = ['\"]([^'\"]+)", f.read(), re.M).group(1)
+    return os.path.join(PKG, f"_torch_calls.torch{version}.{sysconfig.get_config_var('SOABI')}.so")
+
+
+TORCH_CALLS = torch_calls_path()
 
 
 def _torch_dir():
@@ -94,7 +107,7 @@ def _torch_dir():
 
 
 def build_torch_calls(force: bool = False):
-    """Compile _torch_calls.so next to the package (a few seconds).  Without a PyTorch that has CUDA there is nothing to
+    """Compile TORCH_CALLS next to the package (a few seconds).  Without a PyTorch that has CUDA there is nothing to
     build it against: None, and the tensor operators go without it."""
     torch_dir = _torch_dir()
     if torch_dir is None:

@@ -15,6 +15,7 @@ here then does the same and names what is wrong.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from functools import lru_cache
 
@@ -22,6 +23,7 @@ import torch
 
 from . import (LIB_PATH, SFFN_ACT_RELU, SFFN_ACT_RSP, SFFN_ACT_SILU, SFFN_BF16, SFFN_F32, SFFN_I8, SFFN_OK,
                SFFN_ROUTE_NORMALIZE, SFFN_ROUTE_SIGMOID, SFFN_W_KN, SffnError, load, sffn_last_error, sffn_strerror)
+from .build import TORCH_CALLS
 
 _ACT = {"relu": SFFN_ACT_RELU, "rsp": SFFN_ACT_RSP, "silu": SFFN_ACT_SILU}
 _SCORE = {"softmax": 0, "sigmoid": SFFN_ROUTE_SIGMOID}
@@ -38,9 +40,16 @@ class Routing(tuple):
     rows = property(lambda self: self[3])
 
 
+def _load_calls():
+    spec = importlib.util.spec_from_file_location(__package__ + "._torch_calls", TORCH_CALLS)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
 try:
-    from . import _torch_calls as _calls
-except ImportError:  # not built: the same calls, slower
+    _calls = _load_calls()
+except ImportError:  # not built for this PyTorch: the same calls, slower
     _calls = None
 if _calls is not None and os.path.exists(LIB_PATH):
     _calls.bind(*(ctypes.cast(getattr(load(), name), ctypes.c_void_p).value for name in (

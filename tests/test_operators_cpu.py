@@ -203,3 +203,16 @@ def test_a_failed_module_leaves_the_library_built(monkeypatch):
     with pytest.raises(RuntimeError):
         libbuild.main([])
     assert made == ["lib"]
+
+
+def test_module_of_another_pytorch_is_not_loaded(monkeypatch, tmp_path):
+    """The module's name holds PyTorch's version and Python's ABI, so after an upgrade of either another one is looked for."""
+    torch = pytest.importorskip("torch")
+    import sysconfig
+    from activation_sparse_gated_gb300 import operators
+    assert torch.__version__ in libbuild.TORCH_CALLS and sysconfig.get_config_var("SOABI") in libbuild.TORCH_CALLS
+    assert operators._calls is None or operators._calls.__file__ == libbuild.TORCH_CALLS
+    for version in ("2.12.0+cu130", "2.11.1"):
+        with monkeypatch.context() as m:
+            fake_torch(m, tmp_path, version, ["libtorch_cuda.so"])
+            assert version in libbuild.torch_calls_path() and libbuild.torch_calls_path() != libbuild.TORCH_CALLS
