@@ -46,7 +46,9 @@ struct Calls {
 bool takes(PyObject* o, at::ScalarType type, int64_t dim, int device, bool dense, const Tensor** out) {
   if (!THPVariable_Check(o)) return false;
   const Tensor& t = THPVariable_Unpack(o);
-  if (t.scalar_type() != type || t.dim() != dim || !t.is_cuda() || t.requires_grad()) return false;
+  if (t.scalar_type() != type || t.dim() != dim || !t.is_cuda() || t.requires_grad() ||
+      t._fw_grad(0).defined())
+    return false;
   if (device >= 0 && t.get_device() != device) return false;
   if (dense && !t.is_contiguous()) return false;
   *out = &t;

@@ -5,7 +5,8 @@ types and strides, allocate outputs and scratch on the stream the call runs on,
 and pass pointers.  ``stream`` is a torch stream (default: the current one);
 tensors used on another stream than their own are the caller's to order, as
 with any torch operation.  Nothing here is differentiable, and a tensor that
-requires a gradient is refused while gradients are recorded.
+requires a gradient is refused while gradients are recorded, one with a
+forward-mode tangent always.
 
 The ordinary call (fresh outputs, the current stream) goes through
 ``_torch_calls`` (binding/torch_calls.cpp), which checks, allocates and calls the
@@ -20,6 +21,7 @@ import os
 from functools import lru_cache
 
 import torch
+from torch.autograd import forward_ad
 
 from . import (LIB_PATH, SFFN_ACT_RELU, SFFN_ACT_RSP, SFFN_ACT_SILU, SFFN_BF16, SFFN_F32, SFFN_I8, SFFN_OK,
                SFFN_ROUTE_NORMALIZE, SFFN_ROUTE_SIGMOID, SFFN_W_KN, SffnError, load, sffn_last_error, sffn_strerror)
@@ -75,9 +77,13 @@ def _done(rc):
         raise SffnError(rc, sffn_last_error() or sffn_strerror(rc))
 
 
+def _has_tangent(t):
+    return t.is_floating_point() and forward_ad.unpack_dual(t).tangent is not None
+
+
 def _operand(name, t, dtypes, dim, device=None):
     if (isinstance(t, torch.Tensor) and t.ndim == dim and t.dtype in dtypes and t.is_cuda
-            and (device is None or t.device == device) and not t.requires_grad):
+            and (device is None or t.device == device) and not t.requires_grad and not _has_tangent(t)):
         return
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
@@ -85,6 +91,8 @@ def _operand(name, t, dtypes, dim, device=None):
         raise ValueError(f"{name} must have {dim} dimensions, not {t.dim()}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} has type {t.dtype}, not {' or '.join(str(d) for d in dtypes)}")
+    if _has_tangent(t):
+        raise ValueError(f"{name} has a forward-mode tangent: the operators have none")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on the GPU")
     if device is not None and t.device != device:

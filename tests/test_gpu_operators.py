@@ -875,3 +875,33 @@ def test_moe_router_product(T, E, D, dtype):
     # the chosen are the largest, as far as the logits' bounds tell them apart
     left = z.scatter(1, ids.long(), -math.inf).amax(1, keepdim=True)
     assert (z.gather(1, ids.long()) + 2 * dz >= left).all()
+
+
+def dual_calls():
+    import torch.autograd.forward_ad as fw
+    g, E, k, D, H = gen(95), 4, 2, 64, 32
+    x = torch.randn(6, D, generator=g, device=DEV).to(BF)
+    W1, W3, W2t = (torch.randn(E, H, D, generator=g, device=DEV).to(BF) for _ in range(3))
+    z = torch.randn(6, E, generator=g, device=DEV)
+    q, sx = int8_operands(g, 6, D)
+    wq, sw = int8_operands(g, H, D)
+    r, off = sffn.route(z, k), offsets_of([2, 0, 1, 3])
+    dual = lambda t: fw.make_dual(t, torch.ones_like(t))  # noqa: E731
+    return {"route": lambda: sffn.route(dual(z), k),
+            "quantize": lambda: sffn.quantize_tokens(dual(x)),
+            "int8 sx": lambda: sffn.matmul_int8(q, dual(sx), wq, sw),
+            "int8 sw": lambda: sffn.matmul_int8(q, sx, wq, dual(sw)),
+            "grouped x": lambda: sffn.grouped_matmul(dual(x), W1, off),
+            "grouped w": lambda: sffn.grouped_matmul(x, dual(W1), off),
+            "experts x": lambda: sffn.experts_forward(dual(x), r, W1, W3, W2t),
+            "experts weights": lambda: sffn.experts_forward(x, (dual(r.weights), *r[1:]), W1, W3, W2t),
+            "experts W2t": lambda: sffn.experts_forward(x, r, W1, W3, dual(W2t))}
+
+
+@pytest.mark.parametrize("which", ["route", "quantize", "int8 sx", "int8 sw", "grouped x", "grouped w", "experts x",
+                                   "experts weights", "experts W2t"])
+def test_forward_mode_tangents_are_refused(which):
+    import torch.autograd.forward_ad as fw
+    with fw.dual_level():
+        with pytest.raises(ValueError, match="tangent"):
+            dual_calls()[which]()

@@ -216,3 +216,13 @@ def test_module_of_another_pytorch_is_not_loaded(monkeypatch, tmp_path):
         with monkeypatch.context() as m:
             fake_torch(m, tmp_path, version, ["libtorch_cuda.so"])
             assert version in libbuild.torch_calls_path() and libbuild.torch_calls_path() != libbuild.TORCH_CALLS
+
+
+def test_tensor_wrappers_refuse_forward_mode_tangents():
+    torch = pytest.importorskip("torch")
+    import torch.autograd.forward_ad as fw
+    z, x = torch.zeros(4, 8), torch.zeros(4, 64, dtype=torch.bfloat16)
+    with fw.dual_level():
+        for call in (lambda: sffn.route(fw.make_dual(z, z), 2), lambda: sffn.quantize_tokens(fw.make_dual(x, x))):
+            with pytest.raises(ValueError, match="tangent"):
+                call()
