@@ -95,6 +95,10 @@ int sffn_route(const void* logits, long long ld, float* weights, int* ids, int* 
     cudaError_t e = cudaMemsetAsync(offsets, 0, sizeof(int) * (E + 1), s);
     return e == cudaSuccess ? SFFN_OK : cuda_fail("cudaMemsetAsync", e);
   }
+  const unsigned long long nz = ((unsigned long long)(T - 1) * ld + E) * (dtype == SFFN_F32 ? 4 : 2), nc = 4ull * T * k;
+  if (overlap(logits, nz, weights, nc) || overlap(logits, nz, ids, nc) || overlap(logits, nz, rows, nc) ||
+      overlap(logits, nz, offsets, 4ull * (E + 1)))
+    return fail(SFFN_ERR_ARG, "sffn_route: an output overlaps the logits");
   const size_t need = route_workspace(T, E, k);
   if (need > 0 && (!workspace || workspace_bytes < need))
     return fail(SFFN_ERR_ARG, "sffn_route: workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : (size_t)0,
@@ -126,6 +130,9 @@ int sffn_quantize_tokens(const void* x, long long ldx, int8_t* q, float* scales,
   if (!x || !q || !scales) return fail(SFFN_ERR_ARG, "sffn_quantize_tokens: null pointer");
   if (misaligned(x, 2) || misaligned(scales, 4))
     return fail(SFFN_ERR_ALIGN, "sffn_quantize_tokens: a pointer is not aligned to its element");
+  const unsigned long long nx = ((unsigned long long)(T - 1) * ldx + K) * 2;
+  if (overlap(x, nx, q, (unsigned long long)T * K) || overlap(x, nx, scales, 4ull * T))
+    return fail(SFFN_ERR_ARG, "sffn_quantize_tokens: an output overlaps x");
   const cudaError_t e = launch_quantize_tokens(x, ldx, q, scales, T, K, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SFFN_OK : cuda_fail("sffn_quantize_tokens", e);
 }
@@ -165,7 +172,9 @@ int sffn_grouped_matmul(const void* x, long long ldx, const float* sx, const voi
   const unsigned long long eb = i8 ? 1 : 2, yb = y_dtype == SFFN_F32 ? 4 : 2;
   const unsigned long long ny = ((unsigned long long)(R - 1) * ldy + N) * yb;
   if (overlap(x, ((unsigned long long)(XR - 1) * ldx + K) * eb, y, ny) ||
-      overlap(w, (unsigned long long)E * N * K * eb, y, ny) || (need > 0 && overlap(workspace, need, y, ny)))
+      overlap(w, (unsigned long long)E * N * K * eb, y, ny) || (need > 0 && overlap(workspace, need, y, ny)) ||
+      overlap(offsets, 4ull * (E + 1), y, ny) || overlap(index, 4ull * R, y, ny) ||
+      (i8 && (overlap(sx, 4ull * XR, y, ny) || overlap(sw, 4ull * E * N, y, ny))))
     return fail(SFFN_ERR_ARG, "%s: y overlaps an operand or the workspace", fn);
   GmmArgs a;
   a.workspace = need > 0 ? workspace : nullptr;
@@ -233,9 +242,11 @@ int sffn_experts_forward(const void* x, long long ldx, const float* weights, con
   if (!workspace || workspace_bytes < need)
     return fail(SFFN_ERR_ARG, "%s: workspace of %zu bytes, %zu needed", fn, workspace ? workspace_bytes : (size_t)0, need);
   if (misaligned(workspace, 16)) return fail(SFFN_ERR_ALIGN, "%s: workspace is not 16-byte aligned", fn);
-  const unsigned long long ny = 2ull * T * D, nw = 2ull * E * H * D;
+  const unsigned long long ny = 2ull * T * D, nw = 2ull * E * H * D, nc = 4ull * T * k;
   if (overlap(x, 2ull * ((unsigned long long)(T - 1) * ldx + D), y, ny) || overlap(W1, nw, y, ny) ||
-      overlap(W3, nw, y, ny) || overlap(W2t, nw, y, ny) || overlap(workspace, need, y, ny))
+      overlap(W3, nw, y, ny) || overlap(W2t, nw, y, ny) || overlap(workspace, need, y, ny) ||
+      overlap(weights, nc, y, ny) || overlap(ids, nc, y, ny) || overlap(rows, nc, y, ny) ||
+      overlap(offsets, 4ull * (E + 1), y, ny))
     return fail(SFFN_ERR_ARG, "%s: y overlaps an operand or the workspace", fn);
   ExpertsArgs a;
   a.x = x;

@@ -330,7 +330,8 @@ int sffn_forward_noalloc(const void* W1, const void* W3, const void* W2t, const 
  * batches of int8 tokens as products of codes.  These calls have no handle:
  * weights stay where the caller keeps them, scratch is the caller's
  * `workspace` (16-byte aligned, contents don't matter, must not be shared by
- * calls that may overlap), and nothing is kept from one call to the next.
+ * calls that may overlap), and nothing is kept from one call to the next.  An
+ * output whose bytes, first to last, overlap an input's is refused.
  * Every call is asynchronous and ordered on `stream`, may be captured into a
  * graph, checks its arguments before it touches the device, and takes empty
  * inputs (T or R = 0).  All pointers are device pointers; sums are fp32 (int8
@@ -407,7 +408,7 @@ int sffn_matmul_int8(const int8_t* xq, long long ldx, const float* sx, const int
  * offsets[E] are left as they are, offsets past R are cut to R.  SFFN_W_KN
  * (bf16): w is [E, K, N].  K % 8 == 0 (bf16) or K % 16 == 0 (int8), ldx
  * likewise, N % 8 == 0 with SFFN_W_KN; x and w 16-byte aligned; y overlaps
- * neither.  The workspace holds sffn_grouped_workspace() bytes (0 for bf16 and
+ * no other argument.  The workspace holds sffn_grouped_workspace() bytes (0 for bf16 and
  * for short int8 groups; else fp16 copies of the codes).
  */
 enum { SFFN_W_KN = 1 };
@@ -428,7 +429,7 @@ int sffn_grouped_matmul(const void* x, long long ldx, const float* sx, const voi
  * exactly 0, also where its up value is infinite or NaN; a NaN gate is live, so a
  * token that holds a NaN comes out as NaN.  (Weights are taken to be finite: not
  * every form reads those of a dead unit.)  D % 8 == 0, any H >= 1.  x, W1, W3,
- * W2t and y are 16-byte aligned and y overlaps none of them; the workspace holds
+ * W2t and y are 16-byte aligned and y overlaps no other argument; the workspace holds
  * sffn_experts_workspace(T, k, D, H) bytes.
  */
 size_t sffn_experts_workspace(int T, int k, int D, int H);

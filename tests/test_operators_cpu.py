@@ -226,3 +226,27 @@ def test_tensor_wrappers_refuse_forward_mode_tangents():
         for call in (lambda: sffn.route(fw.make_dual(z, z), 2), lambda: sffn.quantize_tokens(fw.make_dual(x, x))):
             with pytest.raises(ValueError, match="tangent"):
                 call()
+
+
+@pytest.mark.parametrize("bad", [dict(weights=X), dict(ids=X + 4), dict(rows=X + 4 * 64 * 4 - 4), dict(offsets=X + 8)])
+def test_route_refuses_outputs_over_its_logits(lib, bad):
+    assert route(lib, **bad) == sffn.SFFN_ERR_ARG
+    assert "overlaps" in sffn.sffn_last_error()
+
+
+@pytest.mark.parametrize("q,s", [(X, S), (X + 2 * 4 * 64 - 1, S), (Y, X + 16)])
+def test_quantize_refuses_outputs_over_x(lib, q, s):
+    assert lib.sffn_quantize_tokens(X, 64, q, s, 4, 64, None) == sffn.SFFN_ERR_ARG
+    assert "overlaps" in sffn.sffn_last_error()
+
+
+@pytest.mark.parametrize("bad", [dict(y=O), dict(index=Y + 64), dict(dtype=sffn.SFFN_I8, sx=Y), dict(dtype=sffn.SFFN_I8, sw=Y + 4)])
+def test_grouped_matmul_refuses_y_over_its_tables(lib, bad):
+    assert grouped(lib, **bad) == sffn.SFFN_ERR_ARG
+    assert "overlaps" in sffn.sffn_last_error()
+
+
+@pytest.mark.parametrize("bad", [dict(weights=Y), dict(ids=Y + 4), dict(offsets=Y + 8), dict(rows=Y)])
+def test_experts_forward_refuses_y_over_its_routing(lib, bad):
+    assert experts(lib, **bad) == sffn.SFFN_ERR_ARG
+    assert "overlaps" in sffn.sffn_last_error()
