@@ -1,6 +1,7 @@
 // ops_api.cu -- the handle-free entry points of include/sffn.h: the router,
 // per-token int8 codes, the int8 product, the products grouped by expert and
 // the gated experts' forward.  Argument checks come before any CUDA call.
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <mutex>
@@ -57,14 +58,15 @@ cudaError_t sffn::ops_error_word(int** p) {
 }
 
 int sffn::ops_num_sms() {
-  static int n = 0;
+  static std::atomic<int> at[64];  // by device: threads may ask at once, and devices differ
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+  int n = at[dev].load(std::memory_order_relaxed);
   if (n == 0) {
-    int dev = 0, v = 0;
-    if (cudaGetDevice(&dev) == cudaSuccess &&
-        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && v > 0)
-      n = v;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 1;
+    at[dev].store(n, std::memory_order_relaxed);
   }
-  return n > 0 ? n : 1;
+  return n;
 }
 
 extern "C" {
