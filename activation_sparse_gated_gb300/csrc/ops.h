@@ -8,7 +8,7 @@
 
 namespace sffn {
 
-// The per-device error word of the handle-free operators (bits DEV_ERR_*).
+// The per-device error word of the handle-free operators (0 or DEV_ERR_TIMEOUT).
 cudaError_t ops_error_word(int** p);
 int ops_num_sms();
 

@@ -15,7 +15,7 @@ using namespace sffn;
 
 namespace {
 
-__device__ int g_ops_error = 0;  // DEV_ERR_* bits of the operators' kernels on this device
+__device__ int g_ops_error = 0;  // DEV_ERR_TIMEOUT, once a wait of an operator's kernel on this device ran out
 
 int fail(int code, const char* fmt, ...) {
   char buf[400];
@@ -281,8 +281,6 @@ int sffn_check(void* stream) {
   if ((e = cudaMemcpy(&v, word, sizeof v, cudaMemcpyDeviceToHost)) != cudaSuccess) return cuda_fail("cudaMemcpy", e);
   if (v == 0) return SFFN_OK;
   if ((e = cudaMemset(word, 0, sizeof v)) != cudaSuccess) return cuda_fail("cudaMemset", e);
-  if (v & DEV_ERR_CHECK)
-    return fail(SFFN_ERR_DEVICE, "an operator's device-side check failed (error word 0x%x); its outputs are invalid", v);
   return fail(SFFN_ERR_TIMEOUT, "an operator's device-side wait ran out of time (error word 0x%x); its outputs are "
               "invalid", v);
 }

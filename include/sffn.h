@@ -438,8 +438,11 @@ int sffn_experts_forward(const void* x, long long ldx, const float* weights, con
                          int D, int H, int act, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
- * Wait for `stream` and report (and clear) a device-side error that any of the
- * operators above recorded on this device: SFFN_ERR_TIMEOUT, SFFN_ERR_DEVICE.
+ * Wait for `stream` and report (and clear) whether a device-side wait of any of
+ * the operators above ran out on this device: SFFN_ERR_TIMEOUT.  The outputs of
+ * such a call are invalid, and nothing else tells.  (A wait lasts microseconds
+ * and gives up after 250 ms, which a process that is held up on a shared GPU may
+ * see.)
  */
 int sffn_check(void* stream);
 
