@@ -52,6 +52,7 @@
 
 #include "common.cuh"
 #include "ops.h"
+#include "sffn.h"
 #include "tc.cuh"
 
 namespace sffn {
@@ -964,6 +965,11 @@ cudaError_t tg_go(const CUtensorMap& mW, const CUtensorMap& mW3, const CUtensorM
   return ops_launch(kernel, dim3((unsigned)(n * c)), threads, smem, s, c, mW, mW3, mX, mXb, p);
 }
 
+// shared memory beside the stages: the epilogue warps' scratch, barriers, the groups' tables
+constexpr size_t tg_fixed(int epilogue_warps, int E) {
+  return epilogue_warps * TG_EPI_BYTES + 1024 + 8 * (2 * 16 + 2 * 16 + 6) + 8 + sizeof(int) * 2 * ((size_t)E + 1) + 64;
+}
+
 }  // namespace
 
 cudaError_t launch_gmm_tc(const GmmArgs& a, int ctas, int nt, cudaStream_t s) {
@@ -978,15 +984,14 @@ cudaError_t launch_gmm_tc(const GmmArgs& a, int ctas, int nt, cudaStream_t s) {
   const size_t yb = a.y_f32 ? 4 : 2;
   p.g.NY = std::max(a.N, a.NY);
   p.vec = ((uintptr_t)a.y & 15) == 0 && a.ldy * yb % 16 == 0 && p.g.NY * yb % 16 == 0;
-  const size_t fixed = (a.i8 ? 4 : 8) * TG_EPI_BYTES + 1024 + 8 * (2 * 16 + 2 * 16 + 6) + 8 +
-                       sizeof(int) * 2 * (size_t)(a.E + 1) + 64;
+  const size_t fixed = tg_fixed(a.i8 ? 4 : 8, a.E);
   const int room = (int)(TG_SMEM - fixed);
-  auto b_bytes = [&] { return (p.NT / ctas + 7) / 8 * 1024; };
-  // int8: three operand stages (two are 10 to 15 % slower) and as many raw ones at least (see the converters' waits)
+  const int ntl = p.NT / ctas, bb = (ntl + 7) / 8 * 1024;
+  // int8: three operand stages (two are 10 to 15 % slower) and as many raw ones at least (see the converters' waits);
+  // 128 rows a tile leave room for them with the tables of as many experts as there may be
   constexpr int least = 3;
-  while (a.i8 && room < 2 * least * b_bytes() + least * (16384 + b_bytes())) p.NT >>= 1;
-  const int ntl = p.NT / ctas;
-  const int st = a.i8 ? 2 * b_bytes() : (gated ? 2 : 1) * 16384 + b_bytes(), raw = a.i8 ? 16384 + b_bytes() : 0;
+  static_assert(tg_fixed(4, SFFN_MAX_EXPERTS) + least * (2 * 16384 + 16384 + 16384) <= TG_SMEM, "int8 stages");
+  const int st = a.i8 ? 2 * bb : (gated ? 2 : 1) * 16384 + bb, raw = a.i8 ? 16384 + bb : 0;
   p.S = a.i8 ? least : std::min(16, room / st);
   p.SR = a.i8 ? std::min(12, (room - p.S * st) / raw) : 0;
   const int wide = (gated ? 2 : 1) * p.NT, wcols = a.i8 ? 64 * p.S : 0;  // TMEM columns: an accumulator, the weights
