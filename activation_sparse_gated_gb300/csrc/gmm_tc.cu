@@ -7,8 +7,9 @@
 //
 // The weights are the M side of the MMA (128 rows of w a block, 256 a pair of
 // blocks with cta_group::2) and the rows of x the N side, whose width is any
-// multiple of 16 (32 for a pair) up to 256: a ragged group reads no more rows
-// than it has.  An MMA of 16 K values takes N / 2 cycles from 96 columns on and 49
+// multiple of 16 (32 for a pair) up to 256, so a ragged tile's MMAs are as wide
+// as its rows.  (Its copies are not: without an index x comes in boxes of 32 rows
+// or of a whole tile, through one in fours.)  An MMA of 16 K values takes N / 2 cycles from 96 columns on and 49
 // below (measured, one block, operands in shared memory): full tensor rate from
 // 128 columns on, 256 halve the traffic of w; and 128 x 16 weights per 49 cycles
 // and SM are above the memory's rate, which is what bounds short groups.
@@ -322,8 +323,9 @@ __device__ __forceinline__ Tile tile_at(const TgArgs& p, const int* s_off, const
 
 // activation() with the device's fast exponential and quotient.  Gate and up leave no room for a second accumulator, so
 // this stands between two tiles' MMAs (4096 tokens, 8 of 64 experts, D = 2560, H = 1024, R-S+ 540 us with the
-// precise ones, 521 so; SiLU 531 / 523).  Its relative error is below 2^-15 wherever the result is a normal number; the
-// product with the up value is then rounded to bf16 (2^-8).
+// precise ones, 521 so; SiLU 531 / 523).  Its relative error is below 2^-15 for z above -87.3; below that, where 1 + exp(-z)
+// passes 2^126, SiLU is 0 instead of something less than 1e-36 from it.  The product with the up value is then rounded to
+// bf16 (2^-8).
 //
 // The product h = A(z) u of a unit whose gate is 0 is exactly 0 whatever its up value, as in the gate-first passes, which
 // do not read it; a NaN gate is not below 0 and stays one.  (The activation's own branch and this one in a single

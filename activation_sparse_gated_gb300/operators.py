@@ -8,6 +8,10 @@ with any torch operation.  Nothing here is differentiable, and a tensor that
 requires a gradient is refused while gradients are recorded, one with a
 forward-mode tangent always.
 
+Calls are asynchronous.  A wait inside a kernel that runs out (250 ms, where
+microseconds are usual) leaves a call's outputs invalid without an error of its
+own: ``sffn_check`` waits for a stream and raises if there was one.
+
 The ordinary call (fresh outputs, the current stream) goes through
 ``_torch_calls`` (binding/torch_calls.cpp), which checks, allocates and calls the
 library in one step and answers None for whatever it does not take; the code

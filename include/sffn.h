@@ -335,9 +335,9 @@ int sffn_forward_noalloc(const void* W1, const void* W3, const void* W2t, const 
  * Every call is asynchronous and ordered on `stream`, may be captured into a
  * graph, checks its arguments before it touches the device, and takes empty
  * inputs (T or R = 0).  All pointers are device pointers; sums are fp32 (int8
- * products: exact integers as long as fp32 holds them), results are rounded
- * once to y's type and do not depend on timing, so a call repeated on the same
- * inputs gives the same bits.
+ * products: exact integers as long as fp32 holds them), results are rounded once
+ * to y's type (each call says what is rounded on the way) and do not depend on
+ * timing, so a call repeated on the same inputs gives the same bits.
  * The operators are inference only, like the rest of the library.
  */
 
@@ -407,9 +407,10 @@ int sffn_matmul_int8(const int8_t* xq, long long ldx, const float* sx, const int
  * ldx), w [E, N, K] dense, y [R, N] (row pitch ldy) bf16 or f32; rows of y past
  * offsets[E] are left as they are, offsets past R are cut to R.  SFFN_W_KN
  * (bf16): w is [E, K, N].  K % 8 == 0 (bf16) or K % 16 == 0 (int8), ldx
- * likewise, N % 8 == 0 with SFFN_W_KN; x and w 16-byte aligned; y overlaps
- * no other argument.  The workspace holds sffn_grouped_workspace() bytes (0 for bf16 and
- * for short int8 groups; else fp16 copies of the codes).
+ * likewise, N % 8 == 0 with SFFN_W_KN; x and w 16-byte aligned; y overlaps no
+ * other argument.  The workspace holds sffn_grouped_workspace() bytes: 0 for bf16
+ * and for short int8 groups, else room for fp16 copies of the codes, 2 K (XR + E N)
+ * bytes, which a call of few tiles leaves unused.
  */
 enum { SFFN_W_KN = 1 };
 size_t sffn_grouped_workspace(int R, int XR, int N, int K, int E, int dtype);
@@ -421,16 +422,20 @@ int sffn_grouped_matmul(const void* x, long long ldx, const float* sx, const voi
 /*
  * The gated experts behind the router:
  *     y_t = sum_j weights[t, j] W2_e (A(W1_e x_t) .* (W3_e x_t)),  e = ids[t, j]
- * in bf16 with fp32 sums.  weights, ids, offsets, rows are sffn_route's outputs
- * for the same T, E, k; W1, W3 are [E, H, D] and W2t is W2 transposed, [E, H, D]
- * (row i of expert e is column i of W2_e), dense; x [T, D] (row pitch ldx), y
- * [T, D] dense, fully written: a token without an open expert gets 0, a choice
- * of weight 0 adds nothing.  A unit whose gate A(W1_e x_t) is 0 is dead and adds
- * exactly 0, also where its up value is infinite or NaN; a NaN gate is live, so a
- * token that holds a NaN comes out as NaN.  (Weights are taken to be finite: not
- * every form reads those of a dead unit.)  D % 8 == 0, any H >= 1.  x, W1, W3,
- * W2t and y are 16-byte aligned and y overlaps no other argument; the workspace holds
- * sffn_experts_workspace(T, k, D, H) bytes.
+ * in bf16 with fp32 sums.  Few tokens (up to two choices an expert, and not many
+ * units in all) keep the hidden value h = A .* up in fp32; for more, which go to
+ * the tensor cores, h is rounded to bf16 once more before W2, and the gate's
+ * exponential and quotient are the device's fast ones (2^-15).  weights, ids,
+ * offsets, rows are sffn_route's outputs for the same T, E, k; W1, W3 are
+ * [E, H, D] and W2t is W2 transposed, [E, H, D] (row i of expert e is column i of
+ * W2_e), dense; x [T, D] (row pitch ldx), y [T, D] dense, fully written: a token
+ * without an open expert gets 0, a choice of weight 0 adds nothing.  A unit whose
+ * gate A(W1_e x_t) is 0 is dead and adds exactly 0, also where its up value is
+ * infinite or NaN; a NaN gate is live, so a token that holds a NaN comes out as
+ * NaN.  (Weights are taken to be finite: not every form reads those of a dead
+ * unit.)  D % 8 == 0, any H >= 1.  x, W1, W3, W2t and y are 16-byte aligned and y
+ * overlaps no other argument; the workspace holds sffn_experts_workspace(T, k, D,
+ * H) bytes, about 2 H + 4 D for every choice.
  */
 size_t sffn_experts_workspace(int T, int k, int D, int H);
 int sffn_experts_forward(const void* x, long long ldx, const float* weights, const int* ids, const int* offsets,
