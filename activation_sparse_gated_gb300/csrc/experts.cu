@@ -10,7 +10,7 @@
 // Measured: one token, 8 of 64 experts, D = 2560, H = 1024, ReLU at 90 %: 20 us
 // with its router (50 MB, 37 % of the copy rate): loads that wait for the
 // choice, for the gate, for the live units, one after the other.  Many tokens
-// are products on the tensor cores (4096 tokens 484 us): gate and up 227, down
+// are products on the tensor cores (4096 tokens 480 to 499 us by the board): gate and up 227, down
 // 148 (its fp32 rows are 335 MB; 127 with rows of bf16), combination 62, the
 // grouped copy of x 31, the router 15.
 #include <algorithm>

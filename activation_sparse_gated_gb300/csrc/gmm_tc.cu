@@ -39,12 +39,13 @@
 // Few tiles and a long sum: the blocks of a cluster cut K and add their partial
 // tiles through distributed shared memory in a fixed order.
 //
-// Measured (us; share of the copy rate / of cuBLAS's burst rate): bf16, 128 rows
-// over 64 experts of 1024 x 2560 44.6 (97 % / 1 %); 16384 ragged rows over 64
-// experts of 7168 x 2560 521 (76 % / 60 %); one group 8192 x 14336 x 4096 499
-// (- / 99 %); int8 8192 x 14336 x 4096 533 (- / 93 %, 40 of it the copies), 77 x
-// 2560 x 7168 14.4 (20 % / 10 %: latency of the chunks' chain and of the launch),
-// 4093 rows over 16 experts of 1000 x 2560 43 (20 % / 25 %: widening; 50 with
+// Measured (us; share of the copy rate / of cuBLAS's burst rate; long ones by the
+// board): bf16, 128 rows over 64 experts of 1024 x 2560 44.1 (97 % / 1 %); 16384
+// ragged rows over 64 experts of 7168 x 2560 502 to 550 (72 % / 57 % at 543); one
+// group 8192 x 14336 x 4096 499 (- / 99 %); int8 8192 x 14336 x 4096 531 to 556 (-
+// / 90 % at 550, 40 us of it the copies), 77 x 2560 x 7168 14.6 (20 % / 10 %:
+// latency of the chunks' chain and of the launch),
+// 4093 rows over 16 experts of 1000 x 2560 43 to 45 (20 % / 25 %: widening; 50 with
 // w widened in shared memory, a value a store and 64 codes a stage).
 #include <cudaTypedefs.h>
 
