@@ -84,19 +84,6 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
 TORCH_CALLS_SRC = os.path.join(PKG, "binding", "torch_calls.cpp")
 
 
-def torch_calls_path() -> str:
-    """Where the module for this Python and the installed PyTorch is.  It reads tensors by the layout in that PyTorch's
-    headers, so its name holds both versions and another's is never loaded."""
-    version, spec = "none", importlib.util.find_spec("torch")
-    if spec is not None and spec.origin:
-        with open(os.path.join(os.path.dirname(spec.origin), "version.py")) as f:
-            version = re.search(r"^__version__ = ['\"]([^'\"]+)", f.read(), re.M).group(1)
-    return os.path.join(PKG, f"_torch_calls.torch{version}.{sysconfig.get_config_var('SOABI')}.so")
-
-
-TORCH_CALLS = torch_calls_path()
-
-
 def _torch_dir():
     """The installed PyTorch's directory; None without one that has CUDA.  (It is not imported.)"""
     spec = importlib.util.find_spec("torch")
@@ -104,6 +91,22 @@ def _torch_dir():
         return None
     d = os.path.dirname(spec.origin)
     return d if os.path.exists(os.path.join(d, "lib", "libtorch_cuda.so")) else None
+
+
+def torch_calls_path() -> str:
+    """Where the module for this Python and the installed PyTorch is.  It reads tensors by the layout in that PyTorch's
+    headers, so its name holds both versions and another's is never loaded."""
+    version, d = "none", _torch_dir()
+    if d is not None:
+        try:
+            with open(os.path.join(d, "version.py")) as f:
+                version = re.search(r"^__version__ = ['\"]([^'\"/]+)", f.read(), re.M).group(1)
+        except (OSError, AttributeError):  # an unusual install: its directory's name in place of a version
+            version = re.sub(r"\W", "_", d)
+    return os.path.join(PKG, f"_torch_calls.torch{version}.{sysconfig.get_config_var('SOABI')}.so")
+
+
+TORCH_CALLS = torch_calls_path()
 
 
 def build_torch_calls(force: bool = False):

@@ -250,3 +250,10 @@ def test_grouped_matmul_refuses_y_over_its_tables(lib, bad):
 def test_experts_forward_refuses_y_over_its_routing(lib, bad):
     assert experts(lib, **bad) == sffn.SFFN_ERR_ARG
     assert "overlaps" in sffn.sffn_last_error()
+
+
+def test_a_pytorch_without_a_readable_version_stops_nothing(monkeypatch, tmp_path):
+    with monkeypatch.context() as m:
+        fake_torch(m, tmp_path, "2.13.0", ["libtorch_cuda.so"])
+        os.remove(tmp_path / "2.13.0" / "torch" / "version.py")
+        assert libbuild.torch_calls_path().endswith(".so") and libbuild.torch_calls_path() != libbuild.TORCH_CALLS
