@@ -10,12 +10,13 @@ The functions mirror the C ABI one to one (``sffn_create``, ``sffn_set_live_frac
 ``sffn_synchronize``, ``sffn_destroy``, ``sffn_strerror``, ``sffn_last_error``,
 ``sffn_version``, ``sffn_debug_timeout_probe``, ``sffn_forward_noalloc``,
 ``sffn_set_weights_int8``, ``sffn_get_weights_int8``, and the handle-free operators ``sffn_route``,
-``sffn_quantize_tokens``, ``sffn_matmul_int8``, ``sffn_grouped_matmul``, ``sffn_experts_forward``
-with ``sffn_check``).  Tensor arguments are passed by
+``sffn_quantize_tokens``, ``sffn_matmul_int8``, ``sffn_grouped_matmul``, ``sffn_experts_forward``,
+``sffn_quantize_int4``, ``sffn_dequantize_int4``, ``sffn_matmul_int4``, ``sffn_gated_up_int4``, ``sffn_gated_up``,
+``sffn_gated_up_backward`` with ``sffn_check``).  Tensor arguments are passed by
 their data pointer; ``stream`` defaults to the current torch stream.
-``SparseFFN`` wraps one handle; ``route``, ``quantize_tokens``, ``matmul_int8``, ``grouped_matmul``
-and ``experts_forward`` (module ``operators``) take and return torch tensors, and ``MoEFFN`` is the
-router with its experts as one layer.
+``SparseFFN`` wraps one handle; the operators without one (module ``operators``) take and return torch
+tensors.  ``MoEFFN`` is the router with its experts as one layer, ``Int4FFN`` a gated FFN of 4-bit weights,
+and ``gated_up`` is differentiable.
 """
 from __future__ import annotations
 
@@ -43,7 +44,9 @@ EXPORTS = ("sffn_create", "sffn_create_ex", "sffn_set_live_threshold", "sffn_set
            "sffn_last_error", "sffn_version", "sffn_debug_timeout_probe", "sffn_forward_noalloc",
            "sffn_set_weights_int8", "sffn_get_weights_int8",
            "sffn_route_workspace", "sffn_route", "sffn_quantize_tokens", "sffn_matmul_int8", "sffn_grouped_matmul",
-           "sffn_grouped_workspace", "sffn_experts_workspace", "sffn_experts_forward", "sffn_check")
+           "sffn_grouped_workspace", "sffn_experts_workspace", "sffn_experts_forward", "sffn_check",
+           "sffn_quantize_int4", "sffn_dequantize_int4", "sffn_int4_workspace", "sffn_matmul_int4", "sffn_gated_up_int4",
+           "sffn_gated_up", "sffn_gated_up_backward_workspace", "sffn_gated_up_backward")
 
 _lib = None
 
@@ -92,6 +95,14 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "sffn_experts_workspace": (sz, [ip] * 4),
         "sffn_experts_forward": (ip, [vp, ll] + [vp] * 8 + [ip] * 6 + [vp, sz, vp]),
         "sffn_check": (ip, [vp]),
+        "sffn_quantize_int4": (ip, [vp, ll, vp, vp, ip, ip, ip, vp]),
+        "sffn_dequantize_int4": (ip, [vp, vp, vp, ll, ip, ip, ip, ip, vp]),
+        "sffn_int4_workspace": (sz, [ip] * 5),
+        "sffn_matmul_int4": (ip, [vp, ll, vp, vp, vp, ll] + [ip] * 5 + [vp, sz, vp]),
+        "sffn_gated_up_int4": (ip, [vp, ll, vp, vp, vp, vp, vp, ll] + [ip] * 5 + [vp, sz, vp]),
+        "sffn_gated_up": (ip, [vp, ll, vp, vp, vp, ll, vp, vp, ll] + [ip] * 4 + [vp]),
+        "sffn_gated_up_backward_workspace": (sz, [ip] * 2),
+        "sffn_gated_up_backward": (ip, [vp, ll, vp, vp, ll, vp, ll] + [vp] * 5 + [ip] * 4 + [vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -349,7 +360,9 @@ class SparseFFN:
             pass
 
 
-_OPERATORS = ("MoEFFN", "Routing", "experts_forward", "grouped_matmul", "matmul_int8", "quantize_tokens", "route")
+_OPERATORS = ("Int4FFN", "MoEFFN", "Routing", "dequantize_int4", "experts_forward", "gated_up", "gated_up_backward",
+              "gated_up_int4", "gated_up_saved", "grouped_matmul", "matmul_int4", "matmul_int8", "quantize_int4",
+              "quantize_tokens", "route")
 
 
 def __getattr__(name):  # the tensor operators import torch: only when they are asked for

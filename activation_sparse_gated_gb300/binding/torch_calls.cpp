@@ -39,6 +39,12 @@ struct Calls {
   decltype(&sffn_grouped_matmul) grouped_matmul = nullptr;
   decltype(&sffn_experts_workspace) experts_workspace = nullptr;
   decltype(&sffn_experts_forward) experts_forward = nullptr;
+  decltype(&sffn_quantize_int4) quantize_int4 = nullptr;
+  decltype(&sffn_dequantize_int4) dequantize_int4 = nullptr;
+  decltype(&sffn_int4_workspace) int4_workspace = nullptr;
+  decltype(&sffn_matmul_int4) matmul_int4 = nullptr;
+  decltype(&sffn_gated_up_int4) gated_up_int4 = nullptr;
+  decltype(&sffn_gated_up) gated_up = nullptr;
 } g;
 
 // A tensor that the call can read as it is: of that type and rank, on that
@@ -87,19 +93,26 @@ int64_t whole(PyObject* o) {
   return v;
 }
 
-PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  if (n != 8) {
-    PyErr_SetString(PyExc_TypeError, "bind takes eight addresses");
-    return nullptr;
+// The N addresses that a bind function takes.
+template <int N>
+bool addresses(PyObject* const* args, Py_ssize_t n, std::array<void*, N>* p) {
+  if (n != N) {
+    PyErr_Format(PyExc_TypeError, "%d addresses are taken", N);
+    return false;
   }
-  std::array<void*, 8> p;
-  for (int i = 0; i < 8; ++i) {
-    p[i] = PyLong_AsVoidPtr(args[i]);
-    if (!p[i]) {
+  for (int i = 0; i < N; ++i) {
+    (*p)[i] = PyLong_AsVoidPtr(args[i]);
+    if (!(*p)[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null address");
-      return nullptr;
+      return false;
     }
   }
+  return true;
+}
+
+PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  std::array<void*, 8> p;
+  if (!addresses<8>(args, n, &p)) return nullptr;
   g.route_workspace = reinterpret_cast<decltype(g.route_workspace)>(p[0]);
   g.route = reinterpret_cast<decltype(g.route)>(p[1]);
   g.quantize_tokens = reinterpret_cast<decltype(g.quantize_tokens)>(p[2]);
@@ -108,6 +121,18 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
   g.grouped_matmul = reinterpret_cast<decltype(g.grouped_matmul)>(p[5]);
   g.experts_workspace = reinterpret_cast<decltype(g.experts_workspace)>(p[6]);
   g.experts_forward = reinterpret_cast<decltype(g.experts_forward)>(p[7]);
+  return none();
+}
+
+PyObject* bind_block(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  std::array<void*, 6> p;
+  if (!addresses<6>(args, n, &p)) return nullptr;
+  g.quantize_int4 = reinterpret_cast<decltype(g.quantize_int4)>(p[0]);
+  g.dequantize_int4 = reinterpret_cast<decltype(g.dequantize_int4)>(p[1]);
+  g.int4_workspace = reinterpret_cast<decltype(g.int4_workspace)>(p[2]);
+  g.matmul_int4 = reinterpret_cast<decltype(g.matmul_int4)>(p[3]);
+  g.gated_up_int4 = reinterpret_cast<decltype(g.gated_up_int4)>(p[4]);
+  g.gated_up = reinterpret_cast<decltype(g.gated_up)>(p[5]);
   return none();
 }
 
@@ -255,6 +280,122 @@ PyObject* experts_forward(PyObject* const* args, Py_ssize_t n) {
   return THPVariable_Wrap(std::move(y));
 }
 
+// A group of columns that shares a scale: 0 or a multiple of 64 (longer than any row: cut), or -1.
+int64_t group_size(PyObject* o) {
+  if (!PyLong_CheckExact(o)) return -1;
+  const int64_t v = whole(o);
+  return v < 0 || v % 64 ? -1 : v < SFFN_MAX_SUM ? v : SFFN_MAX_SUM;
+}
+
+// Packed codes [N, K / 2] and their scales [N, G].
+bool takes_codes(PyObject* codes, PyObject* scales, int64_t group, int device, const Tensor** q, const Tensor** s) {
+  if (!takes(codes, at::kByte, 2, device, true, q)) return false;
+  if (!takes(scales, at::kFloat, 2, (*q)->get_device(), true, s)) return false;
+  const int64_t N = (*q)->size(0), K = 2 * (*q)->size(1);
+  return K > 0 && fits(N) && fits(K) && (*s)->size(0) == N && (*s)->size(1) == (group > 0 ? (K + group - 1) / group : 1);
+}
+
+// quantize_int4(w, group) -> (codes, scales)
+PyObject* quantize_int4(PyObject* const* args, Py_ssize_t n) {
+  const Tensor* w;
+  if (n != 2 || !g.quantize_int4 || !takes(args[0], at::kBFloat16, 2, -1, false, &w)) return none();
+  const int64_t N = w->size(0), K = w->size(1), group = group_size(args[1]);
+  int64_t ld;
+  void* stream;
+  const int device = device_of(*w, &stream);
+  if (device < 0 || group < 0 || !fits(N) || !fits(K) || K < 16 || K % 16 || !pitch(*w, &ld)) return none();
+  Tensor q = make({N, K / 2}, at::kByte, device);
+  Tensor s = make({N, group > 0 ? (K + group - 1) / group : 1}, at::kFloat, device);
+  if (g.quantize_int4(w->data_ptr(), ld, q.data_ptr<uint8_t>(), s.data_ptr<float>(), (int)N, (int)K, (int)group, stream) != SFFN_OK)
+    return none();
+  PyObject* r = PyTuple_New(2);
+  if (!r) return nullptr;
+  PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(std::move(q)));
+  PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(std::move(s)));
+  return r;
+}
+
+// dequantize_int4(codes, scales, group, f32) -> y
+PyObject* dequantize_int4(PyObject* const* args, Py_ssize_t n) {
+  const Tensor *q, *s;
+  if (n != 4 || !g.dequantize_int4) return none();
+  const int64_t group = group_size(args[2]);
+  if (group < 0 || !takes_codes(args[0], args[1], group, -1, &q, &s)) return none();
+  void* stream;
+  const int device = device_of(*q, &stream);
+  if (device < 0) return none();
+  const int64_t N = q->size(0), K = 2 * q->size(1);
+  const bool f32 = args[3] == Py_True;
+  Tensor y = make({N, K}, f32 ? at::kFloat : at::kBFloat16, device);
+  if (g.dequantize_int4(q->data_ptr<uint8_t>(), s->data_ptr<float>(), y.data_ptr(), K, (int)N, (int)K, (int)group,
+                        f32 ? SFFN_F32 : SFFN_BF16, stream) != SFFN_OK)
+    return none();
+  return THPVariable_Wrap(std::move(y));
+}
+
+// matmul_int4(x, wq, sw, group, f32) -> y
+PyObject* matmul_int4(PyObject* const* args, Py_ssize_t n) {
+  const Tensor *x, *q, *s;
+  if (n != 5 || !g.matmul_int4 || !takes(args[0], at::kBFloat16, 2, -1, false, &x)) return none();
+  const int64_t group = group_size(args[3]);
+  void* stream;
+  const int device = device_of(*x, &stream);
+  if (device < 0 || group < 0 || !takes_codes(args[1], args[2], group, device, &q, &s)) return none();
+  const int64_t T = x->size(0), K = x->size(1), N = q->size(0);
+  int64_t ld;
+  if (!fits(T) || K != 2 * q->size(1) || !pitch(*x, &ld)) return none();
+  const bool f32 = args[4] == Py_True;
+  const int type = f32 ? SFFN_F32 : SFFN_BF16;
+  Tensor y = make({T, N}, f32 ? at::kFloat : at::kBFloat16, device), scratch;
+  const size_t nb = g.int4_workspace((int)T, (int)N, (int)K, type, 0);
+  if (nb) scratch = make({(int64_t)nb}, at::kByte, device);
+  if (g.matmul_int4(x->data_ptr(), ld, q->data_ptr<uint8_t>(), s->data_ptr<float>(), y.data_ptr(), N, (int)T, (int)N, (int)K,
+                    (int)group, type, nb ? scratch.data_ptr() : nullptr, nb, stream) != SFFN_OK)
+    return none();
+  return THPVariable_Wrap(std::move(y));
+}
+
+// gated_up_int4(x, w1q, s1, w3q, s3, group, act) -> h
+PyObject* gated_up_int4(PyObject* const* args, Py_ssize_t n) {
+  const Tensor *x, *q1, *s1, *q3, *s3;
+  if (n != 7 || !g.gated_up_int4 || !takes(args[0], at::kBFloat16, 2, -1, false, &x)) return none();
+  const int64_t group = group_size(args[5]);
+  void* stream;
+  const int device = device_of(*x, &stream);
+  if (device < 0 || group < 0 || !takes_codes(args[1], args[2], group, device, &q1, &s1) ||
+      !takes_codes(args[3], args[4], group, device, &q3, &s3) || q3->sizes() != q1->sizes())
+    return none();
+  const int64_t T = x->size(0), D = x->size(1), H = q1->size(0);
+  int64_t ld;
+  if (!fits(T) || D != 2 * q1->size(1) || !pitch(*x, &ld)) return none();
+  Tensor h = make({T, H}, at::kBFloat16, device), scratch;
+  const size_t nb = g.int4_workspace((int)T, (int)H, (int)D, SFFN_BF16, 1);
+  if (nb) scratch = make({(int64_t)nb}, at::kByte, device);
+  if (g.gated_up_int4(x->data_ptr(), ld, q1->data_ptr<uint8_t>(), s1->data_ptr<float>(), q3->data_ptr<uint8_t>(),
+                      s3->data_ptr<float>(), h.data_ptr(), H, (int)T, (int)D, (int)H, (int)group, (int)whole(args[6]),
+                      nb ? scratch.data_ptr() : nullptr, nb, stream) != SFFN_OK)
+    return none();
+  return THPVariable_Wrap(std::move(h));
+}
+
+// gated_up(x, W1, W3, act) -> h, of tensors that require no gradient
+PyObject* gated_up(PyObject* const* args, Py_ssize_t n) {
+  const Tensor *x, *W1, *W3;
+  if (n != 4 || !g.gated_up || !takes(args[0], at::kBFloat16, 2, -1, false, &x)) return none();
+  void* stream;
+  const int device = device_of(*x, &stream);
+  if (device < 0 || !takes(args[1], at::kBFloat16, 2, device, true, &W1) || !takes(args[2], at::kBFloat16, 2, device, true, &W3))
+    return none();
+  const int64_t T = x->size(0), D = x->size(1), H = W1->size(0);
+  int64_t ld;
+  if (!fits(T) || !fits(D) || !fits(H) || W1->size(1) != D || W3->sizes() != W1->sizes() || !pitch(*x, &ld)) return none();
+  Tensor h = make({T, H}, at::kBFloat16, device);
+  if (g.gated_up(x->data_ptr(), ld, W1->data_ptr(), W3->data_ptr(), h.data_ptr(), H, nullptr, nullptr, 0, (int)T, (int)D,
+                 (int)H, (int)whole(args[3]), stream) != SFFN_OK)
+    return none();
+  return THPVariable_Wrap(std::move(h));
+}
+
 // A C++ exception (an allocation that fails, say) becomes PyTorch's Python one.
 template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* guarded(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -270,11 +411,17 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef methods[] = {
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind)), METH_FASTCALL, nullptr},
+    {"bind_block", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind_block)), METH_FASTCALL, nullptr},
     method<route>("route"),
     method<quantize_tokens>("quantize_tokens"),
     method<matmul_int8>("matmul_int8"),
     method<grouped_matmul>("grouped_matmul"),
     method<experts_forward>("experts_forward"),
+    method<quantize_int4>("quantize_int4"),
+    method<dequantize_int4>("dequantize_int4"),
+    method<matmul_int4>("matmul_int4"),
+    method<gated_up_int4>("gated_up_int4"),
+    method<gated_up>("gated_up"),
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -2,8 +2,11 @@
 // groups of more than a few rows:
 //
 //   plain   y[r, n] = sum_k x[s(r), k] w[e, n, k]
-//   gated   h[r, n] = A(sum_k x w1) * (sum_k x w3)      (two products, one pass over x)
+//   gated   h[r, n] = A(sum_k x w1) * (sum_k x w3)      (two products, one pass over x; for training both are stored, too)
 //   int8    y[r, n] = sx sw sum_k xq wq
+//   sums    y[r, n] = sum_k x w + sum_k x' w3            (x beside x' in a row: one accumulator, the gated block's dx)
+//   across  y[r, n] = sum_k x[k, r] w[k, n]              (both operands lie along the result: its weights' gradients)
+//   parts   y[r, n] = sum_k x (w + w')                   (w beside w' in a row: weights of more than 8 bits)
 //
 // The weights are the M side of the MMA (128 rows of w a block, 256 a pair of
 // blocks with cta_group::2) and the rows of x the N side, whose width is any
@@ -87,6 +90,8 @@ struct TgArgs {
   int S;       // operand stages (int8: of widened codes)
   int SR;      // raw stages (int8)
   int wcol;    // int8: first TMEM column of the widened weights
+  int wrap;    // chunk of w from which x's chunks are taken again (KC: none)
+  int half;    // chunk from which the weights are w3's (KC: none)
   int ks;      // blocks of a cluster that cut K between them (1: no cut)
   int cols;    // TMEM columns allocated
   int vec;     // rows of y take 16-byte stores: y, ldy and N are multiples of that
@@ -337,7 +342,8 @@ __device__ __forceinline__ float gate_up(int act, float z, float u) {
   return (act == ACT_SILU ? g == 0.f : z <= 0.f) ? 0.f : g * u;
 }
 
-template <int CTAS, int MODE, bool KN>
+// XT: x is [K, rows], read as the KN weights are: boxes of 64 values of K by 64 rows, MN-major.
+template <int CTAS, int MODE, bool KN, bool XT>
 __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
     gmm_tc_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mW3,
                   const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mXb, const TgArgs p) {
@@ -409,7 +415,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
     for (int e0 = 0; e0 < p.g.E; e0 += 32) {
       const int e = e0 + lane;
       int hi = 0;  // the end of group e, then the largest end up to it
-      if (e < p.g.E) hi = p.g.offsets ? min(max(p.g.offsets[e + 1], 0), p.g.R) : p.g.R;
+      if (e < p.g.E) hi = p.g.offsets ? min(max(p.g.offsets[e + 1], 0), p.g.R) : XT ? (e + 1) * p.g.per : p.g.R;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, hi, o);
@@ -458,7 +464,8 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
       const int nl = q.n / CTAS, nb = q.mt * 128 * CTAS + n0r;
       const int xr = q.r0 + (int)rank * nl;  // this block's rows of x
       const bool big = nl > p.bxr;           // one copy of the whole region, or one small box
-      const uint32_t xbytes = p.g.index ? (uint32_t)nl * 128u : (big ? NTl : (uint32_t)p.bxr) * 128u;
+      const uint32_t xbytes = XT ? (uint32_t)(nl + 63) / 64u * 8192u
+                                 : p.g.index ? (uint32_t)nl * 128u : (big ? NTl : (uint32_t)p.bxr) * 128u;
       const uint32_t tx = ((GATED ? 2 : 1) * AB + xbytes) * CTAS;
       int gy[2][4];
       if (xside && p.g.index) {
@@ -491,8 +498,11 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
           if (lane == 0) {
             if (rank == 0) mbar_arrive_expect_tx(&fb[s], tx);
             if constexpr (KN) {
-              tma_w3d<CTAS>(st, &mW, nb, c * KW, q.e, bar);
-              tma_w3d<CTAS>(st + AB / 2, &mW, nb + 64, c * KW, q.e, bar);
+              const bool second = c >= p.half;
+              const CUtensorMap* map = second ? &mW3 : &mW;
+              const int k = (second ? c - p.half : c) * KW, e = XT ? 0 : q.e;
+              tma_w3d<CTAS>(st, map, nb, k, e, bar);
+              tma_w3d<CTAS>(st + AB / 2, map, nb + 64, k, e, bar);
             } else {
               tma_w3d<CTAS>(st, &mW, c * KW, nb, q.e, bar);
             }
@@ -500,11 +510,15 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
           }
         } else {
           const uint32_t bst = st + (GATED ? 2 : 1) * AB;
-          if (p.g.index) {
+          if constexpr (XT) {
+            if (lane == 0)
+              for (int i = 0; i < nl; i += 64)
+                tma_x2d<CTAS>(bst + (uint32_t)i * 128u, &mX, xr + q.e * (p.g.xper - p.g.per) + i, c * KW, bar);
+          } else if (p.g.index) {
             if (lane < nl / 4) tma_gather4<CTAS>(bst + lane * 512u, &mX, c * KW, gy[0], bar);
             if (lane + 32 < nl / 4) tma_gather4<CTAS>(bst + (lane + 32) * 512u, &mX, c * KW, gy[1], bar);
           } else if (lane == 0) {
-            tma_x2d<CTAS>(bst, big ? &mXb : &mX, c * KW, xr, bar);
+            tma_x2d<CTAS>(bst, big ? &mXb : &mX, (I8 || c < p.wrap ? c : c - p.wrap) * KW, xr, bar);
           }
         }
         if (++s == (uint32_t)S) {
@@ -529,11 +543,11 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
       uint32_t s = 0, par = 0, tl = 0, st = st0;   // st: the stage's address in 16-byte units
       const uint32_t st16 = st_bytes >> 4, eb = smem_u32(empty);
       const uint32_t hi = (uint32_t)(smem_desc(0, 0, 1024, SMEM_LAYOUT_SW128) >> 32);
-      const uint32_t alo0 = (KN ? AB / 2 : 16) >> 4 << 16, blo0 = 1u << 16;  // the leading byte offset
+      const uint32_t alo0 = (KN ? AB / 2 : 16) >> 4 << 16, blo0 = (XT ? AB / 2 : 16) >> 4 << 16;  // the leading byte offset
       bool ok = true;
       for (int t = first; t < total && ok; t += step, ++tl) {
         const Tile q = tile_at<CTAS>(p, s_off, s_pre, t);
-        const uint32_t idesc = (F16 ? 1u << 4 : (1u << 4) | (1u << 7) | (1u << 10)) | ((KN ? 1u : 0u) << 15) |
+        const uint32_t idesc = (F16 ? 1u << 4 : (1u << 4) | (1u << 7) | (1u << 10)) | ((KN ? 1u : 0u) << 15) | ((XT ? 1u : 0u) << 16) |
                                ((uint32_t)(q.n >> 3) << 17) | ((uint32_t)(128 * CTAS >> 4) << 24);
         const uint32_t b = p.nacc == 2 ? tl & 1 : 0, use = p.nacc == 2 ? tl >> 1 : tl;
         if (use > 0 && !__all_sync(0xffffffffu, tg_wait<CTAS == 2>(&acce[b], (use - 1) & 1, abort_flag, p.err))) break;
@@ -557,7 +571,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
 #pragma unroll
             for (int k = 0; k < (I8 ? 0 : 4); ++k) {
               const uint32_t ak = al + (KN ? (k * 2048) >> 4 : 2 * k);
-              tg_mma<CTAS>(d, ak, hi, bl + 2 * k, hi, idesc, k == 0 ? acc : 1u);
+              tg_mma<CTAS>(d, ak, hi, bl + (XT ? (k * 2048) >> 4 : 2 * k), hi, idesc, k == 0 ? acc : 1u);
               if (GATED) tg_mma<CTAS>(d + p.NT, ak + (AB >> 4), hi, bl + 2 * k, hi, idesc, k == 0 ? acc : 1u);
             }
             tg_commit<CTAS>(eb + 8 * s);
@@ -684,6 +698,8 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
       const uint32_t ta = tmem + b * (uint32_t)((GATED ? 2 : 1) * p.NT) + ((uint32_t)(32 * (ew & 3)) << 16);
       const float sw = F16 && nok ? p.g.sw[(size_t)q.e * p.g.N + n] : 0.f;
       const int rows = q.r1 - q.r0;
+      void* const yb = XT && q.e ? p.g.y2 : p.g.y;        // the group's result and
+      const int yr = q.r0 - (XT ? q.e * p.g.per : 0);     // the tile's first row of it
       if (CTAS == 1 && ks > 1) {
         // K is cut over the cluster: every block leaves its partial tile, [row of x][128 rows of w], in the stages
         // (their copies and MMAs are done, and the producers wait for `partd`); then each sums its share of the
@@ -732,6 +748,15 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
           if (GATED) {
             float u[4];
             sum_of(at + up, u);
+            if (p.g.z) {
+              const uint64_t o = (uint64_t)(uint32_t)(q.r0 + r) * (uint64_t)p.g.ldz + nc;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (nc + i < p.g.N) {
+                  p.g.z[o + i] = f[i];
+                  p.g.u[o + i] = u[i];
+                }
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) f[i] = gate_up(p.g.act, f[i], u[i]);
           }
@@ -746,14 +771,14 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) f[i] = f[i] * sx * s4[i];
           }
-          const uint64_t o = (uint64_t)(uint32_t)gr * (uint64_t)p.g.ldy + nc;
+          const uint64_t o = (uint64_t)(uint32_t)(yr + r) * (uint64_t)p.g.ldy + nc;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             if (nc + i < p.g.N) {
               if (p.g.y_f32)
-                reinterpret_cast<float*>(p.g.y)[o + i] = f[i];
+                reinterpret_cast<float*>(yb)[o + i] = f[i];
               else
-                reinterpret_cast<__nv_bfloat16*>(p.g.y)[o + i] = __float2bfloat16_rn(f[i]);
+                reinterpret_cast<__nv_bfloat16*>(yb)[o + i] = __float2bfloat16_rn(f[i]);
             }
         }
         __syncwarp();
@@ -765,7 +790,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
         uint32_t v[32];
         tmem_ld32(ta + c0, v);
         const int left = min(rows - c0, 32);  // rows of this piece, r0 + c0 on
-        const uint64_t y0 = (uint64_t)(uint32_t)(q.r0 + c0) * (uint64_t)p.g.ldy;
+        const uint64_t y0 = (uint64_t)(uint32_t)(yr + c0) * (uint64_t)p.g.ldy;
         float sx = 0.f;  // lane j: the scale of row j
         if (F16 && lane < left) {
           int src = q.r0 + c0 + lane;
@@ -775,10 +800,51 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
           }
           sx = src >= 0 ? p.g.sx[src] : 0.f;
         }
+        auto done = [&] {
+          if (c0 + 32 * (EW / 4) < rows) return;  // this warp has read its last columns
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (CTAS == 2)
+              arrive_remote(cluster_map(smem_u32(&acce[b]), 0));
+            else
+              mbar_arrive(&acce[b]);
+          }
+        };
         if constexpr (GATED) {
           uint32_t u[32];
           tmem_ld32(ta + p.NT + c0, u);
           tmem_ld_wait();
+          done();
+          if (p.g.z) {  // kept as they are, in fp32, through this warp's shared scratch like the result
+            const uint32_t buf = smb + epi0 + (uint32_t)ew * TG_EPI_BYTES;
+            const uint64_t z0 = (uint64_t)(uint32_t)(q.r0 + c0) * (uint64_t)p.g.ldz + (q.mt * 128 * CTAS + n0r + 32 * (ew & 3));
+            const int room = p.g.NY - (q.mt * 128 * CTAS + n0r + 32 * (ew & 3));  // columns from z0 on
+            auto keep = [&](const uint32_t (&val)[32], float* to) {
+              if (!p.vec) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (nok && j < left) to[(uint64_t)j * (uint64_t)p.g.ldz + lane] = __uint_as_float(val[j]);
+                return;
+              }
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) sts4(buf + (uint32_t)(j * TG_EPI_PITCH + lane) * 4u, val[16 * h + j]);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int j = 4 * i + (lane >> 3), c = 4 * (lane & 7);
+                  const uint4 d = lds16a(buf + (uint32_t)(j * TG_EPI_PITCH + c) * 4u);
+                  if (16 * h + j < left && c < room)
+                    *reinterpret_cast<uint4*>(to + (uint64_t)(16 * h + j) * (uint64_t)p.g.ldz + c) = d;
+                }
+                __syncwarp();
+              }
+            };
+            keep(v, p.g.z + z0);
+            keep(u, p.g.u + z0);
+          }
           if (p.g.act == 0) {  // hoisted: as a branch of each value ReLU pays for the others
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(gate_up(0, __uint_as_float(v[j]), __uint_as_float(u[j])));
@@ -789,16 +855,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
           }
         } else {
           tmem_ld_wait();
-        }
-        if (c0 + 32 * (EW / 4) >= rows) {  // this warp has read its last columns
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (CTAS == 2)
-              arrive_remote(cluster_map(smem_u32(&acce[b]), 0));
-            else
-              mbar_arrive(&acce[b]);
-          }
+          done();
         }
         if (p.vec) {
           // through this warp's shared scratch, so that a store carries 16 bytes of a row a lane
@@ -819,7 +876,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
                 const int j = 4 * i + (lane >> 3), c = 4 * (lane & 7);
                 const uint4 d = lds16a(buf + (uint32_t)(j * TG_EPI_PITCH + c) * 4u);
                 if (16 * h + j < left && nc + c < p.g.NY)
-                  *reinterpret_cast<uint4*>(reinterpret_cast<float*>(p.g.y) + y0 +
+                  *reinterpret_cast<uint4*>(reinterpret_cast<float*>(yb) + y0 +
                                             (uint64_t)(16 * h + j) * (uint64_t)p.g.ldy + nc + c) = d;
               }
               __syncwarp();
@@ -840,7 +897,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
               const int j = 8 * i + (lane >> 2), c = 8 * (lane & 3);
               const uint32_t at = buf + (uint32_t)(j * TG_EPI_PITCH + c) * 4u;
               const uint4 d = lds16a(at), e = lds16a(at + 16);
-              __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(p.g.y) + y0 + (uint64_t)(2 * j) * (uint64_t)p.g.ldy + nc + c;
+              __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(yb) + y0 + (uint64_t)(2 * j) * (uint64_t)p.g.ldy + nc + c;
               if (nc + c < p.g.NY) {
                 if (2 * j < left)
                   *reinterpret_cast<uint4*>(y) =
@@ -856,7 +913,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
           }
         } else {
           const uint32_t size = p.g.y_f32 ? 4 : 2;
-          uint8_t* to = reinterpret_cast<uint8_t*>(p.g.y) + (y0 + n) * size;
+          uint8_t* to = reinterpret_cast<uint8_t*>(yb) + (y0 + n) * size;
           const uint64_t pitch = (uint64_t)p.g.ldy * size;
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
@@ -904,18 +961,19 @@ bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, 
 }
 
 bool encode_w(CUtensorMap* m, const void* w, const GmmArgs& a) {
-  const cuuint64_t eb = a.i8 ? 1 : 2, N = (cuuint64_t)a.N, K = (cuuint64_t)a.K;
-  const cuuint64_t in = a.kn ? N : K, out = a.kn ? K : N;
-  const cuuint64_t dims[3] = {in, out, (cuuint64_t)a.E};
-  const cuuint64_t strides[2] = {in * eb, N * K * eb};
+  const cuuint64_t eb = a.i8 ? 1 : 2, N = (cuuint64_t)a.N;
+  const cuuint64_t K = (cuuint64_t)(a.split ? 2 * ((a.K + 63) / 64 * 64) : a.K1 ? a.K1 : a.K);
+  const cuuint64_t in = a.kn ? N : K, out = a.kn ? K : N, row = a.ldw ? (cuuint64_t)a.ldw : in;
+  const cuuint64_t dims[3] = {in, out, a.xt ? 1 : (cuuint64_t)a.E};
+  const cuuint64_t strides[2] = {row * eb, row * out * eb};
   const cuuint32_t box[3] = {a.i8 ? 128u : 64u, a.kn ? 64u : 128u, 1u};
   return encode(m, w, 3, dims, strides, box, a.i8 != 0);
 }
 
-template <int CTAS, int MODE, bool KN>
+template <int CTAS, int MODE, bool KN, bool XT = false>
 cudaError_t tg_go(const CUtensorMap& mW, const CUtensorMap& mW3, const CUtensorMap& mX, const CUtensorMap& mXb,
                   TgArgs p, size_t smem, int sms, cudaStream_t s) {
-  auto kernel = gmm_tc_kernel<CTAS, MODE, KN>;
+  auto kernel = gmm_tc_kernel<CTAS, MODE, KN, XT>;
   constexpr int threads = MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS;
   struct Setup {
     std::once_flag once;
@@ -980,13 +1038,17 @@ cudaError_t launch_gmm_tc(const GmmArgs& a, int ctas, int nt, cudaStream_t s) {
   p.g = a;
   p.NT = nt;
   p.MT = (a.N + 128 * ctas - 1) / (128 * ctas);
-  p.KC = (a.K + 63) / 64;
-  const bool gated = a.w3 != nullptr;
+  const int kc = (a.K + 63) / 64;
+  p.KC = a.split ? 2 * kc : kc;
+  p.wrap = kc;
+  p.half = a.K1 ? kc / 2 : p.KC;
+  const bool gated = a.w3 != nullptr && !a.K1;
   cudaError_t e = ops_error_word(&p.err);
   if (e != cudaSuccess) return e;
   const size_t yb = a.y_f32 ? 4 : 2;
   p.g.NY = std::max(a.N, a.NY);
-  p.vec = ((uintptr_t)a.y & 15) == 0 && a.ldy * yb % 16 == 0 && p.g.NY * yb % 16 == 0;
+  p.vec = ((uintptr_t)a.y & 15) == 0 && a.ldy * yb % 16 == 0 && p.g.NY * yb % 16 == 0 && ((uintptr_t)a.y2 & 15) == 0 &&
+          ((uintptr_t)a.z & 15) == 0 && ((uintptr_t)a.u & 15) == 0 && a.ldz % 4 == 0;
   const size_t fixed = tg_fixed(a.i8 ? 4 : 8, a.E);
   const int room = (int)(TG_SMEM - fixed);
   const int ntl = p.NT / ctas, bb = (ntl + 7) / 8 * 1024;
@@ -1005,8 +1067,13 @@ cudaError_t launch_gmm_tc(const GmmArgs& a, int ctas, int nt, cudaStream_t s) {
   p.cols = cols;
   p.bxr = std::min(ntl, 32);
   CUtensorMap mW, mW3, mX, mXb;
-  if (!encode_w(&mW, a.w, a) || !encode_w(&mW3, gated ? a.w3 : a.w, a)) return cudaErrorInvalidValue;
-  {
+  if (!encode_w(&mW, a.w, a) || !encode_w(&mW3, a.w3 ? a.w3 : a.w, a)) return cudaErrorInvalidValue;
+  if (a.xt) {
+    const cuuint64_t dims[2] = {(cuuint64_t)(a.E * (long long)a.xper), (cuuint64_t)a.K}, strides[1] = {(cuuint64_t)a.ldx * 2};
+    const cuuint32_t box[2] = {64u, 64u};
+    if (!encode(&mX, a.x, 2, dims, strides, box, false)) return cudaErrorInvalidValue;
+    mXb = mX;
+  } else {
     const cuuint64_t eb = a.i8 ? 1 : 2;
     const cuuint64_t dims[2] = {(cuuint64_t)a.K, (cuuint64_t)a.XR}, strides[1] = {(cuuint64_t)a.ldx * eb};
     const cuuint32_t box[2] = {a.i8 ? 128u : 64u, a.index ? 1u : (cuuint32_t)p.bxr};
@@ -1021,6 +1088,9 @@ cudaError_t launch_gmm_tc(const GmmArgs& a, int ctas, int nt, cudaStream_t s) {
   if (gated)
     return ctas == 2 ? tg_go<2, TG_GATED, false>(mW, mW3, mX, mXb, p, smem, sms, s)
                      : tg_go<1, TG_GATED, false>(mW, mW3, mX, mXb, p, smem, sms, s);
+  if (a.xt)
+    return ctas == 2 ? tg_go<2, TG_BF16, true, true>(mW, mW3, mX, mXb, p, smem, sms, s)
+                     : tg_go<1, TG_BF16, true, true>(mW, mW3, mX, mXb, p, smem, sms, s);
   if (a.kn)
     return ctas == 2 ? tg_go<2, TG_BF16, true>(mW, mW3, mX, mXb, p, smem, sms, s)
                      : tg_go<1, TG_BF16, true>(mW, mW3, mX, mXb, p, smem, sms, s);
@@ -1099,7 +1169,7 @@ cudaError_t launch_gmm(const GmmArgs& a, cudaStream_t s) {
   const bool fill = 2 * pairs >= ops_num_sms();
   // Gate and up together: 256 rows a tile take all of TMEM, so their epilogue is not hidden, and still win from 128
   // rows a group on (4096 tokens, 8 of 64 experts, D = 2560, H = 1024: 561 against 643 us; 512 tokens 225 / 211).
-  if (a.w3) return a.R >= 128 * busy && fill && a.N > 128 ? launch_gmm_tc(a, 2, 256, s) : launch_gmm_tc(a, 1, 128, s);
+  if (a.w3 && !a.K1) return a.R >= 128 * busy && fill && a.N > 128 ? launch_gmm_tc(a, 2, 256, s) : launch_gmm_tc(a, 1, 128, s);
   return a.R >= 96 * busy && fill && a.N > 128 ? launch_gmm_tc(a, 2, 256, s) : launch_gmm_tc(a, 1, 128, s);
 }
 

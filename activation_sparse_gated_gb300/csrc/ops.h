@@ -44,6 +44,14 @@ struct GmmArgs {
   int i8 = 0, y_f32 = 0, kn = 0, act = 0;
   int NY = 0;                     // columns of y that may be written (past N: zeros), if more than N
   int f16 = 0;                    // x and w are fp16 copies of int8 codes (with their scales)
+  float *z = nullptr, *u = nullptr;  // gated: the two products themselves, fp32, row pitch ldz (NY columns)
+  long long ldz = 0;
+  int split = 0;                  // w's rows hold two parts of round_up(K, 64) columns each, both multiplied by x
+  int K1 = 0;                     // kn: rows 0 .. K1 of K are w's, rows K / 2 .. K / 2 + K1 w3's (K / 2 = round_up(K1, 64))
+  int xt = 0;                     // kn: x is [K, rows]; group e's rows are its columns from e * xper on, w is every group's
+  int per = 0, xper = 0;          // xt: rows of a group
+  void* y2 = nullptr;             // xt: the second group's result (its first row)
+  long long ldw = 0;              // kn: row pitch of w, if not N
   void* workspace = nullptr;      // gmm_workspace() bytes
 };
 cudaError_t launch_gmm_rows(const GmmArgs& a, cudaStream_t s);
@@ -66,6 +74,51 @@ struct ExpertsArgs {
 };
 size_t experts_workspace(int T, int k, int D, int H);
 cudaError_t launch_experts(const ExpertsArgs& a, cudaStream_t s);
+
+// ---- int4.cu
+struct Int4Args {
+  const void* x;
+  long long ldx;
+  const uint8_t *w, *w3;  // w3: the gated block, else null
+  const float *sw, *s3;
+  void* y;
+  long long ldy;
+  int T, N, K, group, y_f32, act;
+  void* workspace;  // int4_workspace() bytes
+};
+cudaError_t launch_quantize_int4(const void* w, long long ldw, uint8_t* q, float* sc, int N, int K, int group,
+                                 cudaStream_t s);
+cudaError_t launch_dequantize_int4(const uint8_t* q, const float* sc, void* y, long long ldy, int N, int K, int group,
+                                   int y_f32, cudaStream_t s);
+size_t int4_workspace(int T, int N, int K, int split, int gated);  // split: y is fp32, or gated
+cudaError_t launch_matmul_int4(const Int4Args& a, cudaStream_t s);
+
+// ---- gated.cu
+struct GatedArgs {
+  const void* x;
+  long long ldx;
+  const void *W1, *W3;
+  void* h;
+  long long ldh;
+  float *z, *u;  // may be null (both)
+  long long ldz;
+  int T, D, H, act;
+};
+cudaError_t launch_gated_up(const GatedArgs& a, cudaStream_t s);
+struct GatedGradArgs {
+  const void* dh;
+  long long lddh;
+  const float *z, *u;
+  long long ldz;
+  const void* x;
+  long long ldx;
+  const void *W1, *W3;
+  void *dx, *dW1, *dW3;  // each may be null
+  int T, D, H, act;
+  void* workspace;  // gated_grad_workspace() bytes
+};
+size_t gated_grad_workspace(int T, int H);
+cudaError_t launch_gated_grad(const GatedGradArgs& a, cudaStream_t s);
 
 // A launch whose blocks may start while the kernel before it in the stream
 // ends (each kernel waits for that one's results itself).

@@ -1,6 +1,7 @@
 // ops_api.cu -- the handle-free entry points of include/sffn.h: the router,
-// per-token int8 codes, the int8 product, the products grouped by expert and
-// the gated experts' forward.  Argument checks come before any CUDA call.
+// per-token int8 codes, the int8 product, the products grouped by expert, the
+// gated experts' forward, 4-bit weights and their products, and the gated block
+// with its backward pass.  Argument checks come before any CUDA call.
 #include <atomic>
 #include <cstdarg>
 #include <cstdio>
@@ -269,6 +270,249 @@ int sffn_experts_forward(const void* x, long long ldx, const float* weights, con
   a.H = H;
   a.act = act;
   const cudaError_t e = launch_experts(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SFFN_OK : cuda_fail(fn, e);
+}
+
+// The checks that the 4-bit entry points share; G: scales a row.
+static int check_int4(const char* fn, long long N, int K, int group, int* G) {
+  if (N < 1 || N > SFFN_MAX_ROWS) return fail(SFFN_ERR_ARG, "%s: %lld rows of weights, 1..%d are taken", fn, N, SFFN_MAX_ROWS);
+  if (K < 16 || K % 16 != 0 || K > SFFN_MAX_SUM)
+    return fail(SFFN_ERR_ARG, "%s: %d columns of weights: a multiple of 16, at most %d, is taken", fn, K, SFFN_MAX_SUM);
+  if (group < 0 || group % 64 != 0)
+    return fail(SFFN_ERR_ARG, "%s: group=%d must be a multiple of 64, or 0 for one scale a row", fn, group);
+  *G = group > 0 && group < K ? (K - 1) / group + 1 : 1;
+  return SFFN_OK;
+}
+
+int sffn_quantize_int4(const void* w, long long ldw, uint8_t* codes, float* scales, int N, int K, int group, void* stream) {
+  const char* fn = "sffn_quantize_int4";
+  if (N < 0) return fail(SFFN_ERR_ARG, "%s: N=%d", fn, N);
+  int G = 0;
+  const int rc = check_int4(fn, N < 1 ? 1 : N, K, group, &G);
+  if (rc != SFFN_OK) return rc;
+  if (ldw < K || ldw % 8 != 0)
+    return fail(SFFN_ERR_ARG, "%s: w's row pitch %lld must be a multiple of 8 and at least K=%d", fn, ldw, K);
+  if (N == 0) return SFFN_OK;
+  if (!w || !codes || !scales) return fail(SFFN_ERR_ARG, "%s: null pointer", fn);
+  if (misaligned(w, 16) || misaligned(codes, 16)) return fail(SFFN_ERR_ALIGN, "%s: w and codes must be 16-byte aligned", fn);
+  if (misaligned(scales, 4)) return fail(SFFN_ERR_ALIGN, "%s: scales are not aligned to their element", fn);
+  const unsigned long long nw = ((unsigned long long)(N - 1) * ldw + K) * 2, nq = (unsigned long long)N * K / 2, ns = 4ull * N * G;
+  if (overlap(w, nw, codes, nq) || overlap(w, nw, scales, ns) || overlap(codes, nq, scales, ns))
+    return fail(SFFN_ERR_ARG, "%s: an output overlaps w or the other one", fn);
+  const cudaError_t e = launch_quantize_int4(w, ldw, codes, scales, N, K, group, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SFFN_OK : cuda_fail(fn, e);
+}
+
+int sffn_dequantize_int4(const uint8_t* codes, const float* scales, void* y, long long ldy, int N, int K, int group,
+                         int y_dtype, void* stream) {
+  const char* fn = "sffn_dequantize_int4";
+  if (y_dtype != SFFN_BF16 && y_dtype != SFFN_F32) return fail(SFFN_ERR_DTYPE, "%s: y is bf16 or f32", fn);
+  if (N < 0) return fail(SFFN_ERR_ARG, "%s: N=%d", fn, N);
+  int G = 0;
+  const int rc = check_int4(fn, N < 1 ? 1 : N, K, group, &G);
+  if (rc != SFFN_OK) return rc;
+  if (ldy < K || ldy % 8 != 0)
+    return fail(SFFN_ERR_ARG, "%s: y's row pitch %lld must be a multiple of 8 and at least K=%d", fn, ldy, K);
+  if (N == 0) return SFFN_OK;
+  if (!y || !codes || !scales) return fail(SFFN_ERR_ARG, "%s: null pointer", fn);
+  if (misaligned(y, 16) || misaligned(codes, 16)) return fail(SFFN_ERR_ALIGN, "%s: codes and y must be 16-byte aligned", fn);
+  if (misaligned(scales, 4)) return fail(SFFN_ERR_ALIGN, "%s: scales are not aligned to their element", fn);
+  const unsigned long long ny = ((unsigned long long)(N - 1) * ldy + K) * (y_dtype == SFFN_F32 ? 4 : 2);
+  if (overlap(y, ny, codes, (unsigned long long)N * K / 2) || overlap(y, ny, scales, 4ull * N * G))
+    return fail(SFFN_ERR_ARG, "%s: y overlaps codes or scales", fn);
+  const cudaError_t e = launch_dequantize_int4(codes, scales, y, ldy, N, K, group, y_dtype == SFFN_F32,
+                                               static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SFFN_OK : cuda_fail(fn, e);
+}
+
+size_t sffn_int4_workspace(int T, int N, int K, int y_dtype, int gated) {
+  if (T < 1 || N < 1 || K < 1) return 0;
+  return int4_workspace(T, N, K, y_dtype == SFFN_F32 || gated, gated != 0);
+}
+
+// Both products by 4-bit weights; w3 and s3 null: the plain one.
+static int run_int4(const char* fn, const void* x, long long ldx, const uint8_t* w, const float* sw, const uint8_t* w3,
+                    const float* s3, bool gated, void* y, long long ldy, int T, int N, int K, int group, int y_dtype,
+                    int act, void* workspace, size_t workspace_bytes, void* stream) {
+  int G = 0;
+  const int rc = check_int4(fn, N, K, group, &G);
+  if (rc != SFFN_OK) return rc;
+  if (T < 0 || T > SFFN_MAX_ROWS) return fail(SFFN_ERR_ARG, "%s: T=%d outside 0..%d", fn, T, SFFN_MAX_ROWS);
+  if (ldx < K || ldx % 8 != 0)
+    return fail(SFFN_ERR_ARG, "%s: x's row pitch %lld must be a multiple of 8 and at least %d", fn, ldx, K);
+  if (ldy < N) return fail(SFFN_ERR_ARG, "%s: the result's row pitch %lld is below %d", fn, ldy, N);
+  if (T == 0) return SFFN_OK;
+  if (!x || !w || !sw || !y || (gated && (!w3 || !s3))) return fail(SFFN_ERR_ARG, "%s: null pointer", fn);
+  if (misaligned(x, 16) || misaligned(w, 16) || misaligned(w3, 16))
+    return fail(SFFN_ERR_ALIGN, "%s: x and the codes must be 16-byte aligned", fn);
+  if (misaligned(y, y_dtype == SFFN_F32 ? 4 : 2) || misaligned(sw, 4) || misaligned(s3, 4))
+    return fail(SFFN_ERR_ALIGN, "%s: a pointer is not aligned to its element", fn);
+  const size_t need = int4_workspace(T, N, K, y_dtype == SFFN_F32 || gated, gated);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(SFFN_ERR_ARG, "%s: workspace of %zu bytes, %zu needed", fn, workspace ? workspace_bytes : (size_t)0, need);
+  if (need > 0 && misaligned(workspace, 16)) return fail(SFFN_ERR_ALIGN, "%s: workspace is not 16-byte aligned", fn);
+  const unsigned long long ny = ((unsigned long long)(T - 1) * ldy + N) * (y_dtype == SFFN_F32 ? 4 : 2);
+  const unsigned long long nx = ((unsigned long long)(T - 1) * ldx + K) * 2, nw = (unsigned long long)N * K / 2, ns = 4ull * N * G;
+  if (overlap(x, nx, y, ny) || overlap(w, nw, y, ny) || overlap(sw, ns, y, ny) || (gated && (overlap(w3, nw, y, ny) || overlap(s3, ns, y, ny))) ||
+      (need > 0 && overlap(workspace, need, y, ny)))
+    return fail(SFFN_ERR_ARG, "%s: the result overlaps an operand or the workspace", fn);
+  if (need > 0 && (overlap(workspace, need, x, nx) || overlap(workspace, need, w, nw) || overlap(workspace, need, sw, ns) ||
+                   (gated && (overlap(workspace, need, w3, nw) || overlap(workspace, need, s3, ns)))))
+    return fail(SFFN_ERR_ARG, "%s: the workspace overlaps an operand", fn);
+  Int4Args a;
+  a.x = x;
+  a.ldx = ldx;
+  a.w = w;
+  a.w3 = gated ? w3 : nullptr;
+  a.sw = sw;
+  a.s3 = gated ? s3 : nullptr;
+  a.y = y;
+  a.ldy = ldy;
+  a.T = T;
+  a.N = N;
+  a.K = K;
+  a.group = group;
+  a.y_f32 = y_dtype == SFFN_F32;
+  a.act = act;
+  a.workspace = workspace;
+  const cudaError_t e = launch_matmul_int4(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SFFN_OK : cuda_fail(fn, e);
+}
+
+int sffn_matmul_int4(const void* x, long long ldx, const uint8_t* wq, const float* sw, void* y, long long ldy, int T, int N,
+                     int K, int group, int y_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  if (y_dtype != SFFN_BF16 && y_dtype != SFFN_F32) return fail(SFFN_ERR_DTYPE, "sffn_matmul_int4: y is bf16 or f32");
+  return run_int4("sffn_matmul_int4", x, ldx, wq, sw, nullptr, nullptr, false, y, ldy, T, N, K, group, y_dtype, 0, workspace,
+                  workspace_bytes, stream);
+}
+
+int sffn_gated_up_int4(const void* x, long long ldx, const uint8_t* w1, const float* s1, const uint8_t* w3, const float* s3,
+                       void* h, long long ldh, int T, int D, int H, int group, int act, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  if (act != SFFN_ACT_RELU && act != SFFN_ACT_RSP && act != SFFN_ACT_SILU)
+    return fail(SFFN_ERR_ARG, "sffn_gated_up_int4: act %d unknown", act);
+  return run_int4("sffn_gated_up_int4", x, ldx, w1, s1, w3, s3, true, h, ldh, T, H, D, group, SFFN_BF16, act, workspace,
+                  workspace_bytes, stream);
+}
+
+// The checks that the gated block's two passes share.
+static int check_gated(const char* fn, const void* x, long long ldx, const void* W1, const void* W3, int T, int D, int H,
+                       int act) {
+  if (act != SFFN_ACT_RELU && act != SFFN_ACT_RSP && act != SFFN_ACT_SILU)
+    return fail(SFFN_ERR_ARG, "%s: act %d unknown", fn, act);
+  if (D < 8 || D % 8 != 0 || D > SFFN_MAX_SUM || H < 1 || H > SFFN_MAX_SUM)
+    return fail(SFFN_ERR_ARG, "%s: D=%d must be a multiple of 8, D and H=%d at most %d", fn, D, H, SFFN_MAX_SUM);
+  if (T < 0 || T > SFFN_MAX_ROWS) return fail(SFFN_ERR_ARG, "%s: T=%d outside 0..%d", fn, T, SFFN_MAX_ROWS);
+  if (ldx < D || ldx % 8 != 0)
+    return fail(SFFN_ERR_ARG, "%s: x's row pitch %lld must be a multiple of 8 and at least D=%d", fn, ldx, D);
+  if (T > 0 && (!x || !W1 || !W3)) return fail(SFFN_ERR_ARG, "%s: null pointer", fn);
+  if (misaligned(x, 16) || misaligned(W1, 16) || misaligned(W3, 16))
+    return fail(SFFN_ERR_ALIGN, "%s: x, W1 and W3 must be 16-byte aligned", fn);
+  return SFFN_OK;
+}
+
+int sffn_gated_up(const void* x, long long ldx, const void* W1, const void* W3, void* h, long long ldh, float* z, float* u,
+                  long long ldz, int T, int D, int H, int act, void* stream) {
+  const char* fn = "sffn_gated_up";
+  const int rc = check_gated(fn, x, ldx, W1, W3, T, D, H, act);
+  if (rc != SFFN_OK) return rc;
+  if (ldh < H) return fail(SFFN_ERR_ARG, "%s: h's row pitch %lld is below H=%d", fn, ldh, H);
+  if (!z != !u) return fail(SFFN_ERR_ARG, "%s: z and u go together", fn);
+  if (z && ldz < H) return fail(SFFN_ERR_ARG, "%s: z's and u's row pitch %lld is below H=%d", fn, ldz, H);
+  if (T == 0) return SFFN_OK;
+  if (!h) return fail(SFFN_ERR_ARG, "%s: null pointer", fn);
+  if (misaligned(h, 2) || misaligned(z, 4) || misaligned(u, 4))
+    return fail(SFFN_ERR_ALIGN, "%s: a pointer is not aligned to its element", fn);
+  const unsigned long long nx = ((unsigned long long)(T - 1) * ldx + D) * 2, nw = 2ull * H * D;
+  const unsigned long long nh = ((unsigned long long)(T - 1) * ldh + H) * 2, nz = z ? ((unsigned long long)(T - 1) * ldz + H) * 4 : 0;
+  const void* out[3] = {h, z, u};
+  const unsigned long long size[3] = {nh, nz, nz};
+  for (int i = 0; i < 3; ++i)
+    if (overlap(out[i], size[i], x, nx) || overlap(out[i], size[i], W1, nw) || overlap(out[i], size[i], W3, nw) ||
+        overlap(out[i], size[i], out[(i + 1) % 3], size[(i + 1) % 3]))
+      return fail(SFFN_ERR_ARG, "%s: an output overlaps an operand or another output", fn);
+  GatedArgs a;
+  a.x = x;
+  a.ldx = ldx;
+  a.W1 = W1;
+  a.W3 = W3;
+  a.h = h;
+  a.ldh = ldh;
+  a.z = z;
+  a.u = u;
+  a.ldz = z ? ldz : 0;
+  a.T = T;
+  a.D = D;
+  a.H = H;
+  a.act = act;
+  const cudaError_t e = launch_gated_up(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SFFN_OK : cuda_fail(fn, e);
+}
+
+size_t sffn_gated_up_backward_workspace(int T, int H) { return T < 1 || H < 1 ? 0 : gated_grad_workspace(T, H); }
+
+int sffn_gated_up_backward(const void* dh, long long lddh, const float* z, const float* u, long long ldz, const void* x,
+                           long long ldx, const void* W1, const void* W3, void* dx, void* dW1, void* dW3, int T, int D,
+                           int H, int act, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "sffn_gated_up_backward";
+  const int rc = check_gated(fn, x, ldx, W1, W3, T, D, H, act);
+  if (rc != SFFN_OK) return rc;
+  if (lddh < H || ldz < H) return fail(SFFN_ERR_ARG, "%s: a row pitch (dh %lld, z and u %lld) is below H=%d", fn, lddh, ldz, H);
+  if (misaligned(dx, 16) || misaligned(dW1, 16) || misaligned(dW3, 16))
+    return fail(SFFN_ERR_ALIGN, "%s: dx, dW1 and dW3 must be 16-byte aligned", fn);
+  const unsigned long long nw = 2ull * H * D;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (overlap(dW1, nw, dW3, nw)) return fail(SFFN_ERR_ARG, "%s: dW1 and dW3 overlap", fn);
+  if (T == 0) {  // a sum over no tokens
+    for (void* p : {dW1, dW3})
+      if (p) {
+        const cudaError_t e = cudaMemsetAsync(p, 0, nw, s);
+        if (e != cudaSuccess) return cuda_fail("cudaMemsetAsync", e);
+      }
+    return SFFN_OK;
+  }
+  if (!dh || !z || !u) return fail(SFFN_ERR_ARG, "%s: null pointer", fn);
+  if (misaligned(dh, 2) || misaligned(z, 4) || misaligned(u, 4))
+    return fail(SFFN_ERR_ALIGN, "%s: a pointer is not aligned to its element", fn);
+  const size_t need = gated_grad_workspace(T, H);
+  if (!workspace || workspace_bytes < need)
+    return fail(SFFN_ERR_ARG, "%s: workspace of %zu bytes, %zu needed", fn, workspace ? workspace_bytes : (size_t)0, need);
+  if (misaligned(workspace, 16)) return fail(SFFN_ERR_ALIGN, "%s: workspace is not 16-byte aligned", fn);
+  const unsigned long long nx = ((unsigned long long)(T - 1) * ldx + D) * 2, ndh = ((unsigned long long)(T - 1) * lddh + H) * 2;
+  const unsigned long long nz = ((unsigned long long)(T - 1) * ldz + H) * 4, ndx = 2ull * T * D;
+  const void* in[7] = {dh, z, u, x, W1, W3, workspace};
+  const unsigned long long in_size[7] = {ndh, nz, nz, nx, nw, nw, need};
+  const void* out[3] = {dx, dW1, dW3};
+  const unsigned long long size[3] = {ndx, nw, nw};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < 7; ++j)
+      if (overlap(out[i], size[i], in[j], in_size[j]))
+        return fail(SFFN_ERR_ARG, "%s: a gradient overlaps an operand or the workspace", fn);
+    if (overlap(out[i], size[i], out[(i + 1) % 3], size[(i + 1) % 3]))
+      return fail(SFFN_ERR_ARG, "%s: a gradient overlaps another", fn);
+  }
+  for (int j = 0; j < 6; ++j)
+    if (overlap(workspace, need, in[j], in_size[j])) return fail(SFFN_ERR_ARG, "%s: the workspace overlaps an operand", fn);
+  if (!dx && !dW1 && !dW3) return SFFN_OK;
+  GatedGradArgs a;
+  a.dh = dh;
+  a.lddh = lddh;
+  a.z = z;
+  a.u = u;
+  a.ldz = ldz;
+  a.x = x;
+  a.ldx = ldx;
+  a.W1 = W1;
+  a.W3 = W3;
+  a.dx = dx;
+  a.dW1 = dW1;
+  a.dW3 = dW3;
+  a.T = T;
+  a.D = D;
+  a.H = H;
+  a.act = act;
+  a.workspace = workspace;
+  const cudaError_t e = launch_gated_grad(a, s);
   return e == cudaSuccess ? SFFN_OK : cuda_fail(fn, e);
 }
 

@@ -323,7 +323,8 @@ int sffn_forward_noalloc(const void* W1, const void* W3, const void* W2t, const 
                          int* counts, int D, int H, int B, int act, int dtype, void* stream);
 
 /* ------------------------------------------------------------------------
- * Mixture-of-experts and 8-bit operators.
+ * Operators without a handle: mixtures of experts, 8-bit and 4-bit products, and
+ * the gated block with its backward pass.
  *
  * A served cast model runs its experts as many small gated FFNs ("Model Casting
  * and Low-Parameter Gating" casts the expert FFNs of a mixture as well) and
@@ -338,7 +339,8 @@ int sffn_forward_noalloc(const void* W1, const void* W3, const void* W2t, const 
  * products: exact integers as long as fp32 holds them), results are rounded once
  * to y's type (each call says what is rounded on the way) and do not depend on
  * timing, so a call repeated on the same inputs gives the same bits.
- * The operators are inference only, like the rest of the library.
+ * The gated block has a backward pass; the other operators are inference only, like
+ * the rest of the library.
  */
 
 /* int8 codes of both operands (the operators below; not a handle's dtype) */
@@ -441,6 +443,75 @@ size_t sffn_experts_workspace(int T, int k, int D, int H);
 int sffn_experts_forward(const void* x, long long ldx, const float* weights, const int* ids, const int* offsets,
                          const int* rows, const void* W1, const void* W3, const void* W2t, void* y, int T, int E, int k,
                          int D, int H, int act, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * 4-bit weights.  A code is a whole number in -7 .. 7 (a product takes -8 as well);
+ * `group` consecutive columns of a row share one fp32 scale, and a weight is
+ * code * scale.  group is a multiple of 64 (the last group of a row may be
+ * shorter), or 0: one scale a row.  codes [N, K / 2] dense, byte b of a row holding
+ * code 2 b in its low nibble and 2 b + 1 in its high one, two's complement; scales
+ * [N, G] dense, G = ceil(K / group), or 1.  K % 16 == 0, codes 16-byte aligned.
+ * (An int4 handle keeps its weights so: group 64 for W1 and W3, 0 for W2.)
+ *
+ * sffn_quantize_int4: of a bf16 matrix w [N, K] (row pitch ldw, ldw % 8 == 0, 16-byte
+ * aligned), scale = max|w| / 7 over the group, code = round-half-to-even(w / scale),
+ * both decided in binary32 (the rule of the handles' codes).  A group of zeros gets
+ * scale 0 and codes 0, one that holds a NaN or an infinity scale NaN and codes 0.
+ *
+ * sffn_dequantize_int4: y[n, k] = code * scale, rounded to binary32 and from there to
+ * y's type (bf16 or f32); y [N, K], row pitch ldy, ldy % 8 == 0, 16-byte aligned.
+ */
+int sffn_quantize_int4(const void* w, long long ldw, uint8_t* codes, float* scales, int N, int K, int group, void* stream);
+int sffn_dequantize_int4(const uint8_t* codes, const float* scales, void* y, long long ldy, int N, int K, int group,
+                         int y_dtype, void* stream);
+
+/*
+ * Products of bf16 tokens x [T, K] (row pitch ldx, ldx % 8 == 0, 16-byte aligned) by
+ * 4-bit weights (codes, scales and group as above):
+ *   sffn_matmul_int4:    y[t, n] = sum_k x[t, k] w[n, k], y [T, N] (row pitch ldy)
+ *     bf16 or f32;
+ *   sffn_gated_up_int4:  h[t, i] = A(sum_k x[t, k] w1[i, k]) * sum_k x[t, k] w3[i, k],
+ *     h [T, H] (row pitch ldh) bf16; a unit whose gate is 0 is exactly 0, a NaN gate
+ *     is live.
+ * Sums are fp32.  Few tokens (those that need no workspace) multiply the codes
+ * themselves and round nothing but the result.  More tokens go through bf16 copies of
+ * the weights: two parts each, which hold a weight to 2^-16, for y in f32 and for the
+ * gated block; one part, a rounding of each weight to bf16 (2^-8), for y in bf16.
+ * The workspace holds sffn_int4_workspace(T, N, K, y_dtype, gated) bytes (gated: N = H,
+ * K = D; 0 for few tokens: NULL is fine).
+ */
+size_t sffn_int4_workspace(int T, int N, int K, int y_dtype, int gated);
+int sffn_matmul_int4(const void* x, long long ldx, const uint8_t* wq, const float* sw, void* y, long long ldy, int T, int N,
+                     int K, int group, int y_dtype, void* workspace, size_t workspace_bytes, void* stream);
+int sffn_gated_up_int4(const void* x, long long ldx, const uint8_t* w1, const float* s1, const uint8_t* w3, const float* s3,
+                       void* h, long long ldh, int T, int D, int H, int group, int act, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * The gated block, the first half of a gated FFN, in bf16 with fp32 sums:
+ *     h[t, i] = A(z[t, i]) * u[t, i],   z = x W1^T,  u = x W3^T
+ * x [T, D] (row pitch ldx, ldx % 8 == 0), W1 and W3 [H, D] dense, h [T, H] (row pitch
+ * ldh); D % 8 == 0, any H >= 1; x, W1 and W3 16-byte aligned.  A unit whose gate A(z) is
+ * 0 is exactly 0 whatever its up value, a NaN gate is live; many tokens use the device's
+ * fast exponential and quotient (2^-15).  z and u (both or neither) receive the two
+ * products in f32 (row pitch ldz), which the backward pass takes.
+ *
+ * The backward pass, from dh, the gradient of h [T, H] (bf16, row pitch lddh):
+ *     dz = dh u A'(z),  du = dh A(z)
+ *     dx = dz W1 + du W3 [T, D],  dW1 = dz^T x,  dW3 = du^T x [H, D]     (bf16, dense)
+ * each of dx, dW1, dW3 NULL where it is not wanted.  dz and du are rounded to bf16, once;
+ * sums are fp32 and rounded once, and do not depend on timing.  A'(0) is 0 for ReLU and
+ * R-S+ and 1/2 for SiLU; a unit with z <= 0 passes exactly 0 for ReLU and R-S+, whatever
+ * dh and u are.  dx, dW1 and dW3 are 16-byte aligned, overlap no other argument, and are
+ * fully written (T = 0: dW1 = dW3 = 0); the workspace holds
+ * sffn_gated_up_backward_workspace(T, H) bytes.
+ */
+int sffn_gated_up(const void* x, long long ldx, const void* W1, const void* W3, void* h, long long ldh, float* z, float* u,
+                  long long ldz, int T, int D, int H, int act, void* stream);
+size_t sffn_gated_up_backward_workspace(int T, int H);
+int sffn_gated_up_backward(const void* dh, long long lddh, const float* z, const float* u, long long ldz, const void* x,
+                           long long ldx, const void* W1, const void* W3, void* dx, void* dW1, void* dW3, int T, int D,
+                           int H, int act, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Wait for `stream` and report (and clear) whether a device-side wait of any of
