@@ -400,11 +400,16 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
     tma_prefetch_map(&mX);
     if (GATED) tma_prefetch_map(&mW3);
   }
+  // What needs nothing of the kernel before this one comes before the wait for it.  The blocks of a cluster meet first: the
+  // others' barriers exist before anything arrives on them, and a pair's allocation, which takes columns of both blocks'
+  // tensor memory and waits without limit, starts only when both blocks run.  (Launched into the end of another kernel
+  // they may start apart; allocating before they met, one pair in some hundred thousand never got its columns.)  No
+  // second meeting: an MMA that writes the other block's columns waits for copies that block issues after its own
+  // allocation.
+  if (CTAS == 2 || ks > 1) cluster_sync_all();
   if (warp == 2) tg_alloc<CTAS>(tslot, (uint32_t)p.cols);
-  // what needs nothing of the kernel before this one comes before the wait for it
   tc_fence_before();
   __syncthreads();
-  if (CTAS == 2 || ks > 1) cluster_sync_all();  // the other blocks' barriers exist before anything arrives on them
   tc_fence_after();
   const uint32_t tmem = *tslot;
   if (tid == 0) pdl_launch_dependents();

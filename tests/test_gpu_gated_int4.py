@@ -644,3 +644,16 @@ def test_the_layer_holds_an_int4_handles_codes():
     y, z = layer(x).double(), handle(x).double()
     assert ((y - z).norm() / z.norm()).item() < 3 * 2.0 ** -8  # both results are rounded, and the layer's h
     handle.close()
+
+
+def test_long_products_follow_one_another_without_a_stop():
+    """Pair tiles launched into the end of the kernel that makes their weights, some thousand times."""
+    g = gen(42)
+    sets = [(weights4(g, 14336, 4096, 64), randn(g, 2048, 4096)) for _ in range(3)]
+    first = [sffn.matmul_int4(x, *w) for w, x in sets]
+    torch.cuda.synchronize()
+    for n in range(500):
+        got = [sffn.matmul_int4(x, *w) for w, x in sets]
+        if n % 50 == 49:
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(first, got))
