@@ -16,8 +16,11 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <array>
@@ -45,14 +48,18 @@ struct Calls {
   decltype(&sffn_matmul_int4) matmul_int4 = nullptr;
   decltype(&sffn_gated_up_int4) gated_up_int4 = nullptr;
   decltype(&sffn_gated_up) gated_up = nullptr;
+  decltype(&sffn_gated_up_backward_workspace) gated_up_backward_workspace = nullptr;
+  decltype(&sffn_gated_up_backward) gated_up_backward = nullptr;
+  decltype(&sffn_last_error) last_error = nullptr;
 } g;
 
 // A tensor that the call can read as it is: of that type and rank, on that
-// device, dense where asked, nothing recorded of it.
-bool takes(PyObject* o, at::ScalarType type, int64_t dim, int device, bool dense, const Tensor** out) {
+// device, dense where asked, nothing recorded of it (but for a gradient, where
+// the call has one).
+bool takes(PyObject* o, at::ScalarType type, int64_t dim, int device, bool dense, const Tensor** out, bool grad = false) {
   if (!THPVariable_Check(o)) return false;
   const Tensor& t = THPVariable_Unpack(o);
-  if (t.scalar_type() != type || t.dim() != dim || !t.is_cuda() || t.requires_grad() ||
+  if (t.scalar_type() != type || t.dim() != dim || !t.is_cuda() || (!grad && t.requires_grad()) ||
       t._fw_grad(0).defined())
     return false;
   if (device >= 0 && t.get_device() != device) return false;
@@ -125,14 +132,17 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
 }
 
 PyObject* bind_block(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  std::array<void*, 6> p;
-  if (!addresses<6>(args, n, &p)) return nullptr;
+  std::array<void*, 9> p;
+  if (!addresses<9>(args, n, &p)) return nullptr;
   g.quantize_int4 = reinterpret_cast<decltype(g.quantize_int4)>(p[0]);
   g.dequantize_int4 = reinterpret_cast<decltype(g.dequantize_int4)>(p[1]);
   g.int4_workspace = reinterpret_cast<decltype(g.int4_workspace)>(p[2]);
   g.matmul_int4 = reinterpret_cast<decltype(g.matmul_int4)>(p[3]);
   g.gated_up_int4 = reinterpret_cast<decltype(g.gated_up_int4)>(p[4]);
   g.gated_up = reinterpret_cast<decltype(g.gated_up)>(p[5]);
+  g.gated_up_backward_workspace = reinterpret_cast<decltype(g.gated_up_backward_workspace)>(p[6]);
+  g.gated_up_backward = reinterpret_cast<decltype(g.gated_up_backward)>(p[7]);
+  g.last_error = reinterpret_cast<decltype(g.last_error)>(p[8]);
   return none();
 }
 
@@ -378,22 +388,158 @@ PyObject* gated_up_int4(PyObject* const* args, Py_ssize_t n) {
   return THPVariable_Wrap(std::move(h));
 }
 
-// gated_up(x, W1, W3, act) -> h, of tensors that require no gradient
-PyObject* gated_up(PyObject* const* args, Py_ssize_t n) {
+// The operands of the gated block, checked; false: not an ordinary call.
+struct Gated {
   const Tensor *x, *W1, *W3;
-  if (n != 4 || !g.gated_up || !takes(args[0], at::kBFloat16, 2, -1, false, &x)) return none();
+  int64_t T, D, H, ld;
+  int device;
   void* stream;
-  const int device = device_of(*x, &stream);
-  if (device < 0 || !takes(args[1], at::kBFloat16, 2, device, true, &W1) || !takes(args[2], at::kBFloat16, 2, device, true, &W3))
-    return none();
-  const int64_t T = x->size(0), D = x->size(1), H = W1->size(0);
-  int64_t ld;
-  if (!fits(T) || !fits(D) || !fits(H) || W1->size(1) != D || W3->sizes() != W1->sizes() || !pitch(*x, &ld)) return none();
-  Tensor h = make({T, H}, at::kBFloat16, device);
-  if (g.gated_up(x->data_ptr(), ld, W1->data_ptr(), W3->data_ptr(), h.data_ptr(), H, nullptr, nullptr, 0, (int)T, (int)D,
-                 (int)H, (int)whole(args[3]), stream) != SFFN_OK)
-    return none();
+};
+bool takes_gated(PyObject* const* args, bool grad, Gated* a) {
+  if (!takes(args[0], at::kBFloat16, 2, -1, false, &a->x, grad)) return false;
+  a->device = device_of(*a->x, &a->stream);
+  if (a->device < 0 || !takes(args[1], at::kBFloat16, 2, a->device, true, &a->W1, grad) ||
+      !takes(args[2], at::kBFloat16, 2, a->device, true, &a->W3, grad))
+    return false;
+  a->T = a->x->size(0), a->D = a->x->size(1), a->H = a->W1->size(0);
+  return fits(a->T) && fits(a->D) && fits(a->H) && a->W1->size(1) == a->D && a->W3->sizes() == a->W1->sizes() &&
+         pitch(*a->x, &a->ld);
+}
+
+// h (with z and u, if they are given) of checked operands; a status code.
+int run_gated(const Tensor& x, int64_t ld, const Tensor& W1, const Tensor& W3, const Tensor& h, float* z, float* u, int64_t act,
+              void* stream) {
+  const int64_t H = W1.size(0);
+  return g.gated_up(x.data_ptr(), ld, W1.data_ptr(), W3.data_ptr(), h.data_ptr(), H, z, u, H, (int)x.size(0), (int)x.size(1),
+                    (int)H, (int)act, stream);
+}
+
+// dx, dW1 and dW3 (undefined where not wanted) of checked operands; a status code.
+int run_gated_backward(const Tensor& dh, int64_t lddh, const float* z, const float* u, const Tensor& x, int64_t ld,
+                       const Tensor& W1, const Tensor& W3, const Tensor& dx, const Tensor& dW1, const Tensor& dW3, int64_t act,
+                       int device, void* stream) {
+  const int64_t T = x.size(0), D = x.size(1), H = W1.size(0);
+  Tensor scratch;
+  const size_t nb = g.gated_up_backward_workspace((int)T, (int)H);
+  if (nb) scratch = make({(int64_t)nb}, at::kByte, device);
+  auto at_of = [](const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
+  return g.gated_up_backward(dh.data_ptr(), lddh, z, u, H, x.data_ptr(), ld, W1.data_ptr(), W3.data_ptr(), at_of(dx),
+                             at_of(dW1), at_of(dW3), (int)T, (int)D, (int)H, (int)act, at_of(scratch), nb, stream);
+}
+
+// gated_up with its gradient.  z and u, one buffer of [2, T, H], stay in fp32 for the backward pass.
+struct GatedUp : torch::autograd::Function<GatedUp> {
+  static Tensor forward(torch::autograd::AutogradContext* ctx, const Tensor& x, const Tensor& W1, const Tensor& W3,
+                        int64_t act) {
+    void* stream;
+    int64_t ld = 0;
+    const int device = device_of(x, &stream);
+    pitch(x, &ld);
+    const int64_t T = x.size(0), H = W1.size(0);
+    Tensor h = make({T, H}, at::kBFloat16, device), zu = make({2, T, H}, at::kFloat, device);
+    float* z = zu.data_ptr<float>();
+    TORCH_CHECK(run_gated(x, ld, W1, W3, h, z, z + T * H, act, stream) == SFFN_OK, g.last_error());
+    ctx->save_for_backward({x, W1, W3, zu});
+    ctx->saved_data["act"] = act;
+    return h;
+  }
+
+  static torch::autograd::variable_list backward(torch::autograd::AutogradContext* ctx, torch::autograd::variable_list grads) {
+    TORCH_CHECK(c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None,
+                "the backward pass of gated_up is not captured: gated_up_backward is");
+    const auto saved = ctx->get_saved_variables();
+    const Tensor &x = saved[0], &W1 = saved[1], &W3 = saved[2];
+    const int64_t T = x.size(0), D = x.size(1), H = W1.size(0);
+    Tensor dh = grads[0].defined() ? grads[0] : at::zeros({T, H}, x.options());
+    int64_t ld = 0, lddh = 0;
+    if (!pitch(dh, &lddh)) {  // an expanded gradient, say
+      dh = dh.contiguous();
+      lddh = H;
+    }
+    pitch(x, &ld);
+    void* stream;
+    const int device = device_of(x, &stream);
+    TORCH_CHECK(device >= 0, "the tensors are not on the current device");
+    Tensor out[3];
+    bool any = false;
+    for (int i = 0; i < 3; ++i)
+      if (ctx->needs_input_grad(i)) {
+        out[i] = make({i ? H : T, D}, at::kBFloat16, device);
+        any = true;
+      }
+    if (any) {
+      const float* z = saved[3].data_ptr<float>();
+      TORCH_CHECK(run_gated_backward(dh, lddh, z, z + T * H, x, ld, W1, W3, out[0], out[1], out[2],
+                                     ctx->saved_data["act"].toInt(), device, stream) == SFFN_OK,
+                  g.last_error());
+    }
+    if (at::GradMode::is_enabled()) {  // a graph of the backward pass is recorded: it ends here, with an error
+      torch::autograd::variable_list real;
+      for (auto& t : out)
+        if (t.defined()) real.push_back(t.requires_grad_());
+      const auto error = std::make_shared<torch::autograd::DelayedError>("gated_up has no second derivative", real.size());
+      real = (*error)(std::move(real));
+      for (int i = 0, j = 0; i < 3; ++i)
+        if (out[i].defined()) out[i] = real[j++];
+    }
+    return {out[0], out[1], out[2], Tensor()};
+  }
+};
+
+// gated_up(x, W1, W3, act) -> h
+PyObject* gated_up(PyObject* const* args, Py_ssize_t n) {
+  Gated a;
+  if (n != 4 || !g.gated_up || !takes_gated(args, true, &a)) return none();
+  const int64_t act = whole(args[3]);
+  if (at::GradMode::is_enabled() && (a.x->requires_grad() || a.W1->requires_grad() || a.W3->requires_grad())) {
+    if (!g.gated_up_backward || c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None ||
+        a.D % 8 || a.ld % 8 || a.H < 1 || act < SFFN_ACT_RELU || act > SFFN_ACT_SILU)
+      return none();
+    return THPVariable_Wrap(GatedUp::apply(*a.x, *a.W1, *a.W3, act));
+  }
+  Tensor h = make({a.T, a.H}, at::kBFloat16, a.device);
+  if (run_gated(*a.x, a.ld, *a.W1, *a.W3, h, nullptr, nullptr, act, a.stream) != SFFN_OK) return none();
   return THPVariable_Wrap(std::move(h));
+}
+
+// gated_up_saved(x, W1, W3, act) -> (h, z, u)
+PyObject* gated_up_saved(PyObject* const* args, Py_ssize_t n) {
+  Gated a;
+  if (n != 4 || !g.gated_up || !takes_gated(args, false, &a)) return none();
+  Tensor h = make({a.T, a.H}, at::kBFloat16, a.device), z = make({a.T, a.H}, at::kFloat, a.device),
+         u = make({a.T, a.H}, at::kFloat, a.device);
+  if (run_gated(*a.x, a.ld, *a.W1, *a.W3, h, z.data_ptr<float>(), u.data_ptr<float>(), whole(args[3]), a.stream) != SFFN_OK)
+    return none();
+  PyObject* r = PyTuple_New(3);
+  if (!r) return nullptr;
+  PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(std::move(h)));
+  PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(std::move(z)));
+  PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(std::move(u)));
+  return r;
+}
+
+// gated_up_backward(x, W1, W3, act, dh, z, u, need_x, need_1, need_3) -> (dx, dW1, dW3), None where not wanted
+PyObject* gated_up_backward(PyObject* const* args, Py_ssize_t n) {
+  Gated a;
+  const Tensor *dh, *z, *u;
+  if (n != 10 || !g.gated_up_backward || !takes_gated(args, false, &a) || !takes(args[4], at::kBFloat16, 2, a.device, false, &dh) ||
+      !takes(args[5], at::kFloat, 2, a.device, true, &z) || !takes(args[6], at::kFloat, 2, a.device, true, &u))
+    return none();
+  int64_t lddh;
+  for (const Tensor* t : {dh, z, u})
+    if (t->size(0) != a.T || t->size(1) != a.H) return none();
+  if (!pitch(*dh, &lddh)) return none();
+  Tensor out[3];
+  for (int i = 0; i < 3; ++i)
+    if (args[7 + i] == Py_True) out[i] = make({i ? a.H : a.T, a.D}, at::kBFloat16, a.device);
+  if (run_gated_backward(*dh, lddh, z->data_ptr<float>(), u->data_ptr<float>(), *a.x, a.ld, *a.W1, *a.W3, out[0], out[1], out[2],
+                         whole(args[3]), a.device, a.stream) != SFFN_OK)
+    return none();
+  PyObject* r = PyTuple_New(3);
+  if (!r) return nullptr;
+  for (int i = 0; i < 3; ++i)
+    PyTuple_SET_ITEM(r, i, out[i].defined() ? THPVariable_Wrap(std::move(out[i])) : none());
+  return r;
 }
 
 // A C++ exception (an allocation that fails, say) becomes PyTorch's Python one.
@@ -422,6 +568,8 @@ PyMethodDef methods[] = {
     method<matmul_int4>("matmul_int4"),
     method<gated_up_int4>("gated_up_int4"),
     method<gated_up>("gated_up"),
+    method<gated_up_saved>("gated_up_saved"),
+    method<gated_up_backward>("gated_up_backward"),
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -64,7 +64,8 @@ if _calls is not None and os.path.exists(LIB_PATH):
         "sffn_route_workspace", "sffn_route", "sffn_quantize_tokens", "sffn_grouped_workspace", "sffn_matmul_int8",
         "sffn_grouped_matmul", "sffn_experts_workspace", "sffn_experts_forward"))
     _calls.bind_block(*_at("sffn_quantize_int4", "sffn_dequantize_int4", "sffn_int4_workspace", "sffn_matmul_int4",
-                           "sffn_gated_up_int4", "sffn_gated_up"))
+                           "sffn_gated_up_int4", "sffn_gated_up", "sffn_gated_up_backward_workspace",
+                           "sffn_gated_up_backward", "sffn_last_error"))
 
 
 # no stream object in between, where torch offers it
@@ -501,6 +502,10 @@ def gated_up(x, W1, W3, act: str = "relu", out=None, stream=None):
 
 def gated_up_saved(x, W1, W3, act: str = "relu", stream=None):
     """(h, z, u): ``gated_up``'s h with z = x W1^T and u = x W3^T (fp32 [T, H]), which :func:`gated_up_backward` takes."""
+    if stream is None and _calls is not None and act in _ACT:
+        r = _calls.gated_up_saved(x, W1, W3, _ACT[act])
+        if r is not None:
+            return r
     if stream is not None:
         with torch.cuda.stream(stream):
             return gated_up_saved(x, W1, W3, act)
@@ -513,6 +518,10 @@ def gated_up_saved(x, W1, W3, act: str = "relu", stream=None):
 
 def gated_up_backward(dh, z, u, x, W1, W3, act: str = "relu", need=(True, True, True), stream=None):
     """(dx, dW1, dW3) from dh, the gradient of h, and :func:`gated_up_saved`'s z and u; None where ``need`` is false."""
+    if stream is None and _calls is not None and act in _ACT:
+        r = _calls.gated_up_backward(x, W1, W3, _ACT[act], dh, z, u, *(bool(n) for n in need))
+        if r is not None:
+            return r
     if stream is not None:
         with torch.cuda.stream(stream):
             return gated_up_backward(dh, z, u, x, W1, W3, act, need)

@@ -129,10 +129,12 @@ def test_native_calls_decline():
     assert calls.quantize_int4(x, 64) is None and calls.quantize_int4(x, None) is None
     assert calls.dequantize_int4(q, s, 64, False) is None and calls.matmul_int4(x, q, s, 64, False) is None
     assert calls.gated_up_int4(x, q, s, q, s, 64, 0) is None and calls.gated_up(x, x, x, 0) is None
+    assert calls.gated_up_saved(x, x, x, 0) is None
+    assert calls.gated_up_backward(x, x, x, 0, x, s, s, True, True, True) is None
     with pytest.raises(TypeError):
         calls.bind_block(1)
     with pytest.raises(ValueError):
-        calls.bind_block(*[0] * 6)
+        calls.bind_block(*[0] * 9)
 
 
 def test_tensor_wrappers_refuse():
