@@ -73,8 +73,9 @@ constexpr int TG_THREADS = 384, TG_THREADS_I8 = 32 * (TG_CONV_WARP0 + TG_CONV_WA
 constexpr uint64_t TG_TIMEOUT_NS = 250000000ull;
 constexpr size_t TG_SMEM = 227 * 1024;
 constexpr int TG_DEVICES = 64;
-// what a kernel multiplies: bf16; bf16 gate and up together; int8 codes widened in flight; fp16 copies of codes
-enum { TG_BF16, TG_GATED, TG_I8, TG_F16 };
+// what a kernel multiplies: bf16; bf16 gate and up together, and the same for training; int8 codes widened in flight; fp16
+// copies of codes
+enum { TG_BF16, TG_GATED, TG_TRAIN, TG_I8, TG_F16 };
 // the epilogue's shared scratch of a warp: 16 rows of 32 words, 4 words apart (no bank conflicts either way)
 constexpr int TG_EPI_PITCH = 36;
 constexpr int TG_PART = 132;  // words between the rows of a partial tile
@@ -342,13 +343,82 @@ __device__ __forceinline__ float gate_up(int act, float z, float u) {
   return (act == ACT_SILU ? g == 0.f : z <= 0.f) ? 0.f : g * u;
 }
 
+// The product of a row of x and one of w by a whole warp, in fp32.
+__device__ __noinline__ float warp_dot(const uint16_t* x, const uint16_t* w, int K) {
+  float2 acc = make_float2(0.f, 0.f);
+  for (int k = (threadIdx.x & 31) * 8; k < K; k += 256) {
+    float a[8], b[8];
+    Elt<bf16_tag>::unpack(__ldg(reinterpret_cast<const uint4*>(x + k)), a);
+    Elt<bf16_tag>::unpack(__ldg(reinterpret_cast<const uint4*>(w + k)), b);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) ffma2(acc, make_float2(a[2 * j], a[2 * j + 1]), make_float2(b[2 * j], b[2 * j + 1]));
+  }
+  return warp_sum(acc.x + acc.y);
+}
+
+// Signs of a gate's inputs that are kept for the backward pass (32 tokens from row r0 of x on, the lane's unit n; val: their z).
+// ReLU and R-S+ let a unit's gradients pass or not by the sign of z, and an MMA cuts its running sum off at every step: z near
+// 0 is off by up to 2^-24 of the sums' magnitude a step, all one way, and a unit that passes wrongly is off by all of its
+// term (8192 tokens, D = 2560, H = 7168, ReLU: relative error of dx 0.0034, with this 0.0024, which is dz's and dx's own
+// rounding).  So a z that is that small next to its unit's largest is computed again on the CUDA cores, one in some ten
+// thousand.  A token most of whose units are small is small itself, and left as it is, as is a z of exactly 0.
+__device__ __forceinline__ void refine_gate(const GmmArgs& g, const uint32_t (&val)[32], int e, int r0, int left, int n, bool nok,
+                                            float* z, int steps) {
+  const int lane = threadIdx.x & 31;
+  uint32_t top = 0, least = 0xffffffffu;  // magnitudes as bits; 0 - 1 is the largest
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    const uint32_t b = val[j] & 0x7fffffffu;
+    top = max(top, b);
+    least = min(least, b - 1);
+  }
+  const float limit = __uint_as_float(top) * (float)steps * 0x1p-24f;
+  if (!__any_sync(0xffffffffu, nok && __uint_as_float(least) < limit)) return;  // (no number: false)
+  uint32_t near = 0;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    const float a = fabsf(__uint_as_float(val[j]));
+    if (nok && j < left && a > 0.f && a < limit) near |= 1u << j;
+  }
+  for (uint32_t some = __reduce_or_sync(0xffffffffu, near); some != 0; some &= some - 1) {
+    const int j = __ffs((int)some) - 1;
+    uint32_t who = __ballot_sync(0xffffffffu, near >> j & 1);
+    if (__popc(who) > 4) continue;
+    for (; who != 0; who &= who - 1) {
+      const int l = __ffs((int)who) - 1, unit = __shfl_sync(0xffffffffu, n, l);
+      const float v = warp_dot(static_cast<const uint16_t*>(g.x) + (long long)(r0 + j) * g.ldx,
+                               static_cast<const uint16_t*>(g.w) + ((size_t)e * g.N + unit) * g.K, g.K);
+      if (lane == l) z[(uint64_t)j * (uint64_t)g.ldz + lane] = v;
+    }
+  }
+}
+
+// The same of one token r, four units a lane from n on (v: their z), by the token's largest alone.
+__device__ __forceinline__ void refine_row(const GmmArgs& g, float (&v)[4], int e, int r, int n, int steps) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+  const float limit = __uint_as_float(__reduce_max_sync(0xffffffffu, top)) * (float)steps * 0x1p-24f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t who = __ballot_sync(0xffffffffu, n + i < g.N && fabsf(v[i]) > 0.f && fabsf(v[i]) < limit);
+    if (__popc(who) > 4) continue;
+    for (; who != 0; who &= who - 1) {
+      const int l = __ffs((int)who) - 1, unit = __shfl_sync(0xffffffffu, n + i, l);
+      const float z = warp_dot(static_cast<const uint16_t*>(g.x) + (long long)r * g.ldx,
+                               static_cast<const uint16_t*>(g.w) + ((size_t)e * g.N + unit) * g.K, g.K);
+      if ((threadIdx.x & 31) == l) v[i] = z;
+    }
+  }
+}
+
 // XT: x is [K, rows], read as the KN weights are: boxes of 64 values of K by 64 rows, MN-major.
 template <int CTAS, int MODE, bool KN, bool XT>
 __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
     gmm_tc_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mW3,
                   const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mXb, const TgArgs p) {
   static_assert(MODE != TG_I8 || CTAS == 1, "the converters arrive on their own block's barriers");
-  constexpr bool GATED = MODE == TG_GATED, I8 = MODE == TG_I8, F16 = MODE == TG_I8 || MODE == TG_F16;
+  constexpr bool TRAIN = MODE == TG_TRAIN, GATED = TRAIN || MODE == TG_GATED, I8 = MODE == TG_I8, F16 = MODE == TG_I8 || MODE == TG_F16;
   constexpr int EW = I8 ? 4 : 8;  // epilogue warps
   extern __shared__ uint8_t smraw[];
   uint8_t* sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
@@ -753,7 +823,8 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
           if (GATED) {
             float u[4];
             sum_of(at + up, u);
-            if (p.g.z) {
+            if constexpr (TRAIN) {
+              if (p.g.act != ACT_SILU) refine_row(p.g, f, q.e, q.r0 + r, nc, 4 * p.KC);
               const uint64_t o = (uint64_t)(uint32_t)(q.r0 + r) * (uint64_t)p.g.ldz + nc;
 #pragma unroll
               for (int i = 0; i < 4; ++i)
@@ -821,7 +892,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
           tmem_ld32(ta + p.NT + c0, u);
           tmem_ld_wait();
           done();
-          if (p.g.z) {  // kept as they are, in fp32, through this warp's shared scratch like the result
+          if constexpr (TRAIN) {  // kept as they are, in fp32, through this warp's shared scratch like the result
             const uint32_t buf = smb + epi0 + (uint32_t)ew * TG_EPI_BYTES;
             const uint64_t z0 = (uint64_t)(uint32_t)(q.r0 + c0) * (uint64_t)p.g.ldz + (q.mt * 128 * CTAS + n0r + 32 * (ew & 3));
             const int room = p.g.NY - (q.mt * 128 * CTAS + n0r + 32 * (ew & 3));  // columns from z0 on
@@ -849,6 +920,8 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
             };
             keep(v, p.g.z + z0);
             keep(u, p.g.u + z0);
+            __syncwarp();
+            if (p.g.act != ACT_SILU) refine_gate(p.g, v, q.e, q.r0 + c0, left, n, nok, p.g.z + z0, 4 * p.KC);
           }
           if (p.g.act == 0) {  // hoisted: as a branch of each value ReLU pays for the others
 #pragma unroll
@@ -1090,6 +1163,9 @@ cudaError_t launch_gmm_tc(const GmmArgs& a, int ctas, int nt, cudaStream_t s) {
   const int sms = ops_num_sms();
   if (a.i8) return tg_go<1, TG_I8, false>(mW, mW3, mX, mXb, p, smem, sms, s);
   if (a.f16) return tg_go<2, TG_F16, false>(mW, mW3, mX, mXb, p, smem, sms, s);
+  if (a.z)
+    return ctas == 2 ? tg_go<2, TG_TRAIN, false>(mW, mW3, mX, mXb, p, smem, sms, s)
+                     : tg_go<1, TG_TRAIN, false>(mW, mW3, mX, mXb, p, smem, sms, s);
   if (gated)
     return ctas == 2 ? tg_go<2, TG_GATED, false>(mW, mW3, mX, mXb, p, smem, sms, s)
                      : tg_go<1, TG_GATED, false>(mW, mW3, mX, mXb, p, smem, sms, s);

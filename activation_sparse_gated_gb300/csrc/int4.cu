@@ -6,13 +6,19 @@
 // the whole row) shares one fp32 scale s = max|w| / 7, and w stands for code * s.
 // Byte b of a row holds code 2 b in its low nibble and 2 b + 1 in its high one,
 // two's complement: the layout of the handles' int4 weights.
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 #include <mutex>
 
 #include "common.cuh"
 #include "ops.h"
+#include "tc.cuh"
 
 namespace sffn {
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();  // ffn_tc.cu
+
 namespace {
 
 constexpr int I4_GROUP = 64;    // groups are multiples of this many columns
@@ -25,33 +31,36 @@ __device__ __forceinline__ int group_of(int c, uint32_t magic) { return (int)(((
 
 // ------------------------------------------------------------------ codes
 
-// The codes of eight packed bf16 values, a nibble each.  1.5 * 2^23 + v / s rounds to an integer, to even, whose low
-// nibble is the code; the product with 1 / s is off by a few units in the last place, so it decides as the correctly
-// rounded quotient does unless it lies near a half, and only then is that taken.
+// The codes of eight packed bf16 values, a nibble each; inv is 1 / s, correctly rounded.  A code is decided by the correctly
+// rounded quotient, which here comes from inv by Markstein's theorem (1990): q = v inv is within a unit in the last place of v
+// / s, r = v - q s is exact in a fused multiply-add, and q + r inv then rounds to the quotient, ties and all (s = max / 7 of a
+// bf16 value is never just below a power of two, the theorem's exception).  1.5 * 2^23 + quotient rounds to an integer, to
+// even, whose low nibble is the code.  (Ties are common: half a group's maximum is 3.5 scales.  Deciding by v inv alone and
+// dividing what lies near a half took 40.5 us for 14336 x 4096 weights, so often did some lane divide; this takes 28.9.)
 __device__ __forceinline__ uint32_t codes8(const uint4& c, float s, float inv) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-  const float2 round = make_float2(12582912.f, 12582912.f), minus = make_float2(-1.f, -1.f), iv = make_float2(inv, inv);
-  uint32_t out = 0;
-  float far = 0.f;
+  if (!(s > 1e-30f && s < 1e30f)) {  // out of the theorem's range: the residual or inv may underflow
+    uint32_t out = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float v = __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+      out |= ((uint32_t)min(max(__float2int_rn(__fdiv_rn(v, s)), -7), 7) & 15u) << (4 * i);
+    }
+    return out;
+  }
+  const float2 iv = make_float2(inv, inv), minus = make_float2(-s, -s), round = make_float2(12582912.f, 12582912.f);
+  uint32_t pair[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 v = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
-    float2 t = round, d = round;
-    ffma2(t, v, iv);
-    ffma2(d, t, minus);  // the code, negated
-    ffma2(d, v, iv);
-    far = fmaxf(far, fmaxf(fabsf(d.x), fabsf(d.y)));
-    out |= (__float_as_uint(t.x) & 15u) << (8 * i) | (__float_as_uint(t.y) & 15u) << (8 * i + 4);
+    float2 q = make_float2(0.f, 0.f), r = v;
+    ffma2(q, v, iv);
+    ffma2(r, q, minus);
+    ffma2(q, r, iv);
+    const float2 t = fadd2(q, round);
+    pair[i] = (__float_as_uint(t.x) & 15u) | (__float_as_uint(t.y) << 4 & ~15u);  // the low byte
   }
-  if (far < 0.4999f && s > 1e-30f && s < 1e30f) return out;
-  out = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float v = __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
-    const int q = min(max(__float2int_rn(__fdiv_rn(v, s)), -7), 7);
-    out |= ((uint32_t)q & 15u) << (4 * i);
-  }
-  return out;
+  return __byte_perm(__byte_perm(pair[0], pair[1], 0x0040), __byte_perm(pair[2], pair[3], 0x0040), 0x5410);
 }
 
 // the largest |value| of eight, as bits (ordered like the values, NaN above infinity)
@@ -104,11 +113,39 @@ __global__ void __launch_bounds__(32 * I4_WARPS) quantize_int4_kernel(const Quan
     const float s = scale_of(m);
     if ((lane & (LPG - 1)) == 0) a.s[n * a.G + c / (8 * LPG)] = s;
     const bool zero = m == 0 || m >= 0x7f800000u || s == 0.f;
-    *reinterpret_cast<uint32_t*>(a.q + n * (a.K / 2) + c / 2) = zero ? 0u : codes8(v[i], s, __fdiv_rn(1.f, s));
+    *reinterpret_cast<uint32_t*>(a.q + n * (a.K / 2) + c / 2) = zero ? 0u : codes8(v[i], s, __frcp_rn(s));
   }
 }
 
-// Any other group, whole rows among them: a block a group.  Up to V pieces of eight values a thread stay in registers
+// Other groups of up to 2048 columns: a warp a group, up to eight pieces of eight values a lane.
+__global__ void __launch_bounds__(32 * I4_WARPS) quantize_int4_warp_kernel(const QuantArgs a) {
+  const int lane = threadIdx.x & 31, gi = blockIdx.y * I4_WARPS + (threadIdx.x >> 5);
+  pdl_launch_dependents();
+  pdl_wait();
+  if (gi >= a.G) return;
+  const long long n = blockIdx.x;
+  const int c0 = gi * a.group, pieces = min(a.group, a.K - c0) / 8;
+  const uint4* row = reinterpret_cast<const uint4*>(a.w + n * a.ldw + c0);
+  uint32_t* out = reinterpret_cast<uint32_t*>(a.q + n * (a.K / 2) + c0 / 2);
+  uint4 v[8];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (32 * i < pieces) v[i] = lane + 32 * i < pieces ? __ldcs(row + lane + 32 * i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (32 * i < pieces) m = max(m, max8(v[i]));
+  m = __reduce_max_sync(0xffffffffu, m);
+  const float s = scale_of(m);
+  if (lane == 0) a.s[n * a.G + gi] = s;
+  const bool zero = m == 0 || m >= 0x7f800000u || s == 0.f;
+  const float inv = __frcp_rn(s);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (lane + 32 * i < pieces) out[lane + 32 * i] = zero ? 0u : codes8(v[i], s, inv);
+}
+
+// Longer groups, whole rows among them: a block a group.  Up to V pieces of eight values a thread stay in registers
 // between the maximum and the codes; longer groups (V = 0) are read twice.
 template <int V>
 __global__ void __launch_bounds__(32 * I4_WARPS) quantize_int4_wide_kernel(const QuantArgs a) {
@@ -138,7 +175,7 @@ __global__ void __launch_bounds__(32 * I4_WARPS) quantize_int4_wide_kernel(const
   const float s = scale_of(m);
   if (tid == 0) a.s[n * a.G + blockIdx.y] = s;
   const bool zero = m == 0 || m >= 0x7f800000u || s == 0.f;
-  const float inv = __fdiv_rn(1.f, s);
+  const float inv = __frcp_rn(s);
   if constexpr (V > 0) {
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -161,6 +198,9 @@ struct ValueArgs {
   uint32_t magic;
 };
 
+// The code in the low nibble: plus 8 (the caller's XOR) it is u, and the float with bits 0x4b000000 | u is 2^23 + u.
+__device__ __forceinline__ float value_of(uint32_t u) { return __uint_as_float((u & 15u) | 0x4b000000u) - 8388616.f; }
+
 // y = code * scale, eight codes (four bytes) a lane, 1024 columns of a row a warp.  The product is rounded to fp32, then
 // to y's type.  I4_SPLIT: two bf16 matrices side by side whose sum is the value to 2^-16, [high | low], each filled up
 // with zeros to `half` columns.
@@ -174,36 +214,51 @@ __global__ void __launch_bounds__(32 * I4_WARPS) dequantize_int4_kernel(const Va
   const uint8_t* row = (z ? a.q[1] : a.q[0]) + n * (a.K / 2);
   const float* srow = (z ? a.s[1] : a.s[0]) + n * a.G;
   void* y = z ? a.y[1] : a.y[0];
-  uint32_t w[4];
-  float s[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c = c0 + 256 * i;
-    w[i] = 0x88888888u;
-    s[i] = 0.f;
-    if (c < a.K) {
-      w[i] = __ldg(reinterpret_cast<const uint32_t*>(row + c / 2)) ^ 0x88888888u;
-      s[i] = __ldg(srow + group_of(c / I4_GROUP, a.magic));
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c = c0 + 256 * i;
-    if (c >= (MODE == I4_SPLIT ? a.half : a.K)) continue;
+  if constexpr (MODE == I4_F32) {  // four codes a lane eight times, so that a store is 16 bytes of consecutive ones
+    uint32_t v[8];
     float f[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)  // a code plus 8 is a nibble u; the float with bits 0x4b000000 | u is 2^23 + u
-      f[j] = (__uint_as_float((w[i] >> (4 * j) & 15u) | 0x4b000000u) - 8388616.f) * s[i];
-    if constexpr (MODE == I4_F32) {
-      float4* to = reinterpret_cast<float4*>(static_cast<float*>(y) + n * a.ldy + c);
-      to[0] = make_float4(f[0], f[1], f[2], f[3]);
-      to[1] = make_float4(f[4], f[5], f[6], f[7]);
-    } else {
+    for (int i = 0; i < 8; ++i) {
+      const int c = blockIdx.y * I4_UNIT + 128 * i + 4 * lane;
+      v[i] = 0;
+      f[i] = 0.f;
+      if (c < a.K) {
+        v[i] = __ldg(reinterpret_cast<const uint16_t*>(row + c / 2)) ^ 0x8888u;
+        f[i] = __ldg(srow + group_of(c / I4_GROUP, a.magic));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = blockIdx.y * I4_UNIT + 128 * i + 4 * lane;
+      if (c < a.K)
+        __stcs(reinterpret_cast<float4*>(static_cast<float*>(y) + n * a.ldy + c),
+               make_float4(value_of(v[i]) * f[i], value_of(v[i] >> 4) * f[i], value_of(v[i] >> 8) * f[i], value_of(v[i] >> 12) * f[i]));
+    }
+  } else {
+    uint32_t w[4];
+    float s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = c0 + 256 * i;
+      w[i] = 0x88888888u;
+      s[i] = 0.f;
+      if (c < a.K) {
+        w[i] = __ldg(reinterpret_cast<const uint32_t*>(row + c / 2)) ^ 0x88888888u;
+        s[i] = __ldg(srow + group_of(c / I4_GROUP, a.magic));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = c0 + 256 * i;
+      if (c >= (MODE == I4_SPLIT ? a.half : a.K)) continue;
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = value_of(w[i] >> (4 * j)) * s[i];
       uint32_t h[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) h[j] = pack_bf16x2_rn(f[2 * j], f[2 * j + 1]);
-      uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + n * a.ldy + c);
-      *to = make_uint4(h[0], h[1], h[2], h[3]);
+      uint16_t* to = static_cast<uint16_t*>(y) + n * a.ldy + c;
+      *reinterpret_cast<uint4*>(to) = make_uint4(h[0], h[1], h[2], h[3]);
       if constexpr (MODE == I4_SPLIT) {
         uint32_t l[4];
 #pragma unroll
@@ -213,7 +268,7 @@ __global__ void __launch_bounds__(32 * I4_WARPS) dequantize_int4_kernel(const Va
           if (!(fabsf(d1) < 1e38f)) d1 = 0.f;
           l[j] = pack_bf16x2_rn(d0, d1);
         }
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + n * a.ldy + a.half + c) = make_uint4(l[0], l[1], l[2], l[3]);
+        *reinterpret_cast<uint4*>(to + a.half) = make_uint4(l[0], l[1], l[2], l[3]);
       }
     }
   }
@@ -232,14 +287,25 @@ __global__ void __launch_bounds__(32 * I4_WARPS) dequantize_int4_kernel(const Va
 // inside a chunk is the MMA's to choose, as long as both operands agree.  Step i of a chunk takes columns (i, i + 4) and
 // (i + 8, i + 12) of each lane's sixteen, which are nibbles i and i + 4 of its two words.
 //
-// A block takes 16 MR rows of w (of both matrices, GATED) and its warps cut K; their sums meet in shared memory and are
-// added in the warps' order.
+// Up to eight tokens (int4_rows_kernel): a block takes 16 rows of w (of both matrices, GATED), its warps take pairs of
+// chunks in turn, and their sums meet in shared memory and are added in the warps' order.  Measured (us in a graph, one
+// token): 7168 x 2560 4.8 (2.2 TB/s; 2.1 of it a launch), 14336 x 4096 12.1 (2.7 TB/s); gated, two 7168 x 2560 10.3.  What
+// bounds it is instructions: 116 a chunk of 16 rows, 44 of them the codes, at 53 % of the issue slots.  Not faster: scales
+// lane by lane (4.9), eight bytes of codes a lane, one pair of chunks at a time (5.6), a warp's codes and x through a TMA
+// ring (6.6).
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// the same from zero
+__device__ __forceinline__ void mma16816_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // codes i and i + 4 of a word as a pair of bf16
@@ -261,102 +327,133 @@ struct RowsArgs {
   uint32_t magic;
 };
 
-template <int NT, int MR, bool GATED, int U>
+// A(z) u: a NaN gate is live, a dead unit exactly 0.
+__device__ __forceinline__ float gated(int act, float z, float u) {
+  const float gate = z != z ? z : activation(act, z);
+  return gate != 0.f ? gate * u : 0.f;
+}
+
+template <bool GATED>
 __global__ void __launch_bounds__(32 * I4_WARPS) int4_rows_kernel(const RowsArgs a) {
-  constexpr int M = GATED ? 2 * MR : MR, P = 16 * M + 4;  // row tiles; pitch of a token's sums (no bank conflict)
-  extern __shared__ float s_sum[];                        // [warps][8 NT tokens][P]
+  constexpr int M = GATED ? 2 : 1, P = 16 * M + 4;  // matrices; pitch of a token's sums (no bank conflict)
+  constexpr int U = 2;                              // pairs of chunks at a time: a lane of four holds a scale of each chunk
+  __shared__ float s_sum[I4_WARPS * 8 * P];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int n0 = blockIdx.x * 16 * MR, t0 = blockIdx.y * 8 * NT;
+  const int n0 = blockIdx.x * 16, t0 = blockIdx.y * 8;
   pdl_launch_dependents();
   pdl_wait();
-  const int nc = (a.K + 63) / 64, c0 = nc * warp / I4_WARPS, c1 = nc * (warp + 1) / I4_WARPS;
+  const int nc = (a.K + 127) / 128;  // pairs of chunks; the warps take them in turn, so that they read rows together
+  const bool wide = a.K % 32 == 0;  // rows of codes are 16-byte aligned
   const uint8_t* wr[M][2];
   const float* sr[M][2];
 #pragma unroll
   for (int m = 0; m < M; ++m)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int r = min(n0 + 16 * (m % MR) + 8 * h + g, a.N - 1);
-      wr[m][h] = a.w[m / MR] + (size_t)r * (a.K / 2) + 8 * t;
-      sr[m][h] = a.s[m / MR] + (size_t)r * a.G;
+      const int r = min(n0 + 8 * h + g, a.N - 1);
+      wr[m][h] = a.w[m] + (size_t)r * (a.K / 2) + 16 * t;
+      sr[m][h] = a.s[m] + (size_t)r * a.G;
     }
-  const uint16_t* xr[NT];
-#pragma unroll
-  for (int j = 0; j < NT; ++j) xr[j] = a.x + (long long)min(t0 + 8 * j + g, a.T - 1) * a.ldx + 16 * t;
-  float acc[M][NT][4] = {};
-  for (int c = c0; c < c1; c += U) {
-    uint2 w[U][M][2];
-    float s[U][M][2];
-    uint4 x[U][NT][2];
+  const bool low = t < 2;
+  const int col = 32 * (t & 1) + 16 * (t >> 1);  // of the lane's sixteen columns in either chunk
+  const bool token = t0 + g < a.T;
+  const uint16_t* xr = a.x + (long long)min(t0 + g, a.T - 1) * a.ldx + col;
+  float acc[M][4] = {};
+  for (int c = warp; c < nc; c += U * I4_WARPS) {
+    uint4 w[U][M][2];
+    float s[M][2];
+    uint4 x[U][2][2];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const bool in = c + u < c1 && (c + u) * 64 + 16 * t < a.K;
-      const int gi = group_of(c + u, a.magic);
+      const int cu = c + u * I4_WARPS, k = cu * 128 + 32 * t;
 #pragma unroll
       for (int m = 0; m < M; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          w[u][m][h] = in ? __ldg(reinterpret_cast<const uint2*>(wr[m][h] + (c + u) * 32)) : make_uint2(0, 0);
-          s[u][m][h] = c + u < c1 ? __ldg(sr[m][h] + gi) : 0.f;
-        }
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const bool on = in && t0 + 8 * j + g < a.T;
-        const uint4* p = reinterpret_cast<const uint4*>(xr[j] + (c + u) * 64);
-        x[u][j][0] = on ? __ldg(p) : make_uint4(0, 0, 0, 0);
-        x[u][j][1] = on ? __ldg(p + 1) : make_uint4(0, 0, 0, 0);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (c + u >= c1) break;
-#pragma unroll
-      for (int m = 0; m < M; ++m) {
-        float sum[NT][4] = {};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t f[4] = {pair4(w[u][m][0].x, i), pair4(w[u][m][1].x, i), pair4(w[u][m][0].y, i),
-                                 pair4(w[u][m][1].y, i)};
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            const uint4 lo = x[u][j][0], hi = x[u][j][1];
-            const uint32_t sel = i & 1 ? 0x7632 : 0x5410;
-            const uint32_t b0 = i < 2 ? __byte_perm(lo.x, lo.z, sel) : __byte_perm(lo.y, lo.w, sel);
-            const uint32_t b1 = i < 2 ? __byte_perm(hi.x, hi.z, sel) : __byte_perm(hi.y, hi.w, sel);
-            mma16816(sum[j], f, b0, b1);
+          w[u][m][h] = make_uint4(0, 0, 0, 0);
+          const uint8_t* p = wr[m][h] + cu * 64;
+          if (cu < nc && k < a.K) {
+            if (wide) {
+              w[u][m][h] = __ldg(reinterpret_cast<const uint4*>(p));
+            } else {
+              const uint2 v0 = __ldg(reinterpret_cast<const uint2*>(p));
+              const uint2 v1 = k + 16 < a.K ? __ldg(reinterpret_cast<const uint2*>(p) + 1) : make_uint2(0, 0);
+              w[u][m][h] = make_uint4(v0.x, v0.y, v1.x, v1.y);
+            }
           }
         }
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          acc[m][j][0] = fmaf(s[u][m][0], sum[j][0], acc[m][j][0]);
-          acc[m][j][1] = fmaf(s[u][m][0], sum[j][1], acc[m][j][1]);
-          acc[m][j][2] = fmaf(s[u][m][1], sum[j][2], acc[m][j][2]);
-          acc[m][j][3] = fmaf(s[u][m][1], sum[j][3], acc[m][j][3]);
+      for (int q = 0; q < 2; ++q) {
+        const bool on = token && cu < nc && cu * 128 + 64 * q + col < a.K;
+        const uint4* p = reinterpret_cast<const uint4*>(xr + cu * 128 + 64 * q);
+        x[u][q][0] = on ? __ldg(p) : make_uint4(0, 0, 0, 0);
+        x[u][q][1] = on ? __ldg(p + 1) : make_uint4(0, 0, 0, 0);
+      }
+    }
+    {  // lane t's scale is that of the t-th of the four chunks
+      const int ch = 2 * (c + (t >> 1) * I4_WARPS) + (t & 1);
+      const bool in = ch * 64 < a.K;
+      const int gi = group_of(in ? ch : 0, a.magic);
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) s[m][h] = in ? __ldg(sr[m][h] + gi) : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (c + u * I4_WARPS >= nc) break;
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        // lanes t and t + 2 hold 32 columns of the first and of the second chunk: they trade halves, and both hold 16 of each
+        uint2 v[2][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 r = w[u][m][h];
+          const uint32_t gx = __shfl_xor_sync(0xffffffffu, low ? r.z : r.x, 2), gy = __shfl_xor_sync(0xffffffffu, low ? r.w : r.y, 2);
+          v[0][h] = low ? make_uint2(r.x, r.y) : make_uint2(gx, gy);
+          v[1][h] = low ? make_uint2(gx, gy) : make_uint2(r.z, r.w);
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float sum[4];
+          const uint4 lo = x[u][q][0], hi = x[u][q][1];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t f[4] = {pair4(v[q][0].x, i), pair4(v[q][1].x, i), pair4(v[q][0].y, i), pair4(v[q][1].y, i)};
+            const uint32_t sel = i & 1 ? 0x7632 : 0x5410;
+            const uint32_t b0 = i < 2 ? __byte_perm(lo.x, lo.z, sel) : __byte_perm(lo.y, lo.w, sel);
+            const uint32_t b1 = i < 2 ? __byte_perm(hi.x, hi.z, sel) : __byte_perm(hi.y, hi.w, sel);
+            if (i == 0)
+              mma16816_first(sum, f, b0, b1);
+            else
+              mma16816(sum, f, b0, b1);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float sc = __shfl_sync(0xffffffffu, s[m][h], 2 * u + q, 4);
+            acc[m][2 * h] = fmaf(sc, sum[2 * h], acc[m][2 * h]);
+            acc[m][2 * h + 1] = fmaf(sc, sum[2 * h + 1], acc[m][2 * h + 1]);
+          }
         }
       }
     }
   }
-  float* mine = s_sum + warp * (8 * NT * P);
+  float* mine = s_sum + warp * (8 * P);
 #pragma unroll
   for (int m = 0; m < M; ++m)
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) mine[(8 * j + 2 * t + (q & 1)) * P + 16 * m + g + 8 * (q >> 1)] = acc[m][j][q];
+    for (int q = 0; q < 4; ++q) mine[(2 * t + (q & 1)) * P + 16 * m + g + 8 * (q >> 1)] = acc[m][q];
   __syncthreads();
-  for (int i = threadIdx.x; i < 8 * NT * 16 * MR; i += 32 * I4_WARPS) {
-    const int tok = i / (16 * MR), r = i % (16 * MR);
+  for (int i = threadIdx.x; i < 8 * 16; i += 32 * I4_WARPS) {
+    const int tok = i / (16), r = i % (16);
     if (t0 + tok >= a.T || n0 + r >= a.N) continue;
     float v = 0.f, up = 0.f;
 #pragma unroll
-    for (int q = 0; q < I4_WARPS; ++q) {
-      v += s_sum[q * (8 * NT * P) + tok * P + r];
-      if (GATED) up += s_sum[q * (8 * NT * P) + tok * P + 16 * MR + r];
+    for (int q = 0; q < I4_WARPS; ++q) {  // in the warps' order
+      v += s_sum[q * (8 * P) + tok * P + r];
+      if (GATED) up += s_sum[q * (8 * P) + tok * P + 16 + r];
     }
-    if (GATED) {
-      const float gate = v != v ? v : activation(a.act, v);  // a NaN gate is live
-      v = gate != 0.f ? gate * up : 0.f;                     // a dead unit is exactly 0
-    }
+    if (GATED) v = gated(a.act, v, up);
     const size_t at = (size_t)(t0 + tok) * a.ldy + n0 + r;
     if (a.y_f32)
       static_cast<float*>(a.y)[at] = v;
@@ -365,17 +462,273 @@ __global__ void __launch_bounds__(32 * I4_WARPS) int4_rows_kernel(const RowsArgs
   }
 }
 
-template <int NT, int MR, bool GATED, int U>
+template <bool GATED>
 cudaError_t rows_go(const RowsArgs& r, cudaStream_t s) {
-  constexpr size_t smem = sizeof(float) * I4_WARPS * 8 * NT * (16 * (GATED ? 2 * MR : MR) + 4);
-  static_assert(smem <= 48 * 1024, "more than a block has without asking");
-  const dim3 grid((unsigned)((r.N + 16 * MR - 1) / (16 * MR)), (unsigned)((r.T + 8 * NT - 1) / (8 * NT)));
-  return ops_launch(int4_rows_kernel<NT, MR, GATED, U>, grid, 32 * I4_WARPS, smem, s, 1, r);
+  const dim3 grid((unsigned)((r.N + 15) / 16), (unsigned)((r.T + 7) / 8));
+  return ops_launch(int4_rows_kernel<GATED>, grid, 32 * I4_WARPS, 0, s, 1, r);
 }
 
-constexpr int I4_ROWS = 32;  // most tokens of the form above
+constexpr int I4_STAGES = 3;
+constexpr uint64_t I4_TIMEOUT_NS = 250000000ull;
+constexpr uint32_t I4_BOX = 16 * 64;  // bytes of a tile's part of a warp's stage
+
+// The weight row that row g of a tile's MMA stands for: rows g = 0 .. 3 lie in different banks of the 64-byte-swizzled box.
+__device__ __forceinline__ int row_of(int g) { return (g & 1) | (g & 2) << 1 | (g & 4) >> 1; }
+
+bool encode_codes(CUtensorMap* m, const uint8_t* w, int N, int K) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)K / 2, (cuuint64_t)N}, strides[1] = {(cuuint64_t)K / 2};
+  const cuuint32_t box[2] = {64u, 16u}, es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(w), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A kernel's dynamic shared memory beyond what a block has without asking, allowed once on each device.
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes, std::once_flag (&once)[64], cudaError_t (&attr)[64]) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::call_once(once[dev], [&] { attr[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes); });
+  return attr[dev];
+}
+
+// More than eight tokens (int4_tile_kernel, K a multiple of 32): x is what repeats, so a block takes 128 rows of w a tile (M
+// tiles; both matrices, GATED), keeps its share of x in shared memory for all of them, already in the order of the MMA's
+// operands, and lets every warp walk K over its own 16 rows.  A warp's codes come by TMA, boxes of 16 rows by 128 columns
+// (64 bytes), into a ring of its own.  K is cut over the blocks of a cluster, whose sums are added through distributed shared
+// memory in the blocks' order.  Measured (us in a graph): 13 tokens, 2560 x 7168 8.7; 16, 7168 x 2560 7.7; 24, 14336 x 4096
+// 19.2; gated, two 14336 x 4096, 24 tokens 35.5 (each warp with x of its own from L2: 52).
+constexpr int x_chunks(int NT) { return NT == 2 ? 16 : NT == 3 ? 14 : 12; }  // of x that shared memory holds at a time
+constexpr size_t tile_smem(int NT, int M) {
+  return 1024 + std::max<size_t>(I4_WARPS * I4_STAGES * M * I4_BOX + x_chunks(NT) * NT * 1024, sizeof(float) * 8 * NT * (16 * I4_WARPS * M + 4));
+}
+
+template <int NT, int M, bool GATED>
+__global__ void __launch_bounds__(32 * I4_WARPS, 2)
+    int4_tile_kernel(const __grid_constant__ CUtensorMap m0, const __grid_constant__ CUtensorMap m1, const RowsArgs a, int cut,
+                     int* err) {
+  constexpr int MR = GATED ? M / 2 : M, ROWS = 16 * I4_WARPS * MR;  // rows of a matrix
+  constexpr int P = 16 * I4_WARPS * M + 4;                          // pitch of a token's sums
+  constexpr int XC = x_chunks(NT);
+  extern __shared__ uint8_t s_raw[];
+  __shared__ uint64_t bars[I4_WARPS][I4_STAGES];
+  __shared__ int abort_flag;
+  uint8_t* sm = s_raw + ((1024u - (smem_u32(s_raw) & 1023u)) & 1023u);  // the rings, then x [XC][NT][2][lane]; then the sums
+  uint4* s_x = reinterpret_cast<uint4*>(sm + I4_WARPS * I4_STAGES * M * I4_BOX);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int kr = blockIdx.x % cut, n0 = blockIdx.x / cut * ROWS, t0 = blockIdx.y * 8 * NT;
+  const int nd = (a.K + 127) / 128, d0 = nd * kr / cut, d1 = nd * (kr + 1) / cut;  // this block's pairs of chunks
+  uint64_t* full = bars[warp];
+  if (lane == 0) {
+    for (int i = 0; i < I4_STAGES; ++i) mbar_init(&full[i], 1);
+    fence_mbar_init();
+  }
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    tma_prefetch_map(&m0);
+    if (GATED) tma_prefetch_map(&m1);
+  }
+  __syncthreads();
+  pdl_launch_dependents();
+  pdl_wait();
+  float acc[M][NT][4] = {};
+  {
+    uint8_t* ring = sm + warp * (I4_STAGES * M) * I4_BOX;
+    auto fetch = [&](int d, int stage) {
+      if (d >= d1 || lane != 0) return;
+      mbar_arrive_expect_tx(&full[stage], M * I4_BOX);
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+        tma_tile_2d(ring + (stage * M + m) * I4_BOX, m / MR ? &m1 : &m0, d * 64, n0 + 16 * (I4_WARPS * (m % MR) + warp), &full[stage]);
+    };
+#pragma unroll
+    for (int i = 0; i < I4_STAGES; ++i) fetch(d0 + i, i);
+    const float* sr[M][2];
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        sr[m][h] = a.s[m / MR] + (size_t)min(n0 + 16 * (I4_WARPS * (m % MR) + warp) + 8 * h + row_of(g), a.N - 1) * a.G;
+    float s[M][2];  // of the next pair of chunks: lanes with t odd the second one's
+    auto scales = [&](int d) {
+      const bool in = d < d1 && (2 * d + (t & 1)) * 64 < a.K;
+      const int gi = group_of(2 * d + (t & 1), a.magic);
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) s[m][h] = in ? __ldg(sr[m][h] + gi) : 0.f;
+    };
+    scales(d0);
+    // where the lane's eight bytes of the box's two chunks are: 16-byte piece p of row r sits at p ^ (r >> 1 & 3)
+    const int r0 = row_of(g), x3 = r0 >> 1 & 3;
+    const uint32_t at0 = smem_u32(ring) + (uint32_t)(r0 * 64 + (((t >> 1) ^ x3) << 4) + 8 * (t & 1));
+    const uint32_t at1 = smem_u32(ring) + (uint32_t)(r0 * 64 + ((((t >> 1) + 2) ^ x3) << 4) + 8 * (t & 1));
+    int stage = 0;
+    uint32_t par = 0;
+    int done = 0;  // stages multiplied
+    bool ok = true;
+    for (int x0 = d0; x0 < d1; x0 += XC / 2) {
+      const int xn = min(XC / 2, d1 - x0);
+      if (x0 != d0) named_barrier(1, 32 * I4_WARPS);  // the chunks before have been multiplied
+      for (int i = threadIdx.x; i < 2 * xn * NT * 32; i += 32 * I4_WARPS) {
+        const int c = 2 * x0 + i / (NT * 32), tok = t0 + 8 * (i / 32 % NT) + (i & 31) / 4, k = c * 64 + 16 * (i & 3);
+        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+        if (tok < a.T && k < a.K) {
+          const uint4* p = reinterpret_cast<const uint4*>(a.x + (long long)tok * a.ldx + k);
+          lo = __ldg(p);
+          hi = __ldg(p + 1);
+        }
+        // step i of a chunk takes columns (i, i + 4) and (i + 8, i + 12) of a lane's sixteen
+        uint4* to = s_x + (i / 32) * 64 + (i & 31);
+        to[0] = make_uint4(__byte_perm(lo.x, lo.z, 0x5410), __byte_perm(hi.x, hi.z, 0x5410), __byte_perm(lo.x, lo.z, 0x7632),
+                           __byte_perm(hi.x, hi.z, 0x7632));
+        to[32] = make_uint4(__byte_perm(lo.y, lo.w, 0x5410), __byte_perm(hi.y, hi.w, 0x5410), __byte_perm(lo.y, lo.w, 0x7632),
+                            __byte_perm(hi.y, hi.w, 0x7632));
+      }
+      named_barrier(1, 32 * I4_WARPS);
+      for (int d = x0; d < x0 + xn; ++d) {
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[stage], par, &abort_flag, err, I4_TIMEOUT_NS));
+        if (!ok) break;  // (the other copies in flight are waited for below)
+        const uint32_t st = (uint32_t)(stage * M) * I4_BOX;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint2 w[M][2];
+          float sc[M][2];
+#pragma unroll
+          for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                           : "=r"(w[m][h].x), "=r"(w[m][h].y)
+                           : "r"((q ? at1 : at0) + st + (uint32_t)m * I4_BOX + 512u * h));
+              sc[m][h] = __shfl_sync(0xffffffffu, s[m][h], q, 4);
+            }
+          if (q == 1) {
+            __syncwarp();  // the stage is read
+            fetch(d + I4_STAGES, stage);
+            scales(d + 1);
+          }
+          // a chunk's four steps over all the tiles: an MMA follows one that it doesn't wait for
+          float sum[M][NT][4];
+          const uint4* from = s_x + (2 * (d - x0) + q) * NT * 64 + lane;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint4 b[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) b[j] = from[j * 64 + h * 32];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint32_t f[M][4];
+#pragma unroll
+              for (int m = 0; m < M; ++m) {
+                f[m][0] = pair4(w[m][0].x, 2 * h + i);
+                f[m][1] = pair4(w[m][1].x, 2 * h + i);
+                f[m][2] = pair4(w[m][0].y, 2 * h + i);
+                f[m][3] = pair4(w[m][1].y, 2 * h + i);
+              }
+#pragma unroll
+              for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+                  if (h == 0 && i == 0)
+                    mma16816_first(sum[m][j], f[m], b[j].x, b[j].y);
+                  else
+                    mma16816(sum[m][j], f[m], i ? b[j].z : b[j].x, i ? b[j].w : b[j].y);
+                }
+            }
+          }
+#pragma unroll
+          for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[m][j][e] = fmaf(sc[m][e >> 1], sum[m][j][e], acc[m][j][e]);
+        }
+        if (++stage == I4_STAGES) {
+          stage = 0;
+          par ^= 1;
+        }
+        ++done;
+      }
+    }
+    if (!ok && lane == 0)  // after a failed wait, copies in flight land before the block goes on
+      for (int d = done; d < min(done + I4_STAGES, d1 - d0); ++d)
+        mbar_wait_drain(&full[d % I4_STAGES], d / I4_STAGES & 1, I4_TIMEOUT_NS);
+    __syncwarp();
+  }
+  __syncthreads();  // the rings' and x's place becomes the sums'
+  float* sums = reinterpret_cast<float*>(sm);
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        sums[(8 * j + 2 * t + (q & 1)) * P + 16 * (I4_WARPS * m + warp) + row_of(g) + 8 * (q >> 1)] = acc[m][j][q];
+  if (cut > 1)
+    cluster_sync_all();
+  else
+    __syncthreads();
+  // four rows of a token a thread, a block of the cluster its share of them
+  const uint32_t base = smem_u32(sums);
+  const int live = min(8 * NT, a.T - t0);
+  const int end = live * (ROWS / 4) * (kr + 1) / cut;
+  for (int i = live * (ROWS / 4) * kr / cut + threadIdx.x; i < end; i += blockDim.x) {
+    const int tok = i / (ROWS / 4), r = i % (ROWS / 4) * 4;
+    if (n0 + r >= a.N) continue;
+    float v[4] = {}, up[4] = {};
+    for (int k = 0; k < cut; ++k) {
+      const uint32_t at = base + (uint32_t)(tok * P + r) * 4u;
+      const float4 p = cut > 1 ? ld_cluster_f4(cluster_map(at, (uint32_t)k)) : *reinterpret_cast<const float4*>(sums + tok * P + r);
+      v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
+      if (GATED) {
+        const float4 q = cut > 1 ? ld_cluster_f4(cluster_map(at + ROWS * 4u, (uint32_t)k))
+                                 : *reinterpret_cast<const float4*>(sums + tok * P + ROWS + r);
+        up[0] += q.x, up[1] += q.y, up[2] += q.z, up[3] += q.w;
+      }
+    }
+    const size_t at = (size_t)(t0 + tok) * a.ldy + n0 + r;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (n0 + r + q >= a.N) break;
+      if (GATED) v[q] = gated(a.act, v[q], up[q]);
+      if (a.y_f32)
+        static_cast<float*>(a.y)[at + q] = v[q];
+      else
+        static_cast<__nv_bfloat16*>(a.y)[at + q] = __float2bfloat16_rn(v[q]);
+    }
+  }
+  if (cut > 1) cluster_sync_all();  // the sums stay until every block has read them
+}
+
+template <int NT, int M, bool GATED>
+cudaError_t tile_go(const RowsArgs& r, cudaStream_t s) {
+  auto kernel = int4_tile_kernel<NT, M, GATED>;
+  constexpr size_t smem = tile_smem(NT, M);
+  static std::once_flag once[64];
+  static cudaError_t attr[64];
+  cudaError_t e = allow_smem(kernel, smem, once, attr);
+  if (e != cudaSuccess) return e;
+  constexpr int rows = 16 * I4_WARPS * (GATED ? M / 2 : M);
+  const int nb = (r.N + rows - 1) / rows, tb = (r.T + 8 * NT - 1) / (8 * NT), nc = (r.K + 127) / 128;
+  // as many blocks as run at once, two an SM (24 tokens, 14336 x 4096, cut 2 / 3 / 4 / 5 / 8: 29.2 / 24.2 / 19.8 / 19.2 / 25.7 us)
+  const int cut = (int)std::max<long long>(1, std::min<long long>({8, nc / 2, 2ll * ops_num_sms() / ((long long)nb * tb)}));
+  int* err = nullptr;
+  if ((e = ops_error_word(&err)) != cudaSuccess) return e;
+  CUtensorMap m0, m1;
+  if (!encode_codes(&m0, r.w[0], r.N, r.K) || !encode_codes(&m1, GATED ? r.w[1] : r.w[0], r.N, r.K)) return cudaErrorInvalidValue;
+  return ops_launch(kernel, dim3((unsigned)(nb * cut), (unsigned)tb), 32 * I4_WARPS, smem, s, cut, m0, m1, r, cut, err);
+}
 
 size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
+
+// Whether the codes themselves are multiplied, or bf16 copies of them.  (us, codes / copies, N = 7168, K = 2560: bf16 48
+// tokens 15.7 / 17.9, 128 26.7 / 19.6; fp32 64 tokens 15.9 / 26.9; gated 64 tokens 29.2 / 57.5, 128 50.6 / 60.6; N = 14336, K
+// = 4096, bf16, 64 tokens 39.9 / 50.6.)  Rows of codes that TMA does not take go eight tokens at a time.
+bool codes_themselves(int T, int K, int split) { return T <= (K % 32 != 0 ? 32 : split ? 128 : 64); }
 
 // Columns of a copy's row.  A product in fp32, and the gated block, whose gate is a small difference of sums that a
 // weight's rounding to bf16 would reach, take the weights as two bf16 parts each (2^-16); a bf16 product takes one: its
@@ -397,6 +750,10 @@ cudaError_t launch_quantize_int4(const void* w, long long ldw, uint8_t* q, float
     auto kernel = a.group == 64 ? quantize_int4_kernel<8> : a.group == 128 ? quantize_int4_kernel<16> : quantize_int4_kernel<32>;
     return ops_launch(kernel, grid, 32 * I4_WARPS, 0, s, 1, a);
   }
+  // (4096 x 14336 in groups of 512, a block / a warp each: 131 / 31 us)
+  if (a.group <= 2048 && a.G > 1)
+    return ops_launch(quantize_int4_warp_kernel, dim3((unsigned)N, (unsigned)((a.G + I4_WARPS - 1) / I4_WARPS)), 32 * I4_WARPS, 0, s,
+                      1, a);
   const dim3 grid((unsigned)N, (unsigned)a.G);
   const int per = (a.group / 8 + 32 * I4_WARPS - 1) / (32 * I4_WARPS);
   auto kernel = per <= 2 ? quantize_int4_wide_kernel<2> : per <= 8 ? quantize_int4_wide_kernel<8> : quantize_int4_wide_kernel<0>;
@@ -411,25 +768,24 @@ cudaError_t launch_dequantize_int4(const uint8_t* q, const float* sc, void* y, l
 }
 
 size_t int4_workspace(int T, int N, int K, int split, int gated) {
-  return T <= I4_ROWS ? 0 : (gated ? 2 : 1) * round_up(2 * (size_t)N * copy_row(K, split), 256);
+  return codes_themselves(T, K, split) ? 0 : (gated ? 2 : 1) * round_up(2 * (size_t)N * copy_row(K, split), 256);
 }
 
 cudaError_t launch_matmul_int4(const Int4Args& a, cudaStream_t s) {
   const bool gated = a.w3 != nullptr;
-  if (a.T <= I4_ROWS) {
+  const int split = a.y_f32 || gated;
+  if (codes_themselves(a.T, a.K, split)) {
     const RowsArgs r = {static_cast<const uint16_t*>(a.x), a.ldx, {a.w, a.w3}, {a.sw, a.s3}, a.y, a.ldy, a.T, a.N, a.K,
                         groups(a.K, a.group), a.y_f32, a.act, magic_of(a.K, a.group)};
-    if (gated) {
-      if (a.T <= 8) return rows_go<1, 1, true, 4>(r, s);
-      if (a.T <= 16) return rows_go<2, 1, true, 2>(r, s);
-      return rows_go<4, 1, true, 1>(r, s);
-    }
-    if (a.T <= 8) return rows_go<1, 1, false, 4>(r, s);
-    if (a.T <= 16) return rows_go<2, 1, false, 2>(r, s);
-    return rows_go<4, 2, false, 1>(r, s);
+    if (a.T <= 8 || a.K % 32 != 0) return gated ? rows_go<true>(r, s) : rows_go<false>(r, s);
+    if (gated) return a.T <= 16 ? tile_go<2, 2, true>(r, s) : a.T <= 24 ? tile_go<3, 2, true>(r, s) : tile_go<4, 2, true>(r, s);
+    // two tiles a block where the cut of K, eight at most, still fills the SMs (13 tokens, one / two tiles: 14336 x 4096 20.2 /
+    // 15.7 us, 7168 x 2560 7.2 / 8.7, 2560 x 7168 8.7 / 11.0)
+    if ((a.N + 255) / 256 < 2 * ops_num_sms() / 8)
+      return a.T <= 16 ? tile_go<2, 1, false>(r, s) : a.T <= 24 ? tile_go<3, 1, false>(r, s) : tile_go<4, 1, false>(r, s);
+    return a.T <= 16 ? tile_go<2, 2, false>(r, s) : a.T <= 24 ? tile_go<3, 2, false>(r, s) : tile_go<4, 2, false>(r, s);
   }
   // more tokens: the weights as bf16 copies, then the products on the tensor cores
-  const int split = a.y_f32 || gated;
   const size_t row = copy_row(a.K, split), one = round_up(2 * (size_t)a.N * row, 256);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   ValueArgs v = {{a.w, gated ? a.w3 : a.w}, {a.sw, gated ? a.s3 : a.sw}, {ws, ws + one}, (long long)row, a.N, a.K,

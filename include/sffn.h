@@ -473,8 +473,8 @@ int sffn_dequantize_int4(const uint8_t* codes, const float* scales, void* y, lon
  *   sffn_gated_up_int4:  h[t, i] = A(sum_k x[t, k] w1[i, k]) * sum_k x[t, k] w3[i, k],
  *     h [T, H] (row pitch ldh) bf16; a unit whose gate is 0 is exactly 0, a NaN gate
  *     is live.
- * Sums are fp32.  Few tokens (those that need no workspace) multiply the codes
- * themselves and round nothing but the result.  More tokens go through bf16 copies of
+ * Sums are fp32.  Few tokens (those that need no workspace, up to 32, 64 or 128) multiply
+ * the codes themselves and round nothing but the result.  More tokens go through bf16 copies of
  * the weights: two parts each, which hold a weight to 2^-16, for y in f32 and for the
  * gated block; one part, a rounding of each weight to bf16 (2^-8), for y in bf16.
  * The workspace holds sffn_int4_workspace(T, N, K, y_dtype, gated) bytes (gated: N = H,

@@ -503,6 +503,25 @@ def test_backward_of_corrupt_tokens_stays_with_them():
     assert torch.isnan(got[1]).all() and torch.isnan(got[2]).all()  # a sum over the tokens
 
 
+@pytest.mark.parametrize("T,D,H", [(300, 2560, 1024), (2048, 2560, 4100)])
+def test_the_sign_of_a_kept_gate_is_the_sums(T, D, H):
+    """z near 0 is computed again in fp32 (D / 64 steps a lane, their sum in 6 more): its sign is the exact sum's but where
+    the exact sum is within that."""
+    g = gen(36)
+    x, W1, W3 = randn(g, T, D), randn(g, H, D) * D ** -0.5, randn(g, H, D) * D ** -0.5
+    x[T // 2] = 0      # a padded token: exact zeros
+    x[T // 3] *= 1e-9  # a token that is small as a whole
+    W1[H // 2] = 0
+    _, z, _ = sffn.gated_up_saved(x, W1, W3, act="relu")
+    ref = x.double() @ W1.double().T
+    S = x.double().abs() @ W1.double().abs().T
+    assert (z[T // 2] == 0).all() and (z[:, H // 2] == 0).all()
+    wrong = (z.double() * ref < 0) & (ref.abs() > (D / 64 + 8) * 2.0 ** -24 * S)
+    wrong[T // 3] = False
+    assert not wrong.any()
+    close(z, ref, (D + 8) * 2.0 ** -23 * S)
+
+
 def test_gated_no_tokens():
     W1, W3 = randn(gen(29), 24, 64).requires_grad_(), randn(gen(30), 24, 64).requires_grad_()
     x = torch.empty(0, 64, dtype=BF, device=DEV).requires_grad_()
