@@ -493,8 +493,9 @@ PyObject* gated_up(PyObject* const* args, Py_ssize_t n) {
   const int64_t act = whole(args[3]);
   if (at::GradMode::is_enabled() && (a.x->requires_grad() || a.W1->requires_grad() || a.W3->requires_grad())) {
     if (!g.gated_up_backward || c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None ||
-        a.D % 8 || a.ld % 8 || a.H < 1 || act < SFFN_ACT_RELU || act > SFFN_ACT_SILU)
-      return none();
+        a.D % 8 || a.ld % 8 || a.H < 1 || act < SFFN_ACT_RELU || act > SFFN_ACT_SILU ||
+        (((uintptr_t)a.x->data_ptr() | (uintptr_t)a.W1->data_ptr() | (uintptr_t)a.W3->data_ptr()) & 15))
+      return none();  // refused, or not recorded: operators.py says why
     return THPVariable_Wrap(GatedUp::apply(*a.x, *a.W1, *a.W3, act));
   }
   Tensor h = make({a.T, a.H}, at::kBFloat16, a.device);

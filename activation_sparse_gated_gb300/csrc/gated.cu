@@ -21,85 +21,108 @@ namespace sffn {
 namespace {
 
 constexpr int GU_WARPS = 8;
-constexpr int GU_U = 5;                  // pieces of a weight row requested before the first is used
 constexpr int GU_TOKENS = 4;             // most tokens of the gate-first form
+constexpr int GU_U = 5;                   // pieces of a weight row requested before the first is used
 constexpr size_t GU_STAGE = 40 * 1024;   // most bytes of x in shared memory
 
-// A warp takes one hidden unit and the TM tokens together: its row of W1 is read once for them, and its row of W3 only
-// where a token keeps the unit.
-template <int TM, bool STAGED>
+// A warp takes UN hidden units and the TM tokens together: the units' rows of W1 are read once for them, GU_U pieces of each
+// requested before the first is used, and a unit's row of W3 only where a token keeps it.  Bound by memory latency: the rows of
+// W1, then those of W3.  (One token, D = 2560, H = 7168, 10 % of the units live: 9.9 us for 40 MB, 60 % of the copy rate; D =
+// 4096, H = 14336 25 us, 76 %.  Eight or ten pieces ahead: 12.2 and 10.9, 23.7 both.)
+template <int TM, int UN, bool STAGED>
 __global__ void __launch_bounds__(32 * GU_WARPS) gated_rows_kernel(const GatedArgs a) {
   extern __shared__ uint4 s_x[];  // [TM][D / 8]
-  const int lane = threadIdx.x & 31, i = blockIdx.x * GU_WARPS + (threadIdx.x >> 5), n = a.D / 8;
+  const int lane = threadIdx.x & 31, i0 = (blockIdx.x * GU_WARPS + (threadIdx.x >> 5)) * UN, n = a.D / 8;
   pdl_launch_dependents();
   pdl_wait();
   const uint4* x[TM];
 #pragma unroll
   for (int t = 0; t < TM; ++t)  // tokens past T are computed on the last one and not stored
     x[t] = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.x) + (long long)min(t, a.T - 1) * a.ldx);
-  const size_t off = (size_t)min(i, a.H - 1) * a.D;
-  const uint4* w1 = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.W1) + off);
-  const uint4* w3 = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.W3) + off);
-  uint4 w[GU_U];
+  const uint4 *w1[UN], *w3[UN];
 #pragma unroll
-  for (int q = 0; q < GU_U; ++q)  // the first pieces of W1 travel while x is staged
-    w[q] = lane + 32 * q < n ? __ldg(w1 + lane + 32 * q) : make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < UN; ++i) {
+    const size_t off = (size_t)min(i0 + i, a.H - 1) * a.D;
+    w1[i] = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.W1) + off);
+    w3[i] = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.W3) + off);
+  }
+  uint4 w[UN][GU_U];
+  auto request = [&](const uint4* const (&p)[UN], const bool (&on)[UN], int k0) {
+#pragma unroll
+    for (int i = 0; i < UN; ++i)
+#pragma unroll
+      for (int q = 0; q < GU_U; ++q)
+        w[i][q] = on[i] && k0 + 32 * q < n ? __ldg(p[i] + k0 + 32 * q) : make_uint4(0, 0, 0, 0);
+  };
+  bool on[UN];
+#pragma unroll
+  for (int i = 0; i < UN; ++i) on[i] = true;
+  request(w1, on, lane);  // the first pieces of W1 travel while x is staged
   if (STAGED) {
 #pragma unroll
     for (int t = 0; t < TM; ++t)
       for (int k = threadIdx.x; k < n; k += 32 * GU_WARPS) s_x[t * n + k] = __ldg(x[t] + k);
     __syncthreads();
   }
-  if (i >= a.H) return;
-  auto dot = [&](const uint4* wp, bool loaded, float (&out)[TM]) {
-    float2 acc[TM] = {};
+  if (i0 >= a.H) return;
+  auto dots = [&](const uint4* const (&p)[UN], bool loaded, float (&out)[UN][TM]) {
+    float2 acc[UN][TM] = {};
     for (int k0 = lane; k0 < n; k0 += 32 * GU_U) {
-      if (!loaded || k0 != lane) {
-#pragma unroll
-        for (int q = 0; q < GU_U; ++q) w[q] = k0 + 32 * q < n ? __ldg(wp + k0 + 32 * q) : make_uint4(0, 0, 0, 0);
-      }
+      if (!loaded || k0 != lane) request(p, on, k0);
 #pragma unroll
       for (int q = 0; q < GU_U; ++q) {
         const int k = k0 + 32 * q;
         if (k < n) {
-          float u[8];
-          Elt<bf16_tag>::unpack(w[q], u);
+          float v[TM][8];
 #pragma unroll
-          for (int t = 0; t < TM; ++t) {
-            float v[8];
-            Elt<bf16_tag>::unpack(STAGED ? lds16(s_x + t * n + k) : __ldg(x[t] + k), v);
+          for (int t = 0; t < TM; ++t) Elt<bf16_tag>::unpack(STAGED ? lds16(s_x + t * n + k) : __ldg(x[t] + k), v[t]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              ffma2(acc[t], make_float2(u[2 * j], u[2 * j + 1]), make_float2(v[2 * j], v[2 * j + 1]));
+          for (int i = 0; i < UN; ++i) {
+            float u[8];
+            Elt<bf16_tag>::unpack(w[i][q], u);
+#pragma unroll
+            for (int t = 0; t < TM; ++t)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                ffma2(acc[i][t], make_float2(u[2 * j], u[2 * j + 1]), make_float2(v[t][2 * j], v[t][2 * j + 1]));
           }
         }
       }
     }
 #pragma unroll
-    for (int t = 0; t < TM; ++t) out[t] = warp_sum(acc[t].x + acc[t].y);
+    for (int i = 0; i < UN; ++i)
+#pragma unroll
+      for (int t = 0; t < TM; ++t) out[i][t] = on[i] ? warp_sum(acc[i][t].x + acc[i][t].y) : 0.f;
   };
-  float g[TM], u[TM];
-  dot(w1, true, g);
-  bool live = false;
+  float g[UN][TM], u[UN][TM] = {};
+  dots(w1, true, g);
+  bool any = false;
 #pragma unroll
-  for (int t = 0; t < TM; ++t) {
-    g[t] = g[t] != g[t] ? g[t] : activation(a.act, g[t]);  // a NaN gate is live
-    u[t] = 0.f;
-    live = live || g[t] != 0.f;
+  for (int i = 0; i < UN; ++i) {
+    on[i] = false;
+#pragma unroll
+    for (int t = 0; t < TM; ++t) {
+      g[i][t] = g[i][t] != g[i][t] ? g[i][t] : activation(a.act, g[i][t]);  // a NaN gate is live
+      on[i] = on[i] || (g[i][t] != 0.f && i0 + i < a.H);
+    }
+    any = any || on[i];
   }
-  if (live) dot(w3, false, u);
+  if (any) dots(w3, false, u);
 #pragma unroll
-  for (int t = 0; t < TM; ++t)
-    if (lane == t && t < a.T)
-      reinterpret_cast<__nv_bfloat16*>(a.h)[(long long)t * a.ldh + i] = __float2bfloat16_rn(g[t] != 0.f ? g[t] * u[t] : 0.f);
+  for (int i = 0; i < UN; ++i)
+#pragma unroll
+    for (int t = 0; t < TM; ++t)
+      if (lane == i * TM + t && t < a.T && i0 + i < a.H)
+        reinterpret_cast<__nv_bfloat16*>(a.h)[(long long)t * a.ldh + i0 + i] =
+            __float2bfloat16_rn(g[i][t] != 0.f ? g[i][t] * u[i][t] : 0.f);
 }
 
-template <int TM>
+template <int TM, int UN>
 cudaError_t rows_go(const GatedArgs& a, cudaStream_t s) {
-  const dim3 grid((unsigned)((a.H + GU_WARPS - 1) / GU_WARPS));
+  const dim3 grid((unsigned)((a.H + GU_WARPS * UN - 1) / (GU_WARPS * UN)));
   const size_t bytes = TM * 2 * (size_t)a.D;
-  return bytes <= GU_STAGE ? ops_launch(gated_rows_kernel<TM, true>, grid, 32 * GU_WARPS, bytes, s, 1, a)
-                           : ops_launch(gated_rows_kernel<TM, false>, grid, 32 * GU_WARPS, 0, s, 1, a);
+  return bytes <= GU_STAGE ? ops_launch(gated_rows_kernel<TM, UN, true>, grid, 32 * GU_WARPS, bytes, s, 1, a)
+                           : ops_launch(gated_rows_kernel<TM, UN, false>, grid, 32 * GU_WARPS, 0, s, 1, a);
 }
 
 // dz = dh u A'(z) and du = dh A(z) of one element.  A gate that is closed passes nothing, whatever dh and the other factor
@@ -172,7 +195,14 @@ int padded(int H) { return (H + 63) / 64 * 64; }
 }  // namespace
 
 cudaError_t launch_gated_up(const GatedArgs& a, cudaStream_t s) {
-  if (!a.z && a.T <= GU_TOKENS) return a.T == 1 ? rows_go<1>(a, s) : a.T == 2 ? rows_go<2>(a, s) : rows_go<GU_TOKENS>(a, s);
+  // Gate first for one or two tokens, and for up to four where the products' launch is most of their time (us, gate first /
+  // products, ReLU: 2 tokens, D = 4096, H = 14336 31 / 40; 4 tokens, D = 1024, H = 1000 4.1 / 7.3, D = 2560, H = 7168 19.0 /
+  // 16.9).  Two units a warp where one each is more warps than run at once (one token, D = 2560, one / two: H = 7168 ReLU
+  // 10.7 / 9.9, SiLU 15.2 / 13.0, H = 1024 3.9 / 4.4).
+  if (!a.z && a.T <= GU_TOKENS && (a.T <= 2 || (long long)a.H * a.D <= 8 << 20)) {
+    if (a.T == 1) return a.H > 40 * ops_num_sms() ? rows_go<1, 2>(a, s) : rows_go<1, 1>(a, s);
+    return a.T == 2 ? rows_go<2, 1>(a, s) : rows_go<GU_TOKENS, 1>(a, s);
+  }
   GmmArgs p;
   p.x = a.x;
   p.ldx = a.ldx;

@@ -773,8 +773,8 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
       const uint32_t ta = tmem + b * (uint32_t)((GATED ? 2 : 1) * p.NT) + ((uint32_t)(32 * (ew & 3)) << 16);
       const float sw = F16 && nok ? p.g.sw[(size_t)q.e * p.g.N + n] : 0.f;
       const int rows = q.r1 - q.r0;
-      void* const yb = XT && q.e ? p.g.y2 : p.g.y;        // the group's result and
-      const int yr = q.r0 - (XT ? q.e * p.g.per : 0);     // the tile's first row of it
+      auto result = [&]() -> void* { return XT && q.e ? p.g.y2 : p.g.y; };  // the group's, whose rows start at row yr0
+      const int yr0 = XT ? q.e * p.g.per : 0;                              // (neither is kept in registers but for XT)
       if (CTAS == 1 && ks > 1) {
         // K is cut over the cluster: every block leaves its partial tile, [row of x][128 rows of w], in the stages
         // (their copies and MMAs are done, and the producers wait for `partd`); then each sums its share of the
@@ -847,14 +847,14 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) f[i] = f[i] * sx * s4[i];
           }
-          const uint64_t o = (uint64_t)(uint32_t)(yr + r) * (uint64_t)p.g.ldy + nc;
+          const uint64_t o = (uint64_t)(uint32_t)(gr - yr0) * (uint64_t)p.g.ldy + nc;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             if (nc + i < p.g.N) {
               if (p.g.y_f32)
-                reinterpret_cast<float*>(yb)[o + i] = f[i];
+                reinterpret_cast<float*>(result())[o + i] = f[i];
               else
-                reinterpret_cast<__nv_bfloat16*>(yb)[o + i] = __float2bfloat16_rn(f[i]);
+                reinterpret_cast<__nv_bfloat16*>(result())[o + i] = __float2bfloat16_rn(f[i]);
             }
         }
         __syncwarp();
@@ -866,7 +866,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
         uint32_t v[32];
         tmem_ld32(ta + c0, v);
         const int left = min(rows - c0, 32);  // rows of this piece, r0 + c0 on
-        const uint64_t y0 = (uint64_t)(uint32_t)(yr + c0) * (uint64_t)p.g.ldy;
+        const uint64_t y0 = (uint64_t)(uint32_t)(q.r0 - yr0 + c0) * (uint64_t)p.g.ldy;
         float sx = 0.f;  // lane j: the scale of row j
         if (F16 && lane < left) {
           int src = q.r0 + c0 + lane;
@@ -954,7 +954,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
                 const int j = 4 * i + (lane >> 3), c = 4 * (lane & 7);
                 const uint4 d = lds16a(buf + (uint32_t)(j * TG_EPI_PITCH + c) * 4u);
                 if (16 * h + j < left && nc + c < p.g.NY)
-                  *reinterpret_cast<uint4*>(reinterpret_cast<float*>(yb) + y0 +
+                  *reinterpret_cast<uint4*>(reinterpret_cast<float*>(result()) + y0 +
                                             (uint64_t)(16 * h + j) * (uint64_t)p.g.ldy + nc + c) = d;
               }
               __syncwarp();
@@ -975,7 +975,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
               const int j = 8 * i + (lane >> 2), c = 8 * (lane & 3);
               const uint32_t at = buf + (uint32_t)(j * TG_EPI_PITCH + c) * 4u;
               const uint4 d = lds16a(at), e = lds16a(at + 16);
-              __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(yb) + y0 + (uint64_t)(2 * j) * (uint64_t)p.g.ldy + nc + c;
+              __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(result()) + y0 + (uint64_t)(2 * j) * (uint64_t)p.g.ldy + nc + c;
               if (nc + c < p.g.NY) {
                 if (2 * j < left)
                   *reinterpret_cast<uint4*>(y) =
@@ -991,7 +991,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
           }
         } else {
           const uint32_t size = p.g.y_f32 ? 4 : 2;
-          uint8_t* to = reinterpret_cast<uint8_t*>(yb) + (y0 + n) * size;
+          uint8_t* to = reinterpret_cast<uint8_t*>(result()) + (y0 + n) * size;
           const uint64_t pitch = (uint64_t)p.g.ldy * size;
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
