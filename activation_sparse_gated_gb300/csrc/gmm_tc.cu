@@ -365,15 +365,23 @@ __device__ __noinline__ float warp_dot(const uint16_t* x, const uint16_t* w, int
 __device__ __forceinline__ void refine_gate(const GmmArgs& g, const uint32_t (&val)[32], int e, int r0, int left, int n, bool nok,
                                             float* z, int steps) {
   const int lane = threadIdx.x & 31;
-  uint32_t top = 0, least = 0xffffffffu;  // magnitudes as bits; 0 - 1 is the largest
+  float top = 0.f, least = 3e38f;
+  if (left == 32) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    const uint32_t b = val[j] & 0x7fffffffu;
-    top = max(top, b);
-    least = min(least, b - 1);
+    for (int j = 0; j < 32; ++j) {
+      top = fmaxf(top, fabsf(__uint_as_float(val[j])));
+      least = fminf(least, fabsf(__uint_as_float(val[j])));
+    }
+  } else {  // (columns past the rows hold anything)
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j < left) {
+        top = fmaxf(top, fabsf(__uint_as_float(val[j])));
+        least = fminf(least, fabsf(__uint_as_float(val[j])));
+      }
   }
-  const float limit = __uint_as_float(top) * (float)steps * 0x1p-24f;
-  if (!__any_sync(0xffffffffu, nok && __uint_as_float(least) < limit)) return;  // (no number: false)
+  const float limit = top * (float)steps * 0x1p-24f;
+  if (!__any_sync(0xffffffffu, nok && least < limit)) return;
   uint32_t near = 0;
 #pragma unroll
   for (int j = 0; j < 32; ++j) {
@@ -424,7 +432,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
   uint8_t* sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
   constexpr uint32_t AB = 128u * 128u;  // one A region: 128 rows x 128 bytes
   const uint32_t NTl = (uint32_t)p.NT / CTAS;
-  const uint32_t bb = (NTl + 7) / 8 * 1024u;                 // B region
+  const uint32_t bb = (XT ? (NTl + 63) / 64 * 8 : (NTl + 7) / 8) * 1024u;  // B region (XT: boxes of 64 rows)
   // an operand stage; int8: 128 codes of x widened (two 64-wide tiles; the weights' are in TMEM), a raw stage both's
   const uint32_t st_bytes = I8 ? 2 * bb : (GATED ? 2 : 1) * AB + bb, raw_bytes = AB + bb;
   const uint32_t raw0 = (uint32_t)p.S * st_bytes;
@@ -892,30 +900,19 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
           tmem_ld32(ta + p.NT + c0, u);
           tmem_ld_wait();
           done();
-          if constexpr (TRAIN) {  // kept as they are, in fp32, through this warp's shared scratch like the result
-            const uint32_t buf = smb + epi0 + (uint32_t)ew * TG_EPI_BYTES;
+          if constexpr (TRAIN) {
+            // kept as they are, in fp32: a token's 32 units are 128 bytes, stored by the lanes as they have them
             const uint64_t z0 = (uint64_t)(uint32_t)(q.r0 + c0) * (uint64_t)p.g.ldz + (q.mt * 128 * CTAS + n0r + 32 * (ew & 3));
-            const int room = p.g.NY - (q.mt * 128 * CTAS + n0r + 32 * (ew & 3));  // columns from z0 on
+            const bool whole = left == 32 && __all_sync(0xffffffffu, nok);
             auto keep = [&](const uint32_t (&val)[32], float* to) {
-              if (!p.vec) {
+              to += lane;
+              if (whole) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) to[(uint64_t)j * (uint32_t)p.g.ldz] = __uint_as_float(val[j]);
+              } else {
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
-                  if (nok && j < left) to[(uint64_t)j * (uint64_t)p.g.ldz + lane] = __uint_as_float(val[j]);
-                return;
-              }
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) sts4(buf + (uint32_t)(j * TG_EPI_PITCH + lane) * 4u, val[16 * h + j]);
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const int j = 4 * i + (lane >> 3), c = 4 * (lane & 7);
-                  const uint4 d = lds16a(buf + (uint32_t)(j * TG_EPI_PITCH + c) * 4u);
-                  if (16 * h + j < left && c < room)
-                    *reinterpret_cast<uint4*>(to + (uint64_t)(16 * h + j) * (uint64_t)p.g.ldz + c) = d;
-                }
-                __syncwarp();
+                  if (nok && j < left) to[(uint64_t)j * (uint32_t)p.g.ldz] = __uint_as_float(val[j]);
               }
             };
             keep(v, p.g.z + z0);
@@ -1125,11 +1122,10 @@ cudaError_t launch_gmm_tc(const GmmArgs& a, int ctas, int nt, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const size_t yb = a.y_f32 ? 4 : 2;
   p.g.NY = std::max(a.N, a.NY);
-  p.vec = ((uintptr_t)a.y & 15) == 0 && a.ldy * yb % 16 == 0 && p.g.NY * yb % 16 == 0 && ((uintptr_t)a.y2 & 15) == 0 &&
-          ((uintptr_t)a.z & 15) == 0 && ((uintptr_t)a.u & 15) == 0 && a.ldz % 4 == 0;
+  p.vec = ((uintptr_t)a.y & 15) == 0 && a.ldy * yb % 16 == 0 && p.g.NY * yb % 16 == 0 && ((uintptr_t)a.y2 & 15) == 0;
   const size_t fixed = tg_fixed(a.i8 ? 4 : 8, a.E);
   const int room = (int)(TG_SMEM - fixed);
-  const int ntl = p.NT / ctas, bb = (ntl + 7) / 8 * 1024;
+  const int ntl = p.NT / ctas, bb = (a.xt ? (ntl + 63) / 64 * 8 : (ntl + 7) / 8) * 1024;
   // int8: three operand stages (two are 10 to 15 % slower) and as many raw ones at least (see the converters' waits);
   // 128 rows a tile leave room for them with the tables of as many experts as there may be
   constexpr int least = 3;
@@ -1226,6 +1222,35 @@ size_t gmm_workspace(int R, int XR, int N, int K, int E, int i8) {
   return wide(R, E, i8) ? 2 * ((size_t)XR * K + (size_t)E * N * K) : 0;
 }
 
+// Rows of x a pair's tile takes where the host knows every group's length (no offsets): 256, or fewer where that saves enough
+// of the last round of tiles over the SMs.  A 64-wide chunk of K costs a block its MMAs, two cycles a row and product, or its
+// copies, 64 bytes a cycle from L2, whichever is more.  (us, 256 rows / as here: gate and up for training of D = 2560, H = 7168,
+// 1000 tokens 72 / 55, of D = H = 4096, 3000 tokens 149 / 132; dx of D = 2560, H = 7168, 2048 tokens 131 / 118, 8192 tokens
+// 363 / 326.)
+int tile_rows(const GmmArgs& a, bool gated) {
+  const long long pairs = std::max(1, ops_num_sms() / 2), m = a.R / a.E, least = (m + 255) / 256, MT = (a.N + 255) / 256;
+  if (MT * least * a.E >= 16 * pairs) return 256;  // the last of so many rounds is little
+  auto cost = [&](long long n, int per) {
+    const int copied = a.xt ? (per / 2 + 63) / 64 * 64 : per / 2;
+    const long long chunk = std::max((gated ? 4 : 2) * per, (gated ? 512 : 256) + 2 * copied);
+    // gate and up of more than 128 rows leave room for one accumulator: their epilogue is not hidden
+    const long long exposed = gated && per > 128 ? (a.z ? 75 : 30) * per : 0;
+    return (MT * n * a.E + pairs - 1) / pairs * (chunk * ((a.K + 63) / 64) * (a.split ? 2 : 1) + exposed);
+  };
+  int rows = 256;
+  long long best = cost(least, 256) * 97 / 100;
+  for (long long n = least + 1; n <= 2 * least; ++n) {
+    const int per = (int)(((m + n - 1) / n + 31) / 32 * 32);
+    if (per < 128) break;
+    const long long c = cost(n, per);
+    if (c < best) {
+      best = c;
+      rows = per;
+    }
+  }
+  return rows;
+}
+
 cudaError_t launch_gmm(const GmmArgs& a, cudaStream_t s) {
   const int busy = std::min(a.E, a.R);
   if (wide(a.R, a.E, a.i8) && a.workspace && copies_pay(a)) {
@@ -1250,8 +1275,9 @@ cudaError_t launch_gmm(const GmmArgs& a, cudaStream_t s) {
   const bool fill = 2 * pairs >= ops_num_sms();
   // Gate and up together: 256 rows a tile take all of TMEM, so their epilogue is not hidden, and still win from 128
   // rows a group on (4096 tokens, 8 of 64 experts, D = 2560, H = 1024: 561 against 643 us; 512 tokens 225 / 211).
-  if (a.w3 && !a.K1) return a.R >= 128 * busy && fill && a.N > 128 ? launch_gmm_tc(a, 2, 256, s) : launch_gmm_tc(a, 1, 128, s);
-  return a.R >= 96 * busy && fill && a.N > 128 ? launch_gmm_tc(a, 2, 256, s) : launch_gmm_tc(a, 1, 128, s);
+  const int rows = a.offsets ? 256 : tile_rows(a, a.w3 && !a.K1);
+  if (a.w3 && !a.K1) return a.R >= 128 * busy && fill && a.N > 128 ? launch_gmm_tc(a, 2, rows, s) : launch_gmm_tc(a, 1, 128, s);
+  return a.R >= 96 * busy && fill && a.N > 128 ? launch_gmm_tc(a, 2, rows, s) : launch_gmm_tc(a, 1, 128, s);
 }
 
 }  // namespace sffn

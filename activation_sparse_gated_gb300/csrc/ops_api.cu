@@ -418,7 +418,8 @@ int sffn_gated_up(const void* x, long long ldx, const void* W1, const void* W3, 
   if (rc != SFFN_OK) return rc;
   if (ldh < H) return fail(SFFN_ERR_ARG, "%s: h's row pitch %lld is below H=%d", fn, ldh, H);
   if (!z != !u) return fail(SFFN_ERR_ARG, "%s: z and u go together", fn);
-  if (z && ldz < H) return fail(SFFN_ERR_ARG, "%s: z's and u's row pitch %lld is below H=%d", fn, ldz, H);
+  if (z && (ldz < H || ldz > SFFN_MAX_ROWS))
+    return fail(SFFN_ERR_ARG, "%s: z's and u's row pitch %lld is outside H=%d..%d", fn, ldz, H, SFFN_MAX_ROWS);
   if (T == 0) return SFFN_OK;
   if (!h) return fail(SFFN_ERR_ARG, "%s: null pointer", fn);
   if (misaligned(h, 2) || misaligned(z, 4) || misaligned(u, 4))

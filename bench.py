@@ -872,13 +872,15 @@ PROFILE_CASES = {
 }
 
 
-# the mixture-of-experts and 8-bit operators (no handle): --batch is their tokens or rows
-OPERATOR_CASES = ("op-experts", "op-grouped", "op-int8", "op-quantize", "op-route")
+# the operators without a handle: --batch is their tokens or rows
+OPERATOR_CASES = ("op-codes4", "op-experts", "op-gated", "op-gated4", "op-grouped", "op-int4", "op-int8", "op-quantize", "op-route",
+                  "op-train")
 
 
 def run_operator_case(args):
     """`--calls` calls of one operator on inputs of about a layer's size for a profiler capture: 16 experts of D = 2560,
-    H = 1024 with 4 choices a token, an int8 product 7168 x 2560, token codes of 14336 values, a router over 256."""
+    H = 1024 with 4 choices a token, an int8 or int4 product 7168 x 2560, token codes of 14336 values, a router over 256;
+    the gated block of D = 2560, H = 7168 from bf16 or 4-bit weights, its training step, and its weights' 4-bit codes."""
     import torch
     import activation_sparse_gated_gb300 as sffn
     g = torch.Generator(device="cuda").manual_seed(5)
@@ -893,6 +895,19 @@ def run_operator_case(args):
     elif args.profile_case == "op-int8":
         (wq, sw), (xq, sx) = (sffn.quantize_tokens(randn(n, D).to(torch.bfloat16)) for n in (7168, T))
         call = lambda: sffn.matmul_int8(xq, sx, wq, sw)  # noqa: E731
+    elif args.profile_case in ("op-codes4", "op-gated", "op-gated4", "op-int4", "op-train"):
+        W1, W3 = ((randn(7168, D) * D ** -0.5).to(torch.bfloat16) for _ in range(2))
+        x = randn(T, D).to(torch.bfloat16)
+        x[:, -1], W1[:, -1] = 1, -1.28125
+        q1, q3, dh = sffn.quantize_int4(W1), sffn.quantize_int4(W3), randn(T, 7168).to(torch.bfloat16)
+
+        def train():
+            _, z, u = sffn.gated_up_saved(x, W1, W3)
+            return sffn.gated_up_backward(dh, z, u, x, W1, W3)
+
+        call = {"op-codes4": lambda: sffn.dequantize_int4(*sffn.quantize_int4(W3)), "op-gated": lambda: sffn.gated_up(x, W1, W3),
+                "op-gated4": lambda: sffn.gated_up_int4(x, *q1, *q3), "op-int4": lambda: sffn.matmul_int4(x, *q3),
+                "op-train": train}[args.profile_case]
     elif args.profile_case == "op-grouped":
         x, w = randn(T, D).to(torch.bfloat16), randn(E, H, D).to(torch.bfloat16)
         offsets = torch.tensor([T * i // E for i in range(E + 1)], dtype=torch.int32, device="cuda")

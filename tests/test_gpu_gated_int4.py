@@ -339,6 +339,22 @@ def test_backward_against_the_formula(T, D, H, act):
         close(y, ref, bound)
 
 
+@pytest.mark.parametrize("T,D,H,act", [(4100, 1288, 2601, "rsp"), (4096, 1280, 2600, "silu"), (20000, 136, 5000, "relu")])
+def test_training_step_of_pair_tiles(T, D, H, act):
+    """Long enough that every product of the step goes to tiles of a pair of blocks; ragged rows, columns and units."""
+    g = gen(T + H)
+    x, W1, W3, dh = randn(g, T, D), randn(g, H, D) * D ** -0.5, randn(g, H, D) * D ** -0.5, randn(g, T, H)
+    h, z, u = sffn.gated_up_saved(x, W1, W3, act=act)
+    ref = [x.double() @ w.double().T for w in (W1, W3)]
+    off = [(D + 8) * 2.0 ** -23 * (x.double().abs() @ w.double().abs().T) for w in (W1, W3)]
+    check_h(h, *ref, *off, act)
+    close(z, ref[0], off[0])
+    close(u, ref[1], off[1])
+    got = sffn.gated_up_backward(dh, z, u, x, W1, W3, act=act)
+    for y, (want, bound) in zip(got, grads(dh, z, u, x, W1, W3, act)):
+        close(y, want, bound)
+
+
 @pytest.mark.parametrize("act", ACTS)
 def test_backward_against_differences(act):
     """The loss sum(dh h) along a direction, by differences in 64 bits, against the gradients' product with it."""
