@@ -10,6 +10,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 #include "ops.h"
@@ -287,12 +288,13 @@ __global__ void __launch_bounds__(32 * I4_WARPS) dequantize_int4_kernel(const Va
 // inside a chunk is the MMA's to choose, as long as both operands agree.  Step i of a chunk takes columns (i, i + 4) and
 // (i + 8, i + 12) of each lane's sixteen, which are nibbles i and i + 4 of its two words.
 //
-// Up to eight tokens (int4_rows_kernel): a block takes 16 rows of w (of both matrices, GATED), its warps take pairs of
-// chunks in turn, and their sums meet in shared memory and are added in the warps' order.  Measured (us in a graph, one
-// token): 7168 x 2560 4.8 (2.2 TB/s; 2.1 of it a launch), 14336 x 4096 12.1 (2.7 TB/s); gated, two 7168 x 2560 10.3.  What
-// bounds it is instructions: 116 a chunk of 16 rows, 44 of them the codes, at 53 % of the issue slots.  Not faster: scales
-// lane by lane (4.9), eight bytes of codes a lane, one pair of chunks at a time (5.6), a warp's codes and x through a TMA
-// ring (6.6).
+// Up to eight tokens (int4_rows_kernel; up to sixteen with two tiles of tokens, NT): a block takes 16 rows of w (of both
+// matrices, GATED), its W warps take pairs of chunks in turn, and their sums meet in shared memory and are added in the warps'
+// order.  Measured (us in a graph, one token): 7168 x 2560 4.9 (2.1 TB/s; 2.1 of it a launch), 14336 x 4096 11.0 (3.0 TB/s),
+// 2560 x 7168 5.7; gated, two 7168 x 2560 7.9.  What bounds it is instructions and their latency: some 70 a chunk of 16 rows, 44
+// of them the codes.  Loads that no condition guards (a token past T reads the last one's x, missing columns are the last
+// pair's alone) took a third of them out (gated 10.3 -> 7.9).  Not faster: sixteen bytes of codes a lane and halves traded
+// between lanes, one pair at a time, a warp's codes and x through a TMA ring (7168 x 2560 6.6).
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm(
@@ -333,17 +335,14 @@ __device__ __forceinline__ float gated(int act, float z, float u) {
   return gate != 0.f ? gate * u : 0.f;
 }
 
-template <bool GATED>
-__global__ void __launch_bounds__(32 * I4_WARPS) int4_rows_kernel(const RowsArgs a) {
+template <bool GATED, int NT, int W>
+__global__ void __launch_bounds__(32 * W) int4_rows_kernel(const RowsArgs a) {
   constexpr int M = GATED ? 2 : 1, P = 16 * M + 4;  // matrices; pitch of a token's sums (no bank conflict)
-  constexpr int U = 2;                              // pairs of chunks at a time: a lane of four holds a scale of each chunk
-  __shared__ float s_sum[I4_WARPS * 8 * P];
+  __shared__ float s_sum[W * 8 * NT * P];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int n0 = blockIdx.x * 16, t0 = blockIdx.y * 8;
+  const int n0 = blockIdx.x * 16, t0 = blockIdx.y * 8 * NT;
   pdl_launch_dependents();
   pdl_wait();
-  const int nc = (a.K + 127) / 128;  // pairs of chunks; the warps take them in turn, so that they read rows together
-  const bool wide = a.K % 32 == 0;  // rows of codes are 16-byte aligned
   const uint8_t* wr[M][2];
   const float* sr[M][2];
 #pragma unroll
@@ -351,48 +350,41 @@ __global__ void __launch_bounds__(32 * I4_WARPS) int4_rows_kernel(const RowsArgs
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r = min(n0 + 8 * h + g, a.N - 1);
-      wr[m][h] = a.w[m] + (size_t)r * (a.K / 2) + 16 * t;
+      wr[m][h] = a.w[m] + (size_t)r * (a.K / 2) + warp * 64 + 8 * t;
       sr[m][h] = a.s[m] + (size_t)r * a.G;
     }
-  const bool low = t < 2;
-  const int col = 32 * (t & 1) + 16 * (t >> 1);  // of the lane's sixteen columns in either chunk
-  const bool token = t0 + g < a.T;
-  const uint16_t* xr = a.x + (long long)min(t0 + g, a.T - 1) * a.ldx + col;
-  float acc[M][4] = {};
-  for (int c = warp; c < nc; c += U * I4_WARPS) {
-    uint4 w[U][M][2];
+  // tokens past T are computed on the last one and not stored
+  const uint16_t* xr[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) xr[j] = a.x + (long long)min(t0 + 8 * j + g, a.T - 1) * a.ldx + warp * 128 + 16 * t;
+  float acc[M][NT][4] = {};
+  // U pairs of 64-column chunks, W pairs apart, from pair c on.  CUT: the last pair, of which columns may be missing.
+  auto step = [&](auto pairs, auto cut, int c) {
+    constexpr int U = decltype(pairs)::value;
+    constexpr bool CUT = decltype(cut)::value;
+    uint2 w[U][2][M][2];
     float s[M][2];
-    uint4 x[U][2][2];
+    uint4 x[U][2][NT][2];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int cu = c + u * I4_WARPS, k = cu * 128 + 32 * t;
-#pragma unroll
-      for (int m = 0; m < M; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          w[u][m][h] = make_uint4(0, 0, 0, 0);
-          const uint8_t* p = wr[m][h] + cu * 64;
-          if (cu < nc && k < a.K) {
-            if (wide) {
-              w[u][m][h] = __ldg(reinterpret_cast<const uint4*>(p));
-            } else {
-              const uint2 v0 = __ldg(reinterpret_cast<const uint2*>(p));
-              const uint2 v1 = k + 16 < a.K ? __ldg(reinterpret_cast<const uint2*>(p) + 1) : make_uint2(0, 0);
-              w[u][m][h] = make_uint4(v0.x, v0.y, v1.x, v1.y);
-            }
-          }
-        }
+    for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const bool on = token && cu < nc && cu * 128 + 64 * q + col < a.K;
-        const uint4* p = reinterpret_cast<const uint4*>(xr + cu * 128 + 64 * q);
-        x[u][q][0] = on ? __ldg(p) : make_uint4(0, 0, 0, 0);
-        x[u][q][1] = on ? __ldg(p + 1) : make_uint4(0, 0, 0, 0);
+        const bool in = !CUT || c * 128 + 64 * q + 16 * t < a.K;
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            w[u][q][m][h] = in ? __ldg(reinterpret_cast<const uint2*>(wr[m][h] + u * (64 * W) + 32 * q)) : make_uint2(0, 0);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const uint4* p = reinterpret_cast<const uint4*>(xr[j] + u * (128 * W) + 64 * q);
+          x[u][q][j][0] = in ? __ldg(p) : make_uint4(0, 0, 0, 0);
+          x[u][q][j][1] = in ? __ldg(p + 1) : make_uint4(0, 0, 0, 0);
+        }
       }
-    }
-    {  // lane t's scale is that of the t-th of the four chunks
-      const int ch = 2 * (c + (t >> 1) * I4_WARPS) + (t & 1);
-      const bool in = ch * 64 < a.K;
+    {  // lane t of four holds the scale of the t-th of the 2 U chunks
+      const int ch = 2 * (c + (U == 2 ? (t >> 1) * W : 0)) + (t & 1);
+      const bool in = !CUT || ch * 64 < a.K;
       const int gi = group_of(in ? ch : 0, a.magic);
 #pragma unroll
       for (int m = 0; m < M; ++m)
@@ -400,58 +392,74 @@ __global__ void __launch_bounds__(32 * I4_WARPS) int4_rows_kernel(const RowsArgs
         for (int h = 0; h < 2; ++h) s[m][h] = in ? __ldg(sr[m][h] + gi) : 0.f;
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (c + u * I4_WARPS >= nc) break;
+    for (int m = 0; m < M; ++m)
 #pragma unroll
-      for (int m = 0; m < M; ++m) {
-        // lanes t and t + 2 hold 32 columns of the first and of the second chunk: they trade halves, and both hold 16 of each
-        uint2 v[2][2];
+      for (int h = 0; h < 2; ++h) wr[m][h] += U * 64 * W;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 r = w[u][m][h];
-          const uint32_t gx = __shfl_xor_sync(0xffffffffu, low ? r.z : r.x, 2), gy = __shfl_xor_sync(0xffffffffu, low ? r.w : r.y, 2);
-          v[0][h] = low ? make_uint2(r.x, r.y) : make_uint2(gx, gy);
-          v[1][h] = low ? make_uint2(gx, gy) : make_uint2(r.z, r.w);
+    for (int j = 0; j < NT; ++j) xr[j] += U * 128 * W;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        float sum[M][NT][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t sel = i & 1 ? 0x7632 : 0x5410;
+          uint32_t b[NT][2];
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            const uint4 lo = x[u][q][j][0], hi = x[u][q][j][1];
+            b[j][0] = i < 2 ? __byte_perm(lo.x, lo.z, sel) : __byte_perm(lo.y, lo.w, sel);
+            b[j][1] = i < 2 ? __byte_perm(hi.x, hi.z, sel) : __byte_perm(hi.y, hi.w, sel);
+          }
+#pragma unroll
+          for (int m = 0; m < M; ++m) {
+            const uint2 (&v)[2] = w[u][q][m];
+            const uint32_t f[4] = {pair4(v[0].x, i), pair4(v[1].x, i), pair4(v[0].y, i), pair4(v[1].y, i)};
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              if (i == 0)
+                mma16816_first(sum[m][j], f, b[j][0], b[j][1]);
+              else
+                mma16816(sum[m][j], f, b[j][0], b[j][1]);
+            }
+          }
         }
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          float sum[4];
-          const uint4 lo = x[u][q][0], hi = x[u][q][1];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t f[4] = {pair4(v[q][0].x, i), pair4(v[q][1].x, i), pair4(v[q][0].y, i), pair4(v[q][1].y, i)};
-            const uint32_t sel = i & 1 ? 0x7632 : 0x5410;
-            const uint32_t b0 = i < 2 ? __byte_perm(lo.x, lo.z, sel) : __byte_perm(lo.y, lo.w, sel);
-            const uint32_t b1 = i < 2 ? __byte_perm(hi.x, hi.z, sel) : __byte_perm(hi.y, hi.w, sel);
-            if (i == 0)
-              mma16816_first(sum, f, b0, b1);
-            else
-              mma16816(sum, f, b0, b1);
-          }
+        for (int m = 0; m < M; ++m)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float sc = __shfl_sync(0xffffffffu, s[m][h], 2 * u + q, 4);
-            acc[m][2 * h] = fmaf(sc, sum[2 * h], acc[m][2 * h]);
-            acc[m][2 * h + 1] = fmaf(sc, sum[2 * h + 1], acc[m][2 * h + 1]);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              acc[m][j][2 * h] = fmaf(sc, sum[m][j][2 * h], acc[m][j][2 * h]);
+              acc[m][j][2 * h + 1] = fmaf(sc, sum[m][j][2 * h + 1], acc[m][j][2 * h + 1]);
+            }
           }
-        }
       }
-    }
-  }
-  float* mine = s_sum + warp * (8 * P);
+  };
+  const int whole = a.K / 128;  // pairs without a missing column; the warps take them in turn, so that they read rows together
+  int c = warp;
+  if constexpr (NT * M <= 2)
+    for (; c + W < whole; c += 2 * W) step(std::integral_constant<int, 2>(), std::false_type(), c);
+  for (; c < whole; c += W) step(std::integral_constant<int, 1>(), std::false_type(), c);
+  if (c == whole && a.K % 128 != 0) step(std::integral_constant<int, 1>(), std::true_type(), c);
+  float* mine = s_sum + warp * (8 * NT * P);
 #pragma unroll
   for (int m = 0; m < M; ++m)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) mine[(2 * t + (q & 1)) * P + 16 * m + g + 8 * (q >> 1)] = acc[m][q];
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) mine[(8 * j + 2 * t + (q & 1)) * P + 16 * m + g + 8 * (q >> 1)] = acc[m][j][q];
   __syncthreads();
-  for (int i = threadIdx.x; i < 8 * 16; i += 32 * I4_WARPS) {
-    const int tok = i / (16), r = i % (16);
+  for (int i = threadIdx.x; i < 8 * NT * 16; i += 32 * W) {
+    const int tok = i / 16, r = i % 16;
     if (t0 + tok >= a.T || n0 + r >= a.N) continue;
     float v = 0.f, up = 0.f;
 #pragma unroll
-    for (int q = 0; q < I4_WARPS; ++q) {  // in the warps' order
-      v += s_sum[q * (8 * P) + tok * P + r];
-      if (GATED) up += s_sum[q * (8 * P) + tok * P + 16 + r];
+    for (int q = 0; q < W; ++q) {  // in the warps' order
+      v += s_sum[q * (8 * NT * P) + tok * P + r];
+      if (GATED) up += s_sum[q * (8 * NT * P) + tok * P + 16 + r];
     }
     if (GATED) v = gated(a.act, v, up);
     const size_t at = (size_t)(t0 + tok) * a.ldy + n0 + r;
@@ -462,10 +470,14 @@ __global__ void __launch_bounds__(32 * I4_WARPS) int4_rows_kernel(const RowsArgs
   }
 }
 
-template <bool GATED>
+template <bool GATED, int NT>
 cudaError_t rows_go(const RowsArgs& r, cudaStream_t s) {
-  const dim3 grid((unsigned)((r.N + 15) / 16), (unsigned)((r.T + 7) / 8));
-  return ops_launch(int4_rows_kernel<GATED>, grid, 32 * I4_WARPS, 0, s, 1, r);
+  const dim3 grid((unsigned)((r.N + 15) / 16), (unsigned)((r.T + 8 * NT - 1) / (8 * NT)));
+  // sixteen warps a block where all blocks run at once even so (us, eight / sixteen, one token: 2560 x 7168 7.1 / 5.7, 4096 x
+  // 14336 16.5 / 12.6, 7168 x 2560 4.9 / 5.4; gated 1000 x 4096 5.0 / 4.5, 3000 x 2560 5.6 / 5.9)
+  if ((long long)grid.x * grid.y <= (GATED ? 1 : 2) * ops_num_sms())
+    return ops_launch(int4_rows_kernel<GATED, NT, 16>, grid, 32 * 16, 0, s, 1, r);
+  return ops_launch(int4_rows_kernel<GATED, NT, 8>, grid, 32 * 8, 0, s, 1, r);
 }
 
 constexpr int I4_STAGES = 3;
@@ -499,7 +511,7 @@ cudaError_t allow_smem(K kernel, size_t bytes, std::once_flag (&once)[64], cudaE
 // tiles; both matrices, GATED), keeps its share of x in shared memory for all of them, already in the order of the MMA's
 // operands, and lets every warp walk K over its own 16 rows.  A warp's codes come by TMA, boxes of 16 rows by 128 columns
 // (64 bytes), into a ring of its own.  K is cut over the blocks of a cluster, whose sums are added through distributed shared
-// memory in the blocks' order.  Measured (us in a graph): 13 tokens, 2560 x 7168 8.7; 16, 7168 x 2560 7.7; 24, 14336 x 4096
+// memory in the blocks' order.  Measured (us in a graph): 13 tokens, 2560 x 7168 8.7; 32, 7168 x 2560 9.3; 24, 14336 x 4096
 // 19.2; gated, two 14336 x 4096, 24 tokens 35.5 (each warp with x of its own from L2: 52).
 constexpr int x_chunks(int NT) { return NT == 2 ? 16 : NT == 3 ? 14 : 12; }  // of x that shared memory holds at a time
 constexpr size_t tile_smem(int NT, int M) {
@@ -777,13 +789,20 @@ cudaError_t launch_matmul_int4(const Int4Args& a, cudaStream_t s) {
   if (codes_themselves(a.T, a.K, split)) {
     const RowsArgs r = {static_cast<const uint16_t*>(a.x), a.ldx, {a.w, a.w3}, {a.sw, a.s3}, a.y, a.ldy, a.T, a.N, a.K,
                         groups(a.K, a.group), a.y_f32, a.act, magic_of(a.K, a.group)};
-    if (a.T <= 8 || a.K % 32 != 0) return gated ? rows_go<true>(r, s) : rows_go<false>(r, s);
-    if (gated) return a.T <= 16 ? tile_go<2, 2, true>(r, s) : a.T <= 24 ? tile_go<3, 2, true>(r, s) : tile_go<4, 2, true>(r, s);
-    // two tiles a block where the cut of K, eight at most, still fills the SMs (13 tokens, one / two tiles: 14336 x 4096 20.2 /
-    // 15.7 us, 7168 x 2560 7.2 / 8.7, 2560 x 7168 8.7 / 11.0)
-    if ((a.N + 255) / 256 < 2 * ops_num_sms() / 8)
+    if (a.T <= 8) return gated ? rows_go<true, 1>(r, s) : rows_go<false, 1>(r, s);
+    // Up to sixteen tokens, and where TMA does not take the rows of codes, the same with two tiles of tokens: faster than the
+    // tiles below but for long sums whose blocks are one to two an SM (us, this / those, 13 tokens: 7168 x 2560 5.4 / 8.0,
+    // 14336 x 4096 14.9 / 15.7, 1000 x 14336 8.6 / 10.1, 2560 x 7168 8.8 / 8.7, 4096 x 14336 21.8 / 15.4; gated 3000 x 2560
+    // 6.3 / 9.2, 14336 x 4096 26.7 / 27.4).
+    const int blocks = (a.N + 15) / 16, sms = ops_num_sms();
+    if (a.K % 32 != 0 || (a.T <= 16 && (gated || a.K <= 4096 || blocks <= sms || blocks > 2 * sms)))
+      return gated ? rows_go<true, 2>(r, s) : rows_go<false, 2>(r, s);
+    if (gated) return a.T <= 24 ? tile_go<3, 2, true>(r, s) : tile_go<4, 2, true>(r, s);
+    // two tiles a block where the cut of K, eight at most, still fills the SMs (us, one / two tiles: 24 tokens, 14336 x 4096
+    // 20.2 / 19.2; 32 tokens, 7168 x 2560 9.3 / 13.0)
+    if ((a.N + 255) / 256 < 2 * sms / 8)
       return a.T <= 16 ? tile_go<2, 1, false>(r, s) : a.T <= 24 ? tile_go<3, 1, false>(r, s) : tile_go<4, 1, false>(r, s);
-    return a.T <= 16 ? tile_go<2, 2, false>(r, s) : a.T <= 24 ? tile_go<3, 2, false>(r, s) : tile_go<4, 2, false>(r, s);
+    return a.T <= 24 ? tile_go<3, 2, false>(r, s) : tile_go<4, 2, false>(r, s);
   }
   // more tokens: the weights as bf16 copies, then the products on the tensor cores
   const size_t row = copy_row(a.K, split), one = round_up(2 * (size_t)a.N * row, 256);
