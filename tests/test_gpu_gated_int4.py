@@ -231,6 +231,57 @@ def test_int4_codes_past_two_gigabytes():
     assert (last[0::2] == 0.5).all() and (last[1::2] == 1.0).all()
 
 
+@pytest.mark.parametrize("T", [3, 12, 40, 300])
+def test_int4_products_captured_twice(T):
+    """Two graphs of the same calls, each with a workspace of its own, replayed in turn on new tokens."""
+    g = gen(10)
+    one, three = weights4(g, 300, 512, 64), weights4(g, 300, 512, 64)
+    x = randn(g, T, 512)
+
+    def step():
+        return sffn.gated_up_int4(x, *one, *three, act="rsp"), sffn.matmul_int4(x, *one), sffn.matmul_int4(x, *three, dtype="f32")
+
+    step()
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(step())
+        graphs.append(graph)
+    for seed in (1, 2):
+        x.copy_(randn(gen(seed), T, 512))
+        want = step()
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for out in outs:
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+@pytest.mark.parametrize("T", [1, 3, 8, 11, 27])
+def test_int4_the_last_token_is_its_own(T):
+    """Idle columns of a tile may hold the last token's values: none of them reach another token."""
+    g = gen(11)
+    codes, scales = weights4(g, 70, 384, 64)
+    x = randn(g, T, 384)
+    clean = sffn.matmul_int4(x, codes, scales, dtype="f32")
+    x[T - 1] = math.nan
+    y = sffn.matmul_int4(x, codes, scales, dtype="f32")
+    assert torch.isnan(y[T - 1]).all() and torch.equal(y[:T - 1], clean[:T - 1])
+
+
+def test_int4_long_sums_and_many_tokens_repeat_their_bits():
+    g = gen(12)
+    for T, N, K in ((13, 4096, 8192), (100, 515, 2560), (1, 160, 65536), (2, 16, 65520)):
+        codes, scales = weights4(g, N, K, 64)
+        x = randn(g, T, K)
+        y = sffn.matmul_int4(x, codes, scales, dtype="f32")
+        w = meant(codes, scales, 64)
+        close(y, x.double() @ w.T, bound4(x, w, T > ROWS, True))
+        assert all(torch.equal(y, sffn.matmul_int4(x, codes, scales, dtype="f32")) for _ in range(3))
+
+
 # ------------------------------------------------------------------ the gated block
 
 
@@ -435,6 +486,20 @@ def test_gated_up_refuses_what_it_cannot_record():
         dual = torch.autograd.forward_ad.make_dual(x.detach(), torch.ones_like(x))
         with pytest.raises(ValueError, match="tangent"):
             sffn.gated_up(dual, W1, W3)
+
+
+def test_gated_up_refuses_rows_on_top_of_one_another():
+    g = gen(37)
+    W1, W3 = randn(g, 8, 64).requires_grad_(), randn(g, 8, 64)
+    x = randn(g, 1, 64).expand(4, 64)
+    with pytest.raises(sffn.SffnError, match="pitch"):
+        sffn.gated_up(x, W1, W3)
+    with pytest.raises(sffn.SffnError, match="pitch"):
+        sffn.gated_up(x, W1.detach(), W3)
+    x = x.contiguous()
+    _, z, u = sffn.gated_up_saved(x, W1.detach(), W3)
+    with pytest.raises(sffn.SffnError, match="pitch"):
+        sffn.gated_up_backward(randn(g, 1, 8).expand(4, 8), z, u, x, W1.detach(), W3)
 
 
 def test_a_differentiable_call_is_not_captured():
