@@ -85,7 +85,6 @@ struct QuantArgs {
   uint8_t* q;
   float* s;
   int N, K, group, G;
-  uint32_t magic;
 };
 
 // Groups of 64, 128 or 256 columns: LPG = group / 8 lanes hold a group, so a shuffle finds its maximum and the weights
@@ -278,8 +277,9 @@ __global__ void __launch_bounds__(32 * I4_WARPS) dequantize_int4_kernel(const Va
 // ------------------------------------------------------------------ products of few tokens
 //
 // With few tokens the product is a read of the codes, so what counts is bytes in flight and few instructions a code.
-// The multiply-adds go to mma.sync, which takes sixteen rows of w and eight tokens: sixteen weights a lane-instruction
-// where the CUDA cores take one, and its idle columns cost nothing that the memory would not wait for.  A code becomes
+// The multiply-adds go to mma.sync, which takes sixteen rows of w and eight tokens: an instruction for eight weights a lane
+// and all the tokens, where the CUDA cores take one or two weights and one token; columns without a token cost nothing that
+// the codes would not wait for.  A code becomes
 // an exact bf16 in two instructions a pair (the nibble's two's complement plus 8 is u, the bf16 with bits 0x4300 | u is
 // 128 + u, and 128 + u - 136 is the code), the sums of a 64-column chunk are exact products in fp32, and the scale
 // multiplies the chunk's sum: nothing is rounded before the result.
@@ -756,7 +756,7 @@ uint32_t magic_of(int K, int group) { return group_magic(group > 0 && group < K 
 cudaError_t launch_quantize_int4(const void* w, long long ldw, uint8_t* q, float* sc, int N, int K, int group,
                                  cudaStream_t s) {
   QuantArgs a = {static_cast<const uint16_t*>(w), ldw, q, sc, N, K, group > 0 && group < K ? group : K,
-                 groups(K, group), 0};
+                 groups(K, group)};
   if (a.group == 64 || a.group == 128 || a.group == 256) {
     const dim3 grid((unsigned)((N + I4_WARPS - 1) / I4_WARPS), (unsigned)((K + I4_UNIT - 1) / I4_UNIT));
     auto kernel = a.group == 64 ? quantize_int4_kernel<8> : a.group == 128 ? quantize_int4_kernel<16> : quantize_int4_kernel<32>;

@@ -124,6 +124,23 @@ def test_every_bf16_value_beside_every_scale_gets_its_code():
         assert torch.equal(unpack(codes).cpu(), plain_codes(w, 64)[0])
 
 
+def test_every_significand_beside_every_maximum_gets_its_code():
+    """The quotient's roundings depend on the two significands and the distance of the exponents: all of them down to 2^-9."""
+    v = torch.arange(128, 256, device=DEV).float()
+    v = torch.cat([v * 2.0 ** -e for e in range(10)])  # 1280 values below the largest maximum's binade's end
+    v = torch.cat((v, torch.zeros(-len(v) % 63, device=DEV))).view(-1, 63)
+    rows = []
+    for m in range(128, 256):
+        top = torch.full((len(v), 1), float(m), device=DEV)
+        rows.append(torch.cat((torch.where(v <= m, v, torch.zeros_like(v)), top), 1))
+    w = torch.cat(rows) * 2.0 ** -11
+    w = torch.cat((w, -w)).to(BF)
+    codes, scales = sffn.quantize_int4(w, 64)
+    q, s = plain_codes(w, 64)
+    same(scales.cpu(), s)
+    assert torch.equal(unpack(codes).cpu(), q)
+
+
 def test_codes_of_strided_rows_and_none():
     w = randn(gen(4), 40, 400)
     a, b = sffn.quantize_int4(w[:, 8:328]), sffn.quantize_int4(w[:, 8:328].contiguous())
