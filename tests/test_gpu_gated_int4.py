@@ -78,7 +78,7 @@ def same(a, b):
 
 @pytest.mark.parametrize("N,K", [(1, 16), (3, 64), (5, 80), (7, 1008), (16, 1024), (9, 1040), (33, 2560), (2, 16384), (2, 20000),
                                  (1, 65536)])
-@pytest.mark.parametrize("group", [64, 128, 192, 256, 512, None, 65536])
+@pytest.mark.parametrize("group", [64, 128, 192, 256, 512, 1024, 2048, 2112, None, 65536])
 def test_codes_and_values(N, K, group):
     w = randn(gen(N + K), N, K)
     w[N // 2, : min(K, 64)] = 0
