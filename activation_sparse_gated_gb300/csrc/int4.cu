@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(32 * I4_WARPS) dequantize_int4_kernel(const Va
 // Up to eight tokens (int4_rows_kernel; up to sixteen with two tiles of tokens, NT): a block takes 16 rows of w (of both
 // matrices, GATED), its W warps take pairs of chunks in turn, and their sums meet in shared memory and are added in the warps'
 // order.  Measured (us in a graph, one token): 7168 x 2560 4.9 (2.1 TB/s; 2.1 of it a launch), 14336 x 4096 11.0 (3.0 TB/s),
-// 2560 x 7168 5.7; gated, two 7168 x 2560 7.9.  What bounds it is instructions and their latency: some 70 a chunk of 16 rows, 44
+// 2560 x 7168 5.7, 13 tokens 8.0; gated, two 7168 x 2560 7.9.  What bounds it is instructions and their latency: some 70 a chunk of 16 rows, 44
 // of them the codes.  Loads that no condition guards (a token past T reads the last one's x, missing columns are the last
 // pair's alone) took a third of them out (gated 10.3 -> 7.9).  Not faster: sixteen bytes of codes a lane and halves traded
 // between lanes, one pair at a time, a warp's codes and x through a TMA ring (7168 x 2560 6.6).
@@ -481,10 +481,12 @@ __global__ void __launch_bounds__(32 * W) int4_rows_kernel(const RowsArgs a) {
 template <bool GATED, int NT>
 cudaError_t rows_go(const RowsArgs& r, cudaStream_t s) {
   const dim3 grid((unsigned)((r.N + 15) / 16), (unsigned)((r.T + 8 * NT - 1) / (8 * NT)));
-  // sixteen warps a block where all blocks run at once even so (us, eight / sixteen, one token: 2560 x 7168 7.1 / 5.7, 4096 x
-  // 14336 16.5 / 12.6, 7168 x 2560 4.9 / 5.4; gated 1000 x 4096 5.0 / 4.5, 3000 x 2560 5.6 / 5.9)
-  if ((long long)grid.x * grid.y <= (GATED ? 1 : 2) * ops_num_sms())
-    return ops_launch(int4_rows_kernel<GATED, NT, 16>, grid, 32 * 16, 0, s, 1, r);
+  // More warps a block, as many as leave room for two blocks an SM, where that is all blocks at once (us, eight warps / as
+  // here: one token, 2560 x 7168 7.0 / 5.7, 4096 x 4096 5.7 / 4.1, gated 3000 x 2560 5.7 / 4.6; 13 tokens, 2560 x 7168 9.7 / 8.0, 3000
+  // x 2560 4.7 / 3.9; and else: one token, 7168 x 2560 4.9 / 5.6, gated 7.8 / 9.8).  Two tiles of tokens and two matrices have no room.
+  constexpr int many = GATED && NT > 1 ? 8 : GATED || NT > 1 ? 12 : 16;
+  if ((long long)grid.x * grid.y <= 2 * ops_num_sms())
+    return ops_launch(int4_rows_kernel<GATED, NT, many>, grid, 32 * many, 0, s, 1, r);
   return ops_launch(int4_rows_kernel<GATED, NT, 8>, grid, 32 * 8, 0, s, 1, r);
 }
 
@@ -515,13 +517,13 @@ cudaError_t allow_smem(K kernel, size_t bytes, std::once_flag (&once)[64], cudaE
   return attr[dev];
 }
 
-// More than eight tokens (int4_tile_kernel, K a multiple of 32): x is what repeats, so a block takes 128 rows of w a tile (M
+// More than sixteen tokens (int4_tile_kernel, K a multiple of 32): x is what repeats, so a block takes 128 rows of w a tile (M
 // tiles; both matrices, GATED), keeps its share of x in shared memory for all of them, already in the order of the MMA's
 // operands, and lets every warp walk K over its own 16 rows.  A warp's codes come by TMA, boxes of 16 rows by 128 columns
 // (64 bytes), into a ring of its own.  K is cut over the blocks of a cluster, whose sums are added through distributed shared
-// memory in the blocks' order.  Measured (us in a graph): 13 tokens, 2560 x 7168 8.7; 32, 7168 x 2560 9.3; 24, 14336 x 4096
+// memory in the blocks' order.  Measured (us in a graph): 32 tokens, 7168 x 2560 9.3, 2560 x 7168 12.6; 24, 14336 x 4096
 // 19.2; gated, two 14336 x 4096, 24 tokens 35.5 (each warp with x of its own from L2: 52).
-constexpr int x_chunks(int NT) { return NT == 2 ? 16 : NT == 3 ? 14 : 12; }  // of x that shared memory holds at a time
+constexpr int x_chunks(int NT) { return NT == 3 ? 14 : 12; }  // of x that shared memory holds at a time
 constexpr size_t tile_smem(int NT, int M) {
   return 1024 + std::max<size_t>(I4_WARPS * I4_STAGES * M * I4_BOX + x_chunks(NT) * NT * 1024, sizeof(float) * 8 * NT * (16 * I4_WARPS * M + 4));
 }
@@ -800,18 +802,14 @@ cudaError_t launch_matmul_int4(const Int4Args& a, cudaStream_t s) {
     const RowsArgs r = {static_cast<const uint16_t*>(a.x), a.ldx, {a.w, a.w3}, {a.sw, a.s3}, a.y, a.ldy, a.T, a.N, a.K,
                         groups(a.K, a.group), a.y_f32, a.act, magic_of(a.K, a.group)};
     if (a.T <= 8) return gated ? rows_go<true, 1>(r, s) : rows_go<false, 1>(r, s);
-    // Up to sixteen tokens, and where TMA does not take the rows of codes, the same with two tiles of tokens: faster than the
-    // tiles below but for long sums whose blocks are one to two an SM (us, this / those, 13 tokens: 7168 x 2560 5.4 / 8.0,
-    // 14336 x 4096 14.9 / 15.7, 1000 x 14336 8.6 / 10.1, 2560 x 7168 8.8 / 8.7, 4096 x 14336 21.8 / 15.4; gated 3000 x 2560
-    // 6.3 / 9.2, 14336 x 4096 26.7 / 27.4).
-    const int blocks = (a.N + 15) / 16, sms = ops_num_sms();
-    if (a.K % 32 != 0 || (a.T <= 16 && (gated || a.K <= 4096 || blocks <= sms || blocks > 2 * sms)))
-      return gated ? rows_go<true, 2>(r, s) : rows_go<false, 2>(r, s);
+    // Up to sixteen tokens, and where TMA does not take the rows of codes, the same with two tiles of tokens (us, this / the tiles
+    // below, 13 tokens: 7168 x 2560 5.4 / 8.0, 14336 x 4096 14.9 / 15.7, 2560 x 7168 8.0 / 8.7, 4096 x 14336 16.7 / 15.4; gated
+    // 3000 x 2560 6.4 / 9.2, 14336 x 4096 26.7 / 27.4).
+    if (a.T <= 16 || a.K % 32 != 0) return gated ? rows_go<true, 2>(r, s) : rows_go<false, 2>(r, s);
     if (gated) return a.T <= 24 ? tile_go<3, 2, true>(r, s) : tile_go<4, 2, true>(r, s);
     // two tiles a block where the cut of K, eight at most, still fills the SMs (us, one / two tiles: 24 tokens, 14336 x 4096
     // 20.2 / 19.2; 32 tokens, 7168 x 2560 9.3 / 13.0)
-    if ((a.N + 255) / 256 < 2 * sms / 8)
-      return a.T <= 16 ? tile_go<2, 1, false>(r, s) : a.T <= 24 ? tile_go<3, 1, false>(r, s) : tile_go<4, 1, false>(r, s);
+    if ((a.N + 255) / 256 < 2 * ops_num_sms() / 8) return a.T <= 24 ? tile_go<3, 1, false>(r, s) : tile_go<4, 1, false>(r, s);
     return a.T <= 24 ? tile_go<3, 2, false>(r, s) : tile_go<4, 2, false>(r, s);
   }
   // more tokens: the weights as bf16 copies, then the products on the tensor cores
