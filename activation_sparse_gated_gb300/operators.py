@@ -361,7 +361,7 @@ def quantize_int4(w, group=64, stream=None):
     """(codes uint8 [N, K / 2], scales fp32 [N, G]) of bf16 weights w [N, K]: two 4-bit codes a byte, a scale for each
     ``group`` columns of a row (a multiple of 64), or for a whole row (None)."""
     if stream is None and _calls is not None:
-        r = _calls.quantize_int4(w, 0 if group is None else group)
+        r = _calls.quantize_int4(w, 0 if group is None else group or -1)
         if r is not None:
             return r
     if stream is not None:
@@ -381,7 +381,7 @@ def quantize_int4(w, group=64, stream=None):
 def dequantize_int4(codes, scales, group=64, dtype="bf16", out=None, stream=None):
     """The matrix [N, K] of ``dtype`` (or ``out``'s) that ``quantize_int4``'s codes and scales stand for."""
     if stream is None and out is None and _calls is not None and dtype in _OUT:
-        y = _calls.dequantize_int4(codes, scales, 0 if group is None else group, _OUT[dtype][1] == SFFN_F32)
+        y = _calls.dequantize_int4(codes, scales, 0 if group is None else group or -1, _OUT[dtype][1] == SFFN_F32)
         if y is not None:
             return y
     if stream is not None:
@@ -399,7 +399,7 @@ def matmul_int4(x, wq, sw, group=64, dtype="bf16", out=None, stream=None):
     """y[t, n] = sum_k x[t, k] w[n, k] of bf16 tokens x [T, K] and the weights that ``quantize_int4``'s codes wq
     [N, K / 2] and scales sw stand for; y of ``dtype`` (or ``out``'s)."""
     if stream is None and out is None and _calls is not None and dtype in _OUT:
-        y = _calls.matmul_int4(x, wq, sw, 0 if group is None else group, _OUT[dtype][1] == SFFN_F32)
+        y = _calls.matmul_int4(x, wq, sw, 0 if group is None else group or -1, _OUT[dtype][1] == SFFN_F32)
         if y is not None:
             return y
     if stream is not None:
@@ -431,7 +431,7 @@ def gated_up_int4(x, w1q, s1, w3q, s3, group=64, act: str = "relu", out=None, st
     """h = A(x W1^T) * (x W3^T), bf16 [T, H], of bf16 tokens x [T, D] and 4-bit weights W1, W3 [H, D] (codes and scales as
     for :func:`matmul_int4`)."""
     if stream is None and out is None and _calls is not None and act in _ACT:
-        y = _calls.gated_up_int4(x, w1q, s1, w3q, s3, 0 if group is None else group, _ACT[act])
+        y = _calls.gated_up_int4(x, w1q, s1, w3q, s3, 0 if group is None else group or -1, _ACT[act])
         if y is not None:
             return y
     if stream is not None:

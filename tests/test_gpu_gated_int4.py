@@ -485,6 +485,16 @@ def test_autograd_of_a_used_twice_leaf_and_a_view():
     assert torch.equal(V.grad, a + b)
 
 
+def test_int4_groups_that_no_scale_has_are_refused():
+    x, w = randn(gen(41), 4, 128), randn(gen(42), 8, 128)
+    q, s = sffn.quantize_int4(w, None)
+    for group in (0, False, -64, 32, 96, 64.0, "64"):
+        for call in (lambda: sffn.quantize_int4(w, group), lambda: sffn.dequantize_int4(q, s, group),
+                     lambda: sffn.matmul_int4(x, q, s, group), lambda: sffn.gated_up_int4(x, q, s, q, s, group)):
+            with pytest.raises(ValueError, match="group"):
+                call()
+
+
 def test_gated_up_refuses_what_it_cannot_record():
     g = gen(24)
     x, W1, W3 = randn(g, 4, 64).requires_grad_(), randn(g, 8, 64), randn(g, 8, 64)
