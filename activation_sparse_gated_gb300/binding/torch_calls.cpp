@@ -448,15 +448,26 @@ struct GatedUp : torch::autograd::Function<GatedUp> {
     TORCH_CHECK(c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None,
                 "the backward pass of gated_up is not captured: gated_up_backward is");
     const auto saved = ctx->get_saved_variables();
-    const Tensor &x = saved[0], &W1 = saved[1], &W3 = saved[2];
-    const int64_t T = x.size(0), D = x.size(1), H = W1.size(0);
-    Tensor dh = grads[0].defined() ? grads[0] : at::zeros({T, H}, x.options());
+    Tensor x = saved[0], W1 = saved[1], W3 = saved[2], zu = saved[3];
+    for (Tensor* t : {&x, &W1, &W3, &zu}) {  // hooks on saved tensors keep their values, but not their layout
+      const bool right = t->is_cuda() && t->get_device() == x.get_device() &&
+                         t->scalar_type() == (t == &zu ? at::kFloat : at::kBFloat16) && t->dim() == (t == &zu ? 3 : 2);
+      TORCH_CHECK(right, "a saved tensor of gated_up came back with another type, rank or device");
+      if (t != &x) *t = t->contiguous();
+    }
     int64_t ld = 0, lddh = 0;
+    if (!pitch(x, &ld)) {
+      x = x.contiguous();
+      ld = x.size(1);
+    }
+    const int64_t T = x.size(0), D = x.size(1), H = W1.size(0);
+    TORCH_CHECK(W1.size(1) == D && W3.sizes() == W1.sizes() && zu.sizes() == at::IntArrayRef({2, T, H}),
+                "a saved tensor of gated_up came back with another shape");
+    Tensor dh = grads[0].defined() ? grads[0] : at::zeros({T, H}, x.options());
     if (!pitch(dh, &lddh)) {  // an expanded gradient, say
       dh = dh.contiguous();
       lddh = H;
     }
-    pitch(x, &ld);
     void* stream;
     const int device = device_of(x, &stream);
     TORCH_CHECK(device >= 0, "the tensors are not on the current device");
@@ -468,7 +479,7 @@ struct GatedUp : torch::autograd::Function<GatedUp> {
         any = true;
       }
     if (any) {
-      const float* z = saved[3].data_ptr<float>();
+      const float* z = zu.data_ptr<float>();
       TORCH_CHECK(run_gated_backward(dh, lddh, z, z + T * H, x, ld, W1, W3, out[0], out[1], out[2],
                                      ctx->saved_data["act"].toInt(), device, stream) == SFFN_OK,
                   g.last_error());

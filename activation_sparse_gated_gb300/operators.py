@@ -561,6 +561,9 @@ class _GatedUp(torch.autograd.Function):
         if torch.cuda.is_current_stream_capturing():
             raise ValueError("the backward pass of gated_up is not captured: gated_up_backward is")
         x, W1, W3, z, u = ctx.saved_tensors
+        W1, W3, z, u = (t.contiguous() for t in (W1, W3, z, u))  # hooks on saved tensors may change their layout
+        if x.stride(1) != 1:
+            x = x.contiguous()
         if dh.stride(1) != 1 or dh.stride(0) < dh.shape[1]:  # an expanded gradient, say
             dh = dh.contiguous()
         return (*gated_up_backward(dh, z, u, x, W1, W3, ctx.act, ctx.needs_input_grad[:3]), None)

@@ -495,6 +495,31 @@ def test_int4_groups_that_no_scale_has_are_refused():
                 call()
 
 
+def test_autograd_through_hooks_on_saved_tensors():
+    g = gen(43)
+    x, W1, W3 = (randn(g, *s).requires_grad_() for s in ((30, 64), (48, 64), (48, 64)))
+    dh = randn(g, 30, 48)
+    sffn.gated_up(x, W1, W3, act="silu").backward(dh)
+    ref = [t.grad.clone() for t in (x, W1, W3)]
+    ways = {
+        "moved": (lambda t: t.cpu(), lambda t: t.to(DEV)),
+        "transposed": (lambda t: t.transpose(-1, -2).contiguous(), lambda t: t.transpose(-1, -2)),
+        "spread": (lambda t: t.repeat_interleave(2, -1), lambda t: t[..., ::2])}
+    for pack, back in ways.values():
+        for t in (x, W1, W3):
+            t.grad = None
+        with torch.autograd.graph.saved_tensors_hooks(pack, back):
+            h = sffn.gated_up(x, W1, W3, act="silu")
+        h.backward(dh)
+        for t, r in zip((x, W1, W3), ref):
+            assert torch.equal(t.grad, r)
+    for back in (lambda t: t.cpu(), lambda t: t.double(), lambda t: t[..., :40].contiguous(), lambda t: t[:1]):
+        with torch.autograd.graph.saved_tensors_hooks(lambda t: t, back):
+            h = sffn.gated_up(x, W1, W3, act="silu")
+        with pytest.raises(RuntimeError, match="saved tensor|shape|device"):
+            h.backward(dh)
+
+
 def test_gated_up_refuses_what_it_cannot_record():
     g = gen(24)
     x, W1, W3 = randn(g, 4, 64).requires_grad_(), randn(g, 8, 64), randn(g, 8, 64)
