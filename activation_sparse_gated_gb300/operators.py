@@ -92,7 +92,8 @@ def _has_tangent(t):
 
 def _operand(name, t, dtypes, dim, device=None, grad=False):
     if (isinstance(t, torch.Tensor) and t.ndim == dim and t.dtype in dtypes and t.is_cuda
-            and (device is None or t.device == device) and not t.requires_grad and not _has_tangent(t)):
+            and (device is None or t.device == device) and not t.requires_grad and not _has_tangent(t)
+            and max(t.shape, default=0) < 2 ** 31):
         return
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
@@ -100,6 +101,8 @@ def _operand(name, t, dtypes, dim, device=None, grad=False):
         raise ValueError(f"{name} must have {dim} dimensions, not {t.dim()}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} has type {t.dtype}, not {' or '.join(str(d) for d in dtypes)}")
+    if max(t.shape, default=0) >= 2 ** 31:  # the calls below take 32-bit sizes
+        raise ValueError(f"{name} has more than 2^31 - 1 rows or columns")
     if _has_tangent(t):
         raise ValueError(f"{name} has a forward-mode tangent: the operators have none")
     if not t.is_cuda:

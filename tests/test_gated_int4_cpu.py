@@ -155,3 +155,15 @@ def test_tensor_wrappers_refuse():
         sffn.Int4FFN(w, w, w)
     with pytest.raises(ValueError, match="act"):
         sffn.Int4FFN(w, w, w.T, act="gelu")
+
+
+def test_tensor_wrappers_refuse_sizes_past_32_bits():
+    torch = pytest.importorskip("torch")
+    far = 2 ** 32 + 4  # 4 in 32 bits
+    x, w = (torch.empty(n, 64, dtype=torch.bfloat16, device="meta") for n in (far, 8))
+    q, s = torch.empty(far, 32, dtype=torch.uint8, device="meta"), torch.empty(far, 1, device="meta")
+    for make in (lambda: sffn.quantize_int4(x), lambda: sffn.dequantize_int4(q, s), lambda: sffn.matmul_int4(x, q[:8], s[:8]),
+                 lambda: sffn.gated_up_int4(x, q[:8], s[:8], q[:8], s[:8]), lambda: sffn.gated_up(x, w, w),
+                 lambda: sffn.gated_up_saved(x, w, w), lambda: sffn.quantize_tokens(x)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            make()
