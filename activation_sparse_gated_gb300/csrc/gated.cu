@@ -125,6 +125,84 @@ cudaError_t rows_go(const GatedArgs& a, cudaStream_t s) {
                            : ops_launch(gated_rows_kernel<TM, UN, false>, grid, 32 * GU_WARPS, 0, s, 1, a);
 }
 
+// The 2-norm of a row, or a little more, by a warp; norms past 2^63 count as that (a product of two stays in fp32), those of
+// rows that hold an infinity or a NaN, whose sums no second sum betters, as 0.
+__device__ __forceinline__ float row_norm(const uint16_t* row, int D) {
+  const uint4* p = reinterpret_cast<const uint4*>(row);
+  const int lane = threadIdx.x & 31, n = D / 8;
+  float scale = 1.f;
+  for (;;) {
+    float2 acc[4] = {};
+    float top = 0.f;
+    for (int k0 = lane; k0 < n; k0 += 320) {
+      uint4 c[10];
+#pragma unroll
+      for (int q = 0; q < 10; ++q) c[q] = k0 + 32 * q < n ? __ldg(p + k0 + 32 * q) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int q = 0; q < 10; ++q) {
+        float v[8];
+        Elt<bf16_tag>::unpack(c[q], v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          top = fmaxf(top, fabsf(v[j]));
+          v[j] *= scale;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = make_float2(v[2 * j], v[2 * j + 1]);
+          ffma2(acc[j], f, f);
+        }
+      }
+    }
+    const float sum = warp_sum((acc[0].x + acc[0].y + acc[1].x + acc[1].y) + (acc[2].x + acc[2].y + acc[3].x + acc[3].y));
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+    if (sum != sum || !(top < 3.4e38f) || top == 0.f) return 0.f;
+    if (scale != 1.f || (sum > 0x1p-80f && sum < 0x1p120f)) return fminf(1.001f * sqrtf(sum) / scale, 0x1p63f);
+    scale = top < 1.f ? 0x1p100f : 0x1p-100f;  // squares that left fp32: once more, of values that do not
+  }
+}
+
+// |x| of every token and c |w| of every unit of W1, for the signs of the gates (gate_near in gmm_tc.cu).  A caller of the block
+// gives no scratch, so they wait in z and u themselves, where the warp that stores a piece of a tile reads them first: each 32
+// columns of z hold the norms of the GATE_ROWS tokens from their row on (narrower, a column holds the largest of those
+// that share it), and the rows of u that a tile's two halves of the epilogue's warps begin with (tiles of `per` rows) their
+// units'.  Bound by memory: x and W1 in, which the product then finds in L2, and 1 / 32 of z out.  A block takes GATE_ROWS
+// tokens, or as many units, a warp a row of them.
+struct NormArgs {
+  const uint16_t *x, *W1;
+  long long ldx, ldz;
+  float *z, *u;
+  int T, D, H, per, tokens;  // tokens: blocks of them
+  float c;
+};
+__global__ void __launch_bounds__(32 * GATE_ROWS, 2) gate_norms_kernel(const NormArgs a) {
+  __shared__ float s_norm[GATE_ROWS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = threadIdx.x & (GATE_ROWS - 1), slot = threadIdx.x / GATE_ROWS;
+  const bool of_x = blockIdx.x < (unsigned)a.tokens;
+  const int r0 = (of_x ? blockIdx.x : blockIdx.x - a.tokens) * GATE_ROWS;
+  pdl_launch_dependents();
+  pdl_wait();
+  float v = 0.f;
+  if (of_x && r0 + warp < a.T) v = row_norm(a.x + (long long)(r0 + warp) * a.ldx, a.D);
+  if (!of_x && r0 + warp < a.H) v = a.c * row_norm(a.W1 + (size_t)(r0 + warp) * a.D, a.D);
+  if (lane == 0) s_norm[warp] = v;
+  __syncthreads();
+  if (of_x) {
+    float* z = a.z + (long long)r0 * a.ldz;
+    for (int c = slot * 32; c < a.H; c += 32 * 32) {
+      const int cols = min(32, a.H - c);
+      v = s_norm[l];
+      for (int i = l + cols; i < GATE_ROWS; i += cols) v = fmaxf(v, s_norm[i]);
+      if (l < cols) z[c + l] = v;
+    }
+  } else if (r0 + l < a.H) {
+    for (long long i = slot; (i >> 1) * a.per < a.T; i += 32) {
+      const long long r = (i >> 1) * a.per + 32 * (i & 1);
+      if (r < a.T) a.u[r * a.ldz + r0 + l] = s_norm[l];
+    }
+  }
+}
+
 // dz = dh u A'(z) and du = dh A(z) of one element.  A gate that is closed passes nothing, whatever dh and the other factor
 // are: both are 0 where z <= 0 (ReLU, R-S+), and SiLU's are where its value or its slope is 0 in fp32.
 __device__ __forceinline__ float2 gate_grad(int act, float z, float u, float dh) {
@@ -218,6 +296,14 @@ cudaError_t launch_gated_up(const GatedArgs& a, cudaStream_t s) {
   p.u = a.u;
   p.ldz = a.ldz;
   return launch_gmm(p, s);
+}
+
+cudaError_t launch_gate_norms(const GmmArgs& a, int per, cudaStream_t s) {
+  const NormArgs n = {static_cast<const uint16_t*>(a.x), static_cast<const uint16_t*>(a.w), a.ldx, a.ldz, a.z, a.u, a.R, a.K, a.N,
+                      per, (a.R + GATE_ROWS - 1) / GATE_ROWS,
+                      // what the MMAs' steps of 16 cut off of the running sums, and the join of a cut K, see gate_near
+                      (float)(2 * ((a.K + 63) / 64) + 8) * 0x1p-24f};
+  return ops_launch(gate_norms_kernel, dim3((unsigned)(n.tokens + (a.N + GATE_ROWS - 1) / GATE_ROWS)), 32 * GATE_ROWS, 0, s, 1, n);
 }
 
 size_t gated_grad_workspace(int T, int H) { return sizeof(uint16_t) * 2 * (size_t)T * padded(H); }

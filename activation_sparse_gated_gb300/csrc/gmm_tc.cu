@@ -343,81 +343,108 @@ __device__ __forceinline__ float gate_up(int act, float z, float u) {
   return (act == ACT_SILU ? g == 0.f : z <= 0.f) ? 0.f : g * u;
 }
 
-// The product of a row of x and one of w by a whole warp, in fp32.
+// The product of a row of x and one of w by a whole warp, its sum's rounding errors kept beside it (each addition's, exactly,
+// by Knuth's two-sum): the products of bf16 values are exact in fp32 (above its subnormals), so the result is the exact
+// sum's rounding but where that is some 2^-40 of the terms or less.
 __device__ __noinline__ float warp_dot(const uint16_t* x, const uint16_t* w, int K) {
-  float2 acc = make_float2(0.f, 0.f);
-  for (int k = (threadIdx.x & 31) * 8; k < K; k += 256) {
+  float2 sum = make_float2(0.f, 0.f), rest = sum;
+  const float2 minus = make_float2(-1.f, -1.f);
+  auto less = [&](float2 a, float2 b) {  // a - b
+    ffma2(a, b, minus);
+    return a;
+  };
+  auto add = [&](const uint4& p, const uint4& q) {
     float a[8], b[8];
-    Elt<bf16_tag>::unpack(__ldg(reinterpret_cast<const uint4*>(x + k)), a);
-    Elt<bf16_tag>::unpack(__ldg(reinterpret_cast<const uint4*>(w + k)), b);
+    Elt<bf16_tag>::unpack(p, a);
+    Elt<bf16_tag>::unpack(q, b);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) ffma2(acc, make_float2(a[2 * j], a[2 * j + 1]), make_float2(b[2 * j], b[2 * j + 1]));
+    for (int j = 0; j < 4; ++j) {
+      float2 v = make_float2(0.f, 0.f);
+      ffma2(v, make_float2(a[2 * j], a[2 * j + 1]), make_float2(b[2 * j], b[2 * j + 1]));
+      const float2 t = fadd2(sum, v), got = less(t, sum);
+      rest = fadd2(rest, fadd2(less(sum, less(t, got)), less(v, got)));
+      sum = t;
+    }
+  };
+  for (int k0 = (threadIdx.x & 31) * 8; k0 < K; k0 += 2048) {  // eight pieces of both rows in flight
+    uint4 a[8], b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int k = k0 + 256 * i;
+      a[i] = k < K ? __ldg(reinterpret_cast<const uint4*>(x + k)) : make_uint4(0, 0, 0, 0);
+      b[i] = k < K ? __ldg(reinterpret_cast<const uint4*>(w + k)) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) add(a[i], b[i]);
   }
-  return warp_sum(acc.x + acc.y);
+  double v = ((double)sum.x + (double)sum.y) + ((double)rest.x + (double)rest.y);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return (float)v;
 }
 
-// Signs of a gate's inputs that are kept for the backward pass (32 tokens from row r0 of x on, the lane's unit n; val: their z).
-// ReLU and R-S+ let a unit's gradients pass or not by the sign of z, and an MMA cuts its running sum off at every step: z near
-// 0 is off by up to 2^-24 of the sums' magnitude a step, all one way, and a unit that passes wrongly is off by all of its
-// term (8192 tokens, D = 2560, H = 7168, ReLU: relative error of dx 0.0034, with this 0.0024, which is dz's and dx's own
-// rounding).  So a z that is that small next to its unit's largest is computed again on the CUDA cores, one in some ten
-// thousand.  A token most of whose units are small is small itself, and left as it is, as is a z of exactly 0.
-__device__ __forceinline__ void refine_gate(const GmmArgs& g, const uint32_t (&val)[32], int e, int r0, int left, int n, bool nok,
-                                            float* z, int steps) {
-  const int lane = threadIdx.x & 31;
-  float top = 0.f, least = 3e38f;
-  if (left == 32) {
+// Signs of a gate's inputs that are kept for the backward pass.  ReLU and R-S+ let a unit's gradients pass or not by the sign of
+// z, a unit that passes wrongly is off by all of its term, and an MMA cuts its running sum off at every step of 16.  So a z
+// whose sign that may have turned is computed again on the CUDA cores, and h of it: some z in ten thousand.  A step cuts off up
+// to 2^-23 of the running sum, half of that on average, and the running sums of a z next to 0 are at most |x| |w| / 2 (2-norms, by
+// Cauchy and Schwarz: what is summed before and after a step cancel), so a z below steps * 2^-25 |x| |w| is one.  (MMA sums
+// were found off by a third of that at most, running sums that rise to half of |x| |w| and fall among them.  8192
+// tokens, D = 2560, H = 7168: of 235 million signs some 70 are wrong without, none with it, and 14 of plain fp32 sums.  The
+// call takes 418 us with it, 377 without: the norms 17, this and refine_gate 13, norms and product apart the rest.)
+//
+// gate_near: which z (val: of 32 tokens and the lane's unit) those are, a bit each.  wn: |w| of the lane's unit times that factor,
+// tn: |x| of the lane's token; 0 where there is none.
+__device__ __forceinline__ uint32_t gate_near(const uint32_t (&val)[32], float wn, float tn) {
+  const float limit = wn * __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(tn)));
+  float least = 3e38f;  // (columns past the rows hold anything: looked at below)
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      top = fmaxf(top, fabsf(__uint_as_float(val[j])));
-      least = fminf(least, fabsf(__uint_as_float(val[j])));
-    }
-  } else {  // (columns past the rows hold anything)
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < left) {
-        top = fmaxf(top, fabsf(__uint_as_float(val[j])));
-        least = fminf(least, fabsf(__uint_as_float(val[j])));
-      }
-  }
-  const float limit = top * (float)steps * 0x1p-24f;
-  if (!__any_sync(0xffffffffu, nok && least < limit)) return;
+  for (int j = 0; j < 32; ++j) least = fminf(least, fabsf(__uint_as_float(val[j])));
+  if (!__any_sync(0xffffffffu, least < limit)) return 0;
   uint32_t near = 0;
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    const float a = fabsf(__uint_as_float(val[j]));
-    if (nok && j < left && a > 0.f && a < limit) near |= 1u << j;
-  }
+  for (int j = 0; j < 32; ++j)
+    if (fabsf(__uint_as_float(val[j])) < wn * __shfl_sync(0xffffffffu, tn, j)) near |= 1u << j;
+  return near;
+}
+
+// Those z again, and h: 32 tokens from row r0 of x on, the lane's unit n.  This comes when a tile's accumulator is free: it is
+// hidden behind the next tile's MMAs.
+__device__ __forceinline__ void refine_gate(const GmmArgs& g, uint32_t near, int r0, int n) {
+  const int lane = threadIdx.x & 31;
   for (uint32_t some = __reduce_or_sync(0xffffffffu, near); some != 0; some &= some - 1) {
     const int j = __ffs((int)some) - 1;
-    uint32_t who = __ballot_sync(0xffffffffu, near >> j & 1);
-    if (__popc(who) > 4) continue;
-    for (; who != 0; who &= who - 1) {
+    const uint64_t r = (uint64_t)(uint32_t)(r0 + j);
+    for (uint32_t who = __ballot_sync(0xffffffffu, near >> j & 1); who != 0; who &= who - 1) {
       const int l = __ffs((int)who) - 1, unit = __shfl_sync(0xffffffffu, n, l);
-      const float v = warp_dot(static_cast<const uint16_t*>(g.x) + (long long)(r0 + j) * g.ldx,
-                               static_cast<const uint16_t*>(g.w) + ((size_t)e * g.N + unit) * g.K, g.K);
-      if (lane == l) z[(uint64_t)j * (uint64_t)g.ldz + lane] = v;
+      const float z = warp_dot(static_cast<const uint16_t*>(g.x) + r * (uint64_t)g.ldx,
+                               static_cast<const uint16_t*>(g.w) + (size_t)unit * g.K, g.K);
+      if (lane == l) {
+        const uint64_t o = r * (uint64_t)g.ldz + unit;
+        g.z[o] = z;
+        static_cast<__nv_bfloat16*>(g.y)[r * (uint64_t)g.ldy + unit] = __float2bfloat16_rn(gate_up(g.act, z, g.u[o]));
+      }
     }
   }
 }
 
-// The same of one token r, four units a lane from n on (v: their z), by the token's largest alone.
-__device__ __forceinline__ void refine_row(const GmmArgs& g, float (&v)[4], int e, int r, int n, int steps) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-  const float limit = __uint_as_float(__reduce_max_sync(0xffffffffu, top)) * (float)steps * 0x1p-24f;
+// Both for one token r, four units a lane from n on (v: their z), at once.
+__device__ __forceinline__ void refine_row(const GmmArgs& g, float (&v)[4], int r, int n, const float (&wn)[4], float tn) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t who = __ballot_sync(0xffffffffu, n + i < g.N && fabsf(v[i]) > 0.f && fabsf(v[i]) < limit);
-    if (__popc(who) > 4) continue;
+    uint32_t who = __ballot_sync(0xffffffffu, fabsf(v[i]) < wn[i] * tn);
     for (; who != 0; who &= who - 1) {
       const int l = __ffs((int)who) - 1, unit = __shfl_sync(0xffffffffu, n + i, l);
       const float z = warp_dot(static_cast<const uint16_t*>(g.x) + (long long)r * g.ldx,
-                               static_cast<const uint16_t*>(g.w) + ((size_t)e * g.N + unit) * g.K, g.K);
+                               static_cast<const uint16_t*>(g.w) + (size_t)unit * g.K, g.K);
       if ((threadIdx.x & 31) == l) v[i] = z;
     }
   }
+}
+
+// |x| of row r (from row q0, a multiple of GATE_ROWS, on: q0 + r), left in z by gate_norms_kernel for the piece of columns from c on.
+__device__ __forceinline__ float token_norm(const GmmArgs& g, int q0, int r, int c) {
+  const int l = r & (GATE_ROWS - 1), cols = min(32, g.N - c);
+  return __ldcg(g.z + (uint64_t)(uint32_t)(q0 + r - l) * (uint64_t)g.ldz + c + (cols < GATE_ROWS ? l % cols : l));
 }
 
 // XT: x is [K, rows], read as the KN weights are: boxes of 64 values of K by 64 rows, MN-major.
@@ -776,6 +803,17 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
       const uint32_t b = p.nacc == 2 ? tl & 1 : 0, use = p.nacc == 2 ? tl >> 1 : tl;
       const int n = q.mt * 128 * CTAS + n0r + 32 * (ew & 3) + lane;
       const bool nok = n < p.g.N;
+      // for the signs of the gates: |x| of the lane's token of the next piece, |w| of the lane's unit (see gate_near)
+      const bool signs = TRAIN && p.g.act != ACT_SILU;
+      float tn = 0.f, wn = 0.f;
+      auto next_norm = [&](int c0) {
+        tn = signs && n - lane < p.g.N && c0 + lane < q.r1 - q.r0 ? token_norm(p.g, q.r0, c0 + lane, n - lane) : 0.f;
+      };
+      if (TRAIN && ks == 1) {
+        const int c0 = 32 * (ew >> 2);
+        if (signs && nok && c0 < q.r1 - q.r0) wn = __ldcg(p.g.u + (uint64_t)(uint32_t)(q.r0 + c0) * (uint64_t)p.g.ldz + n);
+        next_norm(c0);
+      }
       if (!__all_sync(0xffffffffu, tg_wait<false>(&accf[b], use & 1, abort_flag, p.err))) break;
       tc_fence_after();
       const uint32_t ta = tmem + b * (uint32_t)((GATED ? 2 : 1) * p.NT) + ((uint32_t)(32 * (ew & 3)) << 16);
@@ -788,6 +826,17 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
         // (their copies and MMAs are done, and the producers wait for `partd`); then each sums its share of the
         // rows over the blocks in their order, so the result does not depend on timing.  Gate and up: two tiles.
         const uint32_t up = (uint32_t)(p.NT * TG_PART) * 4u;
+        const int t0 = (int)((long long)rows * kr / ks), t1 = (int)((long long)rows * (kr + 1) / ks);
+        const int nc = q.mt * 128 + 4 * lane;
+        // norms, of the lane's four units and of the warp's rows (the i-th's in lane i), are read before the blocks meet: z
+        // and u are written only after that
+        float w4[4] = {};
+        if (signs) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (nc + i < p.g.N) w4[i] = __ldcg(p.g.u + (uint64_t)(uint32_t)q.r0 * (uint64_t)p.g.ldz + nc + i);
+          if (t0 + ew + EW * lane < t1) tn = token_norm(p.g, q.r0, t0 + ew + EW * lane, q.mt * 128);
+        }
         for (int c0 = 32 * (ew >> 2); c0 < rows; c0 += 32 * (EW / 4)) {
 #pragma unroll
           for (int h = 0; h < (GATED ? 2 : 1); ++h) {
@@ -804,8 +853,6 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
         if (lane == 0) mbar_arrive(&acce[b]);
         if (lane < ks) arrive_remote(cluster_map(smem_u32(partf), (uint32_t)lane));
         if (!__all_sync(0xffffffffu, tg_wait<true>(partf, tl & 1, abort_flag, p.err))) break;
-        const int t0 = (int)((long long)rows * kr / ks), t1 = (int)((long long)rows * (kr + 1) / ks);
-        const int nc = q.mt * 128 + 4 * lane;
         float s4[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) s4[i] = F16 && nc + i < p.g.N ? p.g.sw[(size_t)q.e * p.g.N + nc + i] : 1.f;
@@ -832,7 +879,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
             float u[4];
             sum_of(at + up, u);
             if constexpr (TRAIN) {
-              if (p.g.act != ACT_SILU) refine_row(p.g, f, q.e, q.r0 + r, nc, 4 * p.KC);
+              if (signs) refine_row(p.g, f, q.r0 + r, nc, w4, __shfl_sync(0xffffffffu, tn, (r - t0 - ew) / EW));
               const uint64_t o = (uint64_t)(uint32_t)(q.r0 + r) * (uint64_t)p.g.ldz + nc;
 #pragma unroll
               for (int i = 0; i < 4; ++i)
@@ -870,6 +917,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
         if (t + step < total && !__all_sync(0xffffffffu, tg_wait<true>(partd, tl & 1, abort_flag, p.err))) break;
         continue;
       }
+      uint32_t near[4] = {};  // TRAIN: the z to compute again, a piece each
       for (int c0 = 32 * (ew >> 2); c0 < rows; c0 += 32 * (EW / 4)) {
         uint32_t v[32];
         tmem_ld32(ta + c0, v);
@@ -901,7 +949,7 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
           tmem_ld_wait();
           done();
           if constexpr (TRAIN) {
-            // kept as they are, in fp32: a token's 32 units are 128 bytes, stored by the lanes as they have them
+            // kept in fp32: a token's 32 units are 128 bytes, stored by the lanes as they have them
             const uint64_t z0 = (uint64_t)(uint32_t)(q.r0 + c0) * (uint64_t)p.g.ldz + (q.mt * 128 * CTAS + n0r + 32 * (ew & 3));
             const bool whole = left == 32 && __all_sync(0xffffffffu, nok);
             auto keep = [&](const uint32_t (&val)[32], float* to) {
@@ -915,10 +963,17 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
                   if (nok && j < left) to[(uint64_t)j * (uint32_t)p.g.ldz] = __uint_as_float(val[j]);
               }
             };
+            if (signs) {
+              const float now = tn;
+              next_norm(c0 + 32 * (EW / 4));
+              const uint32_t piece = gate_near(v, wn, now);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (c0 >> 6 == i) near[i] = piece;
+              __syncwarp();  // the norms are read
+            }
             keep(v, p.g.z + z0);
             keep(u, p.g.u + z0);
-            __syncwarp();
-            if (p.g.act != ACT_SILU) refine_gate(p.g, v, q.e, q.r0 + c0, left, n, nok, p.g.z + z0, 4 * p.KC);
           }
           if (p.g.act == 0) {  // hoisted: as a branch of each value ReLU pays for the others
 #pragma unroll
@@ -1003,6 +1058,11 @@ __global__ void __launch_bounds__(MODE == TG_I8 ? TG_THREADS_I8 : TG_THREADS, 1)
             to += pitch;
           }
         }
+      }
+      if constexpr (TRAIN) {
+        __syncwarp();  // h is stored
+#pragma unroll
+        for (int i = 0; i < 4; ++i) refine_gate(p.g, near[i], q.r0 + 32 * (ew >> 2) + 64 * i, n);
       }
       if (32 * (ew >> 2) >= rows) {  // no columns for this warp
         tc_fence_before();
@@ -1159,6 +1219,10 @@ cudaError_t launch_gmm_tc(const GmmArgs& a, int ctas, int nt, cudaStream_t s) {
   const int sms = ops_num_sms();
   if (a.i8) return tg_go<1, TG_I8, false>(mW, mW3, mX, mXb, p, smem, sms, s);
   if (a.f16) return tg_go<2, TG_F16, false>(mW, mW3, mX, mXb, p, smem, sms, s);
+  if (a.z && a.act != ACT_SILU) {  // norms for the signs of the gates; the rows of a tile are tile_at's
+    const int tiles = (a.R + nt - 1) / nt, q = 16 * ctas;
+    if ((e = launch_gate_norms(a, ((a.R + tiles - 1) / tiles + q - 1) / q * q, s)) != cudaSuccess) return e;
+  }
   if (a.z)
     return ctas == 2 ? tg_go<2, TG_TRAIN, false>(mW, mW3, mX, mXb, p, smem, sms, s)
                      : tg_go<1, TG_TRAIN, false>(mW, mW3, mX, mXb, p, smem, sms, s);

@@ -44,7 +44,7 @@ struct GmmArgs {
   int i8 = 0, y_f32 = 0, kn = 0, act = 0;
   int NY = 0;                     // columns of y that may be written (past N: zeros), if more than N
   int f16 = 0;                    // x and w are fp16 copies of int8 codes (with their scales)
-  float *z = nullptr, *u = nullptr;  // gated: the two products themselves, fp32, row pitch ldz (NY columns)
+  float *z = nullptr, *u = nullptr;  // gated: the two products themselves, fp32, row pitch ldz
   long long ldz = 0;
   int split = 0;                  // w's rows hold two parts of round_up(K, 64) columns each, both multiplied by x
   int K1 = 0;                     // kn: rows 0 .. K1 of K are w's, rows K / 2 .. K / 2 + K1 w3's (K / 2 = round_up(K1, 64))
@@ -54,8 +54,10 @@ struct GmmArgs {
   long long ldw = 0;              // kn: row pitch of w, if not N
   void* workspace = nullptr;      // gmm_workspace() bytes
 };
+constexpr int GATE_ROWS = 16;  // rows of z whose norms are side by side; a tile of x starts at a multiple of it
 cudaError_t launch_gmm_rows(const GmmArgs& a, cudaStream_t s);
 cudaError_t launch_gmm_tc(const GmmArgs& a, int ctas, int nt, cudaStream_t s);  // ctas 1 or 2, nt 32 .. 256 (gated: 128)
+cudaError_t launch_gate_norms(const GmmArgs& a, int per, cudaStream_t s);  // gated.cu; per: rows of x a tile
 cudaError_t launch_gmm(const GmmArgs& a, cudaStream_t s);
 size_t gmm_workspace(int R, int XR, int N, int K, int E, int i8);
 

@@ -495,7 +495,8 @@ int sffn_gated_up_int4(const void* x, long long ldx, const uint8_t* w1, const fl
  * 0 is exactly 0 whatever its up value, a NaN gate is live; many tokens use the device's
  * fast exponential and quotient (2^-15).  z and u (both or neither) receive the two
  * products in f32 (row pitch ldz), which the backward pass takes; for ReLU and R-S+, whose
- * gradients go by the sign of z, a z next to 0 is a sum of the CUDA cores', not the tensor cores'.
+ * gradients go by the sign of z, a z so near 0 that the tensor cores' sum may have the wrong sign
+ * is computed again: the exact sum, rounded (and h is of it).
  *
  * The backward pass, from dh, the gradient of h [T, H] (bf16, row pitch lddh):
  *     dz = dh u A'(z),  du = dh A(z)
