@@ -427,6 +427,8 @@ int run_gated_backward(const Tensor& dh, int64_t lddh, const float* z, const flo
                              at_of(dW1), at_of(dW3), (int)T, (int)D, (int)H, (int)act, at_of(scratch), nb, stream);
 }
 
+struct Refused {};  // the library does not take a call: operators.py raises its error
+
 // gated_up with its gradient.  z and u, one buffer of [2, T, H], stay in fp32 for the backward pass.
 struct GatedUp : torch::autograd::Function<GatedUp> {
   static Tensor forward(torch::autograd::AutogradContext* ctx, const Tensor& x, const Tensor& W1, const Tensor& W3,
@@ -438,7 +440,7 @@ struct GatedUp : torch::autograd::Function<GatedUp> {
     const int64_t T = x.size(0), H = W1.size(0);
     Tensor h = make({T, H}, at::kBFloat16, device), zu = make({2, T, H}, at::kFloat, device);
     float* z = zu.data_ptr<float>();
-    TORCH_CHECK(run_gated(x, ld, W1, W3, h, z, z + T * H, act, stream) == SFFN_OK, g.last_error());
+    if (run_gated(x, ld, W1, W3, h, z, z + T * H, act, stream) != SFFN_OK) throw Refused();
     ctx->save_for_backward({x, W1, W3, zu});
     ctx->saved_data["act"] = act;
     return h;
@@ -507,7 +509,11 @@ PyObject* gated_up(PyObject* const* args, Py_ssize_t n) {
         a.D % 8 || a.ld % 8 || a.H < 1 || act < SFFN_ACT_RELU || act > SFFN_ACT_SILU ||
         (((uintptr_t)a.x->data_ptr() | (uintptr_t)a.W1->data_ptr() | (uintptr_t)a.W3->data_ptr()) & 15))
       return none();  // refused, or not recorded: operators.py says why
-    return THPVariable_Wrap(GatedUp::apply(*a.x, *a.W1, *a.W3, act));
+    try {
+      return THPVariable_Wrap(GatedUp::apply(*a.x, *a.W1, *a.W3, act));
+    } catch (const Refused&) {
+      return none();
+    }
   }
   Tensor h = make({a.T, a.H}, at::kBFloat16, a.device);
   if (run_gated(*a.x, a.ld, *a.W1, *a.W3, h, nullptr, nullptr, act, a.stream) != SFFN_OK) return none();
