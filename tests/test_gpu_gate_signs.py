@@ -147,3 +147,20 @@ def test_signs_in_a_captured_step_and_on_two_streams():
     many = [sffn.gated_up_saved(x, W1, W3, stream=s) for _ in range(6) for s in streams]
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for r in many for a, b in zip(r, want))
+
+
+@pytest.mark.parametrize("T,H", [(1, 9000), (50, 9001), (50, 77), (600, 2100)])
+def test_results_with_pitches_of_their_own(T, H):
+    """z, u and h in rows that are longer than they are and start anywhere: what lies between stays."""
+    g = gen(11)
+    D, ld = 520, H + 37
+    x, W1 = cancelling(g, T, D, H)
+    W3 = randn(g, H, D)
+    h, z, u = (torch.full((T, ld), 5.0, dtype=t, device=DEV) for t in (BF, torch.float32, torch.float32))
+    rc = sffn.load().sffn_gated_up(x.data_ptr(), D, W1.data_ptr(), W3.data_ptr(), h.data_ptr() + 2 * 3, ld, z.data_ptr() + 4 * 5,
+                                   u.data_ptr() + 4 * 7, ld, T, D, H, 0, torch.cuda.current_stream().cuda_stream)
+    assert rc == sffn.SFFN_OK
+    want = sffn.gated_up_saved(x, W1, W3)
+    for t, first, w in ((h, 3, want[0]), (z, 5, want[1]), (u, 7, want[2])):
+        assert torch.equal(t[:, first:first + H], w)
+        assert (t[:, :first] == 5).all() and (t[:, first + H:] == 5).all()
