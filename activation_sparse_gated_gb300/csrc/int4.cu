@@ -37,7 +37,8 @@ __device__ __forceinline__ int group_of(int c, uint32_t magic) { return (int)(((
 // / s, r = v - q s is exact in a fused multiply-add, and q + r inv then rounds to the quotient, ties and all (s = max / 7 of a
 // bf16 value is never just below a power of two, the theorem's exception).  1.5 * 2^23 + quotient rounds to an integer, to
 // even, whose low nibble is the code.  (Ties are common: half a group's maximum is 3.5 scales.  Deciding by v inv alone and
-// dividing what lies near a half took 40.5 us for 14336 x 4096 weights, so often did some lane divide; this takes 28.9.)
+// dividing what lies near a half took 40.5 us for 14336 x 4096 weights, so often did some lane divide; this, with nothing else
+// changed, 28.9.)
 __device__ __forceinline__ uint32_t codes8(const uint4& c, float s, float inv) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
   if (!(s > 1e-30f && s < 1e30f)) {  // out of the theorem's range: the residual or inv may underflow
@@ -298,11 +299,12 @@ __global__ void __launch_bounds__(32 * I4_WARPS) dequantize_int4_kernel(const Va
 //
 // Up to eight tokens (int4_rows_kernel; up to sixteen with two tiles of tokens, NT): a block takes 16 rows of w (of both
 // matrices, GATED), its W warps take pairs of chunks in turn, and their sums meet in shared memory and are added in the warps'
-// order.  Measured (us in a graph, one token): 7168 x 2560 4.9 (2.1 TB/s; 2.1 of it a launch), 14336 x 4096 11.0 (3.0 TB/s),
-// 2560 x 7168 5.7, 13 tokens 8.0; gated, two 7168 x 2560 7.9.  What bounds it is instructions and their latency: some 70 a chunk of 16 rows, 44
-// of them the codes.  Loads that no condition guards (a token past T reads the last one's x, missing columns are the last
-// pair's alone) took a third of them out (gated 10.3 -> 7.9).  Not faster: sixteen bytes of codes a lane and halves traded
-// between lanes, one pair at a time, a warp's codes and x through a TMA ring (7168 x 2560 6.6).
+// order.  Measured (us a call in a graph, the same codes again, from L2; one token): 7168 x 2560 4.5 (2.1 of it a launch), 14336 x
+// 4096 9.0, 2560 x 7168 5.5, 13 tokens 7.7; gated, two 7168 x 2560 5.7; codes from memory: 14336 x 4096 11.0 (3.0 TB/s).  What
+// bounds it is instructions and their latency: some 70 a chunk of 16 rows, 44 of them the codes.  Loads that no condition
+// guards (a token past T reads the last one's x, missing columns are the last pair's alone) took a third of them out (gated,
+// codes from memory, 10.3 -> 7.9).  Not faster: sixteen bytes of codes a lane and halves traded between lanes, one pair at a time,
+// a warp's codes and x through a TMA ring (7168 x 2560 6.6).
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm(

@@ -432,7 +432,8 @@ def _hidden(out, T, H, device):
 
 def gated_up_int4(x, w1q, s1, w3q, s3, group=64, act: str = "relu", out=None, stream=None):
     """h = A(x W1^T) * (x W3^T), bf16 [T, H], of bf16 tokens x [T, D] and 4-bit weights W1, W3 [H, D] (codes and scales as
-    for :func:`matmul_int4`)."""
+    for :func:`matmul_int4`).  More than 128 tokens (D not a multiple of 32: 32) go through bf16 copies of the weights, 16 H D
+    bytes during the call."""
     if stream is None and out is None and _calls is not None and act in _ACT:
         y = _calls.gated_up_int4(x, w1q, s1, w3q, s3, 0 if group is None else group or -1, _ACT[act])
         if y is not None:

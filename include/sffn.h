@@ -435,7 +435,7 @@ int sffn_grouped_matmul(const void* x, long long ldx, const float* sx, const voi
  * gate A(W1_e x_t) is 0 is dead and adds exactly 0, also where its up value is
  * infinite or NaN; a NaN gate is live, so a token that holds a NaN comes out as
  * NaN.  (Weights are taken to be finite: not every form reads those of a dead
- * unit.)  D % 8 == 0, any H >= 1.  x, W1, W3, W2t and y are 16-byte aligned and y
+ * unit.)  D % 8 == 0; D, H <= SFFN_MAX_SUM.  x, W1, W3, W2t and y are 16-byte aligned and y
  * overlaps no other argument; the workspace holds sffn_experts_workspace(T, k, D,
  * H) bytes, about 2 H + 4 D for every choice.
  */
@@ -474,11 +474,13 @@ int sffn_dequantize_int4(const uint8_t* codes, const float* scales, void* y, lon
  *     h [T, H] (row pitch ldh) bf16; a unit whose gate is 0 is exactly 0, a NaN gate
  *     is live.
  * Sums are fp32.  Few tokens (those that need no workspace, up to 32, 64 or 128) multiply
- * the codes themselves and round nothing but the result.  More tokens go through bf16 copies of
+ * the codes themselves and round nothing but the result; the scale comes after the sum of 64
+ * codes by x, which has to stay in fp32: |x| < 2^118.  More tokens go through bf16 copies of
  * the weights: two parts each, which hold a weight to 2^-16, for y in f32 and for the
  * gated block; one part, a rounding of each weight to bf16 (2^-8), for y in bf16.
  * The workspace holds sffn_int4_workspace(T, N, K, y_dtype, gated) bytes (gated: N = H,
- * K = D; 0 for few tokens: NULL is fine).
+ * K = D; 0 for few tokens: NULL is fine), the copies: 2 bytes a weight and part, four or eight
+ * times its code's.
  */
 size_t sffn_int4_workspace(int T, int N, int K, int y_dtype, int gated);
 int sffn_matmul_int4(const void* x, long long ldx, const uint8_t* wq, const float* sw, void* y, long long ldy, int T, int N,
@@ -491,7 +493,7 @@ int sffn_gated_up_int4(const void* x, long long ldx, const uint8_t* w1, const fl
  * The gated block, the first half of a gated FFN, in bf16 with fp32 sums:
  *     h[t, i] = A(z[t, i]) * u[t, i],   z = x W1^T,  u = x W3^T
  * x [T, D] (row pitch ldx, ldx % 8 == 0), W1 and W3 [H, D] dense, h [T, H] (row pitch
- * ldh); D % 8 == 0, any H >= 1; x, W1 and W3 16-byte aligned.  A unit whose gate A(z) is
+ * ldh); D % 8 == 0; D, H <= SFFN_MAX_SUM; x, W1 and W3 16-byte aligned.  A unit whose gate A(z) is
  * 0 is exactly 0 whatever its up value, a NaN gate is live; many tokens use the device's
  * fast exponential and quotient (2^-15).  z and u (both or neither) receive the two
  * products in f32 (row pitch ldz), which the backward pass takes; for ReLU and R-S+, whose
